@@ -45,7 +45,8 @@ typedef enum {
   DSA_ERR_WORKSPACE = 4,        /* workspace missing, too small or misaligned */
   DSA_ERR_CUDA = 5,             /* a CUDA runtime call or launch failed */
   DSA_ERR_DEVICE_INDEX = 6,     /* device saw an index outside [-1, T_k) (slot masked) */
-  DSA_ERR_TIMEOUT = 7           /* a bounded device-side wait gave up (CTA exited) */
+  DSA_ERR_TIMEOUT = 7,          /* a bounded device-side wait gave up (CTA exited) */
+  DSA_ERR_CAPACITY = 8          /* dsa_paged_slots: new tokens do not fit (no request got one) */
 } dsa_status_t;
 
 /* Text for a status code (static storage). */
@@ -437,6 +438,113 @@ dsa_status_t dsa_sparse_mla_bwd_noalloc(const dsa_bf16_t* q, const dsa_bf16_t* k
  * counterpart on the pages (library addition).
  */
 dsa_status_t dsa_sparse_mla_bwd_noalloc_read_status(dsa_stream_t stream, int32_t* status_host);
+
+/*
+ * The serving step: rows of a paged cache, prepared, selected and attended to.
+ *
+ * A paged cache is a contiguous bf16 array [num_pages, page_size, D]; request b's
+ * token at position p is row block_table[b, p / page_size] * page_size + p %
+ * page_size of it.  The calls read lengths and tables on the device and never
+ * synchronise, so a step can be captured into a graph and replayed while the
+ * lengths change.  For the same reason they do NOT clear the device error word of
+ * their workspace: zero the workspace's first 256 bytes once when it is made;
+ * the first failure stays there until dsa_read_device_status reads and clears it.
+ * One workspace serves one call at a time; calls on one stream may share it.
+ */
+
+/*
+ * dsa_paged_slots -- pages and cache rows of a step's new tokens, from the
+ * requests' lengths.  Request b holds s = seq_lens[b] tokens in ceil(s / P) pages
+ * and gets n = new_lens[b] more (1 when new_lens is NULL).  Its fresh pages, numbers
+ * ceil(s / P) .. ceil((s + n) / P) - 1 of block_table[b, :], are taken from
+ * free_pages in request order; other entries of the table are left as they are.
+ * The new tokens are packed in request order: token t = cu_new[b] + j has
+ *   positions[t] = s + j,
+ *   slot_map[t] = block_table[b, positions[t] / P] * P + positions[t] % P,
+ * and the entries t >= cu_new[B] are -1 in both.
+ *  seq_lens     device int32 [B], >= 0;  new_lens device int32 [B], >= 0, or NULL
+ *  B            in [0, 8192];  N >= 0: entries of slot_map and positions
+ *  free_pages   device int32 [F]
+ *  block_table  device int32 [B, max_pages] (in, out)
+ *  seq_lens_out device int32 [B] (out) = s + n;  cu_new device int32 [B + 1] (out)
+ *  slot_map, positions  device int32 [N] (out);  pages_taken device int32 [1] (out)
+ *  workspace    >= 256 bytes (the error word)
+ * All or nothing: when a length is negative, a request needs more than max_pages
+ * pages, the fresh pages are more than F or the new tokens more than N, no request
+ * gets a token (slot_map, positions -1; cu_new, pages_taken 0; seq_lens_out =
+ * seq_lens; block_table untouched) and DSA_ERR_CAPACITY is recorded.  A token whose
+ * page number is negative, or whose row is above 2^31 - 1, gets slot -1 and
+ * DSA_ERR_DEVICE_INDEX is recorded.  Outputs must not overlap inputs or each other.
+ */
+dsa_status_t dsa_paged_slots(const int32_t* seq_lens, const int32_t* new_lens, int32_t B, int32_t N, int32_t page_size,
+                             int32_t max_pages, const int32_t* free_pages, int32_t F, int32_t* block_table,
+                             int32_t* seq_lens_out, int32_t* cu_new, int32_t* slot_map, int32_t* positions,
+                             int32_t* pages_taken, void* workspace, size_t workspace_bytes, dsa_stream_t stream);
+
+/*
+ * dsa_norm_rope_fwd -- the norm of a row's first channels and the rotation of its
+ * positions in one pass.  For every row (t, h) of width D:
+ *   norm 1 (rms):   y_c = x_c r weight_c, r = 1 / sqrt(mean x^2 + eps)
+ *   norm 2 (layer): y_c = (x_c - mean) r weight_c + bias_c, r = 1 / sqrt(var + eps)
+ *   norm 0:         y_c = x_c                          (mean, var over c < norm_dim)
+ * for c < norm_dim, y_c = x_c above; then the rope_dim channels from rope_start are
+ * turned in pairs (a, b), number i = 0 .. rope_dim / 2 - 1, by the angle
+ * positions[t] * inv_freq[i] (formed exactly, whatever the position):
+ *   (a, b) -> rope_scale (cos a - sin b, sin a + cos b)
+ * where a pair is the channels (2i, 2i + 1) (interleaved 1) or (i, i + rope_dim / 2).
+ * For the latent rows (norm 1 of 512, rotation of the last 64 of 576), the index
+ * keys (norm 2 of 128, rotation of 64), per-head norms of queries and keys, and the
+ * position channels of wider query rows (a strided view; out may be x itself).
+ *  x            device bf16, row (t, h) at x + t x_stride_t + h x_stride_h (elements; >= 0,
+ *               0 repeats a row), channels contiguous; T >= 0, H >= 1, D in [1, 1024]
+ *  weight, bias device fp32 [norm_dim] or NULL (1 and 0)
+ *  positions    device int32 [T];  inv_freq device fp32 [rope_dim / 2] (both may be NULL
+ *               when rope_dim is 0)
+ *  out          device bf16, row (o, h) at out + o out_stride_t + h out_stride_h, with o = t,
+ *               or o = out_rows[t] when out_rows (device int32 [T]) is given: -1 writes no
+ *               row, other values outside [0, num_out_rows) are skipped and reported
+ *               (DSA_ERR_DEVICE_INDEX); rows named twice get one of the two results.
+ *               The rows of out must not overlap; out may equal x with the same strides
+ *               and no out_rows, and must not overlap x otherwise.
+ *  workspace    >= 256 bytes (the error word)
+ */
+dsa_status_t dsa_norm_rope_fwd(const dsa_bf16_t* x, int64_t x_stride_t, int64_t x_stride_h, int32_t T, int32_t H,
+                               int32_t D, int32_t norm, int32_t norm_dim, const float* weight, const float* bias,
+                               float eps, int32_t rope_start, int32_t rope_dim, int32_t interleaved,
+                               const int32_t* positions, const float* inv_freq, float rope_scale, dsa_bf16_t* out,
+                               int64_t out_stride_t, int64_t out_stride_h, const int32_t* out_rows,
+                               int64_t num_out_rows, void* workspace, size_t workspace_bytes, dsa_stream_t stream);
+
+/*
+ * dsa_norm_rope_bwd -- gradient of dsa_norm_rope_fwd (without out_rows): dx, and
+ * with a norm the sums over all rows dweight[c] and dbias[c] (layer norm).
+ *  dout, x      device bf16 with element strides as in the forward (x may be NULL without a norm)
+ *  dx           device bf16 (out), its rows must not overlap; may equal dout or x with the same strides
+ *  dweight, dbias  device fp32 [norm_dim] (out) or NULL: overwritten when accumulate == 0,
+ *               added to when accumulate == 1
+ *  workspace    >= dsa_norm_rope_bwd_workspace_size(norm_dim) bytes
+ * The sums' order is fixed: equal calls give equal bits.
+ */
+size_t dsa_norm_rope_bwd_workspace_size(int32_t norm_dim);
+dsa_status_t dsa_norm_rope_bwd(const dsa_bf16_t* dout, int64_t dout_stride_t, int64_t dout_stride_h,
+                               const dsa_bf16_t* x, int64_t x_stride_t, int64_t x_stride_h, int32_t T, int32_t H,
+                               int32_t D, int32_t norm, int32_t norm_dim, const float* weight, float eps,
+                               int32_t rope_start, int32_t rope_dim, int32_t interleaved, const int32_t* positions,
+                               const float* inv_freq, float rope_scale, dsa_bf16_t* dx, int64_t dx_stride_t,
+                               int64_t dx_stride_h, float* dweight, float* dbias, int32_t accumulate, void* workspace,
+                               size_t workspace_bytes, dsa_stream_t stream);
+
+/*
+ * dsa_rope_frequencies -- host table of inverse frequencies base^(-2i / rope_dim),
+ * and, for a context stretched by `factor` > 1, scaled by parts (the published
+ * YaRN rule): pairs that turn more than beta_fast times over original_context keep
+ * their frequency, those that turn fewer than beta_slow times are divided by
+ * factor, with a linear ramp between; *rope_scale_host = 0.1 ln(factor) + 1 (1 when
+ * factor is 1).
+ *  inv_freq_host  host fp32 [rope_dim / 2] (out);  rope_scale_host host fp32 (out)
+ */
+dsa_status_t dsa_rope_frequencies(int32_t rope_dim, double base, double factor, int32_t original_context,
+                                  double beta_fast, double beta_slow, float* inv_freq_host, float* rope_scale_host);
 
 /*
  * dsa_set_wait_limit_cycles -- the cycle limit of every bounded device-side

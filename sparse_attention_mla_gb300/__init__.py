@@ -38,9 +38,14 @@ __all__ = [
     "dsa_sparse_mla_bwd",
     "dsa_sparse_mla_bwd_noalloc",
     "dsa_sparse_mla_bwd_noalloc_read_status",
+    "dsa_paged_slots",
+    "dsa_norm_rope_fwd",
+    "dsa_norm_rope_bwd",
+    "dsa_rope_frequencies",
     "dsa_read_device_status",
     "dsa_set_wait_limit_cycles",
     "workspace_size",
+    "paged_workspace_size",
 ]
 
 DSA_OK = 0
@@ -53,6 +58,7 @@ STATUS_NAMES = {
     5: "DSA_ERR_CUDA",
     6: "DSA_ERR_DEVICE_INDEX",
     7: "DSA_ERR_TIMEOUT",
+    8: "DSA_ERR_CAPACITY",
 }
 
 
@@ -68,6 +74,8 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
+_D = ctypes.c_double
+_L = ctypes.c_int64
 
 
 def declared_symbols() -> list[str]:
@@ -139,6 +147,16 @@ def load_library(path: str | None = None):
         for name in ("dsa_packed_metadata", "dsa_indexer_topk", "dsa_indexer_topk_with_scores", "dsa_indexer_topk_scored",
                      "dsa_indexer_topk_cp",
                      "dsa_sparse_mla_fwd", "dsa_sparse_mla_bwd", "dsa_read_device_status"):
+            getattr(lib, name).restype = ctypes.c_int
+        lib.dsa_paged_slots.argtypes = [_P, _P, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+        lib.dsa_norm_rope_fwd.argtypes = [_P, _L, _L, _I, _I, _I, _I, _I, _P, _P, _F, _I, _I, _I, _P, _P, _F, _P, _L,
+                                          _L, _P, _L, _P, _SZ, _P]
+        lib.dsa_norm_rope_bwd_workspace_size.argtypes = [_I]
+        lib.dsa_norm_rope_bwd_workspace_size.restype = _SZ
+        lib.dsa_norm_rope_bwd.argtypes = [_P, _L, _L, _P, _L, _L, _I, _I, _I, _I, _I, _P, _F, _I, _I, _I, _P, _P, _F,
+                                          _P, _L, _L, _P, _P, _I, _P, _SZ, _P]
+        lib.dsa_rope_frequencies.argtypes = [_I, _D, _D, _I, _D, _D, _P, _P]
+        for name in ("dsa_paged_slots", "dsa_norm_rope_fwd", "dsa_norm_rope_bwd", "dsa_rope_frequencies"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -618,6 +636,218 @@ def dsa_sparse_mla_bwd_noalloc_read_status(device=None) -> int:
     _check(lib.dsa_sparse_mla_bwd_noalloc_read_status(_stream(dev), ctypes.byref(st)),
            "dsa_sparse_mla_bwd_noalloc_read_status")
     return st.value
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# The serving step.  These calls may come every few microseconds, so their checks are short: one pass over a tensor's
+# attributes, raw pointers, and a device switch only when the tensors live on another device than the current one.
+# ---------------------------------------------------------------------------------------------------------------
+_NORMS = {"none": 0, "rms": 1, "layer": 2}
+
+
+def paged_workspace_size(kind: str, a: int = 0, b: int = 0) -> int:
+    """Workspace bytes of the serving calls: ("slots"), ("norm_rope_fwd") or ("norm_rope_bwd", rows, norm_dim)."""
+    lib = load_library()
+    if kind in ("slots", "norm_rope_fwd"):
+        return 256
+    if kind == "norm_rope_bwd":
+        return int(lib.dsa_norm_rope_bwd_workspace_size(int(b)))
+    raise ValueError(f"unknown workspace kind {kind!r}")
+
+
+def _dense(t, name, dtype, shape, dev):
+    """Data pointer of a contiguous tensor of this type, shape (None: any extent) and device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    s = t.shape
+    if len(s) != len(shape) or any(n is not None and n != m for n, m in zip(shape, s)):
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(s)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _scratch(workspace, need, dev):
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif not isinstance(workspace, torch.Tensor) or workspace.dtype is not torch.uint8 or workspace.device != dev:
+        raise ValueError(f"workspace must be a uint8 tensor on {dev}")
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.data_ptr(), workspace.numel()
+
+
+def _call(fn, where, dev, *args):
+    """The library call on the tensors' device and its current stream."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if status != DSA_OK:
+        _check(status, where)
+
+
+def dsa_paged_slots(seq_lens, block_table, free_pages, page_size: int, new_lens=None, N: int | None = None,
+                    workspace=None):
+    """Pages and cache rows of a step's new tokens -> (slot_map int32 [N], positions int32 [N], cu_new int32 [B+1],
+    seq_lens_out int32 [B], pages_taken int32 [1]); block_table int32 [B, max_pages] gets the fresh pages, taken
+    from free_pages int32 [F] in request order.  new_lens: int32 [B], or None for one token each.  N: entries of
+    slot_map and positions (at least the new tokens; -1 beyond them), required with new_lens."""
+    lib = _lib or load_library()
+    p_len = _dense(seq_lens, "seq_lens", torch.int32, (None,), None)
+    dev = seq_lens.device
+    B = seq_lens.shape[0]
+    p_tab = _dense(block_table, "block_table", torch.int32, (B, None), dev)
+    p_free = _dense(free_pages, "free_pages", torch.int32, (None,), dev)
+    p_new = None if new_lens is None else _dense(new_lens, "new_lens", torch.int32, (B,), dev)
+    if N is None:
+        if new_lens is not None:
+            raise ValueError("N (entries of slot_map and positions) must be given with new_lens")
+        N = B
+    N = int(N)
+    if N < 0:
+        raise ValueError("N must be >= 0")
+    ws, p_ws, wsb = _scratch(workspace, 256, dev)
+    # one allocation, cut into the five outputs
+    buf = torch.empty(2 * N + 2 * B + 2, dtype=torch.int32, device=dev)
+    slot_map, positions, cu_new, seq_lens_out, taken = buf.split([N, N, B + 1, B, 1])
+    p = buf.data_ptr()
+    _call(lib.dsa_paged_slots, "dsa_paged_slots", dev, p_len, p_new, B, N, int(page_size), block_table.shape[1], p_free,
+          free_pages.shape[0], p_tab, p + 4 * (2 * N + B + 1), p + 8 * N, p, p + 4 * N, p + 4 * (2 * N + 2 * B + 1),
+          p_ws, wsb)
+    return slot_map, positions, cu_new, seq_lens_out, taken
+
+
+def _rows_of(t, name, dev):
+    """(pointer, token stride, head stride, T, H, D) of bf16 rows [T, D] or [T, H, D] with contiguous channels."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    s, st = t.shape, t.stride()
+    if len(s) not in (2, 3):
+        raise ValueError(f"{name} must be [T, D] or [T, H, D], got shape {tuple(s)}")
+    if s[-1] > 1 and st[-1] != 1:
+        raise ValueError(f"the channels of {name} must be contiguous")
+    return t.data_ptr(), st[0], (st[1] if len(s) == 3 else 0), s[0], (s[1] if len(s) == 3 else 1), s[-1]
+
+
+def _norm_rope_args(dev, T, D, inv_freq, positions, norm, norm_dim, weight, bias, rope_start):
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be one of {tuple(_NORMS)}, got {norm!r}")
+    kind = _NORMS[norm]
+    n = (D if kind else 0) if norm_dim is None else int(norm_dim)
+    p_w = None if weight is None else _dense(weight, "weight", torch.float32, (n,), dev)
+    p_b = None if bias is None else _dense(bias, "bias", torch.float32, (n,), dev)
+    R = 0
+    p_f = p_pos = None
+    if inv_freq is not None:
+        p_f = _dense(inv_freq, "inv_freq", torch.float32, (None,), dev)
+        R = 2 * inv_freq.shape[0]
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        p_pos = _dense(positions, "positions", torch.int32, (T,), dev)
+    return kind, n, p_w, p_b, (D - R if rope_start is None else int(rope_start)), R, p_pos, p_f
+
+
+def dsa_norm_rope_fwd(x, inv_freq=None, positions=None, norm: str = "none", norm_dim: int | None = None, weight=None,
+                      bias=None, eps: float = 1e-6, rope_start: int | None = None, interleaved: bool = False,
+                      rope_scale: float = 1.0, out=None, out_rows=None, workspace=None):
+    """Norm of the first norm_dim channels (default: all) and rotation of 2 * len(inv_freq) channels from rope_start
+    (default: the last ones) of bf16 rows x [T, D] or [T, H, D], any strides with contiguous channels -> out, bf16 of
+    x's shape (out may be x).  norm: "none", "rms" or "layer"; weight, bias: fp32 [norm_dim]; positions: int32 [T].
+    out_rows: int32 [T], the row of `out` that each token goes to (-1: none); out is then a cache of rows [rows, D],
+    [rows, H, D] or, for x [T, D], pages [num_pages, page_size, D]."""
+    lib = _lib or load_library()
+    p_x, xt, xh, T, H, D = _rows_of(x, "x", None)
+    dev = x.device
+    kind, n, p_w, p_b, r0, R, p_pos, p_f = _norm_rope_args(dev, T, D, inv_freq, positions, norm, norm_dim, weight, bias,
+                                                           rope_start)
+    p_rows, rows = None, 0
+    if out_rows is not None:
+        if out is None:
+            raise ValueError("out_rows needs the cache to write to (out)")
+        p_rows = _dense(out_rows, "out_rows", torch.int32, (T,), dev)
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+    cache = out
+    if p_rows is not None and x.dim() == 2 and out.dim() == 3:  # pages of rows
+        if not out.is_contiguous():
+            raise ValueError("a paged cache must be contiguous")
+        cache = out.view(-1, out.shape[2])
+    p_o, ot, oh, oT, oH, oD = _rows_of(cache, "out", dev)
+    if (oH, oD) != (H, D) or (p_rows is None and oT != T):
+        raise ValueError(f"out has rows of shape {(oH, oD)} (T = {oT}), x of {(H, D)} (T = {T})")
+    if p_rows is not None:
+        rows = oT
+    ws, p_ws, wsb = _scratch(workspace, 256, dev)
+    _call(lib.dsa_norm_rope_fwd, "dsa_norm_rope_fwd", dev, p_x, xt, xh, T, H, D, kind, n, p_w, p_b, eps, r0, R,
+          1 if interleaved else 0, p_pos, p_f, rope_scale, p_o, ot, oh, p_rows, rows, p_ws, wsb)
+    return out
+
+
+def dsa_norm_rope_bwd(dout, x=None, inv_freq=None, positions=None, norm: str = "none", norm_dim: int | None = None,
+                      weight=None, eps: float = 1e-6, rope_start: int | None = None, interleaved: bool = False,
+                      rope_scale: float = 1.0, with_bias: bool = False, dx=None, dweight=None, dbias=None,
+                      accumulate: bool = False, workspace=None):
+    """Gradient of dsa_norm_rope_fwd -> (dx bf16 of dout's shape, dweight fp32 [norm_dim] or None, dbias fp32
+    [norm_dim] or None).  With a norm, x is the forward's input and dweight is always formed; with_bias (layer norm)
+    forms dbias too.  accumulate: add to the given dweight / dbias.  dx may be dout or x."""
+    lib = _lib or load_library()
+    p_g, gt, gh, T, H, D = _rows_of(dout, "dout", None)
+    dev = dout.device
+    kind, n, p_w, _, r0, R, p_pos, p_f = _norm_rope_args(dev, T, D, inv_freq, positions, norm, norm_dim, weight, None,
+                                                         rope_start)
+    p_x = xt = xh = 0
+    if kind:
+        p_x, xt, xh, xT, xH, xD = _rows_of(x, "x", dev)
+        if (xT, xH, xD) != (T, H, D):
+            raise ValueError(f"x must have the shape of dout, got {tuple(x.shape)} and {tuple(dout.shape)}")
+        if with_bias and kind != 2:
+            raise ValueError("only the layer norm has a bias")
+        if accumulate and (dweight is None or (with_bias and dbias is None)):
+            raise ValueError("accumulate=True needs existing dweight and dbias")
+        if dweight is None:
+            dweight = torch.empty(n, dtype=torch.float32, device=dev)
+        if with_bias and dbias is None:
+            dbias = torch.empty(n, dtype=torch.float32, device=dev)
+    elif dweight is not None or dbias is not None or with_bias:
+        raise ValueError("dweight and dbias belong to a norm")
+    p_dw = None if dweight is None else _dense(dweight, "dweight", torch.float32, (n,), dev)
+    p_db = None if dbias is None else _dense(dbias, "dbias", torch.float32, (n,), dev)
+    if dx is None:
+        dx = torch.empty(dout.shape, dtype=torch.bfloat16, device=dev)
+    p_d, dt, dh, dT, dH, dD = _rows_of(dx, "dx", dev)
+    if (dT, dH, dD) != (T, H, D):
+        raise ValueError(f"dx must have the shape of dout, got {tuple(dx.shape)} and {tuple(dout.shape)}")
+    ws, p_ws, wsb = _scratch(workspace, 256 if workspace is not None else paged_workspace_size("norm_rope_bwd", 0, n), dev)
+    _call(lib.dsa_norm_rope_bwd, "dsa_norm_rope_bwd", dev, p_g, gt, gh, p_x or None, xt, xh, T, H, D, kind, n, p_w, eps,
+          r0, R, 1 if interleaved else 0, p_pos, p_f, rope_scale, p_d, dt, dh, p_dw, p_db, 1 if accumulate else 0,
+          p_ws, wsb)
+    return dx, dweight, dbias
+
+
+def dsa_rope_frequencies(rope_dim: int, base: float = 10000.0, factor: float = 1.0, original_context: int = 4096,
+                         beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """Inverse frequencies of a rotation of rope_dim channels, scaled by parts for a context stretched by `factor`
+    -> (inv_freq fp32 [rope_dim / 2] on `device` (default: the current CUDA device), rope_scale)."""
+    lib = load_library()
+    host = torch.empty(max(0, int(rope_dim) // 2), dtype=torch.float32)
+    scale = ctypes.c_float(1.0)
+    _check(lib.dsa_rope_frequencies(int(rope_dim), float(base), float(factor), int(original_context), float(beta_fast),
+                                    float(beta_slow), _ptr(host), ctypes.byref(scale)), "dsa_rope_frequencies")
+    return host.to("cuda" if device is None else device), scale.value
 
 
 def dsa_set_wait_limit_cycles(cycles: int) -> int:

@@ -182,6 +182,7 @@ const char* dsa_status_string(dsa_status_t s) {
     case DSA_ERR_CUDA: return "DSA_ERR_CUDA";
     case DSA_ERR_DEVICE_INDEX: return "DSA_ERR_DEVICE_INDEX: an index outside [-1, T_k) was masked";
     case DSA_ERR_TIMEOUT: return "DSA_ERR_TIMEOUT: a bounded device wait gave up";
+    case DSA_ERR_CAPACITY: return "DSA_ERR_CAPACITY: the step's new tokens do not fit the pages or the outputs";
   }
   return "unknown dsa_status_t";
 }
