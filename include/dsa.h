@@ -547,6 +547,38 @@ dsa_status_t dsa_rope_frequencies(int32_t rope_dim, double base, double factor, 
                                   double beta_fast, double beta_slow, float* inv_freq_host, float* rope_scale_host);
 
 /*
+ * dsa_paged_mla -- attention of new tokens over a paged latent cache, absorbed MLA
+ * as in dsa_sparse_mla_fwd.  Request b has n = cu_q[b + 1] - cu_q[b] new tokens (one
+ * each when cu_q is NULL), the last n of its seq_lens[b] cached ones: token cu_q[b] + j
+ * sees the v = seq_lens[b] - n + j + 1 positions 0 .. v - 1 (none when v <= 0), or of them
+ * those that its list topk_idx[token, :] names.  With those positions' rows kv:
+ *   z_p = softmax_scale <q[t,h,:], kv_p>,  lse[t,h] = ln(sum_p exp(z_p) [+ exp(attn_sink[h])]),
+ *   out[t,h,:] = sum_p exp(z_p - lse) kv_p[0:Dv];
+ * a token that sees nothing gets out = 0 and lse = -inf (or attn_sink[h]).
+ *  q            device bf16 [N, H, Dqk], Dqk in {512, 576}
+ *  cache        device bf16 [num_pages, page_size, Dqk]; rows that no token sees are not read
+ *  block_table  device int32 [B, max_pages];  seq_lens device int32 [B]
+ *  cu_q         device int32 [B + 1], non-decreasing, within [0, N], or NULL (then N = B);
+ *               rows of out and lse outside [cu_q[0], cu_q[B]) are left as they are
+ *  topk_idx     device int32 [N, K] positions, -1 for no entry, in any order, or NULL with K = 0
+ *               (e.g. of dsa_paged_indexer_topk); an entry named twice counts twice
+ *  topk_len     device int32 [N] or NULL: only the first topk_len[t] entries are looked at
+ *  attn_sink    device fp32 [H] or NULL
+ *  out          device bf16 [N, H, Dv] (out), Dv = 512;  lse device fp32 [N, H] (out);  N H < 2^31
+ *  workspace    >= dsa_paged_mla_workspace_size() bytes, whatever the sizes
+ * Positions beyond the table (p / page_size >= max_pages), entries outside [-1, v) and pages
+ * outside [0, num_pages) are masked and reported (DSA_ERR_DEVICE_INDEX).  The result does not
+ * depend on timing: equal calls on equal devices give equal bits.
+ */
+size_t dsa_paged_mla_workspace_size(void);
+dsa_status_t dsa_paged_mla(const dsa_bf16_t* q, const dsa_bf16_t* cache, const int32_t* block_table,
+                           const int32_t* seq_lens, const int32_t* cu_q, const int32_t* topk_idx,
+                           const int32_t* topk_len, int32_t N, int32_t B, int32_t H, int32_t Dqk, int32_t Dv,
+                           int32_t K, int32_t num_pages, int32_t page_size, int32_t max_pages, float softmax_scale,
+                           const float* attn_sink, dsa_bf16_t* out, float* lse, void* workspace,
+                           size_t workspace_bytes, dsa_stream_t stream);
+
+/*
  * dsa_set_wait_limit_cycles -- the cycle limit of every bounded device-side
  * wait of the kernels launched after the call (process-wide; the default is
  * 2^31 SM cycles, about one second).  A wait that runs past it records

@@ -42,6 +42,7 @@ __all__ = [
     "dsa_norm_rope_fwd",
     "dsa_norm_rope_bwd",
     "dsa_rope_frequencies",
+    "dsa_paged_mla",
     "dsa_read_device_status",
     "dsa_set_wait_limit_cycles",
     "workspace_size",
@@ -156,7 +157,12 @@ def load_library(path: str | None = None):
         lib.dsa_norm_rope_bwd.argtypes = [_P, _L, _L, _P, _L, _L, _I, _I, _I, _I, _I, _P, _F, _I, _I, _I, _P, _P, _F,
                                           _P, _L, _L, _P, _P, _I, _P, _SZ, _P]
         lib.dsa_rope_frequencies.argtypes = [_I, _D, _D, _I, _D, _D, _P, _P]
-        for name in ("dsa_paged_slots", "dsa_norm_rope_fwd", "dsa_norm_rope_bwd", "dsa_rope_frequencies"):
+        lib.dsa_paged_mla_workspace_size.argtypes = []
+        lib.dsa_paged_mla_workspace_size.restype = _SZ
+        lib.dsa_paged_mla.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P,
+                                      _SZ, _P]
+        for name in ("dsa_paged_slots", "dsa_norm_rope_fwd", "dsa_norm_rope_bwd", "dsa_rope_frequencies",
+                     "dsa_paged_mla"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -646,12 +652,15 @@ _NORMS = {"none": 0, "rms": 1, "layer": 2}
 
 
 def paged_workspace_size(kind: str, a: int = 0, b: int = 0) -> int:
-    """Workspace bytes of the serving calls: ("slots"), ("norm_rope_fwd") or ("norm_rope_bwd", rows, norm_dim)."""
+    """Workspace bytes of the serving calls: ("slots"), ("norm_rope_fwd"), ("norm_rope_bwd", rows, norm_dim) or
+    ("mla", N, H)."""
     lib = load_library()
     if kind in ("slots", "norm_rope_fwd"):
         return 256
     if kind == "norm_rope_bwd":
         return int(lib.dsa_norm_rope_bwd_workspace_size(int(b)))
+    if kind == "mla":
+        return int(lib.dsa_paged_mla_workspace_size())
     raise ValueError(f"unknown workspace kind {kind!r}")
 
 
@@ -848,6 +857,52 @@ def dsa_rope_frequencies(rope_dim: int, base: float = 10000.0, factor: float = 1
     _check(lib.dsa_rope_frequencies(int(rope_dim), float(base), float(factor), int(original_context), float(beta_fast),
                                     float(beta_slow), _ptr(host), ctypes.byref(scale)), "dsa_rope_frequencies")
     return host.to("cuda" if device is None else device), scale.value
+
+
+def _paged(cache, D, block_table, seq_lens, cu_q, N, dev):
+    """Pointers and sizes of a paged cache: (cache, table, lengths, cu_q, B, num_pages, page_size, max_pages)."""
+    p_len = _dense(seq_lens, "seq_lens", torch.int32, (None,), dev)
+    B = seq_lens.shape[0]
+    p_tab = _dense(block_table, "block_table", torch.int32, (B, None), dev)
+    p_cache = _dense(cache, "cache", torch.bfloat16, (None, None, D), dev)
+    p_cu = None
+    if cu_q is not None:
+        p_cu = _dense(cu_q, "cu_q", torch.int32, (B + 1,), dev)
+    elif N != B:
+        raise ValueError(f"without cu_q every request has one token: {N} tokens, {B} requests")
+    return p_cache, p_tab, p_len, p_cu, B, cache.shape[0], cache.shape[1], block_table.shape[1]
+
+
+def dsa_paged_mla(q, cache, block_table, seq_lens, softmax_scale: float, cu_q=None, topk_idx=None, topk_len=None,
+                  attn_sink=None, out=None, lse=None, workspace=None, Dv: int = 512):
+    """Attention of new tokens over a paged latent cache -> (out bf16 [N,H,Dv], lse fp32 [N,H]).  q bf16 [N,H,Dqk];
+    cache bf16 [num_pages, page_size, Dqk]; block_table int32 [B, max_pages]; seq_lens int32 [B], the new tokens
+    included; cu_q int32 [B+1], each request's tokens (None: one each).  topk_idx int32 [N,K] (with topk_len
+    int32 [N] or None): attend only to these positions.  attn_sink: fp32 [H] or None."""
+    lib = _lib or load_library()
+    p_q = _dense(q, "q", torch.bfloat16, (None, None, None), None)
+    dev = q.device
+    N, H, D = q.shape
+    p_cache, p_tab, p_len, p_cu, B, pages, page, width = _paged(cache, D, block_table, seq_lens, cu_q, N, dev)
+    K, p_idx, p_tl = 0, None, None
+    if topk_idx is not None:
+        p_idx = _dense(topk_idx, "topk_idx", torch.int32, (N, None), dev)
+        K = topk_idx.shape[1]
+        if topk_len is not None:
+            p_tl = _dense(topk_len, "topk_len", torch.int32, (N,), dev)
+    elif topk_len is not None:
+        raise ValueError("topk_len needs topk_idx")
+    p_sink = None if attn_sink is None else _dense(attn_sink, "attn_sink", torch.float32, (H,), dev)
+    if out is None:
+        out = torch.empty(N, H, Dv, dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty(N, H, dtype=torch.float32, device=dev)
+    p_out = _dense(out, "out", torch.bfloat16, (N, H, Dv), dev)
+    p_lse = _dense(lse, "lse", torch.float32, (N, H), dev)
+    ws, p_ws, wsb = _scratch(workspace, 0 if workspace is not None else paged_workspace_size("mla"), dev)
+    _call(lib.dsa_paged_mla, "dsa_paged_mla", dev, p_q, p_cache, p_tab, p_len, p_cu, p_idx, p_tl, N, B, H, D, Dv, K,
+          pages, page, width, softmax_scale, p_sink, p_out, p_lse, p_ws, wsb)
+    return out, lse
 
 
 def dsa_set_wait_limit_cycles(cycles: int) -> int:

@@ -23,7 +23,7 @@ def lib():
 
 
 def test_names_and_status(lib):
-    for name in ("dsa_paged_slots", "dsa_norm_rope_fwd", "dsa_norm_rope_bwd", "dsa_rope_frequencies"):
+    for name in ("dsa_paged_slots", "dsa_norm_rope_fwd", "dsa_norm_rope_bwd", "dsa_rope_frequencies", "dsa_paged_mla"):
         assert callable(getattr(dsa, name)) and name in dsa.declared_symbols() and hasattr(lib, name)
     assert lib.dsa_status_string(8).decode().startswith(dsa.STATUS_NAMES[8])
 
@@ -93,6 +93,30 @@ def test_backward_workspace(lib):
     need = lib.dsa_norm_rope_bwd_workspace_size(512)
     assert need > lib.dsa_norm_rope_bwd_workspace_size(64) > lib.dsa_norm_rope_bwd_workspace_size(0) == 256
     assert bwd(lib, wsb=need - 1) == 4 and bwd(lib, ws=None) == 4
+
+
+def mla(lib, **kw):
+    a = dict(q=FAKE, c=FAKE, tab=FAKE, ln=FAKE, cu=None, idx=None, il=None, N=4, B=4, H=16, D=576, Dv=512, K=0, pages=8,
+             page=64, mp=4, scale=0.1, sink=None, out=FAKE, lse=FAKE, ws=WS, wsb=1 << 30)
+    a.update(kw)
+    return lib.dsa_paged_mla(a["q"], a["c"], a["tab"], a["ln"], a["cu"], a["idx"], a["il"], a["N"], a["B"], a["H"], a["D"],
+                             a["Dv"], a["K"], a["pages"], a["page"], a["mp"], a["scale"], a["sink"], a["out"], a["lse"],
+                             a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("bad", [dict(N=-1), dict(B=-1), dict(H=0), dict(K=-1), dict(pages=-1), dict(page=0), dict(mp=-1),
+                                 dict(D=500), dict(Dv=256), dict(N=3), dict(scale=0.0), dict(scale=float("nan")),
+                                 dict(idx=FAKE), dict(K=4), dict(il=FAKE), dict(q=None), dict(out=None), dict(lse=None),
+                                 dict(ln=None), dict(tab=None), dict(c=None), dict(q=P(0x10008)), dict(out=P(0x10008)),
+                                 dict(c=P(0x10002)), dict(N=1 << 28, H=64, cu=FAKE)])
+def test_paged_mla_refuses(lib, bad):
+    assert mla(lib, **bad) == 3
+    assert lib.dsa_last_error_message().decode().startswith("dsa_paged_mla")
+
+
+def test_paged_mla_refuses_a_bad_workspace(lib):
+    need = lib.dsa_paged_mla_workspace_size()
+    assert mla(lib, ws=None) == 4 and mla(lib, ws=P(0x100010)) == 4 and mla(lib, wsb=need - 1) == 4
 
 
 def test_the_binding_refuses():
