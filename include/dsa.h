@@ -579,6 +579,32 @@ dsa_status_t dsa_paged_mla(const dsa_bf16_t* q, const dsa_bf16_t* cache, const i
                            size_t workspace_bytes, dsa_stream_t stream);
 
 /*
+ * dsa_paged_indexer_topk -- the selection of new tokens over paged index keys: the
+ * score and ranking of dsa_indexer_topk,
+ *   score(t, p) = sum_h head_weights[t,h] * max(0, <q_idx[t,h,:], k_p>),
+ * over the positions p that token t sees (as in dsa_paged_mla), summed in fp32.  The
+ * n = min(K, positions seen) highest (ties to the lower position; NaN above all) are
+ * written ascending to topk_idx[t, 0:n], then -1 up to K: the lists of dsa_paged_mla.
+ *  q_idx        device bf16 [N, Hi, Di]; Hi in [1, 64], Di = 128
+ *  k_cache      device bf16 [num_pages, page_size, Di]
+ *  head_weights device fp32 [N, Hi]
+ *  block_table, seq_lens, cu_q  as dsa_paged_mla
+ *  K            in [1, 2048]
+ *  max_len      no request is longer (the workspace holds N rows of that many scores)
+ *  topk_idx     device int32 [N, K] (out);  topk_len device int32 [N] (out) or NULL;
+ *               rows outside [cu_q[0], cu_q[B]) are left as they are
+ *  workspace    >= dsa_paged_indexer_topk_workspace_size(N, max_len) bytes
+ * Positions beyond max_len or the table are not ranked, and keys on pages outside
+ * [0, num_pages) count as zero rows; both are reported (DSA_ERR_DEVICE_INDEX).
+ */
+size_t dsa_paged_indexer_topk_workspace_size(int32_t N, int32_t max_len);
+dsa_status_t dsa_paged_indexer_topk(const dsa_bf16_t* q_idx, const dsa_bf16_t* k_cache, const float* head_weights,
+                                    const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_q, int32_t N,
+                                    int32_t B, int32_t Hi, int32_t Di, int32_t K, int32_t num_pages, int32_t page_size,
+                                    int32_t max_pages, int32_t max_len, int32_t* topk_idx, int32_t* topk_len,
+                                    void* workspace, size_t workspace_bytes, dsa_stream_t stream);
+
+/*
  * dsa_set_wait_limit_cycles -- the cycle limit of every bounded device-side
  * wait of the kernels launched after the call (process-wide; the default is
  * 2^31 SM cycles, about one second).  A wait that runs past it records

@@ -43,6 +43,7 @@ __all__ = [
     "dsa_norm_rope_bwd",
     "dsa_rope_frequencies",
     "dsa_paged_mla",
+    "dsa_paged_indexer_topk",
     "dsa_read_device_status",
     "dsa_set_wait_limit_cycles",
     "workspace_size",
@@ -161,8 +162,12 @@ def load_library(path: str | None = None):
         lib.dsa_paged_mla_workspace_size.restype = _SZ
         lib.dsa_paged_mla.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P,
                                       _SZ, _P]
+        lib.dsa_paged_indexer_topk_workspace_size.argtypes = [_I, _I]
+        lib.dsa_paged_indexer_topk_workspace_size.restype = _SZ
+        lib.dsa_paged_indexer_topk.argtypes = [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P,
+                                               _SZ, _P]
         for name in ("dsa_paged_slots", "dsa_norm_rope_fwd", "dsa_norm_rope_bwd", "dsa_rope_frequencies",
-                     "dsa_paged_mla"):
+                     "dsa_paged_mla", "dsa_paged_indexer_topk"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -652,8 +657,8 @@ _NORMS = {"none": 0, "rms": 1, "layer": 2}
 
 
 def paged_workspace_size(kind: str, a: int = 0, b: int = 0) -> int:
-    """Workspace bytes of the serving calls: ("slots"), ("norm_rope_fwd"), ("norm_rope_bwd", rows, norm_dim) or
-    ("mla", N, H)."""
+    """Workspace bytes of the serving calls: ("slots"), ("norm_rope_fwd"), ("norm_rope_bwd", rows, norm_dim),
+    ("mla", N, H) or ("topk", N, max_len)."""
     lib = load_library()
     if kind in ("slots", "norm_rope_fwd"):
         return 256
@@ -661,6 +666,8 @@ def paged_workspace_size(kind: str, a: int = 0, b: int = 0) -> int:
         return int(lib.dsa_norm_rope_bwd_workspace_size(int(b)))
     if kind == "mla":
         return int(lib.dsa_paged_mla_workspace_size())
+    if kind == "topk":
+        return int(lib.dsa_paged_indexer_topk_workspace_size(int(a), int(b)))
     raise ValueError(f"unknown workspace kind {kind!r}")
 
 
@@ -903,6 +910,32 @@ def dsa_paged_mla(q, cache, block_table, seq_lens, softmax_scale: float, cu_q=No
     _call(lib.dsa_paged_mla, "dsa_paged_mla", dev, p_q, p_cache, p_tab, p_len, p_cu, p_idx, p_tl, N, B, H, D, Dv, K,
           pages, page, width, softmax_scale, p_sink, p_out, p_lse, p_ws, wsb)
     return out, lse
+
+
+def dsa_paged_indexer_topk(q_idx, k_cache, head_weights, block_table, seq_lens, K: int, cu_q=None,
+                           max_len: int | None = None, topk_idx=None, topk_len=None, workspace=None):
+    """Top-k selection of new tokens over paged index keys -> (topk_idx int32 [N,K], positions ascending with a -1
+    suffix, topk_len int32 [N]): the lists of dsa_paged_mla.  q_idx bf16 [N,Hi,128]; k_cache bf16 [num_pages,
+    page_size, 128]; head_weights fp32 [N,Hi]; the rest as dsa_paged_mla.  max_len: no request is longer (default:
+    what the table holds); the workspace is N rows of that many fp32 scores."""
+    lib = _lib or load_library()
+    p_q = _dense(q_idx, "q_idx", torch.bfloat16, (None, None, None), None)
+    dev = q_idx.device
+    N, Hi, Di = q_idx.shape
+    p_w = _dense(head_weights, "head_weights", torch.float32, (N, Hi), dev)
+    p_cache, p_tab, p_len, p_cu, B, pages, page, width = _paged(k_cache, Di, block_table, seq_lens, cu_q, N, dev)
+    K = int(K)
+    max_len = min(width * page, 2 ** 31 - 4) if max_len is None else int(max_len)
+    if topk_idx is None:
+        topk_idx = torch.empty(N, K, dtype=torch.int32, device=dev)
+    if topk_len is None:
+        topk_len = torch.empty(N, dtype=torch.int32, device=dev)
+    p_idx = _dense(topk_idx, "topk_idx", torch.int32, (N, K), dev)
+    p_tl = _dense(topk_len, "topk_len", torch.int32, (N,), dev)
+    ws, p_ws, wsb = _scratch(workspace, 0 if workspace is not None else paged_workspace_size("topk", N, max_len), dev)
+    _call(lib.dsa_paged_indexer_topk, "dsa_paged_indexer_topk", dev, p_q, p_cache, p_w, p_tab, p_len, p_cu, N, B, Hi, Di,
+          K, pages, page, width, max_len, p_idx, p_tl, p_ws, wsb)
+    return topk_idx, topk_len
 
 
 def dsa_set_wait_limit_cycles(cycles: int) -> int:

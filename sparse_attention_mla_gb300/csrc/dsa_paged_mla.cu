@@ -29,8 +29,8 @@
 // and an 8 KiB block that the two tiles share.
 #include <cmath>
 
-#include "dsa_device.cuh"
 #include "dsa_host.h"
+#include "dsa_paged.cuh"
 
 namespace dsa {
 namespace pmla {
@@ -214,77 +214,39 @@ struct Walk {
   }
 };
 
-// Whole CTA: the total of tiles, this CTA's share, the unit its range starts in, and the record of the group
-// that it opens and does not finish.
-__device__ void make_plan(const Params& p, Plan* plan, long long* scratch) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int NW = kThreads / 32;
-  const int U = p.topk_idx ? p.N : p.B;
-  long long sum = 0;
-  for (int u = tid; u < U; u += kThreads) {
+// Whole CTA: this CTA's share of the tiles, the unit it starts in, and the record of the group that it opens and
+// does not finish.
+__device__ __forceinline__ void make_plan(const Params& p, Plan* plan, long long* scratch) {
+  if (threadIdx.x == 0) p.records[blockIdx.x] = make_int4(0, 0, 0, 0);
+  auto tiles_of = [&](int u) -> long long {
     const Unit x = unit_of(p, u);
-    sum += (long long)x.groups * x.tiles;
-  }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) scratch[warp] = sum;
-  __syncthreads();
-  long long W = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) W += scratch[w];
-  __syncthreads();
-  const long long C = min((long long)gridDim.x, W), c = blockIdx.x;
-  const long long w0 = c < C ? W * c / C : 0, w1 = c < C ? W * (c + 1) / C : 0;
-  if (tid == 0) {
-    plan->w0 = w0;
-    plan->w1 = w1;
-    plan->u0 = 0;
-    plan->first = 0;
-    p.records[c] = make_int4(0, 0, 0, 0);
-  }
-  __syncthreads();
-  if (w1 <= w0) return;
-  long long base = 0;
-  for (int u0 = 0; u0 < U && base < w1; u0 += kThreads) {
-    const int u = u0 + tid;
-    Unit x{0, 1, 0, 0};
-    if (u < U) x = unit_of(p, u);
-    const long long mine = (long long)x.groups * x.tiles;
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    if (lane == 31) scratch[warp] = inc;
-    __syncthreads();
-    long long before = base, total = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const long long v = scratch[w];
-      if (w < warp) before += v;
-      total += v;
-    }
-    const long long lo = before + inc - mine, hi = before + inc;
-    if (mine > 0 && lo <= w0 && w0 < hi) {
+    return (long long)x.groups * x.tiles;
+  };
+  auto visit = [&](const TileRange& r, int u, long long lo, long long n) {
+    if (lo <= r.w0 && r.w0 < lo + n) {
       plan->u0 = u;
-      plan->first = w0 - lo;
+      plan->first = r.w0 - lo;
     }
-    if (mine > 0 && lo <= w1 - 1 && w1 - 1 < hi) {  // the range's last tile
-      const long long off = w1 - 1 - lo;
+    if (lo <= r.w1 - 1 && r.w1 - 1 < lo + n) {  // the range's last tile
+      const Unit x = unit_of(p, u);
+      const long long off = r.w1 - 1 - lo;
       const int g = (int)(off / x.tiles), tl = (int)(off - (long long)g * x.tiles);
-      const long long opened = w1 - 1 - tl;  // the group's first tile
-      if (tl + 1 < x.tiles && opened >= w0) {
+      const long long opened = r.w1 - 1 - tl;  // the group's first tile
+      if (tl + 1 < x.tiles && opened >= r.w0) {
         const int tb = g / p.HB, hb = g - tb * p.HB;
         const int n0 = x.n0 + tb * p.G, nt = min(p.G, x.n - tb * p.G);
-        const long long end = opened + x.tiles;  // one past its last tile
-        const int last = (int)((end * C - 1) / W);
-        p.records[c] = make_int4(n0 * p.H + hb * 64, p.HB > 1 ? min(64, p.H - hb * 64) : nt * p.H, hb * 64, last);
+        const int last = (int)(((opened + x.tiles) * r.C - 1) / r.W);  // the CTA of its last tile
+        p.records[blockIdx.x] =
+            make_int4(n0 * p.H + hb * 64, p.HB > 1 ? min(64, p.H - hb * 64) : nt * p.H, hb * 64, last);
       }
     }
-    base += total;
-    __syncthreads();
+  };
+  const TileRange r = split_line<kThreads>(p.topk_idx ? p.N : p.B, tiles_of, scratch, visit);
+  if (threadIdx.x == 0) {
+    plan->w0 = r.w0;
+    plan->w1 = r.w1;
   }
+  __syncthreads();
 }
 
 // 16 TMEM lanes x 64 bits, N times: thread t of the warp gets lane base + (t >> 2) + 8 (t & 1) and the columns

@@ -23,7 +23,8 @@ def lib():
 
 
 def test_names_and_status(lib):
-    for name in ("dsa_paged_slots", "dsa_norm_rope_fwd", "dsa_norm_rope_bwd", "dsa_rope_frequencies", "dsa_paged_mla"):
+    for name in ("dsa_paged_slots", "dsa_norm_rope_fwd", "dsa_norm_rope_bwd", "dsa_rope_frequencies", "dsa_paged_mla",
+                 "dsa_paged_indexer_topk"):
         assert callable(getattr(dsa, name)) and name in dsa.declared_symbols() and hasattr(lib, name)
     assert lib.dsa_status_string(8).decode().startswith(dsa.STATUS_NAMES[8])
 
@@ -117,6 +118,30 @@ def test_paged_mla_refuses(lib, bad):
 def test_paged_mla_refuses_a_bad_workspace(lib):
     need = lib.dsa_paged_mla_workspace_size()
     assert mla(lib, ws=None) == 4 and mla(lib, ws=P(0x100010)) == 4 and mla(lib, wsb=need - 1) == 4
+
+
+def topk(lib, **kw):
+    a = dict(q=FAKE, c=FAKE, w=FAKE, tab=FAKE, ln=FAKE, cu=None, N=4, B=4, Hi=64, Di=128, K=64, pages=8, page=64, mp=4,
+             most=256, idx=FAKE, il=None, ws=WS, wsb=1 << 30)
+    a.update(kw)
+    return lib.dsa_paged_indexer_topk(a["q"], a["c"], a["w"], a["tab"], a["ln"], a["cu"], a["N"], a["B"], a["Hi"], a["Di"],
+                                      a["K"], a["pages"], a["page"], a["mp"], a["most"], a["idx"], a["il"], a["ws"],
+                                      a["wsb"], None)
+
+
+@pytest.mark.parametrize("bad", [dict(N=-1), dict(B=-1), dict(Hi=0), dict(Hi=65), dict(Di=64), dict(K=0), dict(K=2049),
+                                 dict(pages=-1), dict(page=0), dict(mp=-1), dict(most=-1), dict(N=3), dict(q=None),
+                                 dict(w=None), dict(idx=None), dict(ln=None), dict(tab=None), dict(c=None),
+                                 dict(q=P(0x10008)), dict(c=P(0x10002)), dict(N=1 << 29, cu=FAKE)])
+def test_paged_indexer_refuses(lib, bad):
+    assert topk(lib, **bad) == 3
+    assert lib.dsa_last_error_message().decode().startswith("dsa_paged_indexer_topk")
+
+
+def test_paged_indexer_refuses_a_bad_workspace(lib):
+    need = lib.dsa_paged_indexer_topk_workspace_size(4, 255)
+    assert need >= 256 + 4 * 256 * 4
+    assert topk(lib, ws=None) == 4 and topk(lib, ws=P(0x100010)) == 4 and topk(lib, wsb=need - 1) == 4
 
 
 def test_the_binding_refuses():
