@@ -12,51 +12,71 @@ struct TileRange {
 
 // Whole CTA of NT threads.  Unit u (of U) has tiles_of(u) tiles; the units' tiles lie end to end.  visit(range, u,
 // lo, n) is called by one thread for every unit [lo, lo + n) up to the range's end that has tiles.  `scratch`: NT / 32
-// words of shared memory.  Two passes over the units (sum, then prefix sums): the lengths come from L2.
+// words of shared memory.  A pass for the sum and one for the prefix sums; up to NT units are looked at only once.
+// Loops and not unrolled code: this runs once, before anything else, and at the time it takes to fetch it.
 template <int NT, class F, class V>
 __device__ __forceinline__ TileRange split_line(int U, const F& tiles_of, long long* scratch, const V& visit) {
   constexpr int NW = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long sum = 0;
-  for (int u = tid; u < U; u += NT) sum += tiles_of(u);
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) scratch[warp] = sum;
-  __syncthreads();
-  TileRange r;
-  r.W = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) r.W += scratch[w];
-  __syncthreads();
-  r.C = min((long long)gridDim.x, r.W);
-  const long long c = blockIdx.x;
-  r.w0 = c < r.C ? r.W * c / r.C : 0;
-  r.w1 = c < r.C ? r.W * (c + 1) / r.C : 0;
-  if (r.w1 <= r.w0) return r;
-  long long base = 0;
-  for (int u0 = 0; u0 < U && base < r.w1; u0 += NT) {
-    const int u = u0 + tid;
-    const long long mine = u < U ? tiles_of(u) : 0;
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+  TileRange r{0, 0, 0, 0};
+  long long mine = 0, before = 0, total = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    long long base = 0;
+#pragma unroll 1
+    for (int u0 = 0; u0 < U; u0 += NT) {
+      const int u = u0 + tid;
+      if (pass == 0 || U > NT) {
+        mine = u < U ? tiles_of(u) : 0;
+        // sums over the CTA: inside the warps, then over the warps' totals
+        long long inc = mine, x = 0;
+#pragma unroll 1
+        for (int level = 0; level < 2; ++level) {
+#pragma unroll 1
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, level ? x : inc, o);
+            if (lane >= o) { if (level) x += y; else inc += y; }
+          }
+          if (level == 0) {
+            if (lane == 31) scratch[warp] = inc;
+            __syncthreads();
+            x = lane < NW ? scratch[lane] : 0;
+            __syncthreads();
+          }
+        }
+        total = __shfl_sync(0xffffffffu, x, 31);
+        before = __shfl_sync(0xffffffffu, x, (warp + 31) & 31);
+        before = inc - mine + (warp ? before : 0);
+      }
+      if (pass == 1 && mine > 0 && base + before < r.w1) visit(r, u, base + before, mine);
+      base += total;
     }
-    if (lane == 31) scratch[warp] = inc;
-    __syncthreads();
-    long long before = base, total = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const long long v = scratch[w];
-      if (w < warp) before += v;
-      total += v;
+    if (pass == 0) {
+      r.W = base;
+      r.C = min((long long)gridDim.x, r.W);
+      if ((long long)blockIdx.x >= r.C) return r;
+      // floor(W c / C) and floor(W (c + 1) / C), with one wide division
+      const unsigned c = blockIdx.x, C = (unsigned)r.C;
+      const long long each = r.W / r.C;
+      const unsigned rest = (unsigned)(r.W - each * r.C);
+      r.w0 = each * c + rest * c / C;
+      r.w1 = each * (c + 1) + rest * (c + 1) / C;
     }
-    if (mine > 0) visit(r, u, before + inc - mine, mine);
-    base += total;
-    __syncthreads();
   }
   return r;
+}
+
+// Last i in [0, n) with a[i] <= v (a non-decreasing, a[0] <= v), by a whole warp: 32 probes at a time.
+__device__ __forceinline__ int warp_last_le(const int32_t* __restrict__ a, int n, int v) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, at < hi && __ldg(a + at) <= v);
+    lo += (31 - __clz(le | 1u)) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
 }
 
 }  // namespace dsa

@@ -24,7 +24,7 @@
 // stale page, NaN included, reaches a product).
 //
 // Warps: 0 issues S^T, 1-8 softmax and epilogue, 9-12 copy tiles into a ring, 13
-// issues P.V.  At width 576 and NH = 64 the ring's two tiles, Q and P need all the
+// issues P.V, 14 announces the runs of tiles (segments) that the CTA's range consists of.  At width 576 and NH = 64 the ring's two tiles, Q and P need all the
 // shared memory: P^T lies over the tile's last chunk (positions, read only by S^T)
 // and an 8 KiB block that the two tiles share.
 #include <cmath>
@@ -39,8 +39,8 @@ constexpr int kTile = 64;
 constexpr int kDv = 512;
 constexpr int kWorkers = 256;
 constexpr int kGather = 128;
-constexpr int kThreads = 32 + kWorkers + kGather + 32;
-constexpr int kRowsPer = kTile / (kGather / 8);  // tile rows per gather thread
+constexpr int kThreads = 32 + kWorkers + kGather + 64;
+constexpr int kSegs = 8;  // segments announced ahead
 constexpr int kMaxCtas = 160;
 constexpr float kRaise = 8.0f;  // log2 units: the running maximum is raised only past this
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
@@ -52,7 +52,7 @@ struct Smem {
   static constexpr int Q_CHUNK = NH * 128;
   // P over the ring only where nothing else fits
   static constexpr bool OVERLAY = NH == 64 && DQK == 576;
-  static constexpr int R = (NH == 64 || DQK == 576) ? 2 : 3;
+  static constexpr int R = 2;  // tiles in the ring
   static constexpr int NS = NH == 64 ? 1 : 2;  // S^T buffers in TMEM
   static constexpr int P_BLOCK = 2 * NH * 128;
   static constexpr int OFF_Q = 0;
@@ -81,13 +81,18 @@ struct Smem {
   __device__ static constexpr int o_col(int m) { return TM_O + m * 2 * NH; }
 };
 
-// misc (bytes)
-constexpr int M_KV = 0, M_PV = 24, M_S = 48, M_SF = 64, M_P = 80, M_Q = 96, M_FIN = 104;  // [3][3][2][2][2][1][2]
-constexpr int M_TMEM = 120, M_ABORT = 124, M_PLAN = 128;  // plan: 64 bytes
-constexpr int M_VALID = 192;                  // uint8 [3][64]
-constexpr int M_STAT = 384, M_FAC = 640;      // float [64] each
-constexpr int M_RED = 896;                    // float [4][64]
-static_assert(M_RED + 1024 <= 2048, "misc layout");
+// misc (bytes).  A tile's chunks land in groups of three, each with its own barrier (S^T starts on the first), and are
+// given back in pairs as P.V reads them.
+constexpr int kLand = 3, kGroups = 3, kPairs = 4;
+constexpr int M_KV = 0, M_PV = 48, M_S = 112, M_SF = 128, M_P = 144, M_Q = 160, M_FIN = 168;  // [2][3] [2][4] [2] [2] [2] 1 [2]
+constexpr int M_SEGF = 184, M_SEGE = M_SEGF + 8 * kSegs;  // [kSegs] each: announced, read by all
+constexpr int M_TMEM = 312, M_ABORT = 316, M_PLAN = 320;  // plan: 56 bytes
+constexpr int M_VALID = 376;                  // uint8 [2][64]
+constexpr int M_SEG = 512;                    // int4 [kSegs][2]
+constexpr int M_RED = 768;                    // float [4][64]; the first row also holds the factors of a rescale
+constexpr int M_STAT = M_RED + 1024;          // float [64]
+static_assert(M_SEGE + 8 * kSegs <= M_TMEM && M_VALID + 128 <= M_SEG && M_SEG + 32 * kSegs <= M_RED && M_STAT + 256 <= 2048,
+              "misc layout");
 
 struct Params {
   const __nv_bfloat16* q;
@@ -99,6 +104,7 @@ struct Params {
   const int32_t* topk_len;
   int N, B, H, K, num_pages, P, max_pages;
   int G, HB;  // tokens per group, head blocks
+  int box;    // rows of a TMA box (32 or a smaller page), 0: every row by cp.async
   float sl2e;
   const float* sink;
   __nv_bfloat16* out;
@@ -110,9 +116,34 @@ struct Params {
   long long wait_limit;
 };
 
+// 2^x in one instruction (results below 2^-126 become 0)
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// A value that is the same in all lanes, in a register of the whole warp.  The loops that issue MMAs run on such
+// counters: only then are the MMAs' descriptors kept in registers of the warp, and an MMA (M = 64, N = 64) is issued
+// every 33 cycles instead of every 60 to 80.
+__device__ __forceinline__ int warp_value(int v) { return (int)__reduce_max_sync(0xffffffffu, (unsigned)v); }
+
+// The bounded wait of dsa_device.cuh, in fewer instructions: a wait that runs out only sets *abort, and the CTA records
+// it when it leaves.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, long long limit) {
+  if (mbar_test(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!*abort) {
+    if (clock64() - t0 >= limit) { *abort = DSA_ERR_TIMEOUT; break; }
+    if (mbar_try_wait(bar, parity)) return true;
+  }
+  return false;
+}
+
 struct Unit {
   int groups, tiles;  // groups of MMA columns, tiles of each
   int n0, n;          // first token, tokens
+  int len, keys;      // length of the request; positions looked at, or entries of the list
 };
 
 // A unit is a request (all its tokens see the same cache) or, with lists, one token.
@@ -120,99 +151,123 @@ __device__ __forceinline__ Unit unit_of(const Params& p, int u) {
   Unit r;
   if (p.topk_idx != nullptr) {
     const int end = p.cu_q ? min(max(__ldg(p.cu_q + p.B), 0), p.N) : p.N;
+    const int begin = p.cu_q ? __ldg(p.cu_q) : 0;
     r.n0 = u;
-    r.n = u < end ? 1 : 0;
-    int len = p.K;
-    if (p.topk_len) len = min(max(__ldg(p.topk_len + u), 0), p.K);
-    r.tiles = max(1, (len + kTile - 1) / kTile);
+    r.n = u >= begin && u < end ? 1 : 0;
+    r.len = 0;
+    r.keys = p.topk_len ? min(max(__ldg(p.topk_len + u), 0), p.K) : p.K;
   } else {
     const int lo = p.cu_q ? min(max(__ldg(p.cu_q + u), 0), p.N) : u;
     const int hi = p.cu_q ? min(max(__ldg(p.cu_q + u + 1), lo), p.N) : u + 1;
     r.n0 = lo;
     r.n = hi - lo;
-    const long long most = (long long)p.max_pages * p.P;
-    const int len = (int)min((long long)max(__ldg(p.seq_lens + u), 0), most);
-    r.tiles = max(1, (int)(((long long)len + kTile - 1) / kTile));
+    r.len = max(__ldg(p.seq_lens + u), 0);
+    r.keys = (int)min((long long)r.len, (long long)p.max_pages * p.P);
   }
+  r.tiles = max(1, (int)(((long long)r.keys + kTile - 1) / kTile));
   r.groups = (r.n + p.G - 1) / p.G * p.HB;
   return r;
 }
 
-// The CTA's range of tiles and where it starts (in shared memory, written by make_plan).
+// The CTA's range of tiles and the unit it starts in (in shared memory, written by make_plan).
 struct Plan {
-  long long w0, w1;      // this CTA's tiles of the whole line
-  int u0, pad;           // unit that holds tile w0
-  long long first;       // w0 minus the unit's first tile
-};
-
-// A run of tiles [t0, t1) of one group.
-struct Seg {
-  int t0, t1, T;
-  int row0, rows;   // rows (token, head) of q, out and lse
-  int head0;        // head of the first row
-  int b;            // request
-  int seen0;        // positions that the group's first token sees
-  int keys;         // positions looked at by any token (dense), or entries of the list
-  int tok;          // first token
-};
-
-struct Walk {
-  const Params& p;
-  int u, g, t;
-  long long left;
+  long long w0, w1;  // this CTA's tiles of the whole line
   Unit un;
-  __device__ __forceinline__ Walk(const Params& p_, const Plan& pl) : p(p_) {
-    left = pl.w1 - pl.w0;
-    u = pl.u0;
-    g = t = 0;
-    if (left > 0) {
-      un = unit_of(p, u);
-      g = (int)(pl.first / un.tiles);
-      t = (int)(pl.first - (long long)g * un.tiles);
-    }
-  }
-  __device__ __forceinline__ bool next(Seg& s) {
-    if (left <= 0) return false;
+  int u, g, t;       // unit, group and tile of tile w0
+};
+
+// A run of tiles [t0, t0 + n) of one group, as announced (two int4).
+struct Seg {
+  int t0, n;
+  int row0;           // first row (token, head) of q, out and lse
+  int rows, head0;    // rows; head of the first row
+  bool whole, opens;  // all tiles of the group; its first one among them
+  int b;              // request
+  int seen0;          // positions that the group's first token sees (may be <= 0)
+  int keys;           // positions looked at by any token, or entries of the list
+};
+constexpr int kReaders = 2 + kWorkers / 32 + kGather / 32;  // warps that read an announcement
+
+__device__ __forceinline__ Seg unpack(const int4 a, const int4 c) {
+  Seg s;
+  s.t0 = a.x;
+  s.n = a.y;
+  s.row0 = a.z;
+  s.rows = a.w & 255;
+  s.whole = a.w & 256;
+  s.opens = a.w & 512;
+  s.head0 = c.w;
+  s.b = c.x;
+  s.seen0 = c.y;
+  s.keys = c.z;
+  return s;
+}
+
+// Announcement k, read by a whole warp; false when the wait ran out.  (A function of its own: called once per segment,
+// and kept out of the roles' loops.)
+__device__ __noinline__ bool read_announcement(uint32_t misc, const int4* ring, int k, volatile int* abort, long long limit,
+                                               Seg& s) {
+  const int at = k % kSegs;
+  if (!__all_sync(0xffffffffu, wait_for(misc + M_SEGF + 8 * at, (k / kSegs) & 1, abort, limit))) return false;
+  s = unpack(ring[2 * at], ring[2 * at + 1]);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(misc + M_SEGE + 8 * at);
+  return true;
+}
+
+// The announcing warp: the segments of the CTA's range, one after the other, into a ring that the other warps read.
+// One copy of this code and of its loads, instead of one per role.
+__device__ __forceinline__ void announce(const Params& p, const Plan& pl, uint32_t full, uint32_t empty, int4* ring,
+                                         volatile int* abort) {
+  const int lane = threadIdx.x & 31;
+  long long left = pl.w1 - pl.w0;
+  int u = pl.u, g = pl.g, t = pl.t;
+  Unit un = pl.un;
+  bool cut = false;
+#pragma unroll 1
+  for (int k = 0; left > 0; ++k) {
+#pragma unroll 1
     while (g >= un.groups) {  // (units are skipped only while tiles are left, so u stays in range)
       un = unit_of(p, ++u);
       g = t = 0;
     }
     const int tb = g / p.HB, hb = g - tb * p.HB;
-    const int n0 = un.n0 + tb * p.G, nt = min(p.G, un.n - tb * p.G);
-    s.tok = n0;
-    s.head0 = hb * 64;
-    s.row0 = n0 * p.H + s.head0;
-    s.rows = p.HB > 1 ? min(64, p.H - s.head0) : nt * p.H;
-    s.T = un.tiles;
-    s.t0 = t;
-    s.t1 = (int)min((long long)un.tiles, t + left);
-    left -= s.t1 - s.t0;
-    if (p.topk_idx == nullptr) {
-      s.b = u;
-      const int len = max(__ldg(p.seq_lens + u), 0);
-      s.keys = (int)min((long long)len, (long long)p.max_pages * p.P);
-      s.seen0 = max(__ldg(p.seq_lens + u), 0) - un.n + tb * p.G + 1;  // may be <= 0: sees nothing
-    } else {
-      int b = n0, lo_tok = n0, hi_tok = n0 + 1;
+    const int n0 = un.n0 + tb * p.G;
+    int4 a, c;
+    a.x = t;
+    a.y = (int)min((long long)(un.tiles - t), left);
+    a.z = n0 * p.H + hb * 64;
+    a.w = (p.HB > 1 ? min(64, p.H - hb * 64) : min(p.G, un.n - tb * p.G) * p.H) | (t == 0 ? 512 : 0) |
+          (t == 0 && a.y == un.tiles ? 256 : 0);
+    c.x = u;
+    c.y = un.len - un.n + tb * p.G + 1;
+    c.z = un.keys;
+    c.w = hb * 64;
+    if (p.topk_idx != nullptr) {
+      int lo = n0, hi = n0 + 1;
+      c.x = n0;
       if (p.cu_q) {
-        int lo = 0, hi = p.B;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (__ldg(p.cu_q + mid) <= n0) lo = mid; else hi = mid;
-        }
-        b = lo;
-        lo_tok = __ldg(p.cu_q + b);
-        hi_tok = __ldg(p.cu_q + b + 1);
+        c.x = warp_last_le(p.cu_q, p.B, n0);
+        lo = __ldg(p.cu_q + c.x);
+        hi = __ldg(p.cu_q + c.x + 1);
       }
-      s.b = b;
-      s.seen0 = max(__ldg(p.seq_lens + b), 0) - (hi_tok - lo_tok) + (n0 - lo_tok) + 1;
-      s.keys = p.topk_len ? min(max(__ldg(p.topk_len + n0), 0), p.K) : p.K;
+      c.y = max(__ldg(p.seq_lens + c.x), 0) - (hi - lo) + (n0 - lo) + 1;
+    } else {
+      cut |= un.keys < un.len;
     }
-    t = s.t1;
+    const int at = k % kSegs;
+    if (k >= kSegs && !wait_for(empty + 8 * at, (k / kSegs - 1) & 1, abort, p.wait_limit)) break;
+    if (lane == 0) {
+      ring[2 * at] = a;
+      ring[2 * at + 1] = c;
+      mbar_arrive(full + 8 * at);
+    }
+    left -= a.y;
+    t += a.y;
     if (t >= un.tiles) { ++g; t = 0; }
-    return true;
   }
-};
+  if (cut && lane == 0) record_error(p.err, DSA_ERR_DEVICE_INDEX);  // the table does not hold a request
+}
 
 // Whole CTA: this CTA's share of the tiles, the unit it starts in, and the record of the group that it opens and
 // does not finish.
@@ -223,12 +278,17 @@ __device__ __forceinline__ void make_plan(const Params& p, Plan* plan, long long
     return (long long)x.groups * x.tiles;
   };
   auto visit = [&](const TileRange& r, int u, long long lo, long long n) {
-    if (lo <= r.w0 && r.w0 < lo + n) {
-      plan->u0 = u;
-      plan->first = r.w0 - lo;
+    const bool starts = lo <= r.w0 && r.w0 < lo + n, ends = lo <= r.w1 - 1 && r.w1 - 1 < lo + n;
+    if (!starts && !ends) return;
+    const Unit x = unit_of(p, u);
+    if (starts) {
+      const long long first = r.w0 - lo;
+      plan->u = u;
+      plan->un = x;
+      plan->g = (int)(first / x.tiles);
+      plan->t = (int)(first - (long long)plan->g * x.tiles);
     }
-    if (lo <= r.w1 - 1 && r.w1 - 1 < lo + n) {  // the range's last tile
-      const Unit x = unit_of(p, u);
+    if (ends) {  // the range's last tile
       const long long off = r.w1 - 1 - lo;
       const int g = (int)(off / x.tiles), tl = (int)(off - (long long)g * x.tiles);
       const long long opened = r.w1 - 1 - tl;  // the group's first tile
@@ -265,17 +325,8 @@ __device__ __forceinline__ void tmem_ld16x64b(uint32_t a, uint32_t (&r)[N]) {
         : "r"(a));
   }
 }
-template <int N>
-__device__ __forceinline__ void tmem_ld_n(uint32_t a, uint32_t (&r)[N]) {
-  if constexpr (N == 8) tmem_ld8(a, r); else tmem_ld32(a, r);
-}
-template <int N>
-__device__ __forceinline__ void tmem_st_n(uint32_t a, const uint32_t (&r)[N]) {
-  if constexpr (N == 8) tmem_st8(a, r); else tmem_st32(a, r);
-}
-
 template <int DQK, int NH>
-__global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap map) {
   using L = Smem<DQK, NH>;
   constexpr int NCH = L::NCH, R = L::R, NS = L::NS;
   constexpr int NHH = NH / 2, NQ = NHH / 2;  // rows per softmax half, per thread
@@ -291,14 +342,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const Params p) 
   Plan* s_plan = reinterpret_cast<Plan*>(misc + M_PLAN);
   volatile uint8_t* s_valid = misc + M_VALID;
   float* s_stat = reinterpret_cast<float*>(misc + M_STAT);
-  float* s_fac = reinterpret_cast<float*>(misc + M_FAC);
+  float* s_fac = reinterpret_cast<float*>(misc + M_RED);  // a column's factor replaces its first maximum or sum
   float* s_red = reinterpret_cast<float*>(misc + M_RED);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // tile i: group g of its chunks has landed; P.V has read pair m of its channels (3: all of it)
+  auto wait_kv = [&](int i, int g) {
+    return wait_for(bar_kv + 8 * ((i % R) * kGroups + g), (i / R) & 1, s_abort, p.wait_limit);
+  };
+  auto wait_pv = [&](int i, int m) {
+    return wait_for(bar_pv + 8 * ((i % R) * kPairs + m), (i / R) & 1, s_abort, p.wait_limit);
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < R; ++s) {
-      mbar_init(bar_kv + 8 * s, kGather + kGather / 8);  // every copying thread's landings, every row flag's writer
-      mbar_init(bar_pv + 8 * s, 1);
+      for (int g = 0; g < kGroups; ++g) mbar_init(bar_kv + 8 * (s * kGroups + g), 2);  // the slot's two gather warps
+      for (int m = 0; m < kPairs; ++m) mbar_init(bar_pv + 8 * (s * kPairs + m), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar_s + 8 * b, 1);
@@ -307,46 +365,61 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const Params p) 
       mbar_init(bar_fin + 8 * b, 1);
     }
     mbar_init(bar_q, kWorkers);
+    for (int k = 0; k < kSegs; ++k) {
+      mbar_init(mb + M_SEGF + 8 * k, 1);
+      mbar_init(mb + M_SEGE + 8 * k, kReaders);
+    }
+    if (p.box > 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
     *s_abort = 0;
     fence_mbar_init();
   }
   make_plan(p, s_plan, reinterpret_cast<long long*>(s_red));
   const Plan plan = *s_plan;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the joining kernel waits for this one's end itself)
   if (plan.w1 <= plan.w0) return;  // (the whole CTA)
   if (warp == 0) {
     tmem_alloc(smem_u32(s_tmem), L::TM_COLS);
     tmem_relinquish();
   }
   __syncthreads();
-  const uint32_t tmem = *s_tmem;
+  const uint32_t tmem = (uint32_t)warp_value((int)*s_tmem);
 
+  const int n_tiles = warp_value((int)(plan.w1 - plan.w0));
+  // announcement k, once per warp
+  auto read_seg = [&](int k, Seg& s) -> bool {
+    return read_announcement(mb, reinterpret_cast<const int4*>(misc + M_SEG), k, s_abort, p.wait_limit, s);
+  };
   if (warp == 0) {
     // ======================= S^T issuer =======================
     constexpr uint32_t kIdS = idesc_bf16(kTile, NH, false, false);
-    Walk walk(p, plan);
-    Seg sg;
-    int i = 0, seg = 0;
-    bool stop = false;
-    while (!stop && walk.next(sg)) {
-      if (!warp_all(mbar_wait(bar_q, seg & 1, s_abort, p.err, p.wait_limit))) break;
-      for (int t = sg.t0; t < sg.t1; ++t, ++i) {
-        const int sl = i % R, sb = i % NS;
-        if (i >= NS && !warp_all(mbar_wait(bar_sf + 8 * sb, ((i / NS) - 1) & 1, s_abort, p.err, p.wait_limit))) { stop = true; break; }
-        if (!warp_all(mbar_wait(bar_kv + 8 * sl, (i / R) & 1, s_abort, p.err, p.wait_limit))) { stop = true; break; }
-        fence_proxy_async_smem();
-        tc_fence_after();
-        const uint64_t b00 = sdesc_sw128(sQ, 16, 1024);
-#pragma unroll 1
-        for (int c = 0; c < NCH; ++c) {
-          const uint64_t a0 = sdesc_sw128(L::chunk(sKV, sl, c), 16, 1024);
-          const uint64_t b0 = b00 + (uint64_t)((c * L::Q_CHUNK) >> 4);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ss_w(tmem + sb * NH, a0 + (uint64_t)(k * 2), b0 + (uint64_t)(k * 2), kIdS, (c | k) ? 1u : 0u);
-        }
-        mma_commit_w(bar_s + 8 * sb);
+    int left = 0, seg = 0;  // tiles left of the segment; segments begun
+    for (int i = 0; i < n_tiles; ++i) {
+      const int sl = i % R, sb = i % NS;
+      if (left == 0) {
+        Seg sg;
+        if (!read_seg(seg, sg)) break;
+        left = warp_value(sg.n);
+        if (!warp_all(wait_for(bar_q, seg & 1, s_abort, p.wait_limit))) break;
+        fence_proxy_async_smem();  // (the queries came by cp.async)
+        ++seg;
       }
-      ++seg;
+      --left;
+      if (i >= NS && !warp_all(wait_for(bar_sf + 8 * sb, ((i / NS) - 1) & 1, s_abort, p.wait_limit))) break;
+      uint64_t b0 = sdesc_sw128(sQ, 16, 1024);
+      bool stop = false;
+#pragma unroll 1
+      for (int c = 0; c < NCH; ++c, b0 += L::Q_CHUNK >> 4) {
+        if (c % kLand == 0) {
+          if (!warp_all(wait_kv(i, c / kLand))) { stop = true; break; }
+          tc_fence_after();
+        }
+        const uint64_t a0 = sdesc_sw128(L::chunk(sKV, sl, c), 16, 1024);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_ss_w(tmem + sb * NH, a0 + (uint64_t)(k * 2), b0 + (uint64_t)(k * 2), kIdS, (c | k) ? 1u : 0u);
+      }
+      if (stop) break;
+      mma_commit_w(bar_s + 8 * sb);
     }
     mma_commit_w(bar_fin);
     volatile int dummy = 0;
@@ -354,117 +427,191 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const Params p) 
     __syncwarp();
   } else if (warp == 13) {
     // ======================= P.V issuer =======================
-    Walk walk(p, plan);
-    Seg sg;
-    int i = 0;
-    bool stop = false;
-    while (!stop && walk.next(sg)) {
-      for (int t = sg.t0; t < sg.t1; ++t, ++i) {
-        const int sl = i % R;
-        if (!warp_all(mbar_wait(bar_p + 8 * (i & 1), (i >> 1) & 1, s_abort, p.err, p.wait_limit))) { stop = true; break; }
-        tc_fence_after();
-        const uint64_t va = sdesc_sw128(L::chunk(sKV, sl, 0), L::CHUNK, 1024);
-        constexpr uint64_t kPair = (2 * L::CHUNK) >> 4;
-        const uint32_t sP = L::p(sKV, i);
-        if constexpr (NH == 64) {  // P^T rows are keys (MN-major), hi and lo blocks of 64 rows' columns 8 KiB apart
-          constexpr uint32_t kId2 = idesc_bf16(128, 128, true, true), kId1 = idesc_bf16(128, 64, true, true);
-          const uint64_t pb = sdesc_sw128(sP, 8192, 1024);
+    int left = 0, seg = 0;
+    for (int i = 0; i < n_tiles; ++i) {
+      const int sl = i % R;
+      uint32_t add = 1;
+      if (left == 0) {
+        Seg sg;
+        if (!read_seg(seg++, sg)) break;
+        left = warp_value(sg.n);
+        add = 0;  // the segment's first tile overwrites O^T
+      }
+      --left;
+      if (!warp_all(wait_for(bar_p + 8 * (i & 1), (i >> 1) & 1, s_abort, p.wait_limit))) break;
+      tc_fence_after();
+      const uint64_t va = sdesc_sw128(L::chunk(sKV, sl, 0), L::CHUNK, 1024);
+      constexpr uint64_t kPair = (2 * L::CHUNK) >> 4;
+      const uint32_t sP = L::p(sKV, i);
+      if constexpr (NH == 64) {  // P^T rows are keys (MN-major), hi and lo blocks of 64 rows' columns 8 KiB apart
+        constexpr uint32_t kId2 = idesc_bf16(128, 128, true, true), kId1 = idesc_bf16(128, 64, true, true);
+        const uint64_t pb = sdesc_sw128(sP, 8192, 1024);
+#pragma unroll 1
+        for (int s = 0; s < 5; ++s) {  // channel tiles 0-2, tile 3 with hi, tile 3 with lo
+          const int m = min(s, 3);
+          const uint32_t id = s < 3 ? kId2 : kId1, on = add | (s == 4);
+          const uint64_t a = va + m * kPair, b = pb + (s == 4 ? 512 : 0);
 #pragma unroll
-          for (int m = 0; m < 3; ++m)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ss_w(tmem + L::o_col(m), va + m * kPair + (uint64_t)(k * 128), pb + (uint64_t)(k * 128), kId2,
-                       (t > sg.t0 || k > 0) ? 1u : 0u);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_ss_w(tmem + L::o_col(3), va + 3 * kPair + (uint64_t)((k & 3) * 128),
-                     pb + (uint64_t)((k >> 2) * 512 + (k & 3) * 128), kId1, (t > sg.t0 || k > 0) ? 1u : 0u);
-        } else {  // P^T rows are [hi rows | lo rows], keys along K
-          constexpr uint32_t kId = idesc_bf16(128, 2 * NH, true, false);
-          const uint64_t pb = sdesc_sw128(sP, 16, 1024);
-#pragma unroll
-          for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ss_w(tmem + L::o_col(m), va + m * kPair + (uint64_t)(k * 128), pb + (uint64_t)(k * 2), kId,
-                       (t > sg.t0 || k > 0) ? 1u : 0u);
+          for (int k = 0; k < 4; ++k)
+            mma_ss_w(tmem + L::o_col(m), a + (uint64_t)(k * 128), b + (uint64_t)(k * 128), id, on | (k > 0));
+          if (s != 3) mma_commit_w(bar_pv + 8 * (sl * kPairs + m));
         }
-        mma_commit_w(bar_pv + 8 * sl);
+      } else {  // P^T rows are [hi rows | lo rows], keys along K
+        constexpr uint32_t kId = idesc_bf16(128, 2 * NH, true, false);
+        const uint64_t pb = sdesc_sw128(sP, 16, 1024);
+#pragma unroll 1
+        for (int m = 0; m < 4; ++m) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss_w(tmem + L::o_col(m), va + m * kPair + (uint64_t)(k * 128), pb + (uint64_t)(k * 2), kId, add | (k > 0));
+          mma_commit_w(bar_pv + 8 * (sl * kPairs + m));
+        }
       }
     }
     mma_commit_w(bar_fin + 8);
     volatile int dummy = 0;
     mbar_wait(bar_fin + 8, 0, &dummy, p.err);
     __syncwarp();
+  } else if (warp == 14) {
+    announce(p, plan, mb + M_SEGF, mb + M_SEGE, reinterpret_cast<int4*>(misc + M_SEG), s_abort);
   } else if (warp >= 9) {
-    // ======================= gather: tiles into the ring =======================
-    const int gt = threadIdx.x - 32 - kWorkers, uc = gt & 7;
-    Walk walk(p, plan);
+    // ======================= gather: two warps per slot of the ring, 32 rows of a tile each =======================
+    // A lane looks one row up, in steps whose loads have a tile of the slot to come back: the list's entry (three tiles
+    // of the slot ahead), the page (two ahead), the row number (one ahead).  Whole rows of whole pages come by TMA (one
+    // lane issues a box of 64 channels; it needs no thread while it lands and no fence before the tensor core reads
+    // it); lists, odd page sizes and the end of a request by 16-byte cp.async, which zero-fills what is masked.
+    const int sl = (warp - 9) >> 1, gw = (warp - 9) & 1, uc = lane & 7;
     Seg sg;
-    int i = 0;
-    bool stop = false;
-    while (!stop && walk.next(sg)) {
-      const int32_t* tab = p.table + (size_t)sg.b * p.max_pages;
-      if (p.topk_idx == nullptr && gt == 0 && sg.keys < __ldg(p.seq_lens + sg.b)) record_error(p.err, DSA_ERR_DEVICE_INDEX);
-      const int32_t* list = p.topk_idx ? p.topk_idx + (size_t)sg.tok * p.K : nullptr;
-      // position of tile row r, or -1; then its cache row
-      auto load_pos = [&](int t, int (&pos)[kRowsPer]) {
-#pragma unroll
-        for (int e = 0; e < kRowsPer; ++e) {
-          const int j = t * kTile + (gt >> 3) + (kGather / 8) * e;
-          int x = -1;
-          if (t < sg.t1 && j < sg.keys) {
-            x = j;
-            if (list) {
-              x = __ldg(list + j);
-              if (x < -1 || (x >= 0 && (x >= sg.seen0 || x >= (long long)p.max_pages * p.P))) {
-                record_error(p.err, DSA_ERR_DEVICE_INDEX);
-                x = -1;
-              }
-            }
-          }
-          pos[e] = x;
+    int seg = 0, base = 0, end = 0, limit = 0;  // this CTA's tiles [base, end) are the segment's
+    struct Look {
+      int pos, b, limit;  // position (then its place in the page), or -1; request; what the position has to stay below
+    };
+    bool bad_index = false, stop = false;
+    auto position = [&](int i) -> Look {
+      Look k{-1, 0, 0};
+      if (i < n_tiles && !stop) {
+#pragma unroll 1
+        while (i >= end) {
+          if (!read_seg(seg, sg)) { stop = true; return k; }
+          ++seg;
+          base = end;
+          end += sg.n;
+          limit = (int)min((long long)p.max_pages * p.P, (long long)(p.topk_idx ? sg.seen0 : sg.keys));
         }
-      };
-      auto load_page = [&](const int (&pos)[kRowsPer], int (&page)[kRowsPer]) {
+        k.b = sg.b;
+        k.limit = limit;
+        const int j = (sg.t0 + i - base) * kTile + gw * 32 + lane;
+        if (j < sg.keys) k.pos = p.topk_idx ? __ldg(p.topk_idx + (size_t)(sg.row0 / p.H) * p.K + j) : j;
+      }
+      return k;
+    };
+    auto page_of = [&](Look& k) -> int {
+      if (k.pos < -1 || k.pos >= k.limit) {
+        bad_index |= k.pos != -1;
+        k.pos = -1;
+      }
+      if (k.pos < 0) return -1;
+      const unsigned at = (unsigned)k.pos / (unsigned)p.P;
+      k.pos -= (int)at * p.P;
+      return __ldg(p.table + (size_t)k.b * p.max_pages + at);
+    };
+    auto row_of = [&](int pos, int page) -> long long {
+      if (pos < 0) return -1;
+      if (page >= 0 && page < p.num_pages) return (long long)page * p.P + pos;
+      bad_index = true;
+      return -1;
+    };
+    Look look[3];
+    int page[2];
+    long long row[2];  // rows of the slot's next two tiles
 #pragma unroll
-        for (int e = 0; e < kRowsPer; ++e) page[e] = pos[e] >= 0 ? __ldg(tab + (unsigned)pos[e] / (unsigned)p.P) : -1;
-      };
-      int pos[kRowsPer], page[kRowsPer];
-      load_pos(sg.t0, pos);
-      load_page(pos, page);
-      for (int t = sg.t0; t < sg.t1; ++t, ++i) {
-        const int sl = i % R;
-        long long row[kRowsPer];
-#pragma unroll
-        for (int e = 0; e < kRowsPer; ++e) {
-          row[e] = -1;
-          if (pos[e] >= 0) {
-            if (page[e] >= 0 && page[e] < p.num_pages) row[e] = (long long)page[e] * p.P + (unsigned)pos[e] % (unsigned)p.P;
-            else record_error(p.err, DSA_ERR_DEVICE_INDEX);
+    for (int k = 0; k < 3; ++k) look[k] = position(sl + k * R);
+    page[0] = page_of(look[0]);
+    page[1] = page_of(look[1]);
+    row[0] = row_of(look[0].pos, page[0]);
+    row[1] = row_of(look[1].pos, page[1]);
+    look[0] = look[2];
+    page[0] = page_of(look[0]);
+    look[1] = position(sl + 3 * R);
+#pragma unroll 1
+    for (int i = sl; i < n_tiles; i += R) {
+      const long long row_d = row[0];
+      // the chunks of pair m (with the last, the ninth too) are free
+      auto slot_free = [&](int m) { return i < R || warp_all(wait_pv(i - R, m)); };
+      // all 32 rows are there, in whole boxes
+      if (p.box > 0 && __all_sync(0xffffffffu, row_d >= 0)) {
+        const int boxes = 32 / p.box;
+        // lane x issues chunk x % 2 of a pair (x % 3 of the last one, where there is a ninth), box x / 2 (x / 3)
+#pragma unroll 1
+        for (int m = 0; m < kPairs; ++m) {
+          if (!slot_free(m)) { stop = true; break; }
+          if (m == 0) {
+            s_valid[sl * kTile + gw * 32 + lane] = 1;
+            __syncwarp();
+            if (lane < kGroups) mbar_expect_tx(bar_kv + 8 * (sl * kGroups + lane), min(kLand, NCH - kLand * lane) * 4096);
+            __syncwarp();
+          }
+          const int w = m == 3 && NCH == 9 ? 3 : 2;
+          const int bx = lane / w, c = 2 * m + lane - bx * w;
+          const int at = (int)__shfl_sync(0xffffffffu, row_d, (bx * p.box) & 31);
+          if (bx < boxes)
+            tma_load_2d(L::chunk(sKV, sl, c) + (gw * 32 + bx * p.box) * 128, &map, c * 64, at,
+                        bar_kv + 8 * (sl * kGroups + c / kLand));
+        }
+        if (stop) break;
+        // the slot's next tile on its way to L2 (the ring's room bounds what can be on its way to the SM)
+        if (__all_sync(0xffffffffu, row[1] >= 0)) {
+#pragma unroll 1
+          for (int x0 = 0; x0 < boxes * NCH; x0 += 32) {
+            const int x = x0 + lane, bx = x / NCH, c = x - bx * NCH;
+            const int at = (int)__shfl_sync(0xffffffffu, row[1], (bx * p.box) & 31);
+            if (x < boxes * NCH)
+              asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(&map), "r"(c * 64), "r"(at)
+                           : "memory");
           }
         }
-        load_pos(t + 1, pos);
-        load_page(pos, page);
-        if (i >= R && !mbar_wait(bar_pv + 8 * sl, ((i / R) - 1) & 1, s_abort, p.err, p.wait_limit)) { stop = true; break; }
+      } else {
+        const __nv_bfloat16* src[8];
+        uint32_t ok = 0;
 #pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const long long at = __shfl_sync(0xffffffffu, row_d, e * 4 + (lane >> 3));
+          ok |= (at >= 0 ? 1u : 0u) << e;
+          src[e] = p.cache + (at >= 0 ? (size_t)at * DQK + uc * 8 : 0);
+        }
+#pragma unroll 1
         for (int c = 0; c < NCH; ++c) {
+          if ((c & 1) == 0 && c < 8 && !slot_free(c >> 1)) { stop = true; break; }
+          if (c == 0) s_valid[sl * kTile + gw * 32 + lane] = row_d >= 0 ? 1 : 0;
           const uint32_t dst = L::chunk(sKV, sl, c);
 #pragma unroll
-          for (int e = 0; e < kRowsPer; ++e) {
-            const int r = (gt >> 3) + (kGather / 8) * e;
-            const bool ok = row[e] >= 0;
-            cp_async16(dst + sw128_off(r, uc), p.cache + (ok ? (size_t)row[e] * DQK + c * 64 + uc * 8 : 0), ok ? 16u : 0u);
+          for (int e = 0; e < 8; ++e) {
+            const bool on = (ok >> e) & 1u;
+            cp_async16(dst + sw128_off(gw * 32 + e * 4 + (lane >> 3), uc), src[e] + (on ? c * 64 : 0), on ? 16u : 0u);
           }
+          if (c % kLand == kLand - 1 || c == NCH - 1) asm volatile("cp.async.commit_group;" ::: "memory");
         }
-        cp_async_arrive(bar_kv + 8 * sl);
-        if (uc == 0) {
-#pragma unroll
-          for (int e = 0; e < kRowsPer; ++e) s_valid[sl * kTile + (gt >> 3) + (kGather / 8) * e] = row[e] >= 0 ? 1 : 0;
-          mbar_arrive(bar_kv + 8 * sl);
-        }
+        if (stop) break;
+        // landings in order
+        auto landed = [&](int g) {
+          fence_proxy_async_smem();  // the copies -> visible to the tensor core
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_kv + 8 * (sl * kGroups + g));
+        };
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+        landed(0);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        landed(1);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        landed(2);
       }
+      row[0] = row[1];
+      row[1] = row_of(look[0].pos, page[0]);
+      look[0] = look[1];
+      page[0] = page_of(look[0]);
+      look[1] = position(i + 4 * R);
     }
+    if (bad_index) record_error(p.err, DSA_ERR_DEVICE_INDEX);
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ======================= softmax + epilogue =======================
@@ -476,6 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const Params p) 
     auto load_q = [&](const Seg& s) {
       constexpr int UNITS = NH * NCH * 8;
       const uint64_t pol = l2_evict_first_policy();
+#pragma unroll 2
       for (int x = tid; x < UNITS; x += kWorkers) {
         const int hh = x / (NCH * 8), rem = x - hh * (NCH * 8), c = rem >> 3, uc = rem & 7;
         const bool ok = hh < s.rows;
@@ -484,46 +632,64 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const Params p) 
       }
       cp_async_arrive(bar_q);
     };
-    // over the warp's 16 keys: the lanes of one parity hold the same rows
-    auto reduce_keys = [&](float v, bool is_max) -> float {
+    // Maxima or sums over the warp's 16 keys of all NQ rows of a thread: the result is that of row sum_row.
+    auto over_keys = [&](float (&v)[NQ], bool is_max) -> float {
+      constexpr int kBit[4] = {16, 8, 4, 1};  // the lanes of one parity
+      int w = 8;
 #pragma unroll
-      for (int o = 1; o <= 16; o <<= 1) {
-        if (o == 2) continue;
-        const float x = __shfl_xor_sync(0xffffffffu, v, o);
-        v = is_max ? fmaxf(v, x) : v + x;
+      for (int s = 0; s < 4; ++s, w >>= 1) {
+        const bool upper = (lane & kBit[s]) != 0;
+        if (w >= NQ) {
+#pragma unroll
+          for (int j = 0; j < NQ; ++j) {
+            const float x = __shfl_xor_sync(0xffffffffu, v[j], kBit[s]);
+            v[j] = is_max ? fmaxf(v[j], x) : v[j] + x;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < w; ++j) {
+            const float send = upper ? v[j] : v[j + w], keep = upper ? v[j + w] : v[j];
+            const float x = __shfl_xor_sync(0xffffffffu, send, kBit[s]);
+            v[j] = is_max ? fmaxf(keep, x) : keep + x;
+          }
+        }
       }
-      return v;
+      return v[0];
     };
-    Walk walk(p, plan);
+    const int sum_row = n0 + (((lane >> 1) & 14) | (lane & 1)) % NQ;
+    auto m_use = [](float m) { return fmaxf(m, -3.0e38f); };  // (a row without a finite score: e^-inf is 0 all the same)
     Seg sg, nx;
-    bool have = walk.next(sg);
-    if (have) load_q(sg);
-    bool aborted = false;
+    bool aborted = !read_seg(0, sg);
+    if (!aborted) load_q(sg);
+    nx = sg;
     int i = 0;
-    while (have && !aborted) {
-      const bool more = walk.next(nx);
-      float l_part[NQ];
+    for (int seg = 1; !aborted; ++seg) {
+      const bool more = i + sg.n < n_tiles;
+      bool bad_seg = more && !read_seg(seg, nx);
+      // this thread's first row: its token in the group, and how many rows of that token there are from it on
+      const int tok0 = (sg.head0 + n0) / p.H, head_left = p.H - ((sg.head0 + n0) - tok0 * p.H);
+      float l_part[NQ], m_run[NQ];  // sum and running maximum (log2 units) of this thread's rows
 #pragma unroll
-      for (int j = 0; j < NQ; ++j) l_part[j] = 0.f;
+      for (int j = 0; j < NQ; ++j) { l_part[j] = 0.f; m_run[j] = -INFINITY; }
       if (qd == 0 && lane < NHH) s_stat[ch * NHH + lane] = -INFINITY;  // (read only after a barrier of the half)
-      for (int t = sg.t0; t < sg.t1; ++t, ++i) {
+      const int t_end = sg.t0 + sg.n;
+#pragma unroll 1
+      for (int t = sg.t0; t < t_end; ++t, ++i) {
         const int sl = i % R, sb = i % NS;
-        bool bad = !mbar_wait(bar_s + 8 * sb, (i / NS) & 1, s_abort, p.err, p.wait_limit);
+        bool bad = bad_seg || !wait_for(bar_s + 8 * sb, (i / NS) & 1, s_abort, p.wait_limit);
         // (complete since before S^T was issued: orders the row flags before their reads below)
-        bad = bad || !mbar_wait(bar_kv + 8 * sl, (i / R) & 1, s_abort, p.err, p.wait_limit);
-        // P of tile i overwrites what P.V of an earlier tile read: of the tile before with the shared block, else
-        // of the one before that
-        constexpr int kBack = L::OVERLAY ? 1 : 2;
-        if (!L::OVERLAY && i >= kBack)
-          bad = bad || !mbar_wait(bar_pv + 8 * ((i - kBack) % R), ((i - kBack) / R) & 1, s_abort, p.err, p.wait_limit);
+        bad = bad || !wait_kv(i, kGroups - 1);
+        // with its own buffers, P of tile i overwrites what P.V of tile i - 2 read
+        if (!L::OVERLAY && i >= 2) bad = bad || !wait_pv(i - 2, 3);
         tc_fence_after();
         uint32_t raw[NQ];
         tmem_ld16x64b<NQ>(tmem_addr(tmem + sb * NH + ch * NHH, qd * 32, 0), raw);
+        const bool valid = s_valid[sl * kTile + r] != 0;
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_sf + 8 * sb);
-        if (t + 1 == sg.t1 && more && !bad) load_q(nx);  // S^T of the segment is done: Q is free
+        if (t + 1 == t_end && more && !bad) load_q(nx);  // S^T of the segment is done: Q is free
         // alternate columns of the half -> NQ consecutive rows: swap half of them with the key's other thread
         float z[NQ];
 #pragma unroll
@@ -532,22 +698,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const Params p) 
           z[2 * j] = __uint_as_float(par ? got : raw[j]);
           z[2 * j + 1] = __uint_as_float(par ? raw[NQ / 2 + j] : got);
         }
-        const bool valid = s_valid[sl * kTile + r] != 0;
         const int pos = t * kTile + r;
-        if (p.topk_idx == nullptr && (t + 1) * (long long)kTile > sg.seen0) {  // some token may not see all of the tile
+        if (!valid) {
+#pragma unroll
+          for (int j = 0; j < NQ; ++j) z[j] = -INFINITY;
+        } else if (p.topk_idx == nullptr && (t + 1) * (long long)kTile > sg.seen0) {  // some token may not see all of it
+          int seen = sg.seen0 + tok0, left = head_left;
 #pragma unroll
           for (int j = 0; j < NQ; ++j) {
-            const int seen = sg.seen0 + (sg.head0 + n0 + j) / p.H;
-            z[j] = (valid && pos < seen) ? z[j] * p.sl2e : -INFINITY;
+            if (pos >= seen) z[j] = -INFINITY;
+            if (--left == 0) { left = p.H; ++seen; }
           }
-        } else {
-#pragma unroll
-          for (int j = 0; j < NQ; ++j) z[j] = valid ? z[j] * p.sl2e : -INFINITY;
         }
         bool mine = t == sg.t0;
         if (!mine) {
+          // a score passes its row's maximum by the threshold (a row without a finite score yet counts)
 #pragma unroll
-          for (int j = 0; j < NQ; ++j) mine |= z[j] > s_stat[n0 + j] + kRaise;
+          for (int j = 0; j < NQ; ++j) mine |= fmaf(z[j], p.sl2e, -m_run[j]) > kRaise;
         }
         bool raise = false;
         if (named_bar_or(bar_id, 128, mine || bad)) {
@@ -555,11 +722,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const Params p) 
           raise = true;
         }
         if (raise) {
+          float top[NQ];
 #pragma unroll
-          for (int j = 0; j < NQ; ++j) {
-            const float wmax = reduce_keys(z[j], true);
-            if ((lane & ~2) == 0) s_red[qd * NH + n0 + j] = wmax;
-          }
+          for (int j = 0; j < NQ; ++j) top[j] = z[j];
+          s_red[qd * NH + sum_row] = over_keys(top, true) * p.sl2e;
           named_bar(bar_id, 128);
           if (qd == 0 && lane < NHH) {
             const int n = ch * NHH + lane;
@@ -570,20 +736,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const Params p) 
           }
           named_bar(bar_id, 128);
 #pragma unroll
-          for (int j = 0; j < NQ; ++j) l_part[j] *= s_fac[n0 + j];
+          for (int j = 0; j < NQ; ++j) {
+            l_part[j] *= s_fac[n0 + j];
+            m_run[j] = s_stat[n0 + j];
+          }
           if (t > sg.t0) {
-            bool okw = mbar_wait(bar_pv + 8 * ((i - 1) % R), ((i - 1) / R) & 1, s_abort, p.err, p.wait_limit);
+            const bool okw = wait_pv(i - 1, 3);
             if (named_bar_or(bar_id, 128, !okw)) { aborted = true; break; }
             tc_fence_after();
 #pragma unroll 1
-            for (int x = 0; x < (NH == 64 ? 7 : 8); ++x) {
-              const uint32_t ta = tmem_addr(tmem + L::o_col(x >> 1) + (x & 1) * NH + ch * NHH, qd * 32, 0);
-              uint32_t ov[NHH];
-              tmem_ld_n<NHH>(ta, ov);
+            for (int x = 0; x < (NH == 64 ? 7 : 8) * (NHH / 8); ++x) {  // 8 columns at a time
+              const int part = x / (NHH / 8), h0 = ch * NHH + (x % (NHH / 8)) * 8;
+              const uint32_t ta = tmem_addr(tmem + L::o_col(part >> 1) + (part & 1) * NH + h0, qd * 32, 0);
+              uint32_t ov[8];
+              tmem_ld8(ta, ov);
               tmem_ld_wait();
 #pragma unroll
-              for (int h = 0; h < NHH; ++h) ov[h] = __float_as_uint(__uint_as_float(ov[h]) * s_fac[ch * NHH + h]);
-              tmem_st_n<NHH>(ta, ov);
+              for (int h = 0; h < 8; ++h) ov[h] = __float_as_uint(__uint_as_float(ov[h]) * s_fac[h0 + h]);
+              tmem_st8(ta, ov);
             }
             tmem_st_wait();
           }
@@ -591,9 +761,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const Params p) 
         uint32_t hi[NQ / 2], lo[NQ / 2];
 #pragma unroll
         for (int j = 0; j < NQ; j += 2) {
-          const float ma = s_stat[n0 + j], mb2 = s_stat[n0 + j + 1];
-          const float pa = exp2f(z[j] - (ma == -INFINITY ? 0.f : ma));
-          const float pb = exp2f(z[j + 1] - (mb2 == -INFINITY ? 0.f : mb2));
+          const float pa = ex2(fmaf(z[j], p.sl2e, -m_use(m_run[j])));
+          const float pb = ex2(fmaf(z[j + 1], p.sl2e, -m_use(m_run[j + 1])));
           l_part[j] += pa;
           l_part[j + 1] += pb;
           const __nv_bfloat162 h2 = __floats2bfloat162_rn(pa, pb);
@@ -602,8 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const Params p) 
           lo[j / 2] = pack_bf16x2(pa - hf.x, pb - hf.y);
         }
         if (L::OVERLAY && i >= 1) {
-          const bool okp = mbar_wait(bar_pv + 8 * ((i - 1) % R), ((i - 1) / R) & 1, s_abort, p.err, p.wait_limit);
-          if (!okp) bad = true;  // (the store below then goes unused: no product is formed after an abort)
+          if (!wait_pv(i - 1, 3)) bad = true;  // (the store below then goes unused: no product is formed after an abort)
         }
         const uint32_t sP = L::p(sKV, i);
         if constexpr (NH == 64) {
@@ -627,20 +795,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const Params p) 
         if (lane == 0 && !bad) mbar_arrive(bar_p + 8 * (i & 1));
       }
       if (!aborted) {
-        const bool got = mbar_wait(bar_pv + 8 * ((i - 1) % R), ((i - 1) / R) & 1, s_abort, p.err, p.wait_limit);
+        const bool got = wait_pv(i - 1, 3);
         aborted = named_bar_or(bar_id, 128, !got);
         tc_fence_after();
       }
       if (aborted) break;
       // ---- the segment's rows: out and lse, or the workspace's partial sums ----
-#pragma unroll
-      for (int j = 0; j < NQ; ++j) {
-        const float l = reduce_keys(l_part[j], false);
-        if ((lane & ~2) == 0) s_red[qd * NH + n0 + j] = l;
-      }
+      s_red[qd * NH + sum_row] = over_keys(l_part, false);
       named_bar(bar_id, 128);
-      const bool whole = sg.t0 == 0 && sg.t1 == sg.T;
-      const int slot = 2 * blockIdx.x + (sg.t0 == 0 ? 1 : 0);
+      const bool whole = sg.whole;
+      const int slot = 2 * blockIdx.x + (sg.opens ? 1 : 0);
       if (qd == 0 && lane < NHH) {
         const int n = ch * NHH + lane;
         const float l = s_red[n] + s_red[NH + n] + s_red[2 * NH + n] + s_red[3 * NH + n];
@@ -660,40 +824,40 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const Params p) 
         s_fac[n] = fac;
       }
       named_bar(bar_id, 128);
+      // a few rows of 32 channels at a time, in a loop: unrolled, this code is longer than the time it takes to fetch it
+      constexpr int kStep = NHH < 16 ? NHH : 16;
 #pragma unroll 1
-      for (int mt = 0; mt < 4; ++mt) {
-        uint32_t oh[NHH];
-        const uint32_t ta = tmem_addr(tmem + L::o_col(mt) + ch * NHH, qd * 32, 0);
-        tmem_ld_n<NHH>(ta, oh);
-        if (NH != 64 || mt < 3) {
-          uint32_t ol[NHH];
-          tmem_ld_n<NHH>(ta + NH, ol);
-          tmem_ld_wait();
-#pragma unroll
-          for (int h = 0; h < NHH; ++h) oh[h] = __float_as_uint(__uint_as_float(oh[h]) + __uint_as_float(ol[h]));
+      for (int x = 0; x < 4 * NHH / kStep; ++x) {
+        const int mt = x / (NHH / kStep), h0 = ch * NHH + (x % (NHH / kStep)) * kStep;
+        uint32_t oh[kStep], ol[kStep];
+        const uint32_t ta = tmem_addr(tmem + L::o_col(mt) + h0, qd * 32, 0);
+        const bool split = NH != 64 || mt < 3;
+        const uint32_t tl = split ? ta + NH : ta;  // (the last tile's hi and lo are one sum)
+        if constexpr (kStep == 16) {
+          tmem_ld16(ta, oh);
+          tmem_ld16(tl, ol);
         } else {
-          tmem_ld_wait();
+          tmem_ld8(ta, oh);
+          tmem_ld8(tl, ol);
         }
+        tmem_ld_wait();
         const int c = mt * 128 + qd * 32 + lane;
-        if (whole) {
+        float* part = p.partial + ((size_t)slot * 64 + h0) * kDv + c;
+        __nv_bfloat16* dst = p.out + (size_t)(sg.row0 + h0) * kDv + c;
 #pragma unroll
-          for (int h = 0; h < NHH; ++h) {
-            const int n = ch * NHH + h;
-            const float f = s_fac[n];
-            if (n < sg.rows) p.out[(size_t)(sg.row0 + n) * kDv + c] = __float2bfloat16_rn(f == 0.f ? 0.f : __uint_as_float(oh[h]) * f);
-          }
-        } else {
-#pragma unroll
-          for (int h = 0; h < NHH; ++h) {
-            const int n = ch * NHH + h;
-            if (n < sg.rows) p.partial[((size_t)slot * 64 + n) * kDv + c] = __uint_as_float(oh[h]);
+        for (int h = 0; h < kStep; ++h) {
+          const float o = __uint_as_float(oh[h]) + (split ? __uint_as_float(ol[h]) : 0.f);
+          if (h0 + h < sg.rows) {
+            const float f = s_fac[h0 + h];
+            if (whole) dst[h * kDv] = __float2bfloat16_rn(f == 0.f ? 0.f : o * f);
+            else part[h * kDv] = o;
           }
         }
       }
       tc_fence_before();
       named_bar(bar_id, 128);  // s_red, s_stat and s_fac have been read
+      if (!more) break;
       sg = nx;
-      have = more;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
@@ -703,69 +867,163 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const Params p) 
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, L::TM_COLS);
+    if (lane == 0 && *s_abort) record_error(p.err, DSA_ERR_TIMEOUT);
   }
 }
 
-// Joins the pieces of the groups that went over several CTAs: one row per half CTA at a time, 128 threads with 4
-// channels each.  Pieces are read in CTA order, so the result does not depend on which came first.
-__global__ void __launch_bounds__(256) paged_mla_join_kernel(const int4* __restrict__ records, int ctas,
-                                                            const float* __restrict__ stats,
-                                                            const float* __restrict__ partial,
-                                                            const float* __restrict__ sink, int H,
-                                                            __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+// Joins the pieces of the groups that went over several CTAs.  A row of few pieces is a team's of 128 threads, 4 channels
+// each; a row of many (one long request over the whole card) is a CTA's, whose eight teams take every eighth piece, so
+// that 152 pieces are 19 loads deep.  Pieces are added in a fixed order, whichever came first.
+constexpr int kJoin = 1024, kTeams = kJoin / 128, kMany = 16;
+__global__ void __launch_bounds__(kJoin) paged_mla_join_kernel(const int4* __restrict__ records, int ctas,
+                                                              const float* __restrict__ stats,
+                                                              const float* __restrict__ partial,
+                                                              const float* __restrict__ sink, int H,
+                                                              __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
   __shared__ int4 rec[kMaxCtas];
-  __shared__ int first[kMaxCtas + 1];
-  for (int c = threadIdx.x; c < ctas; c += 256) rec[c] = records[c];
+  __shared__ int first[2][kMaxCtas + 1];  // rows before each record: of few pieces, of many
+  __shared__ float fac[kMaxCtas];
+  __shared__ float4 acc[kTeams][128];
+  __shared__ float s_l, s_base;
+  const int tid = threadIdx.x, lane = tid & 31, team = tid >> 7, x = tid & 127;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the pieces are still being made
+  if (tid < ctas) rec[tid] = records[tid];
   __syncthreads();
-  if (threadIdx.x < 32) {  // rows before each record
+  if (tid < 64) {
+    const int many = tid >> 5;
     int base = 0;
     for (int c0 = 0; c0 < ctas; c0 += 32) {
-      const int c = c0 + threadIdx.x;
-      const int v = c < ctas ? rec[c].y : 0;
+      const int c = c0 + lane;
+      int v = 0;
+      if (c < ctas && (rec[c].w - c + 1 >= kMany) == (many == 1)) v = rec[c].y;
       int inc = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, o);
-        if ((int)threadIdx.x >= o) inc += x;
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
       }
-      if (c < ctas) first[c] = base + inc - v;
+      if (c < ctas) first[many][c] = base + inc - v;
       base += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (threadIdx.x == 0) first[ctas] = base;
+    if (lane == 0) first[many][ctas] = base;
   }
   __syncthreads();
-  const int total = first[ctas];
-  const int half = threadIdx.x >> 7, x = threadIdx.x & 127;
-  for (int it = blockIdx.x * 2 + half; it < total; it += gridDim.x * 2) {
-    int lo = 0, hi = ctas;  // last c with first[c] <= it
+  auto find = [&](const int* f, int it) -> int {  // last c with f[c] <= it: the record that holds row `it`
+    int lo = 0, hi = ctas;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (first[mid] <= it) lo = mid; else hi = mid;
+      if (f[mid] <= it) lo = mid; else hi = mid;
     }
+    return lo;
+  };
+  auto piece = [&](int lo, int k, int n) -> size_t { return (size_t)(2 * (lo + k) + (k == 0 ? 1 : 0)) * 64 + n; };
+  auto store = [&](int row, float4 o, float l, float base) {
+    const bool empty = l == 0.f;  // nothing is seen, and there is no sink
+    const float inv = empty ? 0.f : 1.f / l;
+    reinterpret_cast<uint2*>(out + (size_t)row * kDv)[x] =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (x == 0) lse[row] = empty ? -INFINITY : base * kLn2 + logf(l);
+  };
+  for (int it = blockIdx.x * kTeams + team; it < first[0][ctas]; it += gridDim.x * kTeams) {
+    const int lo = find(first[0], it);
     const int4 rc = rec[lo];
-    const int n = it - first[lo];
+    const int n = it - first[0][lo], pieces = rc.w - lo + 1;
+    const float* src = partial;
+    float4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      v[k] = k < pieces ? __ldg(reinterpret_cast<const float4*>(src + piece(lo, k, n) * kDv) + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+    // lane k holds piece k's maximum and sum
+    const size_t at = lane < pieces ? piece(lo, lane, n) : 0;
+    const float mc = lane < pieces ? __ldg(stats + at / 64 * 128 + n) : -INFINITY;
+    const float lc = lane < pieces ? __ldg(stats + at / 64 * 128 + 64 + n) : 0.f;
     const float s2 = sink ? __ldg(sink + (rc.z + n) % H) * kLog2e : -INFINITY;
-    float m = s2;
-    for (int c = lo; c <= rc.w; ++c) m = fmaxf(m, __ldg(stats + (size_t)(2 * c + (c == lo)) * 128 + n));
+    float m = fmaxf(mc, s2);
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = __shfl_sync(0xffffffffu, m, 0);
     const float base = m == -INFINITY ? 0.f : m;
-    float l = exp2f(s2 - base);
+    const float f = exp2f(mc - base);
+    float l = lane < pieces ? f * lc : 0.f;
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    l = __shfl_sync(0xffffffffu, l, 0) + exp2f(s2 - base);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = lo; c <= rc.w; ++c) {
-      const int slot = 2 * c + (c == lo);
-      const float f = exp2f(__ldg(stats + (size_t)slot * 128 + n) - base);
-      const float4 v = __ldg(reinterpret_cast<const float4*>(partial + ((size_t)slot * 64 + n) * kDv) + x);
-      l += f * __ldg(stats + (size_t)slot * 128 + 64 + n);
+    for (int k0 = 0; k0 < pieces; k0 += 4) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k0 + k < pieces) {
+          const float w = __shfl_sync(0xffffffffu, f, k0 + k);
+          o.x += w * v[k].x;
+          o.y += w * v[k].y;
+          o.z += w * v[k].z;
+          o.w += w * v[k].w;
+          if (k0 + 4 + k < pieces) v[k] = __ldg(reinterpret_cast<const float4*>(src + piece(lo, k0 + 4 + k, n) * kDv) + x);
+        }
+      }
+    }
+    store(rc.x + n, o, l, base);
+  }
+  for (int it = blockIdx.x; it < first[1][ctas]; it += gridDim.x) {
+    const int lo = find(first[1], it);
+    const int4 rc = rec[lo];
+    const int n = it - first[1][lo], pieces = rc.w - lo + 1;
+    // the first pieces' channels are on their way while the maxima are compared
+    float4 v = __ldg(reinterpret_cast<const float4*>(partial + piece(lo, team, n) * kDv) + x);  // (kMany >= kTeams)
+    if (tid < 32) {
+      const float s2 = sink ? __ldg(sink + (rc.z + n) % H) * kLog2e : -INFINITY;
+      float mc[kMaxCtas / 32], lc[kMaxCtas / 32], m = s2;
+#pragma unroll
+      for (int j = 0; j < kMaxCtas / 32; ++j) {
+        const int k = j * 32 + lane;
+        const size_t at = k < pieces ? piece(lo, k, n) / 64 * 128 + n : 0;
+        mc[j] = k < pieces ? __ldg(stats + at) : -INFINITY;
+        lc[j] = k < pieces ? __ldg(stats + at + 64) : 0.f;
+        m = fmaxf(m, mc[j]);
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float base = m == -INFINITY ? 0.f : m;
+      float l = lane == 0 ? exp2f(s2 - base) : 0.f;
+#pragma unroll
+      for (int j = 0; j < kMaxCtas / 32; ++j) {
+        const int k = j * 32 + lane;
+        const float f = exp2f(mc[j] - base);
+        if (k < pieces) {
+          fac[k] = f;
+          l += f * lc[j];
+        }
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane == 0) { s_l = l; s_base = base; }
+    }
+    __syncthreads();
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = team; k < pieces; k += kTeams) {
+      float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k + kTeams < pieces) w = __ldg(reinterpret_cast<const float4*>(partial + piece(lo, k + kTeams, n) * kDv) + x);
+      const float f = fac[k];
       o.x += f * v.x;
       o.y += f * v.y;
       o.z += f * v.z;
       o.w += f * v.w;
+      v = w;
     }
-    const bool empty = l == 0.f;  // nothing is seen, and there is no sink
-    const float inv = empty ? 0.f : 1.f / l;
-    reinterpret_cast<uint2*>(out + (size_t)(rc.x + n) * kDv)[x] =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (x == 0) lse[rc.x + n] = empty ? -INFINITY : base * kLn2 + logf(l);
+    acc[team][x] = o;
+    __syncthreads();
+    if (team == 0) {
+#pragma unroll
+      for (int k = 1; k < kTeams; ++k) {
+        const float4 w = acc[k][x];
+        o.x += w.x;
+        o.y += w.y;
+        o.z += w.z;
+        o.w += w.w;
+      }
+      store(rc.x + n, o, s_l, s_base);
+    }
+    __syncthreads();
   }
 }
 
@@ -782,14 +1040,14 @@ int cta_count() {
 }
 
 template <int DQK, int NH>
-dsa_status_t launch(Params& p, int ctas, cudaStream_t s) {
+dsa_status_t launch(Params& p, const CUtensorMap& map, int ctas, cudaStream_t s) {
   using L = Smem<DQK, NH>;
   dsa_status_t st = configure_kernel_smem(reinterpret_cast<const void*>(paged_mla_kernel<DQK, NH>), L::TOTAL,
                                           "configuring paged_mla_kernel");
   if (st != DSA_OK) return st;
   p.G = p.topk_idx ? 1 : (p.H <= NH ? NH / p.H : 1);
   p.HB = (p.H + NH - 1) / NH;
-  paged_mla_kernel<DQK, NH><<<ctas, kThreads, L::TOTAL, s>>>(p);
+  paged_mla_kernel<DQK, NH><<<ctas, kThreads, L::TOTAL, s>>>(p, map);
   return cuda_check(cudaGetLastError(), "launching paged_mla_kernel");
 }
 
@@ -858,13 +1116,31 @@ extern "C" dsa_status_t dsa_paged_mla(const dsa_bf16_t* q, const dsa_bf16_t* cac
   p.stats = reinterpret_cast<float*>(ws + kErrorWordBytes + pmla::kRecordBytes);
   p.partial = reinterpret_cast<float*>(ws + kErrorWordBytes + pmla::kRecordBytes + pmla::kStatBytes);
   p.wait_limit = wait_limit_cycles();
+  // rows that follow one another in the cache, 32 or a whole page of them at a time
+  p.box = 0;
+  CUtensorMap map{};
+  if (!topk_idx && num_pages > 0 && (page_size % 32 == 0 || 32 % page_size == 0) && page_size >= 8 &&
+      (int64_t)num_pages * page_size <= 0x7fffffffll) {
+    p.box = page_size < 32 ? page_size : 32;
+    if ((st = make_map_2d_bf16(&map, cache, (uint64_t)num_pages * page_size, Dqk, Dqk, 64, p.box)) != DSA_OK) return st;
+  }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // 16 columns while all rows of a request (or of a list) fit: fewer products of zero columns, a longer ring
   const int64_t rows = (int64_t)H * (topk_idx ? 1 : (N + B - 1) / B);
-  if (rows <= 16) st = Dqk == 576 ? pmla::launch<576, 16>(p, ctas, s) : pmla::launch<512, 16>(p, ctas, s);
-  else st = Dqk == 576 ? pmla::launch<576, 64>(p, ctas, s) : pmla::launch<512, 64>(p, ctas, s);
+  if (rows <= 16) st = Dqk == 576 ? pmla::launch<576, 16>(p, map, ctas, s) : pmla::launch<512, 16>(p, map, ctas, s);
+  else st = Dqk == 576 ? pmla::launch<576, 64>(p, map, ctas, s) : pmla::launch<512, 64>(p, map, ctas, s);
   if (st != DSA_OK) return st;
-  pmla::paged_mla_join_kernel<<<2 * ctas, 256, 0, s>>>(p.records, ctas, p.stats, p.partial, attn_sink, H, p.out, lse);
-  st = cuda_check(cudaGetLastError(), "launching paged_mla_join_kernel");
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * ctas);
+  cfg.blockDim = dim3(pmla::kJoin);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  st = cuda_check(cudaLaunchKernelEx(&cfg, pmla::paged_mla_join_kernel, (const int4*)p.records, ctas, (const float*)p.stats,
+                                     (const float*)p.partial, attn_sink, H, p.out, lse),
+                  "launching paged_mla_join_kernel");
   return st == DSA_OK ? ok() : st;
 }
