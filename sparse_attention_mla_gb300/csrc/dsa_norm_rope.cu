@@ -11,13 +11,17 @@
 //   dw = sum g xh, db = sum g,  gw = g w,
 //   dx = r (gw - [mean gw] - xh mean(gw xh))     ([..] in the layer norm only).
 //
-// What bounds it: DRAM, 4 bytes a channel forward and 6 backward.  So the rows
-// stay in registers between the one read and the one write, LPR lanes to a row
-// (8 for 64 channels, 16 for 128, else a warp), 16 bytes a lane, the next row's
-// loads in flight while this one is worked on.  The cosines and sines depend on
-// the token alone: a group of lanes keeps one token and walks its heads, so they
-// are formed once for up to 16 heads, spread over the lanes, and kept in shared
-// memory.
+// What bounds it: DRAM, 4 bytes a channel forward and 6 backward; at 8 channels a
+// lane the instructions come close behind.  So the rows stay in registers between
+// the one read and the one write, LPR lanes to a row (8 for 64 channels, 16 for
+// 128, else a warp), 16 bytes a lane and two fp32 operations an instruction; a
+// group of lanes takes U consecutive rows (up to 4) at once, the next U on their
+// way meanwhile, and the CTAs stay, so that the table of frequencies is made once.
+// The cosines and sines depend on the token alone: they are formed once per token
+// of a group's run of rows, spread over its lanes, in shared memory.  Measured: the
+// position channels of 16384 x 64 heads (128 of every 1152 bytes) 60 us at 4.5 TB/s,
+// 131104 rows of 128 with the norm 23 us at 2.9 TB/s, the gradient of 32768 rows of
+// 128 with the layer norm 19 us at 1.3 TB/s (three batches of rows a group: latency).
 //
 // Angles: positions reach millions, and position times frequency in fp32 is then
 // off by 0.1 rad.  The frequency is held as a 64-bit binary fraction of a turn, so
@@ -25,6 +29,7 @@
 // 32 bits are the angle.  Sums and statistics are fp32; rows are rounded to bf16
 // once, when written.
 #include <cmath>
+#include <type_traits>
 
 #include "dsa_device.cuh"
 #include "dsa_host.h"
@@ -32,10 +37,13 @@
 namespace dsa {
 namespace nrope {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kMaxD = 1024;
-constexpr int kMaxPartials = 608;  // CTAs of a backward launch: each leaves one row of dw and db
+constexpr int kMaxPartials = 608;  // CTAs of a backward launch with parameters: each leaves one row of dw and db
 enum { kNone = 0, kRms = 1, kLayer = 2 };
+
+// CTAs of an SM, by the registers that a lane's channels take.
+__host__ __device__ constexpr int ctas_per_sm(int VEC, int NIT) { return NIT <= 2 && VEC == 8 ? 2 : 1; }
 
 struct Rows {
   const __nv_bfloat16* x;
@@ -49,16 +57,40 @@ struct Rows {
   const int32_t* pos;
   const float* inv_freq;
   float rscale;
-  int hpt;        // heads that a group of lanes takes of one token
-  int64_t tasks;  // T * ceil(H / hpt)
+  int rows, run;  // T * H; consecutive rows of a group of lanes (a multiple of U)
 };
+
+// Two fp32 operations in one instruction, each rounded as the scalar one.
+__device__ __forceinline__ uint64_t pack2(float2 a) {
+  return (uint64_t)__float_as_uint(a.x) | ((uint64_t)__float_as_uint(a.y) << 32);
+}
+__device__ __forceinline__ float2 unpack2(uint64_t r) {
+  return make_float2(__uint_as_float((uint32_t)r), __uint_as_float((uint32_t)(r >> 32)));
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
+  return unpack2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
+  return unpack2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)), "l"(pack2(c)));
+  return unpack2(r);
+}
 
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// A row in registers: E = VEC * NIT channels per lane, channel c = (it * LPR + l) * VEC + e.
+// A row in registers: per lane NIT accesses of VEC channels, channel c = (it * LPR + l) * VEC + e; in fp32 as pairs of
+// neighbours (on the scalar path a pair is one channel and a zero).
 template <int VEC, int LPR, int NIT>
-struct Raw {
+struct Row {
+  static constexpr int PP = VEC == 8 ? 4 : 1, P = PP * NIT;  // pairs per access, per lane
   uint4 v[VEC == 8 ? NIT : 1];
   uint16_t s[VEC == 8 ? 1 : NIT];
   __device__ __forceinline__ void load(const __nv_bfloat16* row, int D, int l, bool on) {
@@ -74,35 +106,32 @@ struct Raw {
       }
     }
   }
-  __device__ __forceinline__ void values(float (&f)[VEC * NIT]) const {
+  __device__ __forceinline__ void values(float2 (&f)[P]) const {
 #pragma unroll
     for (int it = 0; it < NIT; ++it) {
       if constexpr (VEC == 8) {
         const uint32_t u[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          f[it * 8 + 2 * k] = bf_lo(u[k]);
-          f[it * 8 + 2 * k + 1] = bf_hi(u[k]);
-        }
+        for (int k = 0; k < 4; ++k) f[it * 4 + k] = make_float2(bf_lo(u[k]), bf_hi(u[k]));
       } else {
-        f[it] = __uint_as_float((uint32_t)s[it] << 16);
+        f[it] = make_float2(__uint_as_float((uint32_t)s[it] << 16), 0.f);
       }
     }
   }
 };
 
 template <int VEC, int LPR, int NIT>
-__device__ __forceinline__ void store_row(__nv_bfloat16* row, int D, int l, const float (&f)[VEC * NIT]) {
+__device__ __forceinline__ void store_row(__nv_bfloat16* row, int D, int l, const float2 (&f)[Row<VEC, LPR, NIT>::P]) {
 #pragma unroll
   for (int it = 0; it < NIT; ++it) {
     const int c = (it * LPR + l) * VEC;
     if (c >= D) continue;
     if constexpr (VEC == 8) {
       *reinterpret_cast<uint4*>(row + c) =
-          make_uint4(pack_bf16x2(f[it * 8], f[it * 8 + 1]), pack_bf16x2(f[it * 8 + 2], f[it * 8 + 3]),
-                     pack_bf16x2(f[it * 8 + 4], f[it * 8 + 5]), pack_bf16x2(f[it * 8 + 6], f[it * 8 + 7]));
+          make_uint4(pack_bf16x2(f[it * 4].x, f[it * 4].y), pack_bf16x2(f[it * 4 + 1].x, f[it * 4 + 1].y),
+                     pack_bf16x2(f[it * 4 + 2].x, f[it * 4 + 2].y), pack_bf16x2(f[it * 4 + 3].x, f[it * 4 + 3].y));
     } else {
-      row[c] = __float2bfloat16_rn(f[it]);
+      row[c] = __float2bfloat16_rn(f[it].x);
     }
   }
 }
@@ -114,23 +143,24 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// Shared memory: the fractions of a turn per position [R/2], then per group of lanes the token's
-// (scaled) cosines and sines [R/2] and R channels for the exchange between the two of a pair.
+// Shared memory: the fractions of a turn per position [R/2], then per group of lanes the (scaled) cosines and sines of
+// the last U tokens [U][R/2] (token t in slot t % U) and R channels for the exchange between the two of a pair.
 struct Shared {
   uint64_t* turn;
   float2* cs;
   float* stage;
 };
+template <int U>
 __device__ __forceinline__ Shared carve(uint8_t* raw, int R, int group) {
   const int half = R >> 1;
   Shared s;
   s.turn = reinterpret_cast<uint64_t*>(raw);
-  uint8_t* mine = raw + (size_t)half * 8 + (size_t)group * half * 16;
+  uint8_t* mine = raw + (size_t)half * 8 + (size_t)group * half * 8 * (U + 1);
   s.cs = reinterpret_cast<float2*>(mine);
-  s.stage = reinterpret_cast<float*>(mine + (size_t)half * 8);
+  s.stage = reinterpret_cast<float*>(mine + (size_t)half * 8 * U);
   return s;
 }
-inline int shared_bytes(int R, int groups) { return (R >> 1) * 8 + groups * (R >> 1) * 16; }
+inline int shared_bytes(int R, int groups, int U) { return (R >> 1) * 8 * (1 + groups * (U + 1)); }
 
 __device__ __forceinline__ void fill_turns(uint64_t* turn, const Rows& p) {
   for (int i = threadIdx.x; i < (p.R >> 1); i += kThreads) {
@@ -141,230 +171,391 @@ __device__ __forceinline__ void fill_turns(uint64_t* turn, const Rows& p) {
 }
 
 template <int LPR>
-__device__ __forceinline__ void fill_cos_sin(const Shared& s, const Rows& p, int t, int l) {
-  const int64_t pos = __ldg(p.pos + t);
+__device__ __forceinline__ void fill_cos_sin(float2* cs, const uint64_t* turn, const Rows& p, int64_t pos, int l) {
   for (int i = l; i < (p.R >> 1); i += LPR) {
-    const int32_t frac = (int32_t)(((uint64_t)pos * s.turn[i]) >> 32);  // signed: [-1/2, 1/2) of a turn
+    const int32_t frac = (int32_t)(((uint64_t)pos * turn[i]) >> 32);  // signed: [-1/2, 1/2) of a turn
     float sn, c;
     sincospif((float)frac * 4.656612873077393e-10f, &sn, &c);  // 2^-31: half turns
-    s.cs[i] = make_float2(c * p.rscale, sn * p.rscale);
+    cs[i] = make_float2(c * p.rscale, sn * p.rscale);
   }
 }
 
-// Turns the row's rotated channels in place; back = -1 turns the other way (the transpose).
-template <int VEC, int LPR, int NIT>
-__device__ __forceinline__ void rotate(float (&f)[VEC * NIT], const Shared& s, const Rows& p, int l, float back) {
-  if (p.R == 0) return;
-  const int half = p.R >> 1;
-  if (VEC == 8 && p.inter) {  // both of a pair are in this lane (r0 is even on this path)
+// How a rotation reaches the other half of a pair.  kPairs: interleaved pairs inside a lane's whole accesses.  kLanes:
+// half layout, the other half is the same channel of the lane R / 16 away, and all rotated channels are in access `it`
+// of the row.  kShared: any layout, through shared memory.
+enum { kShared = 0, kPairs = 1, kLanes = 2 };
+
+// A token's cosines and sines as this lane needs them, and the turn of a row by them; back = -1 turns the other way
+// (the transpose).
+template <int VEC, int LPR, int NIT, int ROT>
+struct Turn {
+  static constexpr int PP = Row<VEC, LPR, NIT>::PP, P = Row<VEC, LPR, NIT>::P;
+  float2 a[ROT == kPairs ? P : 4], b[4];
+  int it, other;
+  bool in;
+  const float2* cs;
+  // `table`: any of the group's tables (a group without rows turns zeros by whatever is there)
+  __device__ __forceinline__ void init(const float2* table, const Rows& p, int l) {
+    cs = table;
 #pragma unroll
-    for (int it = 0; it < NIT; ++it) {
-      const int u0 = (it * LPR + l) * VEC - p.r0;
+    for (int e = 0; e < 4; ++e) b[e] = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < VEC; e += 2) {
-        const int u = u0 + e;
-        if (u < 0 || u >= p.R) continue;
-        const float2 c = s.cs[u >> 1];
-        const float sn = c.y * back, a = f[it * VEC + e], b = f[it * VEC + (e | (VEC > 1))];
-        f[it * VEC + e] = a * c.x - b * sn;
-        f[it * VEC + (e | (VEC > 1))] = b * c.x + a * sn;
+    for (int i = 0; i < (ROT == kPairs ? P : 4); ++i) a[i] = make_float2(1.f, 0.f);
+    it = ROT == kLanes ? p.r0 / (LPR * VEC) : 0;
+    const int u0 = (it * LPR + l) * VEC - p.r0;
+    in = u0 >= 0 && u0 < p.R;
+    const int half = p.R >> 1;
+    other = (l + (u0 >= half ? -(half / 8) : half / 8)) & (LPR - 1);
+  }
+  __device__ __forceinline__ void load(const float2* table, const Rows& p, int l, float back) {
+    cs = table;
+    if constexpr (ROT == kPairs) {
+#pragma unroll
+      for (int k = 0; k < NIT; ++k) {
+        const int u0 = (k * LPR + l) * VEC - p.r0;
+        if (u0 < 0 || u0 >= p.R) continue;
+        const float4* q = reinterpret_cast<const float4*>(table + (u0 >> 1));
+        const float4 x = q[0], y = q[1];
+        a[k * PP] = make_float2(x.x, x.y * back);
+        a[k * PP + 1 % PP] = make_float2(x.z, x.w * back);
+        a[k * PP + 2 % PP] = make_float2(y.x, y.y * back);
+        a[k * PP + 3 % PP] = make_float2(y.z, y.w * back);
+      }
+    } else if constexpr (ROT == kLanes) {
+      const int u0 = (it * LPR + l) * VEC - p.r0, half = p.R >> 1;
+      const bool second = u0 >= half;
+      const float4* q = reinterpret_cast<const float4*>(table + (in ? (second ? u0 - half : u0) : 0));
+      const float sign = second ? back : -back;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 c = q[e];
+        a[e] = in ? make_float2(c.x, c.z) : make_float2(1.f, 1.f);
+        b[e] = in ? make_float2(c.y * sign, c.w * sign) : make_float2(0.f, 0.f);
       }
     }
-    return;
   }
-  __syncwarp();  // the row before has been read
+  __device__ __forceinline__ void apply(float2 (&f)[P], float* stage, const Rows& p, int l, float back) const {
+    if constexpr (ROT == kPairs) {
 #pragma unroll
-  for (int it = 0; it < NIT; ++it)
+      for (int i = 0; i < P; ++i) {
+        const float2 x = f[i];
+        f[i] = make_float2(x.x * a[i].x - x.y * a[i].y, x.y * a[i].x + x.x * a[i].y);
+      }
+    } else if constexpr (ROT == kLanes) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int u = (it * LPR + l) * VEC + e - p.r0;
-      if (u >= 0 && u < p.R) s.stage[u] = f[it * VEC + e];
+      for (int k = 0; k < NIT; ++k) {
+        if (NIT > 1 && k != it) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = (k * PP + e) % P;  // (the remainder only keeps the unused scalar shape in range)
+          const float2 y = make_float2(__shfl_sync(0xffffffffu, f[i].x, other, LPR), __shfl_sync(0xffffffffu, f[i].y, other, LPR));
+          f[i] = fma2(f[i], a[e], mul2(y, b[e]));
+        }
+      }
+    } else {
+      if (p.R == 0) return;
+      const int half = p.R >> 1;
+      constexpr int W = VEC == 8 ? 2 : 1;  // channels of a pair of values
+      __syncwarp();  // the row before has been read
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const int u = ((i / PP) * LPR + l) * VEC + (i % PP) * 2 + e - p.r0;
+          if (u >= 0 && u < p.R) stage[u] = e ? f[i].y : f[i].x;
+        }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const int u = ((i / PP) * LPR + l) * VEC + (i % PP) * 2 + e - p.r0;
+          if (u < 0 || u >= p.R) continue;
+          const bool second = p.inter ? (u & 1) : (u >= half);
+          const int k = p.inter ? (u >> 1) : (second ? u - half : u);
+          const int partner = p.inter ? (u ^ 1) : (second ? u - half : u + half);
+          const float2 c = cs[k];
+          const float sn = second ? c.y * back : -c.y * back;
+          float& x = e ? f[i].y : f[i].x;
+          x = x * c.x + stage[partner] * sn;
+        }
     }
-  __syncwarp();
+  }
+};
+
+// weight or bias of this lane's channels below n (`none` where there is no array; 16-byte loads on the vector path,
+// where n is a multiple of 8)
+template <int VEC, int LPR, int NIT>
+__device__ __forceinline__ void load_param(float2 (&v)[Row<VEC, LPR, NIT>::P], const float* a, float none, int n, int l) {
+  constexpr int PP = Row<VEC, LPR, NIT>::PP;
 #pragma unroll
-  for (int it = 0; it < NIT; ++it)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int u = (it * LPR + l) * VEC + e - p.r0;
-      if (u < 0 || u >= p.R) continue;
-      const bool second = p.inter ? (u & 1) : (u >= half);
-      const int i = p.inter ? (u >> 1) : (second ? u - half : u);
-      const int other = p.inter ? (u ^ 1) : (second ? u - half : u + half);
-      const float2 c = s.cs[i];
-      const float sn = second ? c.y * back : -c.y * back;
-      f[it * VEC + e] = f[it * VEC + e] * c.x + s.stage[other] * sn;
+  for (int it = 0; it < NIT; ++it) {
+    const int c0 = (it * LPR + l) * VEC;
+    const bool on = a != nullptr && c0 < n;
+    if constexpr (VEC == 8) {
+      float4 x = make_float4(none, none, none, none), y = x;
+      if (on) {
+        x = __ldg(reinterpret_cast<const float4*>(a + c0));
+        y = __ldg(reinterpret_cast<const float4*>(a + c0) + 1);
+      }
+      v[it * PP] = make_float2(x.x, x.y);
+      v[it * PP + 1] = make_float2(x.z, x.w);
+      v[it * PP + 2] = make_float2(y.x, y.y);
+      v[it * PP + 3] = make_float2(y.z, y.w);
+    } else {
+      v[it] = make_float2(on ? __ldg(a + c0) : none, 0.f);
     }
+  }
 }
 
-// weight or bias of this lane's channels below n (`none` where there is no array)
-template <int VEC, int LPR, int NIT>
-__device__ __forceinline__ float param(const float* a, float none, int n, int l, int k) {
-  const int c = ((k / VEC) * LPR + l) * VEC + (k % VEC);
-  return (a != nullptr && c < n) ? __ldg(a + c) : none;
-}
+// A group's run of rows, U at a time: their tokens and heads, and the tokens' cosines and sines as they come up.
+template <int LPR, int U>
+struct Run {
+  int row, end, t, h;  // next row, end of the run; token and head of the next row
+  int filled;          // last token whose cosines and sines are there
+  __device__ __forceinline__ void begin(const Rows& p, int64_t first) {
+    row = first < p.rows ? (int)first : p.rows;
+    end = (int)min((int64_t)p.rows, first + p.run);
+    t = row / p.H;
+    h = row - t * p.H;
+    filled = t - 1;
+  }
+  // the next U rows (t = -1: none) and their positions
+  __device__ __forceinline__ void batch(const Rows& p, int (&tt)[U], int (&hh)[U], int (&pos)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      tt[u] = row < end ? t : -1;
+      hh[u] = h;
+      pos[u] = p.R > 0 && row < end ? __ldg(p.pos + t) : 0;
+      ++row;
+      if (++h == p.H) { h = 0; ++t; }
+    }
+  }
+  // the cosines and sines of a batch's tokens
+  __device__ __forceinline__ void cos_sin(const Rows& p, const Shared& s, const int (&tt)[U], const int (&pos)[U], int l) {
+    if (p.R == 0) return;
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (tt[u] > filled) {
+        fill_cos_sin<LPR>(s.cs + (size_t)(tt[u] % U) * (p.R >> 1), s.turn, p, pos[u], l);
+        filled = tt[u];
+      }
+    }
+    __syncwarp();
+  }
+};
 
-template <int VEC, int LPR, int NIT>
-__global__ void __launch_bounds__(kThreads)
+template <int VEC, int LPR, int NIT, int ROT, int U>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(VEC, NIT))
     norm_rope_fwd_kernel(const Rows p, __nv_bfloat16* out, int64_t os_t, int64_t os_h,
                          const int32_t* __restrict__ out_rows, int64_t num_rows, int* __restrict__ err) {
-  constexpr int E = VEC * NIT, GPW = 32 / LPR, GPB = kThreads / LPR;
+  using R = Row<VEC, LPR, NIT>;
+  constexpr int GPB = kThreads / LPR, P = R::P, PP = R::PP;
   extern __shared__ __align__(16) uint8_t raw_sh[];
   const int lane = threadIdx.x & 31, l = lane & (LPR - 1), group = threadIdx.x / LPR;
-  const Shared s = carve(raw_sh, p.R, group);
-  fill_turns(s.turn, p);
-  __syncthreads();
-  const int nhb = (p.H + p.hpt - 1) / p.hpt;
-  const float inv_n = p.n > 0 ? 1.f / (float)p.n : 0.f;
-  // the groups of a warp run the same trip counts; `on` marks the ones that have a row
-  const int64_t first = (int64_t)blockIdx.x * GPB + group, step = (int64_t)gridDim.x * GPB;
-  const int64_t warp_first = first - (lane / LPR);
-  Raw<VEC, LPR, NIT> cur;
-  auto row_of = [&](int64_t task, int hh, bool& on, int& t, int& h) {
-    t = (int)(task / nhb);
-    h = (int)(task - (int64_t)t * nhb) * p.hpt + hh;
-    on = task < p.tasks && h < p.H;
-  };
-  auto fetch = [&](int64_t task, int hh) {
-    bool on;
-    int t, h;
-    row_of(task, hh, on, t, h);
-    cur.load(p.x + (on ? t * p.xs_t + h * p.xs_h : 0), p.D, l, on);
-  };
-  fetch(first, 0);
-  for (int64_t k = 0; warp_first + k * step < p.tasks; ++k) {
-    const int64_t task = first + k * step;
-    if (p.R > 0) {
-      __syncwarp();
-      if (task < p.tasks) fill_cos_sin<LPR>(s, p, (int)(task / nhb), l);
-      __syncwarp();
+  const Shared s = carve<U>(raw_sh, p.R, group);
+  // rows on their way while the ones before are worked on
+  Run<LPR, U> run;
+  int nt[U], nh[U], np[U], no[U];
+  R nraw[U];
+  auto fetch = [&]() {
+    run.batch(p, nt, nh, np);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      nraw[u].load(p.x + (nt[u] >= 0 ? nt[u] * p.xs_t + nh[u] * p.xs_h : 0), p.D, l, nt[u] >= 0);
+      no[u] = out_rows != nullptr && nt[u] >= 0 ? __ldg(out_rows + nt[u]) : nt[u];
     }
-    for (int hh = 0; hh < p.hpt; ++hh) {
-      bool on;
-      int t, h;
-      row_of(task, hh, on, t, h);
-      float f[E];
-      cur.values(f);
-      if (hh + 1 < p.hpt) fetch(task, hh + 1);
-      else fetch(task + step, 0);
-      if (p.kind != kNone) {
-        float mean = 0.f, ss = 0.f;
-        if (p.kind == kLayer) {
+  };
+  int64_t first = ((int64_t)blockIdx.x * GPB + group) * p.run;
+  run.begin(p, first);
+  fetch();
+  fill_turns(s.turn, p);
+  const float inv_n = p.n > 0 ? 1.f / (float)p.n : 0.f;
+  float2 w[NIT == 1 ? P : 1];  // the weights stay in registers where a lane has 8 channels
+  if constexpr (NIT == 1) load_param<VEC, LPR, NIT>(w, p.w, 1.f, p.n, l);
+  Turn<VEC, LPR, NIT, ROT> turn;
+  turn.init(s.cs, p, l);
+  __syncthreads();
+  const int64_t step = (int64_t)gridDim.x * GPB * p.run;
+  // the groups of a warp run the same trip counts
+  for (int64_t warp_first = first - (int64_t)(lane / LPR) * p.run; warp_first < p.rows; warp_first += step) {
+    int turned = -1;  // the token whose cosines and sines `turn` holds
+#pragma unroll 1
+    for (int k = 0; k < p.run; k += U) {
+      int tt[U], hh[U], pos[U], o[U];
+      R raw[U];
 #pragma unroll
-          for (int i = 0; i < E; ++i) mean += (((i / VEC) * LPR + l) * VEC + (i % VEC) < p.n) ? f[i] : 0.f;
-          mean = group_sum<LPR>(mean) * inv_n;
-        }
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const bool in = ((i / VEC) * LPR + l) * VEC + (i % VEC) < p.n;
-          if (in) f[i] -= mean;
-          ss += in ? f[i] * f[i] : 0.f;
-        }
-        const float r = rsqrtf(group_sum<LPR>(ss) * inv_n + p.eps);
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          if (((i / VEC) * LPR + l) * VEC + (i % VEC) < p.n)
-            f[i] = f[i] * r * param<VEC, LPR, NIT>(p.w, 1.f, p.n, l, i) + param<VEC, LPR, NIT>(p.b, 0.f, p.n, l, i);
+      for (int u = 0; u < U; ++u) {
+        tt[u] = nt[u];
+        hh[u] = nh[u];
+        pos[u] = np[u];
+        o[u] = no[u];
+        raw[u] = nraw[u];
+        if (out_rows != nullptr && tt[u] >= 0 && (o[u] < -1 || o[u] >= num_rows)) {
+          if (l == 0) record_error(err, DSA_ERR_DEVICE_INDEX);
+          o[u] = -1;
         }
       }
-      rotate<VEC, LPR, NIT>(f, s, p, l, 1.f);
-      if (on) {
-        int64_t o = t;
-        if (out_rows != nullptr) {
-          o = __ldg(out_rows + t);
-          if (o < -1 || o >= num_rows) {
-            if (l == 0) record_error(err, DSA_ERR_DEVICE_INDEX);
-            o = -1;
+      run.cos_sin(p, s, tt, pos, l);
+      if (k + U >= p.run) {
+        first += step;
+        run.begin(p, first);
+      }
+      fetch();
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float2 f[P];
+        raw[u].values(f);
+        if (p.kind != kNone) {
+          float2 mean = make_float2(0.f, 0.f), ss = mean;
+          if (p.kind == kLayer) {
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+              if (((i / PP) * LPR + l) * VEC < p.n) mean = add2(mean, f[i]);
+            const float m = -group_sum<LPR>(mean.x + mean.y) * inv_n;
+            mean = make_float2(m, VEC == 8 ? m : 0.f);
+          }
+#pragma unroll
+          for (int i = 0; i < P; ++i)
+            if (((i / PP) * LPR + l) * VEC < p.n) {
+              if (p.kind == kLayer) f[i] = add2(f[i], mean);
+              ss = fma2(f[i], f[i], ss);
+            }
+          const float r = rsqrtf(group_sum<LPR>(ss.x + ss.y) * inv_n + p.eps);
+          const float2 r2 = make_float2(r, r);
+          float2 v[P];
+          if constexpr (NIT > 1) load_param<VEC, LPR, NIT>(v, p.w, 1.f, p.n, l);
+#pragma unroll
+          for (int i = 0; i < P; ++i)
+            if (((i / PP) * LPR + l) * VEC < p.n) f[i] = mul2(mul2(f[i], r2), NIT == 1 ? w[i % (NIT == 1 ? P : 1)] : v[i]);
+          if (p.b != nullptr) {
+            load_param<VEC, LPR, NIT>(v, p.b, 0.f, p.n, l);
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+              if (((i / PP) * LPR + l) * VEC < p.n) f[i] = add2(f[i], v[i]);
           }
         }
-        if (o >= 0) store_row<VEC, LPR, NIT>(out + o * os_t + h * os_h, p.D, l, f);
+        if (p.R > 0) {
+          if (tt[u] >= 0 && tt[u] != turned) {
+            turn.load(s.cs + (size_t)(tt[u] % U) * (p.R >> 1), p, l, 1.f);
+            turned = tt[u];
+          }
+          turn.apply(f, s.stage, p, l, 1.f);
+        }
+        if (o[u] >= 0) store_row<VEC, LPR, NIT>(out + o[u] * os_t + hh[u] * os_h, p.D, l, f);
       }
     }
   }
 }
 
-template <int VEC, int LPR, int NIT>
-__global__ void __launch_bounds__(kThreads)
+template <int VEC, int LPR, int NIT, int ROT, int U>
+__global__ void __launch_bounds__(kThreads, NIT == 1 ? 2 : ctas_per_sm(VEC, NIT))
     norm_rope_bwd_kernel(const Rows p, const __nv_bfloat16* dout, int64_t gs_t, int64_t gs_h, __nv_bfloat16* dx,
                          int64_t ds_t, int64_t ds_h, float* __restrict__ partials) {
-  constexpr int E = VEC * NIT, GPB = kThreads / LPR;
+  using R = Row<VEC, LPR, NIT>;
+  constexpr int GPB = kThreads / LPR, P = R::P, PP = R::PP;
   extern __shared__ __align__(16) uint8_t raw_sh[];
   const int lane = threadIdx.x & 31, l = lane & (LPR - 1), group = threadIdx.x / LPR;
-  const Shared s = carve(raw_sh, p.R, group);
-  fill_turns(s.turn, p);
-  __syncthreads();
-  const int nhb = (p.H + p.hpt - 1) / p.hpt;
-  const float inv_n = p.n > 0 ? 1.f / (float)p.n : 0.f;
-  const int64_t first = (int64_t)blockIdx.x * GPB + group, step = (int64_t)gridDim.x * GPB;
-  const int64_t warp_first = first - (lane / LPR);
-  float dw[E], db[E];
+  const Shared s = carve<U>(raw_sh, p.R, group);
+  // rows on their way while the ones before are worked on
+  Run<LPR, U> run;
+  int nt[U], nh[U], np[U];
+  R ng[U], nx[U];
+  auto fetch = [&]() {
+    run.batch(p, nt, nh, np);
 #pragma unroll
-  for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.f;
-  Raw<VEC, LPR, NIT> gcur, xcur;
-  auto row_of = [&](int64_t task, int hh, bool& on, int& t, int& h) {
-    t = (int)(task / nhb);
-    h = (int)(task - (int64_t)t * nhb) * p.hpt + hh;
-    on = task < p.tasks && h < p.H;
-  };
-  auto fetch = [&](int64_t task, int hh) {
-    bool on;
-    int t, h;
-    row_of(task, hh, on, t, h);
-    gcur.load(dout + (on ? t * gs_t + h * gs_h : 0), p.D, l, on);
-    if (p.kind != kNone) xcur.load(p.x + (on ? t * p.xs_t + h * p.xs_h : 0), p.n, l, on);
-  };
-  fetch(first, 0);
-  for (int64_t k = 0; warp_first + k * step < p.tasks; ++k) {
-    const int64_t task = first + k * step;
-    if (p.R > 0) {
-      __syncwarp();
-      if (task < p.tasks) fill_cos_sin<LPR>(s, p, (int)(task / nhb), l);
-      __syncwarp();
+    for (int u = 0; u < U; ++u) {
+      const bool on = nt[u] >= 0;
+      ng[u].load(dout + (on ? nt[u] * gs_t + nh[u] * gs_h : 0), p.D, l, on);
+      if (p.kind != kNone) nx[u].load(p.x + (on ? nt[u] * p.xs_t + nh[u] * p.xs_h : 0), p.n, l, on);
     }
-    for (int hh = 0; hh < p.hpt; ++hh) {
-      bool on;
-      int t, h;
-      row_of(task, hh, on, t, h);
-      float g[E], x[E];
-      gcur.values(g);
-      if (p.kind != kNone) xcur.values(x);
-      if (hh + 1 < p.hpt) fetch(task, hh + 1);
-      else fetch(task + step, 0);
-      rotate<VEC, LPR, NIT>(g, s, p, l, -1.f);
-      if (p.kind != kNone) {
-        float sx = 0.f, sg = 0.f;
-        if (p.kind == kLayer) {
+  };
+  int64_t first = ((int64_t)blockIdx.x * GPB + group) * p.run;
+  run.begin(p, first);
+  fetch();
+  fill_turns(s.turn, p);
+  const float inv_n = p.n > 0 ? 1.f / (float)p.n : 0.f;
+  float2 w1[NIT == 1 ? P : 1];
+  if constexpr (NIT == 1) load_param<VEC, LPR, NIT>(w1, p.w, 1.f, p.n, l);
+  Turn<VEC, LPR, NIT, ROT> turn;
+  turn.init(s.cs, p, l);
+  __syncthreads();
+  const int64_t step = (int64_t)gridDim.x * GPB * p.run;
+  float2 dw[P], db[P];
 #pragma unroll
-          for (int i = 0; i < E; ++i) {
-            const bool in = ((i / VEC) * LPR + l) * VEC + (i % VEC) < p.n;
-            sx += in ? x[i] : 0.f;
-            sg += in ? g[i] * param<VEC, LPR, NIT>(p.w, 1.f, p.n, l, i) : 0.f;
-          }
-          sx = group_sum<LPR>(sx) * inv_n;
-          sg = group_sum<LPR>(sg) * inv_n;
-        }
-        float ss = 0.f, sgx = 0.f;
+  for (int i = 0; i < P; ++i) dw[i] = db[i] = make_float2(0.f, 0.f);
+  for (int64_t warp_first = first - (int64_t)(lane / LPR) * p.run; warp_first < p.rows; warp_first += step) {
+    int turned = -1;
+#pragma unroll 1
+    for (int k = 0; k < p.run; k += U) {
+      int tt[U], hh[U], pos[U];
+      R graw[U], xraw[U];
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const bool in = ((i / VEC) * LPR + l) * VEC + (i % VEC) < p.n;
-          x[i] = in ? x[i] - sx : 0.f;
-          ss += x[i] * x[i];
-          sgx += in ? g[i] * param<VEC, LPR, NIT>(p.w, 1.f, p.n, l, i) * x[i] : 0.f;
-        }
-        ss = group_sum<LPR>(ss);
-        sgx = group_sum<LPR>(sgx);
-        const float r = rsqrtf(ss * inv_n + p.eps);
-        const float m = sgx * r * inv_n;  // mean(gw xh)
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const bool in = ((i / VEC) * LPR + l) * VEC + (i % VEC) < p.n;
-          if (!in || !on) continue;
-          const float xh = x[i] * r;
-          dw[i] += g[i] * xh;
-          db[i] += g[i];
-          g[i] = r * (g[i] * param<VEC, LPR, NIT>(p.w, 1.f, p.n, l, i) - sg - xh * m);
-        }
+      for (int u = 0; u < U; ++u) {
+        tt[u] = nt[u];
+        hh[u] = nh[u];
+        pos[u] = np[u];
+        graw[u] = ng[u];
+        xraw[u] = nx[u];
       }
-      if (on) store_row<VEC, LPR, NIT>(dx + t * ds_t + h * ds_h, p.D, l, g);
+      run.cos_sin(p, s, tt, pos, l);
+      if (k + U >= p.run) {
+        first += step;
+        run.begin(p, first);
+      }
+      fetch();
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool on = tt[u] >= 0;
+        float2 g[P];
+        graw[u].values(g);
+        if (p.R > 0) {
+          if (on && tt[u] != turned) {
+            turn.load(s.cs + (size_t)(tt[u] % U) * (p.R >> 1), p, l, -1.f);
+            turned = tt[u];
+          }
+          turn.apply(g, s.stage, p, l, -1.f);
+        }
+        if (p.kind != kNone) {
+          float2 x[P], v[NIT == 1 ? 1 : P];
+          xraw[u].values(x);
+          if constexpr (NIT > 1) load_param<VEC, LPR, NIT>(v, p.w, 1.f, p.n, l);
+          auto weight = [&](int i) -> float2 { return NIT == 1 ? w1[i % (NIT == 1 ? P : 1)] : v[i % (NIT == 1 ? 1 : P)]; };
+          float2 sx = make_float2(0.f, 0.f), sg = sx;
+          if (p.kind == kLayer) {
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+              if (((i / PP) * LPR + l) * VEC < p.n) {
+                sx = add2(sx, x[i]);
+                sg = fma2(g[i], weight(i), sg);
+              }
+            const float a = -group_sum<LPR>(sx.x + sx.y) * inv_n, c = -group_sum<LPR>(sg.x + sg.y) * inv_n;
+            sx = make_float2(a, VEC == 8 ? a : 0.f);
+            sg = make_float2(c, VEC == 8 ? c : 0.f);
+          }
+          float2 ss = make_float2(0.f, 0.f), sgx = ss;
+#pragma unroll
+          for (int i = 0; i < P; ++i)
+            if (((i / PP) * LPR + l) * VEC < p.n) {
+              x[i] = add2(x[i], sx);
+              ss = fma2(x[i], x[i], ss);
+              sgx = fma2(mul2(g[i], weight(i)), x[i], sgx);
+            }
+          const float sum = group_sum<LPR>(ss.x + ss.y), dot = group_sum<LPR>(sgx.x + sgx.y);
+          const float r = rsqrtf(sum * inv_n + p.eps);
+          const float2 r2 = make_float2(r, r), m2 = make_float2(-dot * r * inv_n, -dot * r * inv_n);  // -mean(gw xh)
+#pragma unroll
+          for (int i = 0; i < P; ++i)
+            if (on && ((i / PP) * LPR + l) * VEC < p.n) {
+              const float2 xh = mul2(x[i], r2);
+              dw[i] = fma2(g[i], xh, dw[i]);
+              db[i] = add2(db[i], g[i]);
+              g[i] = mul2(r2, fma2(xh, m2, fma2(g[i], weight(i), sg)));
+            }
+        }
+        if (on) store_row<VEC, LPR, NIT>(dx + tt[u] * ds_t + hh[u] * ds_h, p.D, l, g);
+      }
     }
   }
   if (partials == nullptr) return;
@@ -372,22 +563,25 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int o = LPR; o < 32; o <<= 1) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
-      db[i] += __shfl_xor_sync(0xffffffffu, db[i], o);
+    for (int i = 0; i < P; ++i) {
+      dw[i].x += __shfl_xor_sync(0xffffffffu, dw[i].x, o);
+      dw[i].y += __shfl_xor_sync(0xffffffffu, dw[i].y, o);
+      db[i].x += __shfl_xor_sync(0xffffffffu, db[i].x, o);
+      db[i].y += __shfl_xor_sync(0xffffffffu, db[i].y, o);
     }
   }
-  __shared__ float acc[2][kMaxD];
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if ((threadIdx.x >> 5) == w && lane < LPR) {
+  __shared__ float acc[2][VEC * LPR * NIT];
+  for (int q = 0; q < kThreads / 32; ++q) {
+    if ((threadIdx.x >> 5) == q && lane < LPR) {
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int c = ((i / VEC) * LPR + l) * VEC + (i % VEC);
-        if (c < p.n) {
-          acc[0][c] = w ? acc[0][c] + dw[i] : dw[i];
-          acc[1][c] = w ? acc[1][c] + db[i] : db[i];
+      for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int e = 0; e < (VEC == 8 ? 2 : 1); ++e) {
+          const int c = ((i / PP) * LPR + l) * VEC + (i % PP) * 2 + e;
+          const float a = e ? dw[i].y : dw[i].x, d = e ? db[i].y : db[i].x;
+          acc[0][c] = q ? acc[0][c] + a : a;
+          acc[1][c] = q ? acc[1][c] + d : d;
         }
-      }
     }
     __syncthreads();
   }
@@ -420,29 +614,51 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// Calls f<VEC, LPR, NIT>: 16-byte accesses where every row starts on a 16-byte boundary and the pairs of an
-// interleaved rotation stay inside one; else one channel at a time.
-template <class F>
-dsa_status_t dispatch(bool vec, int D, F&& f) {
-  if (vec) {
-    if (D <= 64) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
-    if (D <= 128) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
-    if (D <= 256) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
-    if (D <= 512) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 32>{}, std::integral_constant<int, 2>{});
-    if (D <= 768) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 32>{}, std::integral_constant<int, 3>{});
-    return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{});
+template <int V, int L, int N, int T>
+struct Shape {
+  static constexpr int VEC = V, LPR = L, NIT = N, ROT = T;
+};
+
+// The 16-byte path with LPR lanes to a row: whole accesses are rotated where r0 and R are multiples of 8 (the tables of
+// cosines then start on 16 bytes too).
+template <int LPR, int NIT, class F>
+dsa_status_t dispatch_rotation(const Rows& p, F&& f) {
+  if (p.r0 % 8 == 0 && p.R % 8 == 0) {
+    if (p.inter || p.R == 0) return f(Shape<8, LPR, NIT, kPairs>{});
+    if (p.R % 16 == 0 && p.r0 / 8 / LPR == ((p.r0 + p.R) / 8 - 1) / LPR) return f(Shape<8, LPR, NIT, kLanes>{});
   }
-  if (D <= 128) return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{});
-  return f(std::integral_constant<int, 1>{}, std::integral_constant<int, 32>{}, std::integral_constant<int, 32>{});
+  return f(Shape<8, LPR, NIT, kShared>{});
 }
 
-// Heads a group of lanes takes of one token: up to 16 share a token's cosines and sines, fewer while the
-// launch has too few groups to fill the card (152 SMs x 64 groups).
-inline int heads_per_task(int64_t T, int H, int R) {
-  if (R == 0) return 1;
-  int hpt = 1;
-  while (hpt < 16 && hpt < H && T * ((H + 2 * hpt - 1) / (2 * hpt)) >= 152 * 64) hpt *= 2;
-  return hpt;
+// Calls f with the lanes of a row: 16-byte accesses where every row and the parameters start on a 16-byte boundary and
+// the norm covers whole accesses; else one channel at a time.
+template <class F>
+dsa_status_t dispatch(bool vec, const Rows& p, F&& f) {
+  if (vec) {
+    if (p.D <= 64) return dispatch_rotation<8, 1>(p, f);
+    if (p.D <= 128) return dispatch_rotation<16, 1>(p, f);
+    if (p.D <= 256) return dispatch_rotation<32, 1>(p, f);
+    if (p.D <= 512) return dispatch_rotation<32, 2>(p, f);
+    if (p.D <= 768) return dispatch_rotation<32, 3>(p, f);
+    return dispatch_rotation<32, 4>(p, f);
+  }
+  return p.D <= 128 ? f(Shape<1, 32, 4, kShared>{}) : f(Shape<1, 32, 32, kShared>{});
+}
+
+// Shared memory beyond the 48 KiB that every kernel has (wide rotations; `fixed`: what the kernel declares itself).
+inline dsa_status_t allow_shared(const void* kernel, int bytes, int fixed) {
+  if (bytes + fixed <= 48 * 1024) return DSA_OK;
+  return cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 104 * 1024),
+                    "shared memory of the norm and rotation");
+}
+
+// Rows of a group's run: the rows over the groups that the card holds at once, so that one wave of CTAs takes them all,
+// while that is at most 32; 16 beyond it (many waves, whose last one matters less).  A token's heads in one run share
+// its cosines and sines.
+inline int run_of(int64_t rows, int LPR, int U, int per_sm) {
+  const int64_t groups = (int64_t)152 * per_sm * (kThreads / LPR);
+  const int64_t run = ((rows + groups - 1) / groups + U - 1) / U * U;
+  return run <= 32 ? (int)(run < U ? U : run) : 16;
 }
 
 dsa_status_t check_rows(const char* who, Rows& p, int norm, int norm_dim, const float* weight, const float* bias,
@@ -479,8 +695,8 @@ dsa_status_t check_rows(const char* who, Rows& p, int norm, int norm_dim, const 
   p.pos = positions;
   p.inv_freq = inv_freq;
   p.rscale = rope_scale;
-  p.hpt = heads_per_task(p.T, p.H, rope_dim);
-  p.tasks = (int64_t)p.T * ((p.H + p.hpt - 1) / p.hpt);
+  if ((int64_t)p.T * p.H > 0x7fffffffll) return fail(DSA_ERR_INVALID_ARGUMENT, "%s: T * H must be below 2^31", who);
+  p.rows = p.T * p.H;
   return DSA_OK;
 }
 
@@ -531,14 +747,21 @@ extern "C" dsa_status_t dsa_norm_rope_fwd(const dsa_bf16_t* x, int64_t x_stride_
   if ((st = check_device()) != DSA_OK) return st;
   if (T == 0) return ok();
   const bool vec = D % 8 == 0 && nrope::vec_rows(x, x_stride_t, x_stride_h) &&
-                   nrope::vec_rows(out, out_stride_t, out_stride_h) && !(interleaved && (rope_start & 1));
-  st = nrope::dispatch(vec, D, [&](auto v, auto lpr, auto nit) -> dsa_status_t {
-    constexpr int VEC = decltype(v)::value, LPR = decltype(lpr)::value, NIT = decltype(nit)::value;
-    constexpr int GPB = nrope::kThreads / LPR;
-    const int64_t want = (p.tasks + GPB - 1) / GPB;
-    const int blocks = (int)(want < 152 * 16 ? want : 152 * 16);
-    nrope::norm_rope_fwd_kernel<VEC, LPR, NIT>
-        <<<blocks, nrope::kThreads, nrope::shared_bytes(p.R, GPB), reinterpret_cast<cudaStream_t>(stream)>>>(
+                   nrope::vec_rows(out, out_stride_t, out_stride_h) && norm_dim % 8 == 0 && aligned16(weight) &&
+                   aligned16(bias);
+  st = nrope::dispatch(vec, p, [&](auto shape) -> dsa_status_t {
+    using S = decltype(shape);
+    constexpr int U = S::VEC == 1 || S::NIT > 2 ? 1 : S::NIT > 1 ? 2 : 4, GPB = nrope::kThreads / S::LPR;
+    p.run = nrope::run_of(p.rows, S::LPR, U, nrope::ctas_per_sm(S::VEC, S::NIT));
+    const int64_t want = ((int64_t)p.rows + (int64_t)GPB * p.run - 1) / ((int64_t)GPB * p.run);
+    const int64_t most = 152 * nrope::ctas_per_sm(S::VEC, S::NIT);  // (a CTA that stays forms its table once)
+    const int blocks = (int)(want < most ? want : most);
+    const int smem = nrope::shared_bytes(p.R, GPB, U);
+    dsa_status_t ok_smem = nrope::allow_shared(
+        reinterpret_cast<const void*>(nrope::norm_rope_fwd_kernel<S::VEC, S::LPR, S::NIT, S::ROT, U>), smem, 0);
+    if (ok_smem != DSA_OK) return ok_smem;
+    nrope::norm_rope_fwd_kernel<S::VEC, S::LPR, S::NIT, S::ROT, U>
+        <<<blocks, nrope::kThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(
             p, reinterpret_cast<__nv_bfloat16*>(out), out_stride_t, out_stride_h, out_rows, num_out_rows,
             reinterpret_cast<int*>(workspace));
     return cuda_check(cudaGetLastError(), "launching norm_rope_fwd_kernel");
@@ -589,15 +812,20 @@ extern "C" dsa_status_t dsa_norm_rope_bwd(const dsa_bf16_t* dout, int64_t dout_s
   int blocks = 0;
   if (T > 0) {
     const bool vec = D % 8 == 0 && nrope::vec_rows(dout, dout_stride_t, dout_stride_h) &&
-                     nrope::vec_rows(dx, dx_stride_t, dx_stride_h) && !(interleaved && (rope_start & 1)) &&
-                     (!norm || (norm_dim % 8 == 0 && nrope::vec_rows(x, x_stride_t, x_stride_h)));
-    st = nrope::dispatch(vec, D, [&](auto v, auto lpr, auto nit) -> dsa_status_t {
-      constexpr int VEC = decltype(v)::value, LPR = decltype(lpr)::value, NIT = decltype(nit)::value;
-      constexpr int GPB = nrope::kThreads / LPR;
-      const int64_t want = (p.tasks + GPB - 1) / GPB;
-      const int most = partials ? nrope::kMaxPartials : 152 * 16;
+                     nrope::vec_rows(dx, dx_stride_t, dx_stride_h) &&
+                     (!norm || (norm_dim % 8 == 0 && nrope::vec_rows(x, x_stride_t, x_stride_h))) && aligned16(weight);
+    st = nrope::dispatch(vec, p, [&](auto shape) -> dsa_status_t {
+      using S = decltype(shape);
+      constexpr int U = S::VEC == 1 || S::NIT > 1 ? 1 : 2, GPB = nrope::kThreads / S::LPR;
+      p.run = nrope::run_of(p.rows, S::LPR, U, S::NIT == 1 ? 2 : nrope::ctas_per_sm(S::VEC, S::NIT));
+      const int64_t want = ((int64_t)p.rows + (int64_t)GPB * p.run - 1) / ((int64_t)GPB * p.run);
+      const int most = partials ? nrope::kMaxPartials : 152 * 4;
       blocks = (int)(want < most ? want : most);
-      nrope::norm_rope_bwd_kernel<VEC, LPR, NIT><<<blocks, nrope::kThreads, nrope::shared_bytes(p.R, GPB), s>>>(
+      const int smem = nrope::shared_bytes(p.R, GPB, U);
+      dsa_status_t ok_smem = nrope::allow_shared(
+          reinterpret_cast<const void*>(nrope::norm_rope_bwd_kernel<S::VEC, S::LPR, S::NIT, S::ROT, U>), smem, 8192);
+      if (ok_smem != DSA_OK) return ok_smem;
+      nrope::norm_rope_bwd_kernel<S::VEC, S::LPR, S::NIT, S::ROT, U><<<blocks, nrope::kThreads, smem, s>>>(
           p, reinterpret_cast<const __nv_bfloat16*>(dout), dout_stride_t, dout_stride_h,
           reinterpret_cast<__nv_bfloat16*>(dx), dx_stride_t, dx_stride_h, partials);
       return cuda_check(cudaGetLastError(), "launching norm_rope_bwd_kernel");
