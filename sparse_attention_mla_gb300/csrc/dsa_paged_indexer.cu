@@ -10,12 +10,15 @@
 // to end and cut into equal ranges, one CTA per SM, so one long request fills the
 // card; keys are on the MMA's M axis, the (token, head) pairs of up to 256 / heads
 // tokens of a request on N, and a TMEM lane is a key, whose thread sums its heads.
-// The second finds each token's K best with a cluster of 1 to 8 CTAs per token (by
-// the longest length there can be): the scores, as integers of the same order, stay
-// in registers; histograms of 11 bits, starting below the bits that all scores
-// share, narrow the K-th down, summed over the cluster through distributed shared
-// memory; then one ordered compaction.  Every step is exact and without order
-// effects, so equal calls give equal lists.
+// A ring of four tiles (128 KB) keeps DRAM busy, filled by TMA where pages allow it,
+// else by cp.async.  The second kernel finds each token's K best with a cluster of 1
+// to 8 CTAs per token (by the longest length there can be): the scores, as integers
+// of the same order, stay in registers; histograms of 11 bits, starting below the
+// bits that all scores share, narrow the K-th down, every CTA adding up all CTAs'
+// bins through distributed shared memory (one cluster barrier a histogram); then
+// one ordered compaction.  What bounds it is that chain of barriers, not its work;
+// it is launched early and looks its request up while the scores are being made.
+// Every step is exact and without order effects, so equal calls give equal lists.
 #include <cooperative_groups.h>
 
 #include <cmath>
@@ -31,15 +34,18 @@ namespace cg = cooperative_groups;
 constexpr int kD = 128;          // index width
 constexpr int kTile = 128;       // keys per tile (MMA M)
 constexpr int kCols = 256;       // (token, head) columns of a group (MMA N)
-constexpr int kRing = 4;
-constexpr int kThreads = 32 * 14;  // MMA, 8 epilogue, 4 gather, 1 query warp
+constexpr int kRing = 4;         // tiles, one gather warp each
+constexpr int kThreads = 32 * 15;  // MMA, 8 scores, 4 gather, 1 query, 1 announcing warp
+constexpr int kReaders = 14;
+constexpr int kSegs = 8;
 constexpr int kMaxCtas = 160;
 
 constexpr int Q_CHUNK = kCols * 128, K_CHUNK = kTile * 128;
 constexpr int OFF_Q = 0, OFF_K = 2 * Q_CHUNK, OFF_W = OFF_K + kRing * 2 * K_CHUNK, OFF_MISC = OFF_W + 2 * kCols * 4;
-constexpr int SMEM = OFF_MISC + 512 + 1024;
+constexpr int SMEM = OFF_MISC + 1024 + 1024;
 constexpr int M_K = 0, M_KF = 32, M_S = 64, M_SF = 80, M_Q = 96, M_SEG = 104, M_FIN = 112, M_TMEM = 120, M_ABORT = 124,
-              M_PLAN = 128, M_SCRATCH = 192;
+              M_PLAN = 128, M_SCRATCH = 192, M_ANN = 320, M_READ = M_ANN + 8 * kSegs, M_RING = M_READ + 8 * kSegs;
+static_assert(M_RING + 32 * kSegs <= 1024 && M_SCRATCH + 8 * (kThreads / 32) <= M_ANN, "misc layout");
 
 struct Params {
   const __nv_bfloat16* q;
@@ -51,6 +57,7 @@ struct Params {
   int N, B, Hi, num_pages, P, max_pages, max_len;
   float* scores;      // [N][stride]
   long long stride;
+  int box;  // rows of a TMA box (32 or a smaller page), 0: every row by cp.async
   int* err;
   long long wait_limit;
 };
@@ -77,56 +84,61 @@ __device__ __forceinline__ Request request_of(const Params& p, int b) {
 }
 
 struct Plan {
-  long long w0, w1, first;
-  int u0, pad;
+  long long w0, w1;
+  int u, g, t, pad;  // request, group and tile of tile w0
 };
 
+// A run of tiles [t0, t0 + n) of one group of a request's tokens, as announced (two int4).
 struct Seg {
-  int t0, t1, tok, nt, b, keys;
+  int t0, n, tok, nt, b, keys;
 };
+
+__device__ __noinline__ bool read_announcement(uint32_t misc, const int4* ring, int k, volatile int* abort, long long limit,
+                                               Seg& s) {
+  const int at = k % kSegs;
+  if (!__all_sync(0xffffffffu, wait_for(misc + M_ANN + 8 * at, (k / kSegs) & 1, abort, limit))) return false;
+  const int4 a = ring[2 * at], c = ring[2 * at + 1];
+  s = Seg{a.x, a.y, a.z, a.w, c.x, c.y};
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(misc + M_READ + 8 * at);
+  return true;
+}
 
 template <int G>
-struct Walk {
-  const Params& p;
-  int u, g, t, groups, tiles;
-  long long left;
-  Request rq;
-  __device__ __forceinline__ void load() {
-    rq = request_of(p, u);
-    groups = (rq.n + G - 1) / G;
-    tiles = (rq.keys + kTile - 1) / kTile;
-    if (tiles == 0) groups = 0;
-  }
-  __device__ __forceinline__ Walk(const Params& p_, const Plan& pl) : p(p_) {
-    left = pl.w1 - pl.w0;
-    u = pl.u0;
-    load();
-    g = tiles > 0 ? (int)(pl.first / tiles) : 0;
-    t = tiles > 0 ? (int)(pl.first - (long long)g * tiles) : 0;
-  }
-  __device__ __forceinline__ bool next(Seg& s) {
-    if (left <= 0) return false;
-    while (g >= groups) {
-      ++u;
-      load();
+__device__ __forceinline__ void announce(const Params& p, const Plan& pl, uint32_t misc, int4* ring, volatile int* abort) {
+  const int lane = threadIdx.x & 31;
+  long long left = pl.w1 - pl.w0;
+  int u = pl.u, g = pl.g, t = pl.t;
+  Request rq = request_of(p, u);
+  bool cut = false;
+#pragma unroll 1
+  for (int k = 0; left > 0; ++k) {
+    int tiles = (rq.keys + kTile - 1) / kTile;
+#pragma unroll 1
+    while (tiles == 0 || g * G >= rq.n) {  // (requests are skipped only while tiles are left)
+      rq = request_of(p, ++u);
+      tiles = (rq.keys + kTile - 1) / kTile;
       g = t = 0;
     }
-    s.tok = rq.n0 + g * G;
-    s.nt = min(G, rq.n - g * G);
-    s.b = u;
-    s.keys = rq.keys;
-    s.t0 = t;
-    s.t1 = (int)min((long long)tiles, t + left);
-    left -= s.t1 - s.t0;
-    t = s.t1;
+    cut |= rq.keys < rq.len;
+    const int n = (int)min((long long)(tiles - t), left), at = k % kSegs;
+    if (k >= kSegs && !wait_for(misc + M_READ + 8 * at, (k / kSegs - 1) & 1, abort, p.wait_limit)) break;
+    if (lane == 0) {
+      ring[2 * at] = make_int4(t, n, rq.n0 + g * G, min(G, rq.n - g * G));
+      ring[2 * at + 1] = make_int4(u, rq.keys, 0, 0);
+      mbar_arrive(misc + M_ANN + 8 * at);
+    }
+    left -= n;
+    t += n;
     if (t >= tiles) { ++g; t = 0; }
-    return true;
   }
-};
+  if (cut && lane == 0) record_error(p.err, DSA_ERR_DEVICE_INDEX);  // longer than max_len or the table
+}
 
 // HP: heads per token, rounded up to 8, 16, 32 or 64 (the rest are zero rows)
 template <int HP>
-__global__ void __launch_bounds__(kThreads, 1) paged_score_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_score_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap map) {
   constexpr int G = kCols / HP;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -139,20 +151,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_score_kernel(const Params p
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kRing; ++s) {
-      mbar_init(mb + M_K + 8 * s, 128);
+      mbar_init(mb + M_K + 8 * s, 1);
       mbar_init(mb + M_KF + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(mb + M_S + 8 * b, 1);
       mbar_init(mb + M_SF + 8 * b, 4);
     }
-    mbar_init(mb + M_Q, 32);
+    for (int k = 0; k < kSegs; ++k) {
+      mbar_init(mb + M_ANN + 8 * k, 1);
+      mbar_init(mb + M_READ + 8 * k, kReaders);
+    }
+    mbar_init(mb + M_Q, 1);
     mbar_init(mb + M_SEG, 1);
     mbar_init(mb + M_FIN, 1);
     *s_abort = 0;
-    s_plan->u0 = 0;
-    s_plan->first = 0;
     fence_mbar_init();
+    if (p.box > 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
   }
   auto tiles_of = [&](int u) -> long long {
     const Request r = request_of(p, u);
@@ -160,11 +175,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_score_kernel(const Params p
   };
   auto visit = [&](const TileRange& r, int u, long long lo, long long n) {
     if (lo <= r.w0 && r.w0 < lo + n) {
-      s_plan->u0 = u;
-      s_plan->first = r.w0 - lo;
+      const int tiles = (request_of(p, u).keys + kTile - 1) / kTile;
+      s_plan->u = u;
+      s_plan->g = (int)((r.w0 - lo) / tiles);
+      s_plan->t = (int)((r.w0 - lo) - (long long)s_plan->g * tiles);
     }
   };
-  __syncthreads();
   const TileRange rg = split_line<kThreads>(p.B, tiles_of, reinterpret_cast<long long*>(misc + M_SCRATCH), visit);
   if (threadIdx.x == 0) {
     s_plan->w0 = rg.w0;
@@ -172,118 +188,173 @@ __global__ void __launch_bounds__(kThreads, 1) paged_score_kernel(const Params p
   }
   __syncthreads();
   const Plan plan = *s_plan;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the selection waits for this kernel's end itself)
   if (plan.w1 <= plan.w0) return;
   if (warp == 0) {
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
   }
   __syncthreads();
-  const uint32_t tmem = *s_tmem;
-  Walk<G> walk(p, plan);
+  const uint32_t tmem = (uint32_t)warp_value((int)*s_tmem);
+  const int n_tiles = warp_value((int)(plan.w1 - plan.w0));
+  int4* ring = reinterpret_cast<int4*>(misc + M_RING);
+  auto read_seg = [&](int k, Seg& s) -> bool { return read_announcement(mb, ring, k, s_abort, p.wait_limit, s); };
   Seg sg;
-  int i = 0, seg = 0;
 
   if (warp == 0) {
     // ======================= MMA issuer =======================
-    bool stop = false;
-    while (!stop && walk.next(sg)) {
-      const uint32_t id = idesc_bf16(kTile, (sg.nt * HP + 15) & ~15, false, false);
-      if (!warp_all(mbar_wait(mb + M_Q, seg & 1, s_abort, p.err, p.wait_limit))) break;
-      for (int t = sg.t0; t < sg.t1; ++t, ++i) {
-        const int sl = i % kRing, sb = i & 1;
-        if (i >= 2 && !warp_all(mbar_wait(mb + M_SF + 8 * sb, ((i >> 1) - 1) & 1, s_abort, p.err, p.wait_limit))) { stop = true; break; }
-        if (!warp_all(mbar_wait(mb + M_K + 8 * sl, (i / kRing) & 1, s_abort, p.err, p.wait_limit))) { stop = true; break; }
-        fence_proxy_async_smem();
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint64_t a = sdesc_sw128(sK + (sl * 2 + c) * K_CHUNK, 16, 1024), b = sdesc_sw128(sQ + c * Q_CHUNK, 16, 1024);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ss_w(tmem + sb * kCols, a + (uint64_t)(k * 2), b + (uint64_t)(k * 2), id, (c | k) ? 1u : 0u);
-        }
-        mma_commit_w(mb + M_KF + 8 * sl);
-        mma_commit_w(mb + M_S + 8 * sb);
+    int left = 0, seg = 0;
+    uint32_t id = 0;
+    for (int i = 0; i < n_tiles; ++i) {
+      const int sl = i % kRing, sb = i & 1;
+      if (left == 0) {
+        if (!read_seg(seg, sg)) break;
+        left = warp_value(sg.n);
+        id = idesc_bf16(kTile, (warp_value(sg.nt) * HP + 15) & ~15, false, false);
+        if (!warp_all(wait_for(mb + M_Q, seg & 1, s_abort, p.wait_limit))) break;
+        ++seg;
       }
-      mma_commit_w(mb + M_SEG);
-      ++seg;
+      --left;
+      if (i >= 2 && !warp_all(wait_for(mb + M_SF + 8 * sb, ((i >> 1) - 1) & 1, s_abort, p.wait_limit))) break;
+      if (!warp_all(wait_for(mb + M_K + 8 * sl, (i / kRing) & 1, s_abort, p.wait_limit))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint64_t a = sdesc_sw128(sK + (sl * 2 + c) * K_CHUNK, 16, 1024), b = sdesc_sw128(sQ + c * Q_CHUNK, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_ss_w(tmem + sb * kCols, a + (uint64_t)(k * 2), b + (uint64_t)(k * 2), id, (c | k) ? 1u : 0u);
+      }
+      mma_commit_w(mb + M_KF + 8 * sl);
+      mma_commit_w(mb + M_S + 8 * sb);
+      if (left == 0) mma_commit_w(mb + M_SEG);
     }
     mma_commit_w(mb + M_FIN);
     volatile int dummy = 0;
     mbar_wait(mb + M_FIN, 0, &dummy, p.err);
     __syncwarp();
+  } else if (warp == 14) {
+    announce<G>(p, plan, mb, ring, s_abort);
   } else if (warp == 13) {
     // ======================= queries of a segment, once the products of the one before are done =======================
-    while (walk.next(sg)) {
-      if (seg > 0 && !mbar_wait(mb + M_SEG, (seg - 1) & 1, s_abort, p.err, p.wait_limit)) break;
+    int done = 0;
+    for (int seg = 0; done < n_tiles; ++seg) {
+      if (!read_seg(seg, sg)) break;
+      done += sg.n;
+      if (seg > 0 && !wait_for(mb + M_SEG, (seg - 1) & 1, s_abort, p.wait_limit)) break;
       const int rows = ((sg.nt * HP + 15) & ~15);
+#pragma unroll 4
       for (int x = lane; x < rows * 16; x += 32) {
         const int n = x >> 4, u = x & 15, tok = n / HP, h = n - tok * HP;
         const bool ok = tok < sg.nt && h < p.Hi;
         cp_async16(sQ + (u >> 3) * Q_CHUNK + sw128_off(n, u & 7),
                    p.q + (ok ? ((size_t)(sg.tok + tok) * p.Hi + h) * kD + u * 8 : 0), ok ? 16u : 0u);
       }
-      cp_async_arrive(mb + M_Q);
-      ++seg;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(mb + M_Q);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= 9) {
-    // ======================= gather: warp g copies rows 32 g .. of a tile, two rows at a time =======================
-    const int gw = warp - 9;
-    bool stop = false;
-    while (!stop && walk.next(sg)) {
-      const int32_t* tab = p.table + (size_t)sg.b * p.max_pages;
-      if (gw == 0 && lane == 0 && sg.keys < __ldg(p.seq_lens + sg.b)) record_error(p.err, DSA_ERR_DEVICE_INDEX);
-      auto page_at = [&](int t) -> int {  // page of this lane's row of tile t; -1 past the end
-        const int pos = t * kTile + gw * 32 + lane;
-        return (t < sg.t1 && pos < sg.keys) ? __ldg(tab + (unsigned)pos / (unsigned)p.P) : -1;
-      };
-      int page = page_at(sg.t0);
-      for (int t = sg.t0; t < sg.t1; ++t, ++i) {
-        const int sl = i % kRing;
-        const int pos = t * kTile + gw * 32 + lane;
-        long long row = -1;
-        if (pos < sg.keys) {
-          if (page >= 0 && page < p.num_pages) row = (long long)page * p.P + (unsigned)pos % (unsigned)p.P;
-          else record_error(p.err, DSA_ERR_DEVICE_INDEX);
-        }
-        page = page_at(t + 1);
-        if (i >= kRing && !warp_all(mbar_wait(mb + M_KF + 8 * sl, ((i / kRing) - 1) & 1, s_abort, p.err, p.wait_limit))) { stop = true; break; }
-        const int u = lane & 15;
-        const uint32_t dst = sK + (sl * 2 + (u >> 3)) * K_CHUNK;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int rr = 2 * e + (lane >> 4);
-          const long long src = __shfl_sync(0xffffffffu, row, rr);
-          cp_async16(dst + sw128_off(gw * 32 + rr, u & 7), p.cache + (src >= 0 ? (size_t)src * kD + u * 8 : 0),
-                     src >= 0 ? 16u : 0u);
-        }
-        cp_async_arrive(mb + M_K + 8 * sl);
+    // ======================= gather: a warp owns a slot of the ring and fills it with every fourth tile =======================
+    // A lane looks four rows up, a tile of the slot ahead.  32 rows that are all there come by TMA in whole boxes; others by
+    // cp.async, zero-filled where there is no key.
+    const int sl = warp - 9;
+    int seg = 0, base = 0, end = 0;
+    bool bad = false, stop = false;
+    int page[4], at[4];  // of the rows 32 k + lane: page, place in it (-1: no key)
+    auto look_up = [&](int i) {
+      if (i >= n_tiles) return;
+#pragma unroll 1
+      while (i >= end) {
+        if (!read_seg(seg, sg)) { stop = true; return; }
+        ++seg;
+        base = end;
+        end += sg.n;
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int pos = (sg.t0 + i - base) * kTile + 32 * k + lane;
+        at[k] = page[k] = -1;
+        if (pos < sg.keys) {
+          const unsigned q = (unsigned)pos / (unsigned)p.P;
+          at[k] = pos - (int)q * p.P;
+          page[k] = __ldg(p.table + (size_t)sg.b * p.max_pages + q);
+        }
+      }
+    };
+    look_up(sl);
+#pragma unroll 1
+    for (int i = sl; i < n_tiles && !stop; i += kRing) {
+      long long row[4];
+      unsigned whole = 0;  // bit k: rows 32 k .. are all there
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool ok = page[k] >= 0 && page[k] < p.num_pages && at[k] >= 0;
+        bad |= at[k] >= 0 && !ok;
+        row[k] = ok ? (long long)page[k] * p.P + at[k] : -1;
+        if (p.box > 0 && __all_sync(0xffffffffu, ok)) whole |= 1u << k;
+      }
+      if (i >= kRing && !warp_all(wait_for(mb + M_KF + 8 * sl, ((i / kRing) - 1) & 1, s_abort, p.wait_limit))) break;
+      const uint32_t bar = mb + M_K + 8 * sl;
+      if (lane == 0 && whole)
+        asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(__popc(whole) * 8192) : "memory");
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (whole & (1u << k)) {
+          const int boxes = 32 / p.box, bx = lane >> 1, c = lane & 1;
+          const int src = (int)__shfl_sync(0xffffffffu, row[k], (bx * p.box) & 31);
+          if (bx < boxes) tma_load_2d(sK + (sl * 2 + c) * K_CHUNK + (32 * k + bx * p.box) * 128, &map, c * 64, src, bar);
+        } else {
+          const int u = lane & 15;
+          const uint32_t dst = sK + (sl * 2 + (u >> 3)) * K_CHUNK;
+#pragma unroll 4
+          for (int e = 0; e < 16; ++e) {
+            const int rr = 2 * e + (lane >> 4);
+            const long long src = __shfl_sync(0xffffffffu, row[k], rr);
+            cp_async16(dst + sw128_off(32 * k + rr, u & 7), p.cache + (src >= 0 ? (size_t)src * kD + u * 8 : 0),
+                       src >= 0 ? 16u : 0u);
+          }
+        }
+      }
+      look_up(i + kRing);
+      if (whole != 15u) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();  // the copies -> visible to the tensor core
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive(bar);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (bad) record_error(p.err, DSA_ERR_DEVICE_INDEX);
   } else {
     // ======================= scores: two groups of four warps take alternate tiles; a thread is a key =======================
     const int grp = (warp - 1) >> 2, qd = warp & 3;
     float* s_w = reinterpret_cast<float*>(smem + OFF_W) + grp * kCols;
     bool stop = false;
-    while (walk.next(sg)) {
-      const int cols = sg.nt * HP;
+    int i = 0;
+    for (int seg = 0; i < n_tiles; ++seg) {
+      if (!stop && !read_seg(seg, sg)) stop = true;
       // the weights of the segment before have been read; all four warps leave together after a failed wait
       if (named_bar_or(1 + grp, 128, stop)) break;
+      const int cols = sg.nt * HP;
       for (int x = ((warp - 1) & 3) * 32 + lane; x < cols; x += 128) {
         const int tok = x / HP, h = x - tok * HP;
         s_w[x] = h < p.Hi ? __ldg(p.w + (size_t)(sg.tok + tok) * p.Hi + h) : 0.f;
       }
       named_bar(1 + grp, 128);
-      for (int t = sg.t0; t < sg.t1; ++t, ++i) {
-        if ((i & 1) != grp) continue;
-        if (!warp_all(mbar_wait(mb + M_S + 8 * grp, (i >> 1) & 1, s_abort, p.err, p.wait_limit))) { stop = true; break; }
+      const int t_end = sg.t0 + sg.n;
+      for (int t = sg.t0; t < t_end; ++t, ++i) {
+        if ((i & 1) != grp || stop) continue;
+        if (!warp_all(wait_for(mb + M_S + 8 * grp, (i >> 1) & 1, s_abort, p.wait_limit))) { stop = true; continue; }
         tc_fence_after();
         const int pos = t * kTile + qd * 32 + lane;
         float* out = p.scores + (size_t)sg.tok * p.stride + pos;
         const bool in = pos < sg.keys;
         float acc = 0.f;
+#pragma unroll 1
         for (int c0 = 0; c0 < cols; c0 += 32) {
           uint32_t v[32];
           tmem_ld32(tmem_addr(tmem + grp * kCols + c0, qd * 32, 0), v);
@@ -332,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_score_kernel(const Params p
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+    if (lane == 0 && *s_abort) record_error(p.err, DSA_ERR_TIMEOUT);
   }
 }
 
@@ -350,32 +422,28 @@ __device__ __forceinline__ uint32_t order_of(float s) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive sum of v over the CTA's threads, and the total.  `sh`: 33 words.
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* sh, uint32_t& total) {
+// Exclusive sum of v over the CTA's threads (T: 32 or 64 bits), and the total.  `sh`: 32 words of T that no other scan
+// in flight uses.
+template <class T>
+__device__ __forceinline__ T block_scan(T v, T* sh, T& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t inc = v;
+  T inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+    const T x = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += x;
   }
-  __syncthreads();  // sh may still be in use
   if (lane == 31) sh[warp] = inc;
   __syncthreads();
-  if (warp == 0) {
-    const uint32_t mine = sh[lane];
-    uint32_t s = mine;
+  T s = sh[lane];  // every warp sums the warps' totals itself
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += x;
-    }
-    sh[lane] = s - mine;
-    if (lane == 31) sh[32] = s;
+  for (int o = 1; o < 32; o <<= 1) {
+    const T x = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += x;
   }
-  __syncthreads();
-  total = sh[32];
-  return sh[warp] + inc - v;
+  total = __shfl_sync(0xffffffffu, s, 31);
+  const T before = __shfl_sync(0xffffffffu, s, (warp + 31) & 31);
+  return (warp ? before : 0) + inc - v;
 }
 
 template <int CS>
@@ -383,21 +451,18 @@ __global__ void __launch_bounds__(kSel, 1)
     paged_select_kernel(const float* __restrict__ scores, long long stride, const int32_t* __restrict__ seq_lens,
                         const int32_t* __restrict__ cu_q, int N, int B, int K, int max_keys, int32_t* __restrict__ topk_idx,
                         int32_t* __restrict__ topk_len) {
-  __shared__ uint32_t hist[kBins], tot[kBins];
-  __shared__ uint32_t sh[33];
-  __shared__ uint32_t box[2 * CS];       // min / max, later above / tied counts, of every CTA of the cluster
-  __shared__ uint32_t pick[4];
+  __shared__ uint32_t hist[2][kBins];
+  __shared__ unsigned long long sh[2][32];
+  __shared__ uint32_t box[2], pick[6];  // this CTA's smallest and largest; the bin of the K-th
   const int n = blockIdx.x / CS, rank = blockIdx.x % CS, tid = threadIdx.x;
   // the token's request and what it sees (the same in the whole cluster)
   int b = n, lo_tok = n, hi_tok = n + 1;
   if (cu_q) {
-    if (n < __ldg(cu_q) || n >= __ldg(cu_q + B)) return;
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(cu_q + mid) <= n) lo = mid; else hi = mid;
+    if (n < __ldg(cu_q) || n >= __ldg(cu_q + B)) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // (this kernel does not end before the one with the scores)
+      return;
     }
-    b = lo;
+    b = warp_last_le(cu_q, B, n);
     lo_tok = __ldg(cu_q + b);
     hi_tok = __ldg(cu_q + b + 1);
   }
@@ -408,10 +473,12 @@ __global__ void __launch_bounds__(kSel, 1)
   if (topk_len != nullptr && rank == 0 && tid == 0) topk_len[n] = kept;
   for (int j = rank * kSel + tid; j < K; j += CS * kSel)
     if (j >= kept || v <= K) out[j] = j < kept ? j : -1;
-  if (v <= K) return;
+  if (v <= K) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
 
   cg::cluster_group cl = cg::this_cluster();
-  if constexpr (CS > 1) cl.sync();  // every CTA of the cluster runs before its shared memory is written from outside
   // this CTA's piece of the row, a multiple of 4 so that the 16-byte loads stay aligned
   const int piece = ((v + CS - 1) / CS + 3) & ~3;
   const int begin = min(v, rank * piece), end = min(v, begin + piece);
@@ -433,6 +500,10 @@ __global__ void __launch_bounds__(kSel, 1)
   };
 #pragma unroll
   for (int j = 0; j < kPer; ++j) key[j] = 0u;
+  if (tid == 0) { box[0] = 0xffffffffu; box[1] = 0u; }
+  hist[0][tid] = hist[0][tid + kSel] = 0u;
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores
   if (rounds == 1) load(0);
 
   // smallest and largest: the bits above the highest one where they differ are shared by all
@@ -447,136 +518,107 @@ __global__ void __launch_bounds__(kSel, 1)
   }
   mn = __reduce_min_sync(0xffffffffu, mn);
   mx = __reduce_max_sync(0xffffffffu, mx);
-  if (tid == 0) { pick[0] = 0xffffffffu; pick[1] = 0u; }
-  __syncthreads();
-  if ((tid & 31) == 0) { atomicMin(&pick[0], mn); atomicMax(&pick[1], mx); }
-  __syncthreads();
-  if (tid < CS) {
-    uint32_t* to = cl.map_shared_rank(box, tid);
-    to[2 * rank] = pick[0];
-    to[2 * rank + 1] = pick[1];
-  }
-  cl.sync();
+  if ((tid & 31) == 0) { atomicMin(&box[0], mn); atomicMax(&box[1], mx); }
+  if constexpr (CS > 1) {
+    cl.sync();
 #pragma unroll
-  for (int c = 0; c < CS; ++c) { mn = min(mn, box[2 * c]); mx = max(mx, box[2 * c + 1]); }
+    for (int c = 0; c < CS; ++c) {
+      const uint32_t* q = cl.map_shared_rank(box, c);
+      mn = min(mn, q[0]);
+      mx = max(mx, q[1]);
+    }
+  } else {
+    __syncthreads();
+    mn = box[0];
+    mx = box[1];
+  }
 
   // narrow the K-th largest down: `prefix` holds its bits from `bit` upwards, `need` how many of the scores that
   // share them are still to be taken
   int bit = mn == mx ? 0 : 32 - __clz(mn ^ mx);
   uint32_t prefix = bit == 32 ? 0u : (mx >> bit) << bit;
   int need = K;
-  bool all = false;  // every score that shares the prefix is taken
-  while (bit > 0 && !all) {
+  uint32_t at = 0, tied = (uint32_t)begin;  // entries of the row, and of its tied scores, before this CTA's piece
+  bool all = false;                         // every score that shares the prefix is taken
+  for (int pass = 0; bit > 0 && !all; ++pass) {
     const int shift = max(0, bit - 11);
     const uint32_t mask = (1u << (bit - shift)) - 1u;
-    for (int x = tid; x < kBins; x += kSel) hist[x] = 0u;
-    __syncthreads();
+    uint32_t* h = hist[pass & 1];
     for (int r = 0; r < rounds; ++r) {
       if (rounds > 1) load(r);
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const uint32_t d = key[j] ^ prefix;
-        if (key[j] && (bit == 32 || (d >> bit) == 0u)) atomicAdd(&hist[(key[j] >> shift) & mask], 1u);
+        if (key[j] && (bit == 32 || (d >> bit) == 0u)) atomicAdd(&h[(key[j] >> shift) & mask], 1u);
       }
     }
-    if constexpr (CS > 1) {
-      cl.sync();
-      // this CTA adds a slice of the bins over the cluster and gives the sums to all
-      constexpr int kSlice = kBins / CS;
-      for (int x = tid; x < kSlice; x += kSel) {
-        const int at = rank * kSlice + x;
-        uint32_t s = 0u;
+    if constexpr (CS > 1) cl.sync(); else __syncthreads();
+    // the next histogram's bins (read by no CTA since the barrier before this one)
+    hist[(pass + 1) & 1][tid] = hist[(pass + 1) & 1][tid + kSel] = 0u;
+    // bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t, summed over the cluster (low words) and over
+    // the CTAs before this one (high words)
+    unsigned long long h1 = 0, h0 = 0;
 #pragma unroll
-        for (int c = 0; c < CS; ++c) s += cl.map_shared_rank(hist, c)[at];
-#pragma unroll
-        for (int c = 0; c < CS; ++c) cl.map_shared_rank(tot, c)[at] = s;
-      }
-      cl.sync();
-    } else {
-      __syncthreads();
+    for (int c = 0; c < CS; ++c) {
+      const uint32_t* q = CS > 1 ? cl.map_shared_rank(h, c) : h;
+      const uint2 x = *reinterpret_cast<const uint2*>(q + kBins - 2 - 2 * tid);
+      const unsigned long long w = c < rank ? 0x100000001ull : 1ull;
+      h1 += w * x.y;
+      h0 += w * x.x;
     }
-    const uint32_t* h = CS > 1 ? tot : hist;
-    // bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t
-    const uint32_t h1 = h[kBins - 1 - 2 * tid], h0 = h[kBins - 2 - 2 * tid];
-    uint32_t total;
-    const uint32_t above = block_scan(h1 + h0, sh, total);
-    if (above < (uint32_t)need && above + h1 >= (uint32_t)need) {
-      pick[0] = kBins - 1 - 2 * tid;
-      pick[1] = above;
-      pick[2] = h1;
-    } else if (above + h1 < (uint32_t)need && above + h1 + h0 >= (uint32_t)need) {
-      pick[0] = kBins - 2 - 2 * tid;
-      pick[1] = above + h1;
-      pick[2] = h0;
+    unsigned long long total;
+    const unsigned long long above = block_scan(h1 + h0, sh[pass & 1], total), mid = above + h1;
+    const uint32_t a0 = (uint32_t)above, a1 = (uint32_t)mid, a2 = (uint32_t)(mid + h0);
+    const bool first = a0 < (uint32_t)need && a1 >= (uint32_t)need;
+    if (first || (a1 < (uint32_t)need && a2 >= (uint32_t)need)) {
+      const unsigned long long up = first ? above : mid, in = first ? h1 : h0;
+      pick[0] = kBins - (first ? 1 : 2) - 2 * tid;
+      pick[1] = (uint32_t)up;
+      pick[2] = (uint32_t)(up >> 32);
+      pick[3] = (uint32_t)in;
+      pick[4] = (uint32_t)(in >> 32);
     }
     __syncthreads();
     prefix |= pick[0] << shift;
     need -= (int)pick[1];
-    all = (int)pick[2] == need;
+    at += pick[2];
+    tied = pick[4];
+    all = (int)pick[3] == need;
     bit = shift;
     __syncthreads();
   }
+  // (no CTA leaves while another may still read its shared memory; the last such reads are behind us)
+  if constexpr (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   // taken: above the prefix's class, and the first `need` of the class in order of position
-  auto is_above = [&](uint32_t k) { return bit == 32 ? false : (k >> bit) > (prefix >> bit); };
-  auto is_tied = [&](uint32_t k) { return k != 0u && (bit == 32 || (k >> bit) == (prefix >> bit)); };
-  uint32_t ca = 0, ct = 0;
+  at += min(tied, (uint32_t)need);
   for (int r = 0; r < rounds; ++r) {
     if (rounds > 1) load(r);
+    uint32_t c = 0;  // above, and tied from bit 16 (a round holds 16384)
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      ca += is_above(key[j]) ? 1u : 0u;
-      ct += is_tied(key[j]) ? 1u : 0u;
+      const uint32_t k = key[j] >> bit, q = prefix >> bit;  // (bit < 32: a histogram or equal scores)
+      c += k > q ? 1u : (k == q && key[j] ? 0x10000u : 0u);
     }
-  }
-  if (tid == 0) { pick[0] = 0u; pick[1] = 0u; }
-  __syncthreads();
-  ca = __reduce_add_sync(0xffffffffu, ca);
-  ct = __reduce_add_sync(0xffffffffu, ct);
-  if ((tid & 31) == 0) { atomicAdd(&pick[0], ca); atomicAdd(&pick[1], ct); }
-  __syncthreads();
-  uint32_t at = 0, tied = 0;  // entries of this row, and of its tied ones, before this CTA's piece
-  if constexpr (CS > 1) {
-    cl.sync();  // (box has been read by all)
-    if (tid < CS) {
-      uint32_t* to = cl.map_shared_rank(box, tid);
-      to[2 * rank] = pick[0];
-      to[2 * rank + 1] = pick[1];
-    }
-    cl.sync();  // (also: no CTA leaves while another still reads or writes its shared memory)
-#pragma unroll
-    for (int c = 0; c < CS; ++c) {
-      if (c < rank) {
-        const uint32_t a = box[2 * c], e = box[2 * c + 1];
-        at += a + (tied >= (uint32_t)need ? 0u : min(e, (uint32_t)need - tied));
-        tied += e;
-      }
-    }
-  }
-  for (int r = 0; r < rounds; ++r) {
-    if (rounds > 1) load(r);
-    uint32_t a = 0, e = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      a += is_above(key[j]) ? 1u : 0u;
-      e += is_tied(key[j]) ? 1u : 0u;
-    }
-    uint32_t ta, te;
-    const uint32_t sa = block_scan(a, sh, ta), se = block_scan(e, sh, te);
-    uint32_t my_tied = tied + se;
-    uint32_t o = at + sa + (min(my_tied, (uint32_t)need) - min(tied, (uint32_t)need));
+    uint32_t sum;
+    if (r) __syncthreads();
+    const uint32_t before = block_scan(c, reinterpret_cast<uint32_t*>(sh[0]) + 32 * (r & 1), sum);
+    uint32_t my_tied = tied + (before >> 16);
+    uint32_t o = at + (before & 0xffffu) + (min(my_tied, (uint32_t)need) - min(tied, (uint32_t)need));
     const int p0 = begin + r * kRound + tid * kPer;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      bool take = is_above(key[j]);
-      if (is_tied(key[j])) {
+      const uint32_t k = key[j] >> bit, q = prefix >> bit;
+      bool take = k > q;
+      if (key[j] && k == q) {
         take = my_tied < (uint32_t)need;
         ++my_tied;
       }
       if (take) out[o++] = p0 + j;
     }
-    at += ta + (min(tied + te, (uint32_t)need) - min(tied, (uint32_t)need));
-    tied += te;
+    at += (sum & 0xffffu) + (min(tied + (sum >> 16), (uint32_t)need) - min(tied, (uint32_t)need));
+    tied += sum >> 16;
   }
+  if constexpr (CS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 inline long long stride_of(long long max_len) { return (max_len + 3) / 4 * 4; }
@@ -591,11 +633,11 @@ inline int cluster_of(int N, long long max_len) {
 }
 
 template <int HP>
-dsa_status_t launch_scores(const Params& p, int ctas, cudaStream_t s) {
+dsa_status_t launch_scores(const Params& p, const CUtensorMap& map, int ctas, cudaStream_t s) {
   dsa_status_t st = configure_kernel_smem(reinterpret_cast<const void*>(paged_score_kernel<HP>), SMEM,
                                           "configuring paged_score_kernel");
   if (st != DSA_OK) return st;
-  paged_score_kernel<HP><<<ctas, kThreads, SMEM, s>>>(p);
+  paged_score_kernel<HP><<<ctas, kThreads, SMEM, s>>>(p, map);
   return cuda_check(cudaGetLastError(), "launching paged_score_kernel");
 }
 
@@ -605,12 +647,14 @@ dsa_status_t launch_select(const Params& p, int K, int max_keys, int32_t* idx, i
   cfg.gridDim = dim3((unsigned)p.N * CS);
   cfg.blockDim = dim3(kSel);
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = CS;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = CS;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = CS > 1 ? 2 : 1;
   return cuda_check(cudaLaunchKernelEx(&cfg, paged_select_kernel<CS>, (const float*)p.scores, p.stride, p.seq_lens, p.cu_q,
                                        p.N, p.B, K, max_keys, idx, len),
                     "launching paged_select_kernel");
@@ -675,10 +719,17 @@ extern "C" dsa_status_t dsa_paged_indexer_topk(const dsa_bf16_t* q_idx, const ds
   p.scores = reinterpret_cast<float*>(reinterpret_cast<char*>(workspace) + kErrorWordBytes);
   p.wait_limit = wait_limit_cycles();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (Hi <= 8) st = pidx::launch_scores<8>(p, ctas, s);
-  else if (Hi <= 16) st = pidx::launch_scores<16>(p, ctas, s);
-  else if (Hi <= 32) st = pidx::launch_scores<32>(p, ctas, s);
-  else st = pidx::launch_scores<64>(p, ctas, s);
+  // rows that follow one another in the cache, 32 or a whole page of them at a time
+  CUtensorMap map{};
+  if (num_pages > 0 && (page_size % 32 == 0 || 32 % page_size == 0) && page_size >= 8 &&
+      (int64_t)num_pages * page_size <= 0x7fffffffll) {
+    p.box = page_size < 32 ? page_size : 32;
+    if ((st = make_map_2d_bf16(&map, k_cache, (uint64_t)num_pages * page_size, Di, Di, 64, p.box)) != DSA_OK) return st;
+  }
+  if (Hi <= 8) st = pidx::launch_scores<8>(p, map, ctas, s);
+  else if (Hi <= 16) st = pidx::launch_scores<16>(p, map, ctas, s);
+  else if (Hi <= 32) st = pidx::launch_scores<32>(p, map, ctas, s);
+  else st = pidx::launch_scores<64>(p, map, ctas, s);
   if (st != DSA_OK) return st;
   const int64_t table_len = (int64_t)max_pages * page_size;
   const int max_keys = (int)(table_len < max_len ? table_len : max_len);
