@@ -656,6 +656,14 @@ def dsa_sparse_mla_bwd_noalloc_read_status(device=None) -> int:
 _NORMS = {"none": 0, "rms": 1, "layer": 2}
 
 
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same without the Stream object around it, where torch has it (a third of a short call's time)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
 def paged_workspace_size(kind: str, a: int = 0, b: int = 0) -> int:
     """Workspace bytes of the serving calls: ("slots"), ("norm_rope_fwd"), ("norm_rope_bwd", rows, norm_dim),
     ("mla", N, H) or ("topk", N, max_len)."""
@@ -673,6 +681,15 @@ def paged_workspace_size(kind: str, a: int = 0, b: int = 0) -> int:
 
 def _dense(t, name, dtype, shape, dev):
     """Data pointer of a contiguous tensor of this type, shape (None: any extent) and device."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and \
+            (dev is None or t.device == dev):
+        s = t.shape
+        if len(s) == len(shape):
+            for n, m in zip(shape, s):
+                if n is not None and n != m:
+                    break
+            else:
+                return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
@@ -681,15 +698,13 @@ def _dense(t, name, dtype, shape, dev):
         raise ValueError(f"{name} must be a CUDA tensor")
     if dev is not None and t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    s = t.shape
-    if len(s) != len(shape) or any(n is not None and n != m for n, m in zip(shape, s)):
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(s)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must have shape {tuple('any' if n is None else n for n in shape)}, got {tuple(t.shape)}")
 
 
 def _scratch(workspace, need, dev):
+    """(workspace, pointer, bytes): the caller's uint8 tensor, or one of `need` bytes."""
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     elif not isinstance(workspace, torch.Tensor) or workspace.dtype is not torch.uint8 or workspace.device != dev:
@@ -701,11 +716,12 @@ def _scratch(workspace, need, dev):
 
 def _call(fn, where, dev, *args):
     """The library call on the tensors' device and its current stream."""
-    if dev.index != torch.cuda.current_device():
+    index = dev.index
+    if index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = fn(*args, _raw_stream(index))
     else:
-        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+        status = fn(*args, _raw_stream(index))
     if status != DSA_OK:
         _check(status, where)
 
@@ -733,7 +749,7 @@ def dsa_paged_slots(seq_lens, block_table, free_pages, page_size: int, new_lens=
     ws, p_ws, wsb = _scratch(workspace, 256, dev)
     # one allocation, cut into the five outputs
     buf = torch.empty(2 * N + 2 * B + 2, dtype=torch.int32, device=dev)
-    slot_map, positions, cu_new, seq_lens_out, taken = buf.split([N, N, B + 1, B, 1])
+    slot_map, positions, cu_new, seq_lens_out, taken = buf.split_with_sizes((N, N, B + 1, B, 1))
     p = buf.data_ptr()
     _call(lib.dsa_paged_slots, "dsa_paged_slots", dev, p_len, p_new, B, N, int(page_size), block_table.shape[1], p_free,
           free_pages.shape[0], p_tab, p + 4 * (2 * N + B + 1), p + 8 * N, p, p + 4 * N, p + 4 * (2 * N + 2 * B + 1),

@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < n_tiles; ++i) {
       const int sl = i % kRing, sb = i & 1;
       if (left == 0) {
-        if (!read_seg(seg, sg)) break;
+        if (!warp_all(read_seg(seg, sg))) break;
         left = warp_value(sg.n);
         id = idesc_bf16(kTile, (warp_value(sg.nt) * HP + 15) & ~15, false, false);
         if (!warp_all(wait_for(mb + M_Q, seg & 1, s_abort, p.wait_limit))) break;
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ======================= queries of a segment, once the products of the one before are done =======================
     int done = 0;
     for (int seg = 0; done < n_tiles; ++seg) {
-      if (!read_seg(seg, sg)) break;
+      if (!warp_all(read_seg(seg, sg))) break;
       done += sg.n;
       if (seg > 0 && !wait_for(mb + M_SEG, (seg - 1) & 1, s_abort, p.wait_limit)) break;
       const int rows = ((sg.nt * HP + 15) & ~15);
@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     look_up(sl);
+    int armed = -1;  // the slot's last tile
 #pragma unroll 1
     for (int i = sl; i < n_tiles && !stop; i += kRing) {
       long long row[4];
@@ -326,8 +327,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       if (lane == 0) mbar_arrive(bar);
+      armed = i;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    volatile int dummy = 0;  // nothing lands after the CTA has left
+    if (armed >= 0) mbar_wait(mb + M_K + 8 * sl, (armed / kRing) & 1, &dummy, p.err);
     if (bad) record_error(p.err, DSA_ERR_DEVICE_INDEX);
   } else {
     // ======================= scores: two groups of four warps take alternate tiles; a thread is a key =======================

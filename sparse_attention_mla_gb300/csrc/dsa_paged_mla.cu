@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
       const int sl = i % R, sb = i % NS;
       if (left == 0) {
         Seg sg;
-        if (!read_seg(seg, sg)) break;
+        if (!warp_all(read_seg(seg, sg))) break;
         left = warp_value(sg.n);
         if (!warp_all(wait_for(bar_q, seg & 1, s_abort, p.wait_limit))) break;
         fence_proxy_async_smem();  // (the queries came by cp.async)
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
       uint32_t add = 1;
       if (left == 0) {
         Seg sg;
-        if (!read_seg(seg++, sg)) break;
+        if (!warp_all(read_seg(seg++, sg))) break;
         left = warp_value(sg.n);
         add = 0;  // the segment's first tile overwrites O^T
       }
@@ -516,8 +516,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
     look[0] = look[2];
     page[0] = page_of(look[0]);
     look[1] = position(sl + 3 * R);
+    int armed = -1, next = sl;  // the slot's last tile that this warp has answered for, and the one after it
 #pragma unroll 1
-    for (int i = sl; i < n_tiles; i += R) {
+    for (int i = sl; i < n_tiles && !stop; i += R) {
       const long long row_d = row[0];
       // the chunks of pair m (with the last, the ninth too) are free
       auto slot_free = [&](int m) { return i < R || warp_all(wait_pv(i - R, m)); };
@@ -527,7 +528,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
         // lane x issues chunk x % 2 of a pair (x % 3 of the last one, where there is a ninth), box x / 2 (x / 3)
 #pragma unroll 1
         for (int m = 0; m < kPairs; ++m) {
-          if (!slot_free(m)) { stop = true; break; }
+          // (a tile once begun is issued to its end: what is on its way can then be waited for)
+          if (!stop && !slot_free(m)) {
+            stop = true;
+            if (m == 0) break;
+          }
           if (m == 0) {
             s_valid[sl * kTile + gw * 32 + lane] = 1;
             __syncwarp();
@@ -540,6 +545,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
           if (bx < boxes)
             tma_load_2d(L::chunk(sKV, sl, c) + (gw * 32 + bx * p.box) * 128, &map, c * 64, at,
                         bar_kv + 8 * (sl * kGroups + c / kLand));
+          armed = i;
+          next = i + R;
         }
         if (stop) break;
         // the slot's next tile on its way to L2 (the ring's room bounds what can be on its way to the SM)
@@ -587,6 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
         landed(1);
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         landed(2);
+        armed = i;
+        next = i + R;
       }
       row[0] = row[1];
       row[1] = row_of(look[0].pos, page[0]);
@@ -596,6 +605,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
     }
     if (bad_index) record_error(p.err, DSA_ERR_DEVICE_INDEX);
     asm volatile("cp.async.wait_all;" ::: "memory");
+    // Nothing lands after the CTA has left: the slot's last tile is waited for, and where the wait for room ran out, the
+    // other warp of the slot, which may have begun the next one, gets this warp's part of it.
+    volatile int dummy = 0;
+    if (armed >= 0)
+      for (int g = 0; g < kGroups; ++g) mbar_wait(bar_kv + 8 * (sl * kGroups + g), (armed / R) & 1, &dummy, p.err);
+    __syncwarp();
+    if (next < n_tiles && lane < kGroups) mbar_arrive(bar_kv + 8 * (sl * kGroups + lane));
   } else {
     // ======================= softmax + epilogue =======================
     const int tid = threadIdx.x - 32, wk = warp - 1, qd = warp & 3, ch = wk >> 2;
