@@ -11,6 +11,26 @@ namespace dsa {
 // every 33 cycles instead of every 60 to 80.
 __device__ __forceinline__ int warp_value(int v) { return (int)__reduce_max_sync(0xffffffffu, (unsigned)v); }
 
+// Four MMAs on consecutive 16-element steps of K (the descriptors step by SA and SB), issued by one elected lane: the
+// election and the predicate of the first one (add to D or overwrite it) once for all four.  The issuing warps' pace is
+// the pace at which their instructions arrive next to the other roles' code.
+template <int SA, int SB>
+__device__ __forceinline__ void mma4_w(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add_first) {
+  asm volatile(
+      "{\n\t.reg .pred p, q, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 q, 0, 0;\n\t"
+      "add.s64 a1, %1, %5;\n\tadd.s64 a2, %1, %6;\n\tadd.s64 a3, %1, %7;\n\t"
+      "add.s64 b1, %2, %8;\n\tadd.s64 b2, %2, %9;\n\tadd.s64 b3, %2, %10;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(add_first), "n"(SA), "n"(2 * SA), "n"(3 * SA), "n"(SB), "n"(2 * SB), "n"(3 * SB)
+      : "memory");
+}
+
 // The bounded wait of dsa_device.cuh, in fewer instructions: a wait that runs out only sets *abort, and the CTA records
 // it when it leaves.
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, long long limit) {

@@ -203,31 +203,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ======================= MMA issuer =======================
-    int left = 0, seg = 0;
-    uint32_t id = 0;
-    for (int i = 0; i < n_tiles; ++i) {
-      const int sl = i % kRing, sb = i & 1;
-      if (left == 0) {
-        if (!warp_all(read_seg(seg, sg))) break;
-        left = warp_value(sg.n);
-        id = idesc_bf16(kTile, (warp_value(sg.nt) * HP + 15) & ~15, false, false);
-        if (!warp_all(wait_for(mb + M_Q, seg & 1, s_abort, p.wait_limit))) break;
-        ++seg;
-      }
-      --left;
-      if (i >= 2 && !warp_all(wait_for(mb + M_SF + 8 * sb, ((i >> 1) - 1) & 1, s_abort, p.wait_limit))) break;
-      if (!warp_all(wait_for(mb + M_K + 8 * sl, (i / kRing) & 1, s_abort, p.wait_limit))) break;
-      tc_fence_after();
+    int done = 0;
+    for (int seg = 0; done < n_tiles; ++seg) {
+      if (!warp_all(read_seg(seg, sg))) break;
+      if (!warp_all(wait_for(mb + M_Q, seg & 1, s_abort, p.wait_limit))) break;
+      // what the loop needs in registers of the warp (a call does not keep them)
+      const int n = warp_value(sg.n);
+      const uint32_t id = idesc_bf16(kTile, (warp_value(sg.nt) * HP + 15) & ~15, false, false);
+      const uint32_t d0 = (uint32_t)warp_value((int)tmem), q0 = (uint32_t)warp_value((int)sQ), k0 = (uint32_t)warp_value((int)sK);
+      int i = warp_value(done);
+      done += n;
+      bool stop = false;
+#pragma unroll 1
+      for (int t = 0; t < n; ++t, ++i) {
+        const int sl = i % kRing, sb = i & 1;
+        if (i >= 2 && !warp_all(wait_for(mb + M_SF + 8 * sb, ((i >> 1) - 1) & 1, s_abort, p.wait_limit))) { stop = true; break; }
+        if (!warp_all(wait_for(mb + M_K + 8 * sl, (i / kRing) & 1, s_abort, p.wait_limit))) { stop = true; break; }
+        tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const uint64_t a = sdesc_sw128(sK + (sl * 2 + c) * K_CHUNK, 16, 1024), b = sdesc_sw128(sQ + c * Q_CHUNK, 16, 1024);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_ss_w(tmem + sb * kCols, a + (uint64_t)(k * 2), b + (uint64_t)(k * 2), id, (c | k) ? 1u : 0u);
+        for (int c = 0; c < 2; ++c) {
+          const uint64_t a = sdesc_sw128(k0 + (sl * 2 + c) * K_CHUNK, 16, 1024), b = sdesc_sw128(q0 + c * Q_CHUNK, 16, 1024);
+          mma4_w<2, 2>(d0 + sb * kCols, a, b, id, c);
+        }
+        mma_commit_w(mb + M_KF + 8 * sl);
+        mma_commit_w(mb + M_S + 8 * sb);
       }
-      mma_commit_w(mb + M_KF + 8 * sl);
-      mma_commit_w(mb + M_S + 8 * sb);
-      if (left == 0) mma_commit_w(mb + M_SEG);
+      if (stop) break;
+      mma_commit_w(mb + M_SEG);
     }
     mma_commit_w(mb + M_FIN);
     volatile int dummy = 0;

@@ -64,6 +64,8 @@ struct Smem {
   static constexpr int TOTAL = OFF_MISC + MISC + 1024;  // + alignment slack
   static_assert(TOTAL <= 232448, "shared memory budget");
   static_assert(NH == 64 || 4 * 2 * NH + NS * NH <= 256, "TMEM budget");
+  // of the matrix descriptors (16-byte units): from chunk to chunk, from slot to slot
+  static constexpr int STEP = CHUNK >> 4, SLOT = (OVERLAY ? 11 : NCH) * STEP;
   // Overlay: [tile 0: chunks 0-7][its chunk 8][shared block][chunk 8 of tile 1][tile 1: chunks 0-7]
   __device__ static constexpr uint32_t chunk(uint32_t kv, int slot, int c) {
     if (!OVERLAY) return kv + (uint32_t)(slot * NCH + c) * CHUNK;
@@ -375,34 +377,38 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
   if (warp == 0) {
     // ======================= S^T issuer =======================
     constexpr uint32_t kIdS = idesc_bf16(kTile, NH, false, false);
-    int left = 0, seg = 0;  // tiles left of the segment; segments begun
-    for (int i = 0; i < n_tiles; ++i) {
-      const int sl = i % R, sb = i % NS;
-      if (left == 0) {
-        Seg sg;
-        if (!warp_all(read_seg(seg, sg))) break;
-        left = warp_value(sg.n);
-        if (!warp_all(wait_for(bar_q, seg & 1, s_abort, p.wait_limit))) break;
-        fence_proxy_async_smem();  // (the queries came by cp.async)
-        ++seg;
-      }
-      --left;
-      if (i >= NS && !warp_all(wait_for(bar_sf + 8 * sb, ((i / NS) - 1) & 1, s_abort, p.wait_limit))) break;
-      uint64_t b0 = sdesc_sw128(sQ, 16, 1024);
+    int done = 0;
+    for (int seg = 0; done < n_tiles; ++seg) {
+      Seg sg;
+      if (!warp_all(read_seg(seg, sg))) break;
+      if (!warp_all(wait_for(bar_q, seg & 1, s_abort, p.wait_limit))) break;
+      fence_proxy_async_smem();  // (the queries came by cp.async)
+      // what the loop needs in registers of the warp (a call does not keep them)
+      const int n = warp_value(sg.n);
+      const uint32_t d0 = (uint32_t)warp_value((int)tmem), q0 = (uint32_t)warp_value((int)sQ), kv0 = (uint32_t)warp_value((int)sKV);
+      int i = warp_value(done);
+      done += n;
       bool stop = false;
 #pragma unroll 1
-      for (int c = 0; c < NCH; ++c, b0 += L::Q_CHUNK >> 4) {
-        if (c % kLand == 0) {
-          if (!warp_all(wait_kv(i, c / kLand))) { stop = true; break; }
-          tc_fence_after();
-        }
-        const uint64_t a0 = sdesc_sw128(L::chunk(sKV, sl, c), 16, 1024);
+      for (int k0 = 0; k0 < n; ++k0, ++i) {
+        const int sl = i % R, sb = i % NS;
+        if (i >= NS && !warp_all(wait_for(bar_sf + 8 * sb, ((i / NS) - 1) & 1, s_abort, p.wait_limit))) { stop = true; break; }
+        // the chunks' descriptors by constant steps from the tile's (chunk 8 lies elsewhere in the overlaid ring)
+        const uint64_t a0 = sdesc_sw128(kv0, 16, 1024) + (uint64_t)(uint32_t)(sl * L::SLOT);
+        const uint64_t a8 = sdesc_sw128(kv0, 16, 1024) + (uint64_t)(uint32_t)((L::OVERLAY ? (sl ? 10 : 8) * L::STEP : sl * L::SLOT + 8 * L::STEP));
+        const uint64_t b0 = sdesc_sw128(q0, 16, 1024);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_ss_w(tmem + sb * NH, a0 + (uint64_t)(k * 2), b0 + (uint64_t)(k * 2), kIdS, (c | k) ? 1u : 0u);
+        for (int c = 0; c < NCH; ++c) {
+          if (c % kLand == 0) {
+            if (!warp_all(wait_kv(i, c / kLand))) { stop = true; break; }
+            tc_fence_after();
+          }
+          mma4_w<2, 2>(d0 + sb * NH, c == 8 ? a8 : a0 + c * L::STEP, b0 + c * (L::Q_CHUNK >> 4), kIdS, c);
+        }
+        if (stop) break;
+        mma_commit_w(bar_s + 8 * sb);
       }
       if (stop) break;
-      mma_commit_w(bar_s + 8 * sb);
     }
     mma_commit_w(bar_fin);
     volatile int dummy = 0;
@@ -410,46 +416,46 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
     __syncwarp();
   } else if (warp == 13) {
     // ======================= P.V issuer =======================
-    int left = 0, seg = 0;
-    for (int i = 0; i < n_tiles; ++i) {
-      const int sl = i % R;
-      uint32_t add = 1;
-      if (left == 0) {
-        Seg sg;
-        if (!warp_all(read_seg(seg++, sg))) break;
-        left = warp_value(sg.n);
-        add = 0;  // the segment's first tile overwrites O^T
-      }
-      --left;
-      if (!warp_all(wait_for(bar_p + 8 * (i & 1), (i >> 1) & 1, s_abort, p.wait_limit))) break;
-      tc_fence_after();
-      const uint64_t va = sdesc_sw128(L::chunk(sKV, sl, 0), L::CHUNK, 1024);
-      constexpr uint64_t kPair = (2 * L::CHUNK) >> 4;
-      const uint32_t sP = L::p(sKV, i);
-      if constexpr (NH == 64) {  // P^T rows are keys (MN-major), hi and lo blocks of 64 rows' columns 8 KiB apart
-        constexpr uint32_t kId2 = idesc_bf16(128, 128, true, true), kId1 = idesc_bf16(128, 64, true, true);
-        const uint64_t pb = sdesc_sw128(sP, 8192, 1024);
+    int done = 0;
+    for (int seg = 0; done < n_tiles; ++seg) {
+      Seg sg;
+      if (!warp_all(read_seg(seg, sg))) break;
+      const int n = warp_value(sg.n);
+      const uint32_t d0 = (uint32_t)warp_value((int)tmem), kv0 = (uint32_t)warp_value((int)sKV);
+      int i = warp_value(done);
+      done += n;
+      bool stop = false;
 #pragma unroll 1
-        for (int s = 0; s < 5; ++s) {  // channel tiles 0-2, tile 3 with hi, tile 3 with lo
-          const int m = min(s, 3);
-          const uint32_t id = s < 3 ? kId2 : kId1, on = add | (s == 4);
-          const uint64_t a = va + m * kPair, b = pb + (s == 4 ? 512 : 0);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ss_w(tmem + L::o_col(m), a + (uint64_t)(k * 128), b + (uint64_t)(k * 128), id, on | (k > 0));
-          if (s != 3) mma_commit_w(bar_pv + 8 * (sl * kPairs + m));
-        }
-      } else {  // P^T rows are [hi rows | lo rows], keys along K
-        constexpr uint32_t kId = idesc_bf16(128, 2 * NH, true, false);
-        const uint64_t pb = sdesc_sw128(sP, 16, 1024);
+      for (int k0 = 0; k0 < n; ++k0, ++i) {
+        const int sl = i % R;
+        const uint32_t add = k0 > 0;  // the segment's first tile overwrites O^T
+        if (!warp_all(wait_for(bar_p + 8 * (i & 1), (i >> 1) & 1, s_abort, p.wait_limit))) { stop = true; break; }
+        tc_fence_after();
+        const uint64_t va = sdesc_sw128(L::chunk(kv0, sl, 0), L::CHUNK, 1024);
+        constexpr uint64_t kPair = (2 * L::CHUNK) >> 4;
+        const uint32_t sP = L::p(kv0, i);
+        if constexpr (NH == 64) {  // P^T rows are keys (MN-major), hi and lo blocks of 64 rows' columns 8 KiB apart
+          constexpr uint32_t kId2 = idesc_bf16(128, 128, true, true), kId1 = idesc_bf16(128, 64, true, true);
+          const uint64_t pb = sdesc_sw128(sP, 8192, 1024);
 #pragma unroll 1
-        for (int m = 0; m < 4; ++m) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ss_w(tmem + L::o_col(m), va + m * kPair + (uint64_t)(k * 128), pb + (uint64_t)(k * 2), kId, add | (k > 0));
-          mma_commit_w(bar_pv + 8 * (sl * kPairs + m));
+          for (int s = 0; s < 5; ++s) {  // channel tiles 0-2, tile 3 with hi, tile 3 with lo
+            const int m = min(s, 3);
+            const uint32_t id = s < 3 ? kId2 : kId1, on = add | (s == 4);
+            const uint64_t a = va + m * kPair, b = pb + (s == 4 ? 512 : 0);
+            mma4_w<128, 128>(d0 + L::o_col(m), a, b, id, on);
+            if (s != 3) mma_commit_w(bar_pv + 8 * (sl * kPairs + m));
+          }
+        } else {  // P^T rows are [hi rows | lo rows], keys along K
+          constexpr uint32_t kId = idesc_bf16(128, 2 * NH, true, false);
+          const uint64_t pb = sdesc_sw128(sP, 16, 1024);
+#pragma unroll 1
+          for (int m = 0; m < 4; ++m) {
+            mma4_w<128, 2>(d0 + L::o_col(m), va + m * kPair, pb, kId, add);
+            mma_commit_w(bar_pv + 8 * (sl * kPairs + m));
+          }
         }
       }
+      if (stop) break;
     }
     mma_commit_w(bar_fin + 8);
     volatile int dummy = 0;
