@@ -31,6 +31,22 @@ __device__ __forceinline__ void mma4_w(uint32_t d_tmem, uint64_t a, uint64_t b, 
       : "memory");
 }
 
+// TMA by one elected lane of a warp whose operands are the warp's (see warp_value): issued lane by lane, with operands of
+// their own, the same copies take several times as long.
+__device__ __forceinline__ void tma_load_2d_w(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_2d_w(const CUtensorMap* map, int32_t c0, int32_t c1) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n\t}" ::"l"(map), "r"(c0), "r"(c1)
+      : "memory");
+}
+
 // The bounded wait of dsa_device.cuh, in fewer instructions: a wait that runs out only sets *abort, and the CTA records
 // it when it leaves.
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, long long limit) {

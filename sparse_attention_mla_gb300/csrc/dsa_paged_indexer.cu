@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     look_up(sl);
+    const uint32_t land = (uint32_t)warp_value((int)(sK + sl * 2 * K_CHUNK)), land_bar = (uint32_t)warp_value((int)(mb + M_K + 8 * sl));
     int armed = -1;  // the slot's last tile
 #pragma unroll 1
     for (int i = sl; i < n_tiles && !stop; i += kRing) {
@@ -307,9 +308,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if (whole & (1u << k)) {
-          const int boxes = 32 / p.box, bx = lane >> 1, c = lane & 1;
-          const int src = (int)__shfl_sync(0xffffffffu, row[k], (bx * p.box) & 31);
-          if (bx < boxes) tma_load_2d(sK + (sl * 2 + c) * K_CHUNK + (32 * k + bx * p.box) * 128, &map, c * 64, src, bar);
+#pragma unroll 1
+          for (int at0 = 0; at0 < 32; at0 += p.box) {
+            const int src = warp_value((int)__shfl_sync(0xffffffffu, row[k], at0));
+            tma_load_2d_w(land + (32 * k + at0) * 128, &map, 0, src, land_bar);
+            tma_load_2d_w(land + (32 * k + at0) * 128 + K_CHUNK, &map, 64, src, land_bar);
+          }
         } else {
           const int u = lane & 15;
           const uint32_t dst = sK + (sl * 2 + (u >> 3)) * K_CHUNK;

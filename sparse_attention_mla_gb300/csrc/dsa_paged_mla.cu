@@ -522,6 +522,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
     look[0] = look[2];
     page[0] = page_of(look[0]);
     look[1] = position(sl + 3 * R);
+    // where this warp's rows of the slot go (chunk 8 apart), and the slot's barriers
+    const uint32_t land = (uint32_t)warp_value((int)(L::chunk(sKV, sl, 0) + gw * 4096));
+    const uint32_t land8 = (uint32_t)warp_value((int)(L::chunk(sKV, sl, NCH - 1) + gw * 4096));
+    const uint32_t landed_bar = (uint32_t)warp_value((int)(bar_kv + 8 * sl * kGroups));
     int armed = -1, next = sl;  // the slot's last tile that this warp has answered for, and the one after it
 #pragma unroll 1
     for (int i = sl; i < n_tiles && !stop; i += R) {
@@ -531,7 +535,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
       // all 32 rows are there, in whole boxes
       if (p.box > 0 && __all_sync(0xffffffffu, row_d >= 0)) {
         const int boxes = 32 / p.box;
-        // lane x issues chunk x % 2 of a pair (x % 3 of the last one, where there is a ninth), box x / 2 (x / 3)
 #pragma unroll 1
         for (int m = 0; m < kPairs; ++m) {
           // (a tile once begun is issued to its end: what is on its way can then be waited for)
@@ -545,12 +548,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
             if (lane < kGroups) mbar_expect_tx(bar_kv + 8 * (sl * kGroups + lane), min(kLand, NCH - kLand * lane) * 4096);
             __syncwarp();
           }
-          const int w = m == 3 && NCH == 9 ? 3 : 2;
-          const int bx = lane / w, c = 2 * m + lane - bx * w;
-          const int at = (int)__shfl_sync(0xffffffffu, row_d, (bx * p.box) & 31);
-          if (bx < boxes)
-            tma_load_2d(L::chunk(sKV, sl, c) + (gw * 32 + bx * p.box) * 128, &map, c * 64, at,
-                        bar_kv + 8 * (sl * kGroups + c / kLand));
+#pragma unroll 1
+          for (int bx = 0; bx < boxes; ++bx) {
+            const int at = warp_value((int)__shfl_sync(0xffffffffu, row_d, (bx * p.box) & 31));
+            const uint32_t to = land + bx * p.box * 128;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              tma_load_2d_w(to + (2 * m + x) * L::CHUNK, &map, (2 * m + x) * 64, at, landed_bar + 8 * ((2 * m + x) / kLand));
+            if (NCH == 9 && m == 3) tma_load_2d_w(land8 + bx * p.box * 128, &map, 512, at, landed_bar + 16);
+          }
           armed = i;
           next = i + R;
         }
@@ -558,12 +564,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
         // the slot's next tile on its way to L2 (the ring's room bounds what can be on its way to the SM)
         if (__all_sync(0xffffffffu, row[1] >= 0)) {
 #pragma unroll 1
-          for (int x0 = 0; x0 < boxes * NCH; x0 += 32) {
-            const int x = x0 + lane, bx = x / NCH, c = x - bx * NCH;
-            const int at = (int)__shfl_sync(0xffffffffu, row[1], (bx * p.box) & 31);
-            if (x < boxes * NCH)
-              asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(&map), "r"(c * 64), "r"(at)
-                           : "memory");
+          for (int bx = 0; bx < boxes; ++bx) {
+            const int at = warp_value((int)__shfl_sync(0xffffffffu, row[1], (bx * p.box) & 31));
+#pragma unroll
+            for (int c = 0; c < NCH; ++c) tma_prefetch_2d_w(&map, c * 64, at);
           }
         }
       } else {
