@@ -458,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, NIT == 1 ? 2 : ctas_per_sm(VEC, NIT)
   extern __shared__ __align__(16) uint8_t raw_sh[];
   const int lane = threadIdx.x & 31, l = lane & (LPR - 1), group = threadIdx.x / LPR;
   const Shared s = carve<U>(raw_sh, p.R, group);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the sum over the CTAs waits for this kernel's end)
   // rows on their way while the ones before are worked on
   Run<LPR, U> run;
   int nt[U], nh[U], np[U];
@@ -521,7 +522,10 @@ __global__ void __launch_bounds__(kThreads, NIT == 1 ? 2 : ctas_per_sm(VEC, NIT)
           float2 x[P], v[NIT == 1 ? 1 : P];
           xraw[u].values(x);
           if constexpr (NIT > 1) load_param<VEC, LPR, NIT>(v, p.w, 1.f, p.n, l);
-          auto weight = [&](int i) -> float2 { return NIT == 1 ? w1[i % (NIT == 1 ? P : 1)] : v[i % (NIT == 1 ? 1 : P)]; };
+          auto weight = [&](int i) -> float2 {
+            if constexpr (NIT == 1) return w1[i];
+            else return v[i];
+          };
           float2 sx = make_float2(0.f, 0.f), sg = sx;
           if (p.kind == kLayer) {
 #pragma unroll
@@ -593,14 +597,17 @@ __global__ void __launch_bounds__(kThreads, NIT == 1 ? 2 : ctas_per_sm(VEC, NIT)
 
 // Sums the CTAs' partial rows in a fixed order: 32 channels per CTA, 32 warps along the rows.
 __global__ void __launch_bounds__(1024)
-    norm_rope_sum_kernel(const float* __restrict__ partials, int count, int n, float* __restrict__ dweight,
+    norm_rope_sum_kernel(const float* partials, int count, int n, float* __restrict__ dweight,
                          float* __restrict__ dbias, int accumulate) {
   __shared__ float sh[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
-  if (c < 2 * n)
-    for (int r = w; r < count; r += 32) v += __ldg(partials + (size_t)r * 2 * n + c);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the rows are still being worked on
+  if (c < 2 * n) {
+#pragma unroll 8
+    for (int r = w; r < count; r += 32) v += __ldcg(partials + (size_t)r * 2 * n + c);
+  }
   sh[w][lane] = v;
   __syncthreads();
   v = sh[lane][w];  // channel w of this CTA, warp `lane`'s sum
@@ -833,9 +840,19 @@ extern "C" dsa_status_t dsa_norm_rope_bwd(const dsa_bf16_t* dout, int64_t dout_s
     if (st != DSA_OK) return st;
   }
   if (partials) {
-    nrope::norm_rope_sum_kernel<<<(2 * norm_dim + 31) / 32, 1024, 0, s>>>(partials, blocks, norm_dim, dweight, dbias,
-                                                                         accumulate);
-    if ((st = cuda_check(cudaGetLastError(), "launching norm_rope_sum_kernel")) != DSA_OK) return st;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((2 * norm_dim + 31) / 32);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = blocks > 0 ? 1 : 0;
+    st = cuda_check(cudaLaunchKernelEx(&cfg, nrope::norm_rope_sum_kernel, (const float*)partials, blocks, norm_dim, dweight,
+                                       dbias, accumulate),
+                    "launching norm_rope_sum_kernel");
+    if (st != DSA_OK) return st;
   }
   return ok();
 }
