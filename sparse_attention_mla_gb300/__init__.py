@@ -747,13 +747,11 @@ def dsa_paged_slots(seq_lens, block_table, free_pages, page_size: int, new_lens=
     if N < 0:
         raise ValueError("N must be >= 0")
     ws, p_ws, wsb = _scratch(workspace, 256, dev)
-    # one allocation, cut into the five outputs
-    buf = torch.empty(2 * N + 2 * B + 2, dtype=torch.int32, device=dev)
-    slot_map, positions, cu_new, seq_lens_out, taken = buf.split_with_sizes((N, N, B + 1, B, 1))
-    p = buf.data_ptr()
+    slot_map, positions, cu_new, seq_lens_out, taken = [torch.empty(n, dtype=torch.int32, device=dev)
+                                                        for n in (N, N, B + 1, B, 1)]
     _call(lib.dsa_paged_slots, "dsa_paged_slots", dev, p_len, p_new, B, N, int(page_size), block_table.shape[1], p_free,
-          free_pages.shape[0], p_tab, p + 4 * (2 * N + B + 1), p + 8 * N, p, p + 4 * N, p + 4 * (2 * N + 2 * B + 1),
-          p_ws, wsb)
+          free_pages.shape[0], p_tab, seq_lens_out.data_ptr(), cu_new.data_ptr(), slot_map.data_ptr(),
+          positions.data_ptr(), taken.data_ptr(), p_ws, wsb)
     return slot_map, positions, cu_new, seq_lens_out, taken
 
 
