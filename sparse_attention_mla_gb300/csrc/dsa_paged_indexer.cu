@@ -458,7 +458,7 @@ __device__ __forceinline__ T block_scan(T v, T* sh, T& total) {
 
 template <int CS>
 __global__ void __launch_bounds__(kSel, 1)
-    paged_select_kernel(const float* __restrict__ scores, long long stride, const int32_t* __restrict__ seq_lens,
+    paged_select_kernel(const float* scores, long long stride, const int32_t* __restrict__ seq_lens,
                         const int32_t* __restrict__ cu_q, int N, int B, int K, int max_keys, int32_t* __restrict__ topk_idx,
                         int32_t* __restrict__ topk_len) {
   __shared__ uint32_t hist[2][kBins];
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kSel, 1)
   if (tid == 0) { box[0] = 0xffffffffu; box[1] = 0u; }
   hist[0][tid] = hist[0][tid + kSel] = 0u;
   __syncthreads();
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores (made during this kernel: no constant data)
   if (rounds == 1) load(0);
 
   // smallest and largest: the bits above the highest one where they differ are shared by all

@@ -895,8 +895,9 @@ __global__ void __launch_bounds__(kJoin) paged_mla_join_kernel(const int4* __res
   __shared__ float4 acc[kTeams][128];
   __shared__ float s_l, s_base;
   const int tid = threadIdx.x, lane = tid & 31, team = tid >> 7, x = tid & 127;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the pieces are still being made
-  if (tid < ctas) rec[tid] = records[tid];
+  // launched while the pieces are still being made; what the first kernel writes is read from L2, not as constant data
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (tid < ctas) rec[tid] = __ldcg(records + tid);
   __syncthreads();
   if (tid < 64) {
     const int many = tid >> 5;
@@ -941,11 +942,11 @@ __global__ void __launch_bounds__(kJoin) paged_mla_join_kernel(const int4* __res
     float4 v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      v[k] = k < pieces ? __ldg(reinterpret_cast<const float4*>(src + piece(lo, k, n) * kDv) + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[k] = k < pieces ? __ldcg(reinterpret_cast<const float4*>(src + piece(lo, k, n) * kDv) + x) : make_float4(0.f, 0.f, 0.f, 0.f);
     // lane k holds piece k's maximum and sum
     const size_t at = lane < pieces ? piece(lo, lane, n) : 0;
-    const float mc = lane < pieces ? __ldg(stats + at / 64 * 128 + n) : -INFINITY;
-    const float lc = lane < pieces ? __ldg(stats + at / 64 * 128 + 64 + n) : 0.f;
+    const float mc = lane < pieces ? __ldcg(stats + at / 64 * 128 + n) : -INFINITY;
+    const float lc = lane < pieces ? __ldcg(stats + at / 64 * 128 + 64 + n) : 0.f;
     const float s2 = sink ? __ldg(sink + (rc.z + n) % H) * kLog2e : -INFINITY;
     float m = fmaxf(mc, s2);
 #pragma unroll
@@ -967,7 +968,7 @@ __global__ void __launch_bounds__(kJoin) paged_mla_join_kernel(const int4* __res
           o.y += w * v[k].y;
           o.z += w * v[k].z;
           o.w += w * v[k].w;
-          if (k0 + 4 + k < pieces) v[k] = __ldg(reinterpret_cast<const float4*>(src + piece(lo, k0 + 4 + k, n) * kDv) + x);
+          if (k0 + 4 + k < pieces) v[k] = __ldcg(reinterpret_cast<const float4*>(src + piece(lo, k0 + 4 + k, n) * kDv) + x);
         }
       }
     }
@@ -978,7 +979,7 @@ __global__ void __launch_bounds__(kJoin) paged_mla_join_kernel(const int4* __res
     const int4 rc = rec[lo];
     const int n = it - first[1][lo], pieces = rc.w - lo + 1;
     // the first pieces' channels are on their way while the maxima are compared
-    float4 v = __ldg(reinterpret_cast<const float4*>(partial + piece(lo, team, n) * kDv) + x);  // (kMany >= kTeams)
+    float4 v = __ldcg(reinterpret_cast<const float4*>(partial + piece(lo, team, n) * kDv) + x);  // (kMany >= kTeams)
     if (tid < 32) {
       const float s2 = sink ? __ldg(sink + (rc.z + n) % H) * kLog2e : -INFINITY;
       float mc[kMaxCtas / 32], lc[kMaxCtas / 32], m = s2;
@@ -986,8 +987,8 @@ __global__ void __launch_bounds__(kJoin) paged_mla_join_kernel(const int4* __res
       for (int j = 0; j < kMaxCtas / 32; ++j) {
         const int k = j * 32 + lane;
         const size_t at = k < pieces ? piece(lo, k, n) / 64 * 128 + n : 0;
-        mc[j] = k < pieces ? __ldg(stats + at) : -INFINITY;
-        lc[j] = k < pieces ? __ldg(stats + at + 64) : 0.f;
+        mc[j] = k < pieces ? __ldcg(stats + at) : -INFINITY;
+        lc[j] = k < pieces ? __ldcg(stats + at + 64) : 0.f;
         m = fmaxf(m, mc[j]);
       }
 #pragma unroll
@@ -1011,7 +1012,7 @@ __global__ void __launch_bounds__(kJoin) paged_mla_join_kernel(const int4* __res
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = team; k < pieces; k += kTeams) {
       float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (k + kTeams < pieces) w = __ldg(reinterpret_cast<const float4*>(partial + piece(lo, k + kTeams, n) * kDv) + x);
+      if (k + kTeams < pieces) w = __ldcg(reinterpret_cast<const float4*>(partial + piece(lo, k + kTeams, n) * kDv) + x);
       const float f = fac[k];
       o.x += f * v.x;
       o.y += f * v.y;
