@@ -496,7 +496,8 @@ dsa_status_t dsa_paged_slots(const int32_t* seq_lens, const int32_t* new_lens, i
  * keys (norm 2 of 128, rotation of 64), per-head norms of queries and keys, and the
  * position channels of wider query rows (a strided view; out may be x itself).
  *  x            device bf16, row (t, h) at x + t x_stride_t + h x_stride_h (elements; >= 0,
- *               0 repeats a row), channels contiguous; T >= 0, H >= 1, D in [1, 1024]
+ *               0 repeats a row), channels contiguous; T >= 0, H >= 1, T H <= 2^31 - 65,
+ *               D in [1, 1024]
  *  weight, bias device fp32 [norm_dim] or NULL (1 and 0)
  *  positions    device int32 [T];  inv_freq device fp32 [rope_dim / 2] (both may be NULL
  *               when rope_dim is 0)
@@ -590,7 +591,8 @@ dsa_status_t dsa_paged_mla(const dsa_bf16_t* q, const dsa_bf16_t* cache, const i
  *  head_weights device fp32 [N, Hi]
  *  block_table, seq_lens, cu_q  as dsa_paged_mla
  *  K            in [1, 2048]
- *  max_len      no request is longer (the workspace holds N rows of that many scores)
+ *  max_len      no request is longer (the workspace holds N rows of that many scores);
+ *               at most 2^30
  *  topk_idx     device int32 [N, K] (out);  topk_len device int32 [N] (out) or NULL;
  *               rows outside [cu_q[0], cu_q[B]) are left as they are
  *  workspace    >= dsa_paged_indexer_topk_workspace_size(N, max_len) bytes

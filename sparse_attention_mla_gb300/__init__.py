@@ -931,7 +931,7 @@ def dsa_paged_indexer_topk(q_idx, k_cache, head_weights, block_table, seq_lens, 
     """Top-k selection of new tokens over paged index keys -> (topk_idx int32 [N,K], positions ascending with a -1
     suffix, topk_len int32 [N]): the lists of dsa_paged_mla.  q_idx bf16 [N,Hi,128]; k_cache bf16 [num_pages,
     page_size, 128]; head_weights fp32 [N,Hi]; the rest as dsa_paged_mla.  max_len: no request is longer (default:
-    what the table holds); the workspace is N rows of that many fp32 scores."""
+    what the table holds), at most 2^30; the workspace is N rows of that many fp32 scores."""
     lib = _lib or load_library()
     p_q = _dense(q_idx, "q_idx", torch.bfloat16, (None, None, None), None)
     dev = q_idx.device
@@ -939,7 +939,7 @@ def dsa_paged_indexer_topk(q_idx, k_cache, head_weights, block_table, seq_lens, 
     p_w = _dense(head_weights, "head_weights", torch.float32, (N, Hi), dev)
     p_cache, p_tab, p_len, p_cu, B, pages, page, width = _paged(k_cache, Di, block_table, seq_lens, cu_q, N, dev)
     K = int(K)
-    max_len = min(width * page, 2 ** 31 - 4) if max_len is None else int(max_len)
+    max_len = min(width * page, 2 ** 30) if max_len is None else int(max_len)
     if topk_idx is None:
         topk_idx = torch.empty(N, K, dtype=torch.int32, device=dev)
     if topk_len is None:

@@ -39,6 +39,7 @@ namespace nrope {
 
 constexpr int kThreads = 256;
 constexpr int kMaxD = 1024;
+constexpr int64_t kMaxRows = 0x7fffffffll - 64;  // (a run counts up to 32 rows past the last one)
 constexpr int kMaxPartials = 608;  // CTAs of a backward launch with parameters: each leaves one row of dw and db
 enum { kNone = 0, kRms = 1, kLayer = 2 };
 
@@ -702,7 +703,8 @@ dsa_status_t check_rows(const char* who, Rows& p, int norm, int norm_dim, const 
   p.pos = positions;
   p.inv_freq = inv_freq;
   p.rscale = rope_scale;
-  if ((int64_t)p.T * p.H > 0x7fffffffll) return fail(DSA_ERR_INVALID_ARGUMENT, "%s: T * H must be below 2^31", who);
+  if ((int64_t)p.T * p.H > kMaxRows)
+    return fail(DSA_ERR_INVALID_ARGUMENT, "%s: T * H must be at most %lld", who, (long long)kMaxRows);
   p.rows = p.T * p.H;
   return DSA_OK;
 }

@@ -40,6 +40,7 @@ constexpr int kReaders = 14;
 constexpr int kSegs = 8;
 constexpr int kMaxCtas = 160;
 
+constexpr int kMaxLen = 1 << 30;  // (positions are counted past a row's end by up to a round of the selection)
 constexpr int Q_CHUNK = kCols * 128, K_CHUNK = kTile * 128;
 constexpr int OFF_Q = 0, OFF_K = 2 * Q_CHUNK, OFF_W = OFF_K + kRing * 2 * K_CHUNK, OFF_MISC = OFF_W + 2 * kCols * 4;
 constexpr int SMEM = OFF_MISC + 1024 + 1024;
@@ -694,6 +695,7 @@ extern "C" dsa_status_t dsa_paged_indexer_topk(const dsa_bf16_t* q_idx, const ds
   if (Hi < 1 || Hi > 64 || Di != pidx::kD)
     return fail(DSA_ERR_INVALID_ARGUMENT, "%s: need Hi in [1, 64] and Di = 128 (got %d, %d)", who, Hi, Di);
   if (K < 1 || K > 2048) return fail(DSA_ERR_INVALID_ARGUMENT, "%s: K must be in [1, 2048] (got %d)", who, K);
+  if (max_len > pidx::kMaxLen) return fail(DSA_ERR_INVALID_ARGUMENT, "%s: max_len must be at most 2^30 (got %d)", who, max_len);
   if ((int64_t)N * 8 > 0x7fffffffll) return fail(DSA_ERR_INVALID_ARGUMENT, "%s: N is too large (%d)", who, N);
   if (!cu_q && N != B)
     return fail(DSA_ERR_INVALID_ARGUMENT, "%s: without cu_q every request has one token (N = %d, B = %d)", who, N, B);

@@ -81,23 +81,23 @@ __global__ void __launch_bounds__(kThreads)
   bad = __syncthreads_or(bad);
   if (tid == 0) { cu[B] = (int)tok; base[B] = (int)pag; }
   __syncthreads();
-  const int g0 = blockIdx.x * kThreads + tid, gstep = gridDim.x * kThreads;
+  const unsigned g0 = blockIdx.x * kThreads + tid, gstep = gridDim.x * kThreads;  // (unsigned: N may be 2^31 - 1)
   if (bad) {  // all or nothing: no request gets a token
-    for (int t = g0; t < N; t += gstep) { slot_map[t] = -1; positions[t] = -1; }
-    for (int b = g0; b <= B; b += gstep) {
+    for (unsigned t = g0; t < (unsigned)N; t += gstep) { slot_map[t] = -1; positions[t] = -1; }
+    for (unsigned b = g0; b <= (unsigned)B; b += gstep) {
       cu_new[b] = 0;
-      if (b < B) seq_lens_out[b] = __ldg(seq_lens + b);
+      if (b < (unsigned)B) seq_lens_out[b] = __ldg(seq_lens + b);
     }
     if (g0 == 0) { *pages_taken = 0; record_error(err, DSA_ERR_CAPACITY); }
     return;
   }
   const int total = cu[B], fresh = base[B];
-  for (int t = g0; t < N; t += gstep) {
+  for (unsigned t = g0; t < (unsigned)N; t += gstep) {
     int slot = -1, pos = -1;
-    if (t < total) {
-      const int b = last_le(cu, B, t);  // (skips requests without new tokens)
+    if (t < (unsigned)total) {
+      const int b = last_le(cu, B, (int)t);  // (skips requests without new tokens)
       const int s = __ldg(seq_lens + b);
-      pos = s + (t - cu[b]);
+      pos = s + ((int)t - cu[b]);
       const int pi = pos / P, first = (int)ceil_div(s, P);
       // a fresh page is read from the free list: its table entry may still be being written by another CTA
       const int page = pi >= first ? __ldg(free_pages + base[b] + (pi - first))
@@ -109,14 +109,14 @@ __global__ void __launch_bounds__(kThreads)
     slot_map[t] = slot;
     positions[t] = pos;
   }
-  for (int i = g0; i < fresh; i += gstep) {
-    const int b = last_le(base, B, i);
-    const int col = (int)ceil_div(__ldg(seq_lens + b), P) + (i - base[b]);
+  for (unsigned i = g0; i < (unsigned)fresh; i += gstep) {
+    const int b = last_le(base, B, (int)i);
+    const int col = (int)ceil_div(__ldg(seq_lens + b), P) + ((int)i - base[b]);
     block_table[(size_t)b * max_pages + col] = __ldg(free_pages + i);
   }
-  for (int b = g0; b <= B; b += gstep) {
+  for (unsigned b = g0; b <= (unsigned)B; b += gstep) {
     cu_new[b] = cu[b];
-    if (b < B) seq_lens_out[b] = __ldg(seq_lens + b) + (cu[b + 1] - cu[b]);
+    if (b < (unsigned)B) seq_lens_out[b] = __ldg(seq_lens + b) + (cu[b + 1] - cu[b]);
   }
   if (g0 == 0) *pages_taken = fresh;
 }

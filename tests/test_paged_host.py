@@ -144,6 +144,15 @@ def test_paged_indexer_refuses_a_bad_workspace(lib):
     assert topk(lib, ws=None) == 4 and topk(lib, ws=P(0x100010)) == 4 and topk(lib, wsb=need - 1) == 4
 
 
+def test_sizes_past_what_a_kernel_counts_are_refused(lib):
+    # rows are counted up to a run past the last one, positions up to a round past a row's end
+    for f in (fwd, bwd):
+        assert f(lib, T=2 ** 31 - 64) == 3 and f(lib, T=2 ** 30, H=2, D=64, n=64, r0=0, xt=128, xh=64, ot=128, oh=64, dt=128, dh=64,
+                                                 gt=128, gh=64) == 3
+        assert "T * H" in lib.dsa_last_error_message().decode()
+    assert topk(lib, most=2 ** 30 + 1) == 3 and "max_len" in lib.dsa_last_error_message().decode()
+
+
 def test_the_binding_refuses():
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     i = torch.zeros(4, dtype=torch.int32)
