@@ -16,12 +16,13 @@
 // the one read and the one write, LPR lanes to a row (8 for 64 channels, 16 for
 // 128, else a warp), 16 bytes a lane and two fp32 operations an instruction; a
 // group of lanes takes U consecutive rows (up to 4) at once, the next U on their
-// way meanwhile, and the CTAs stay, so that the table of frequencies is made once.
+// way meanwhile, and the CTAs stay, so that the table of frequencies is made once;
+// a row's place is the last one's plus a step (as two products of 64 bits 6 % more).
 // The cosines and sines depend on the token alone: they are formed once per token
 // of a group's run of rows, spread over its lanes, in shared memory.  Measured: the
-// position channels of 16384 x 64 heads (128 of every 1152 bytes) 60 us at 4.5 TB/s,
-// 131104 rows of 128 with the norm 23 us at 2.9 TB/s, the gradient of 32768 rows of
-// 128 with the layer norm 19 us at 1.3 TB/s (three batches of rows a group: latency).
+// position channels of 16384 x 64 heads (128 of every 1152 bytes) 54 us at 5.0 TB/s,
+// 131104 rows of 128 with the norm 18 us at 3.8 TB/s, the gradient of 32768 rows of
+// 128 with the layer norm 18 us at 1.4 TB/s (four batches of rows a group: latency).
 //
 // Angles: positions reach millions, and position times frequency in fp32 is then
 // off by 0.1 rad.  The frequency is held as a 64-bit binary fraction of a turn, so
@@ -41,14 +42,20 @@ constexpr int kThreads = 256;
 constexpr int kMaxD = 1024;
 constexpr int64_t kMaxRows = 0x7fffffffll - 64;  // (a run counts up to 32 rows past the last one)
 constexpr int kMaxPartials = 608;  // CTAs of a backward launch with parameters: each leaves one row of dw and db
-enum { kNone = 0, kRms = 1, kLayer = 2 };
+enum { kAny = -1, kNone = 0, kRms = 1, kLayer = 2 };  // (kAny: a kernel that reads the norm from its arguments)
 
 // CTAs of an SM, by the registers that a lane's channels take.
 __host__ __device__ constexpr int ctas_per_sm(int VEC, int NIT) { return NIT <= 2 && VEC == 8 ? 2 : 1; }
 
+// Steps in elements from a token and from a head to the next, and from a token's last head to the next token's first.
+struct Step {
+  int64_t t, h, wrap;
+};
+inline Step step_of(int64_t t, int64_t h, int H) { return Step{t, h, t - (int64_t)(H - 1) * h}; }
+
 struct Rows {
   const __nv_bfloat16* x;
-  int64_t xs_t, xs_h;
+  Step xs;
   int T, H, D;
   int kind, n;
   const float* w;
@@ -309,27 +316,40 @@ __device__ __forceinline__ void load_param(float2 (&v)[Row<VEC, LPR, NIT>::P], c
   }
 }
 
-// A group's run of rows, U at a time: their tokens and heads, and the tokens' cosines and sines as they come up.
-template <int LPR, int U>
+// A group's run of rows, U at a time: their tokens and heads, where they lie in NA arrays (by steps: a row's place costs
+// no products), and the tokens' cosines and sines as they come up.
+template <int LPR, int U, int NA>
 struct Run {
   int row, end, t, h;  // next row, end of the run; token and head of the next row
   int filled;          // last token whose cosines and sines are there
-  __device__ __forceinline__ void begin(const Rows& p, int64_t first) {
+  int64_t at[NA];      // the next row in each array
+  __device__ __forceinline__ void begin(const Rows& p, int64_t first, const Step (&st)[NA]) {
     row = first < p.rows ? (int)first : p.rows;
     end = (int)min((int64_t)p.rows, first + p.run);
     t = row / p.H;
     h = row - t * p.H;
     filled = t - 1;
+#pragma unroll
+    for (int a = 0; a < NA; ++a) at[a] = t * st[a].t + h * st[a].h;
   }
-  // the next U rows (t = -1: none) and their positions
-  __device__ __forceinline__ void batch(const Rows& p, int (&tt)[U], int (&hh)[U], int (&pos)[U]) {
+  // the next U rows (t = -1: none), their places and their positions
+  __device__ __forceinline__ void batch(const Rows& p, const Step (&st)[NA], int (&tt)[U], int (&hh)[U], int (&pos)[U],
+                                        int64_t (&place)[NA][U]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      tt[u] = row < end ? t : -1;
+      const bool on = row < end;
+      tt[u] = on ? t : -1;
       hh[u] = h;
-      pos[u] = p.R > 0 && row < end ? __ldg(p.pos + t) : 0;
+      pos[u] = p.R > 0 && on ? __ldg(p.pos + t) : 0;
+      const bool last = h + 1 == p.H;
+#pragma unroll
+      for (int a = 0; a < NA; ++a) {
+        place[a][u] = on ? at[a] : 0;
+        at[a] += last ? st[a].wrap : st[a].h;
+      }
       ++row;
-      if (++h == p.H) { h = 0; ++t; }
+      t += last ? 1 : 0;
+      h = last ? 0 : h + 1;
     }
   }
   // the cosines and sines of a batch's tokens
@@ -347,29 +367,34 @@ struct Run {
   }
 };
 
-template <int VEC, int LPR, int NIT, int ROT, int U>
+// ROWS: out_rows may say where a token's rows go; else they follow one another.
+template <int VEC, int LPR, int NIT, int ROT, int U, int KIND, bool ROWS>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(VEC, NIT))
-    norm_rope_fwd_kernel(const Rows p, __nv_bfloat16* out, int64_t os_t, int64_t os_h,
-                         const int32_t* __restrict__ out_rows, int64_t num_rows, int* __restrict__ err) {
+    norm_rope_fwd_kernel(const Rows p, __nv_bfloat16* out, const Step os, const int32_t* __restrict__ out_rows,
+                         int64_t num_rows, int* __restrict__ err) {
   using R = Row<VEC, LPR, NIT>;
+  const int kind = KIND == kAny ? p.kind : KIND;
+  const bool by_rows = ROWS && out_rows != nullptr;
   constexpr int GPB = kThreads / LPR, P = R::P, PP = R::PP;
   extern __shared__ __align__(16) uint8_t raw_sh[];
   const int lane = threadIdx.x & 31, l = lane & (LPR - 1), group = threadIdx.x / LPR;
   const Shared s = carve<U>(raw_sh, p.R, group);
   // rows on their way while the ones before are worked on
-  Run<LPR, U> run;
+  Run<LPR, U, 1> run;
+  const Step steps[1] = {p.xs};
   int nt[U], nh[U], np[U], no[U];
   R nraw[U];
   auto fetch = [&]() {
-    run.batch(p, nt, nh, np);
+    int64_t place[1][U];
+    run.batch(p, steps, nt, nh, np, place);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      nraw[u].load(p.x + (nt[u] >= 0 ? nt[u] * p.xs_t + nh[u] * p.xs_h : 0), p.D, l, nt[u] >= 0);
-      no[u] = out_rows != nullptr && nt[u] >= 0 ? __ldg(out_rows + nt[u]) : nt[u];
+      nraw[u].load(p.x + place[0][u], p.D, l, nt[u] >= 0);
+      no[u] = by_rows && nt[u] >= 0 ? __ldg(out_rows + nt[u]) : nt[u];
     }
   };
   int64_t first = ((int64_t)blockIdx.x * GPB + group) * p.run;
-  run.begin(p, first);
+  run.begin(p, first, steps);
   fetch();
   fill_turns(s.turn, p);
   const float inv_n = p.n > 0 ? 1.f / (float)p.n : 0.f;
@@ -382,6 +407,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(VEC, NIT))
   // the groups of a warp run the same trip counts
   for (int64_t warp_first = first - (int64_t)(lane / LPR) * p.run; warp_first < p.rows; warp_first += step) {
     int turned = -1;  // the token whose cosines and sines `turn` holds
+    int64_t to = nt[0] * os.t + nh[0] * os.h;  // where the next row goes
 #pragma unroll 1
     for (int k = 0; k < p.run; k += U) {
       int tt[U], hh[U], pos[U], o[U];
@@ -393,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(VEC, NIT))
         pos[u] = np[u];
         o[u] = no[u];
         raw[u] = nraw[u];
-        if (out_rows != nullptr && tt[u] >= 0 && (o[u] < -1 || o[u] >= num_rows)) {
+        if (by_rows && tt[u] >= 0 && (o[u] < -1 || o[u] >= num_rows)) {
           if (l == 0) record_error(err, DSA_ERR_DEVICE_INDEX);
           o[u] = -1;
         }
@@ -401,16 +427,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(VEC, NIT))
       run.cos_sin(p, s, tt, pos, l);
       if (k + U >= p.run) {
         first += step;
-        run.begin(p, first);
+        run.begin(p, first, steps);
       }
       fetch();
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float2 f[P];
         raw[u].values(f);
-        if (p.kind != kNone) {
+        if (kind != kNone) {
           float2 mean = make_float2(0.f, 0.f), ss = mean;
-          if (p.kind == kLayer) {
+          if (kind == kLayer) {
 #pragma unroll
             for (int i = 0; i < P; ++i)
               if (((i / PP) * LPR + l) * VEC < p.n) mean = add2(mean, f[i]);
@@ -420,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(VEC, NIT))
 #pragma unroll
           for (int i = 0; i < P; ++i)
             if (((i / PP) * LPR + l) * VEC < p.n) {
-              if (p.kind == kLayer) f[i] = add2(f[i], mean);
+              if (kind == kLayer) f[i] = add2(f[i], mean);
               ss = fma2(f[i], f[i], ss);
             }
           const float r = rsqrtf(group_sum<LPR>(ss.x + ss.y) * inv_n + p.eps);
@@ -430,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(VEC, NIT))
 #pragma unroll
           for (int i = 0; i < P; ++i)
             if (((i / PP) * LPR + l) * VEC < p.n) f[i] = mul2(mul2(f[i], r2), NIT == 1 ? w[i % (NIT == 1 ? P : 1)] : v[i]);
-          if (p.b != nullptr) {
+          if (kind == kLayer && p.b != nullptr) {
             load_param<VEC, LPR, NIT>(v, p.b, 0.f, p.n, l);
 #pragma unroll
             for (int i = 0; i < P; ++i)
@@ -444,7 +470,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(VEC, NIT))
           }
           turn.apply(f, s.stage, p, l, 1.f);
         }
-        if (o[u] >= 0) store_row<VEC, LPR, NIT>(out + o[u] * os_t + hh[u] * os_h, p.D, l, f);
+        if (o[u] >= 0) store_row<VEC, LPR, NIT>(out + (by_rows ? o[u] * os.t + hh[u] * os.h : to), p.D, l, f);
+        to += hh[u] + 1 == p.H ? os.wrap : os.h;
       }
     }
   }
@@ -452,29 +479,32 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(VEC, NIT))
 
 template <int VEC, int LPR, int NIT, int ROT, int U>
 __global__ void __launch_bounds__(kThreads, NIT == 1 ? 2 : ctas_per_sm(VEC, NIT))
-    norm_rope_bwd_kernel(const Rows p, const __nv_bfloat16* dout, int64_t gs_t, int64_t gs_h, __nv_bfloat16* dx,
-                         int64_t ds_t, int64_t ds_h, float* __restrict__ partials) {
+    norm_rope_bwd_kernel(const Rows p, const __nv_bfloat16* dout, const Step gs, __nv_bfloat16* dx, const Step ds,
+                         float* __restrict__ partials) {
   using R = Row<VEC, LPR, NIT>;
+  const int kind = p.kind;
   constexpr int GPB = kThreads / LPR, P = R::P, PP = R::PP;
   extern __shared__ __align__(16) uint8_t raw_sh[];
   const int lane = threadIdx.x & 31, l = lane & (LPR - 1), group = threadIdx.x / LPR;
   const Shared s = carve<U>(raw_sh, p.R, group);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the sum over the CTAs waits for this kernel's end)
   // rows on their way while the ones before are worked on
-  Run<LPR, U> run;
+  Run<LPR, U, 2> run;
+  const Step steps[2] = {gs, p.xs};
   int nt[U], nh[U], np[U];
   R ng[U], nx[U];
   auto fetch = [&]() {
-    run.batch(p, nt, nh, np);
+    int64_t place[2][U];
+    run.batch(p, steps, nt, nh, np, place);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const bool on = nt[u] >= 0;
-      ng[u].load(dout + (on ? nt[u] * gs_t + nh[u] * gs_h : 0), p.D, l, on);
-      if (p.kind != kNone) nx[u].load(p.x + (on ? nt[u] * p.xs_t + nh[u] * p.xs_h : 0), p.n, l, on);
+      ng[u].load(dout + place[0][u], p.D, l, on);
+      if (kind != kNone) nx[u].load(p.x + place[1][u], p.n, l, on);
     }
   };
   int64_t first = ((int64_t)blockIdx.x * GPB + group) * p.run;
-  run.begin(p, first);
+  run.begin(p, first, steps);
   fetch();
   fill_turns(s.turn, p);
   const float inv_n = p.n > 0 ? 1.f / (float)p.n : 0.f;
@@ -489,6 +519,7 @@ __global__ void __launch_bounds__(kThreads, NIT == 1 ? 2 : ctas_per_sm(VEC, NIT)
   for (int i = 0; i < P; ++i) dw[i] = db[i] = make_float2(0.f, 0.f);
   for (int64_t warp_first = first - (int64_t)(lane / LPR) * p.run; warp_first < p.rows; warp_first += step) {
     int turned = -1;
+    int64_t to = nt[0] * ds.t + nh[0] * ds.h;  // where the next row goes
 #pragma unroll 1
     for (int k = 0; k < p.run; k += U) {
       int tt[U], hh[U], pos[U];
@@ -504,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, NIT == 1 ? 2 : ctas_per_sm(VEC, NIT)
       run.cos_sin(p, s, tt, pos, l);
       if (k + U >= p.run) {
         first += step;
-        run.begin(p, first);
+        run.begin(p, first, steps);
       }
       fetch();
 #pragma unroll
@@ -519,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, NIT == 1 ? 2 : ctas_per_sm(VEC, NIT)
           }
           turn.apply(g, s.stage, p, l, -1.f);
         }
-        if (p.kind != kNone) {
+        if (kind != kNone) {
           float2 x[P], v[NIT == 1 ? 1 : P];
           xraw[u].values(x);
           if constexpr (NIT > 1) load_param<VEC, LPR, NIT>(v, p.w, 1.f, p.n, l);
@@ -528,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, NIT == 1 ? 2 : ctas_per_sm(VEC, NIT)
             else return v[i];
           };
           float2 sx = make_float2(0.f, 0.f), sg = sx;
-          if (p.kind == kLayer) {
+          if (kind == kLayer) {
 #pragma unroll
             for (int i = 0; i < P; ++i)
               if (((i / PP) * LPR + l) * VEC < p.n) {
@@ -559,7 +590,8 @@ __global__ void __launch_bounds__(kThreads, NIT == 1 ? 2 : ctas_per_sm(VEC, NIT)
               g[i] = mul2(r2, fma2(xh, m2, fma2(g[i], weight(i), sg)));
             }
         }
-        if (on) store_row<VEC, LPR, NIT>(dx + tt[u] * ds_t + hh[u] * ds_h, p.D, l, g);
+        if (on) store_row<VEC, LPR, NIT>(dx + to, p.D, l, g);
+        to += hh[u] + 1 == p.H ? ds.wrap : ds.h;
       }
     }
   }
@@ -622,18 +654,28 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-template <int V, int L, int N, int T>
+template <int V, int L, int N, int T, int K = kAny>
 struct Shape {
-  static constexpr int VEC = V, LPR = L, NIT = N, ROT = T;
+  static constexpr int VEC = V, LPR = L, NIT = N, ROT = T, KIND = K;
 };
+
+// A forward kernel for each norm where a row's instructions count: the 16-byte path with a rotation in registers.
+// (131104 rows of 128, rms and rotation: 20.4 us, 23.4 us with the norm as an argument; in the backward 1 %, not worth
+// its kernels.)
+template <int LPR, int NIT, int ROT, class F>
+dsa_status_t dispatch_norm(const Rows& p, F&& f) {
+  if (p.kind == kRms) return f(Shape<8, LPR, NIT, ROT, kRms>{});
+  if (p.kind == kLayer) return f(Shape<8, LPR, NIT, ROT, kLayer>{});
+  return f(Shape<8, LPR, NIT, ROT, kNone>{});
+}
 
 // The 16-byte path with LPR lanes to a row: whole accesses are rotated where r0 and R are multiples of 8 (the tables of
 // cosines then start on 16 bytes too).
 template <int LPR, int NIT, class F>
 dsa_status_t dispatch_rotation(const Rows& p, F&& f) {
   if (p.r0 % 8 == 0 && p.R % 8 == 0) {
-    if (p.inter || p.R == 0) return f(Shape<8, LPR, NIT, kPairs>{});
-    if (p.R % 16 == 0 && p.r0 / 8 / LPR == ((p.r0 + p.R) / 8 - 1) / LPR) return f(Shape<8, LPR, NIT, kLanes>{});
+    if (p.inter || p.R == 0) return dispatch_norm<LPR, NIT, kPairs>(p, f);
+    if (p.R % 16 == 0 && p.r0 / 8 / LPR == ((p.r0 + p.R) / 8 - 1) / LPR) return dispatch_norm<LPR, NIT, kLanes>(p, f);
   }
   return f(Shape<8, LPR, NIT, kShared>{});
 }
@@ -733,8 +775,7 @@ extern "C" dsa_status_t dsa_norm_rope_fwd(const dsa_bf16_t* x, int64_t x_stride_
   const char* who = "dsa_norm_rope_fwd";
   nrope::Rows p{};
   p.x = reinterpret_cast<const __nv_bfloat16*>(x);
-  p.xs_t = x_stride_t;
-  p.xs_h = x_stride_h;
+  p.xs = nrope::step_of(x_stride_t, x_stride_h, H);
   p.T = T;
   p.H = H;
   p.D = D;
@@ -766,13 +807,13 @@ extern "C" dsa_status_t dsa_norm_rope_fwd(const dsa_bf16_t* x, int64_t x_stride_
     const int64_t most = 152 * nrope::ctas_per_sm(S::VEC, S::NIT);  // (a CTA that stays forms its table once)
     const int blocks = (int)(want < most ? want : most);
     const int smem = nrope::shared_bytes(p.R, GPB, U);
-    dsa_status_t ok_smem = nrope::allow_shared(
-        reinterpret_cast<const void*>(nrope::norm_rope_fwd_kernel<S::VEC, S::LPR, S::NIT, S::ROT, U>), smem, 0);
+    auto kernel = out_rows ? nrope::norm_rope_fwd_kernel<S::VEC, S::LPR, S::NIT, S::ROT, U, S::KIND, true>
+                           : nrope::norm_rope_fwd_kernel<S::VEC, S::LPR, S::NIT, S::ROT, U, S::KIND, S::KIND == nrope::kAny>;
+    dsa_status_t ok_smem = nrope::allow_shared(reinterpret_cast<const void*>(kernel), smem, 0);
     if (ok_smem != DSA_OK) return ok_smem;
-    nrope::norm_rope_fwd_kernel<S::VEC, S::LPR, S::NIT, S::ROT, U>
-        <<<blocks, nrope::kThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(
-            p, reinterpret_cast<__nv_bfloat16*>(out), out_stride_t, out_stride_h, out_rows, num_out_rows,
-            reinterpret_cast<int*>(workspace));
+    kernel<<<blocks, nrope::kThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(
+        p, reinterpret_cast<__nv_bfloat16*>(out), nrope::step_of(out_stride_t, out_stride_h, H), out_rows, num_out_rows,
+        reinterpret_cast<int*>(workspace));
     return cuda_check(cudaGetLastError(), "launching norm_rope_fwd_kernel");
   });
   return st == DSA_OK ? ok() : st;
@@ -793,8 +834,7 @@ extern "C" dsa_status_t dsa_norm_rope_bwd(const dsa_bf16_t* dout, int64_t dout_s
   const char* who = "dsa_norm_rope_bwd";
   nrope::Rows p{};
   p.x = reinterpret_cast<const __nv_bfloat16*>(x);
-  p.xs_t = x_stride_t;
-  p.xs_h = x_stride_h;
+  p.xs = nrope::step_of(x_stride_t, x_stride_h, H);
   p.T = T;
   p.H = H;
   p.D = D;
@@ -831,12 +871,13 @@ extern "C" dsa_status_t dsa_norm_rope_bwd(const dsa_bf16_t* dout, int64_t dout_s
       const int most = partials ? nrope::kMaxPartials : 152 * 4;
       blocks = (int)(want < most ? want : most);
       const int smem = nrope::shared_bytes(p.R, GPB, U);
-      dsa_status_t ok_smem = nrope::allow_shared(
-          reinterpret_cast<const void*>(nrope::norm_rope_bwd_kernel<S::VEC, S::LPR, S::NIT, S::ROT, U>), smem, 8192);
+      auto kernel = nrope::norm_rope_bwd_kernel<S::VEC, S::LPR, S::NIT, S::ROT, U>;
+      dsa_status_t ok_smem = nrope::allow_shared(reinterpret_cast<const void*>(kernel), smem, 8192);
       if (ok_smem != DSA_OK) return ok_smem;
-      nrope::norm_rope_bwd_kernel<S::VEC, S::LPR, S::NIT, S::ROT, U><<<blocks, nrope::kThreads, smem, s>>>(
-          p, reinterpret_cast<const __nv_bfloat16*>(dout), dout_stride_t, dout_stride_h,
-          reinterpret_cast<__nv_bfloat16*>(dx), dx_stride_t, dx_stride_h, partials);
+      kernel<<<blocks, nrope::kThreads, smem, s>>>(p, reinterpret_cast<const __nv_bfloat16*>(dout),
+                                                   nrope::step_of(dout_stride_t, dout_stride_h, H),
+                                                   reinterpret_cast<__nv_bfloat16*>(dx),
+                                                   nrope::step_of(dx_stride_t, dx_stride_h, H), partials);
       return cuda_check(cudaGetLastError(), "launching norm_rope_bwd_kernel");
     });
     if (st != DSA_OK) return st;
