@@ -7,8 +7,9 @@
 namespace dsa {
 
 // A value that is the same in all lanes, in a register of the whole warp.  The loops that issue MMAs run on such
-// counters: only then are the MMAs' descriptors kept in registers of the warp, and an MMA (M = 64, N = 64) is issued
-// every 33 cycles instead of every 60 to 80.
+// counters: only then are the MMAs' descriptors kept in registers of the warp.  An MMA (M = 64, N = 64) alone on the SM
+// is then issued every 33 cycles, which is what it takes, instead of every 60 to 80; next to the other roles of the
+// attention over the paged cache every 45.
 __device__ __forceinline__ int warp_value(int v) { return (int)__reduce_max_sync(0xffffffffu, (unsigned)v); }
 
 // Four MMAs on consecutive 16-element steps of K (the descriptors step by SA and SB), issued by one elected lane: the

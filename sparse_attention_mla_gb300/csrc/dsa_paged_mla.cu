@@ -5,7 +5,7 @@
 // before, or the ones of its list),  lse = ln sum e^{z_p},
 // out = sum e^{z_p - lse} kv_p[0:512].  One latent row serves all heads, so the
 // floor is one read of every visible row; at 64 heads the tensor core needs about
-// three quarters of the time that DRAM needs for a tile, at 128 it is the bound.
+// three quarters of the time that DRAM needs for a tile (2340 of 3135 cycles).
 //
 // Split: the (token, head) rows of a request that share its cache are packed into
 // groups of NH = 16 or 64 MMA columns; a group's positions are cut into tiles of 64,
@@ -19,14 +19,23 @@
 // A tile: S^T[key, row] = KV Q^T (M = 64 keys), an online softmax with a lazily
 // raised maximum, O^T[channel, row] += V^T P^T (M = 128 channels), P as bf16 hi + lo
 // side by side on the N axis, so that O keeps about fp32 accuracy (P in bf16 alone
-// would add as much error as the output's own rounding).  Rows are copied by 16-byte
-// cp.async, which takes any page size and order and zero-fills what is masked (no
-// stale page, NaN included, reaches a product).
+// would add as much error as the output's own rounding).  Rows that follow one another
+// in whole pages come by TMA, 32 rows of 64 channels a copy; lists, other page sizes and
+// a request's end by 16-byte cp.async, which takes any row and zero-fills what is masked
+// (no stale page, NaN included, reaches a product).
 //
 // Warps: 0 issues S^T, 1-8 softmax and epilogue, 9-12 copy tiles into a ring, 13
-// issues P.V, 14 announces the runs of tiles (segments) that the CTA's range consists of.  At width 576 and NH = 64 the ring's two tiles, Q and P need all the
-// shared memory: P^T lies over the tile's last chunk (positions, read only by S^T)
-// and an 8 KiB block that the two tiles share.
+// issues P.V, 14 announces the runs of tiles (segments) that the CTA's range consists
+// of.  At width 576 and NH = 64 the ring's two tiles, Q and P need all the shared
+// memory: P^T lies over the tile's last chunk (positions, read only by S^T) and an
+// 8 KiB block that the two tiles share.
+//
+// Measured: 674,000 positions of 64 requests, 64 heads, 175 us (4.4 TB/s); 131072
+// positions, two tokens of 128 heads, 126 us (four groups of rows, each reading the cache,
+// three times of four from L2); 48 lists of 2048 rows 66 us; 1000 positions, 16 heads, 15 us.
+// What bounds it: a tile passes its copy (1350 cycles, as fast as an SM takes one), S^T
+// (1700), the softmax (1600) and P.V (1200) one after the other, and shared memory holds two,
+// so that a tile takes 3650 cycles; the two kernels' starts and the join are 20 us on top.
 #include <cmath>
 
 #include "dsa_host.h"
