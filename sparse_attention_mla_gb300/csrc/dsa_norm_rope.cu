@@ -33,6 +33,7 @@
 #include <type_traits>
 
 #include "dsa_device.cuh"
+#include "dsa_f32x2.cuh"
 #include "dsa_host.h"
 
 namespace dsa {
@@ -67,29 +68,6 @@ struct Rows {
   float rscale;
   int rows, run;  // T * H; consecutive rows of a group of lanes (a multiple of U)
 };
-
-// Two fp32 operations in one instruction, each rounded as the scalar one.
-__device__ __forceinline__ uint64_t pack2(float2 a) {
-  return (uint64_t)__float_as_uint(a.x) | ((uint64_t)__float_as_uint(a.y) << 32);
-}
-__device__ __forceinline__ float2 unpack2(uint64_t r) {
-  return make_float2(__uint_as_float((uint32_t)r), __uint_as_float((uint32_t)(r >> 32)));
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
-  return unpack2(r);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
-  return unpack2(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)), "l"(pack2(c)));
-  return unpack2(r);
-}
 
 __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }

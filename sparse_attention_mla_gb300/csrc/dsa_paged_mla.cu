@@ -38,6 +38,7 @@
 // so that a tile takes 3650 cycles; the two kernels' starts and the join are 20 us on top.
 #include <cmath>
 
+#include "dsa_f32x2.cuh"
 #include "dsa_host.h"
 #include "dsa_paged.cuh"
 
@@ -675,7 +676,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
       return v[0];
     };
     const int sum_row = n0 + (((lane >> 1) & 14) | (lane & 1)) % NQ;
-    auto m_use = [](float m) { return fmaxf(m, -3.0e38f); };  // (a row without a finite score: e^-inf is 0 all the same)
     Seg sg, nx;
     bool aborted = !read_seg(0, sg);
     if (!aborted) load_q(sg);
@@ -686,9 +686,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
       bool bad_seg = more && !read_seg(seg, nx);
       // this thread's first row: its token in the group, and how many rows of that token there are from it on
       const int tok0 = (sg.head0 + n0) / p.H, head_left = p.H - ((sg.head0 + n0) - tok0 * p.H);
-      float l_part[NQ], m_run[NQ];  // sum and running maximum (log2 units) of this thread's rows
+      // sums and minus the running maxima (log2 units) of this thread's rows, in pairs; a row without a finite score yet
+      // has a maximum of -3e38, which any finite score passes and which leaves e^-inf at 0
+      float2 l_part[NQ / 2], m_neg[NQ / 2];
 #pragma unroll
-      for (int j = 0; j < NQ; ++j) { l_part[j] = 0.f; m_run[j] = -INFINITY; }
+      for (int j = 0; j < NQ / 2; ++j) { l_part[j] = make_float2(0.f, 0.f); m_neg[j] = make_float2(3.0e38f, 3.0e38f); }
       if (qd == 0 && lane < NHH) s_stat[ch * NHH + lane] = -INFINITY;  // (read only after a barrier of the half)
       const int t_end = sg.t0 + sg.n;
 #pragma unroll 1
@@ -728,11 +730,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
             if (--left == 0) { left = p.H; ++seen; }
           }
         }
+        // the exponents; a score may pass its row's maximum by the threshold
+        const float2 scale = make_float2(p.sl2e, p.sl2e);
+        float2 e[NQ / 2];
         bool mine = t == sg.t0;
-        if (!mine) {
-          // a score passes its row's maximum by the threshold (a row without a finite score yet counts)
 #pragma unroll
-          for (int j = 0; j < NQ; ++j) mine |= fmaf(z[j], p.sl2e, -m_run[j]) > kRaise;
+        for (int j = 0; j < NQ / 2; ++j) {
+          e[j] = fma2(make_float2(z[2 * j], z[2 * j + 1]), scale, m_neg[j]);
+          mine |= e[j].x > kRaise || e[j].y > kRaise;
         }
         bool raise = false;
         if (named_bar_or(bar_id, 128, mine || bad)) {
@@ -754,9 +759,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
           }
           named_bar(bar_id, 128);
 #pragma unroll
-          for (int j = 0; j < NQ; ++j) {
-            l_part[j] *= s_fac[n0 + j];
-            m_run[j] = s_stat[n0 + j];
+          for (int j = 0; j < NQ / 2; ++j) {
+            l_part[j] = mul2(l_part[j], make_float2(s_fac[n0 + 2 * j], s_fac[n0 + 2 * j + 1]));
+            m_neg[j] = make_float2(-fmaxf(s_stat[n0 + 2 * j], -3.0e38f), -fmaxf(s_stat[n0 + 2 * j + 1], -3.0e38f));
+            e[j] = fma2(make_float2(z[2 * j], z[2 * j + 1]), scale, m_neg[j]);
           }
           if (t > sg.t0) {
             const bool okw = wait_pv(i - 1, 3);
@@ -778,15 +784,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
         }
         uint32_t hi[NQ / 2], lo[NQ / 2];
 #pragma unroll
-        for (int j = 0; j < NQ; j += 2) {
-          const float pa = ex2(fmaf(z[j], p.sl2e, -m_use(m_run[j])));
-          const float pb = ex2(fmaf(z[j + 1], p.sl2e, -m_use(m_run[j + 1])));
-          l_part[j] += pa;
-          l_part[j + 1] += pb;
-          const __nv_bfloat162 h2 = __floats2bfloat162_rn(pa, pb);
-          const float2 hf = __bfloat1622float2(h2);
-          hi[j / 2] = *reinterpret_cast<const uint32_t*>(&h2);
-          lo[j / 2] = pack_bf16x2(pa - hf.x, pb - hf.y);
+        for (int j = 0; j < NQ / 2; ++j) {
+          const float2 w = make_float2(ex2(e[j].x), ex2(e[j].y));
+          l_part[j] = add2(l_part[j], w);
+          hi[j] = pack_bf16x2(w.x, w.y);
+          const float2 rest = add2(w, make_float2(__uint_as_float((hi[j] << 16) ^ 0x80000000u),
+                                                  __uint_as_float((hi[j] & 0xffff0000u) ^ 0x80000000u)));
+          lo[j] = pack_bf16x2(rest.x, rest.y);
         }
         if (L::OVERLAY && i >= 1) {
           if (!wait_pv(i - 1, 3)) bad = true;  // (the store below then goes unused: no product is formed after an abort)
@@ -819,7 +823,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
       }
       if (aborted) break;
       // ---- the segment's rows: out and lse, or the workspace's partial sums ----
-      s_red[qd * NH + sum_row] = over_keys(l_part, false);
+      float sums[NQ];
+#pragma unroll
+      for (int j = 0; j < NQ / 2; ++j) { sums[2 * j] = l_part[j].x; sums[2 * j + 1] = l_part[j].y; }
+      s_red[qd * NH + sum_row] = over_keys(sums, false);
       named_bar(bar_id, 128);
       const bool whole = sg.whole;
       const int slot = 2 * blockIdx.x + (sg.opens ? 1 : 0);
