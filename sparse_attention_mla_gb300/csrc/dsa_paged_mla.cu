@@ -897,52 +897,56 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
 }
 
 // Joins the pieces of the groups that went over several CTAs.  A row of few pieces is a team's of 128 threads, 4 channels
-// each; a row of many (one long request over the whole card) is a CTA's, whose eight teams take every eighth piece, so
-// that 152 pieces are 19 loads deep.  Pieces are added in a fixed order, whichever came first.
-constexpr int kJoin = 1024, kTeams = kJoin / 128, kMany = 16;
-__global__ void __launch_bounds__(kJoin) paged_mla_join_kernel(const int4* __restrict__ records, int ctas,
-                                                              const float* __restrict__ stats,
-                                                              const float* __restrict__ partial,
-                                                              const float* __restrict__ sink, int H,
-                                                              __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
+// each; a row of many (one long request over the whole card) is a CTA's, whose teams take every fourth piece.  Pieces are
+// added in a fixed order, whichever came first.  Two CTAs of 512 threads an SM, all at once: as one of 1024 (with its 64
+// registers a thread) the second half of them waited for the first, and took 7 us longer.  The records are made lists of
+// by ballots, since code that runs once costs the time to fetch it (a scan in a loop: 4 us more).
+constexpr int kJoin = 512, kTeams = kJoin / 128, kMany = 16;
+constexpr int kGroupsOf = 64 / kTeams;  // of a record's rows, a row for each team
+__global__ void __launch_bounds__(kJoin, 2) paged_mla_join_kernel(const int4* __restrict__ records, int ctas,
+                                                                 const float* __restrict__ stats,
+                                                                 const float* __restrict__ partial,
+                                                                 const float* __restrict__ sink, int H,
+                                                                 __nv_bfloat16* __restrict__ out, float* __restrict__ lse) {
   __shared__ int4 rec[kMaxCtas];
-  __shared__ int first[2][kMaxCtas + 1];  // rows before each record: of few pieces, of many
+  __shared__ int list[2][kMaxCtas];  // records of few pieces, of many
+  __shared__ int count[2][kMaxCtas / 32];
   __shared__ float fac[kMaxCtas];
   __shared__ float4 acc[kTeams][128];
   __shared__ float s_l, s_base;
   const int tid = threadIdx.x, lane = tid & 31, team = tid >> 7, x = tid & 127;
   // launched while the pieces are still being made; what the first kernel writes is read from L2, not as constant data
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (tid < ctas) rec[tid] = __ldcg(records + tid);
-  __syncthreads();
-  if (tid < 64) {
-    const int many = tid >> 5;
-    int base = 0;
-    for (int c0 = 0; c0 < ctas; c0 += 32) {
-      const int c = c0 + lane;
-      int v = 0;
-      if (c < ctas && (rec[c].w - c + 1 >= kMany) == (many == 1)) v = rec[c].y;
-      int inc = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      if (c < ctas) first[many][c] = base + inc - v;
-      base += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (lane == 0) first[many][ctas] = base;
+  unsigned mine[2] = {0, 0};
+  if (tid < kMaxCtas) {
+    const int4 rc = tid < ctas ? __ldcg(records + tid) : make_int4(0, 0, 0, 0);
+    rec[tid] = rc;
+    const bool many = rc.w - tid + 1 >= kMany;
+    mine[0] = __ballot_sync(0xffffffffu, rc.y > 0 && !many);
+    mine[1] = __ballot_sync(0xffffffffu, rc.y > 0 && many);
+    if (lane < 2) count[lane][tid >> 5] = __popc(lane ? mine[1] : mine[0]);
   }
   __syncthreads();
-  auto find = [&](const int* f, int it) -> int {  // last c with f[c] <= it: the record that holds row `it`
-    int lo = 0, hi = ctas;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (f[mid] <= it) lo = mid; else hi = mid;
+  int total[2] = {0, 0};
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    int before = 0;
+#pragma unroll
+    for (int w = 0; w < kMaxCtas / 32; ++w) {
+      before += w < (tid >> 5) ? count[m][w] : 0;
+      total[m] += count[m][w];
     }
-    return lo;
-  };
+    if ((mine[m] >> lane) & 1u) list[m][before + __popc(mine[m] & ((1u << lane) - 1u))] = tid;
+  }
+  __syncthreads();
   auto piece = [&](int lo, int k, int n) -> size_t { return (size_t)(2 * (lo + k) + (k == 0 ? 1 : 0)) * 64 + n; };
+  auto part = [&](int lo, int k, int n) { return __ldcg(reinterpret_cast<const float4*>(partial + piece(lo, k, n) * kDv) + x); };
+  auto add = [](float4& o, float f, float4 v) {
+    o.x += f * v.x;
+    o.y += f * v.y;
+    o.z += f * v.z;
+    o.w += f * v.w;
+  };
   auto store = [&](int row, float4 o, float l, float base) {
     const bool empty = l == 0.f;  // nothing is seen, and there is no sink
     const float inv = empty ? 0.f : 1.f / l;
@@ -950,15 +954,14 @@ __global__ void __launch_bounds__(kJoin) paged_mla_join_kernel(const int4* __res
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     if (x == 0) lse[row] = empty ? -INFINITY : base * kLn2 + logf(l);
   };
-  for (int it = blockIdx.x * kTeams + team; it < first[0][ctas]; it += gridDim.x * kTeams) {
-    const int lo = find(first[0], it);
+  for (int it = blockIdx.x; it < total[0] * kGroupsOf; it += gridDim.x) {
+    const int lo = list[0][it / kGroupsOf];
     const int4 rc = rec[lo];
-    const int n = it - first[0][lo], pieces = rc.w - lo + 1;
-    const float* src = partial;
+    const int n = it % kGroupsOf * kTeams + team, pieces = rc.w - lo + 1;
+    if (n >= rc.y) continue;
     float4 v[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      v[k] = k < pieces ? __ldcg(reinterpret_cast<const float4*>(src + piece(lo, k, n) * kDv) + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < 4; ++k) v[k] = k < pieces ? part(lo, k, n) : make_float4(0.f, 0.f, 0.f, 0.f);
     // lane k holds piece k's maximum and sum
     const size_t at = lane < pieces ? piece(lo, lane, n) : 0;
     const float mc = lane < pieces ? __ldcg(stats + at / 64 * 128 + n) : -INFINITY;
@@ -979,23 +982,22 @@ __global__ void __launch_bounds__(kJoin) paged_mla_join_kernel(const int4* __res
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if (k0 + k < pieces) {
-          const float w = __shfl_sync(0xffffffffu, f, k0 + k);
-          o.x += w * v[k].x;
-          o.y += w * v[k].y;
-          o.z += w * v[k].z;
-          o.w += w * v[k].w;
-          if (k0 + 4 + k < pieces) v[k] = __ldcg(reinterpret_cast<const float4*>(src + piece(lo, k0 + 4 + k, n) * kDv) + x);
+          add(o, __shfl_sync(0xffffffffu, f, k0 + k), v[k]);
+          if (k0 + 4 + k < pieces) v[k] = part(lo, k0 + 4 + k, n);
         }
       }
     }
     store(rc.x + n, o, l, base);
   }
-  for (int it = blockIdx.x; it < first[1][ctas]; it += gridDim.x) {
-    const int lo = find(first[1], it);
+  for (int it = blockIdx.x; it < total[1] * 64; it += gridDim.x) {
+    const int lo = list[1][it / 64];
     const int4 rc = rec[lo];
-    const int n = it - first[1][lo], pieces = rc.w - lo + 1;
+    const int n = it % 64, pieces = rc.w - lo + 1;
+    if (n >= rc.y) continue;
     // the first pieces' channels are on their way while the maxima are compared
-    float4 v = __ldcg(reinterpret_cast<const float4*>(partial + piece(lo, team, n) * kDv) + x);  // (kMany >= kTeams)
+    float4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = part(lo, team + j * kTeams, n);  // (kMany >= 4 kTeams)
     if (tid < 32) {
       const float s2 = sink ? __ldg(sink + (rc.z + n) % H) * kLog2e : -INFINITY;
       float mc[kMaxCtas / 32], lc[kMaxCtas / 32], m = s2;
@@ -1026,32 +1028,27 @@ __global__ void __launch_bounds__(kJoin) paged_mla_join_kernel(const int4* __res
     }
     __syncthreads();
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = team; k < pieces; k += kTeams) {
-      float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (k + kTeams < pieces) w = __ldcg(reinterpret_cast<const float4*>(partial + piece(lo, k + kTeams, n) * kDv) + x);
-      const float f = fac[k];
-      o.x += f * v.x;
-      o.y += f * v.y;
-      o.z += f * v.z;
-      o.w += f * v.w;
-      v = w;
+    for (int k0 = team; k0 < pieces; k0 += 4 * kTeams) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = k0 + j * kTeams;
+        if (k < pieces) {
+          add(o, fac[k], v[j]);
+          if (k + 4 * kTeams < pieces) v[j] = part(lo, k + 4 * kTeams, n);
+        }
+      }
     }
     acc[team][x] = o;
     __syncthreads();
     if (team == 0) {
 #pragma unroll
-      for (int k = 1; k < kTeams; ++k) {
-        const float4 w = acc[k][x];
-        o.x += w.x;
-        o.y += w.y;
-        o.z += w.z;
-        o.w += w.w;
-      }
+      for (int k = 1; k < kTeams; ++k) add(o, 1.f, acc[k][x]);
       store(rc.x + n, o, s_l, s_base);
     }
     __syncthreads();
   }
 }
+static_assert(kMany >= 4 * kTeams && kMany <= 16 && 64 % kTeams == 0, "join: pieces and rows");
 
 constexpr size_t kRecordBytes = kMaxCtas * sizeof(int4);
 constexpr size_t kStatBytes = (size_t)2 * kMaxCtas * 128 * sizeof(float);
