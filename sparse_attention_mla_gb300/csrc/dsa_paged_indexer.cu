@@ -18,7 +18,7 @@
 // bins through distributed shared memory (one cluster barrier a histogram); then
 // one ordered compaction.  What bounds it is that chain of barriers, not its work;
 // it is launched early and looks its request up while the scores are being made.
-// Measured: one request of 65536 keys 24 us (two starts and the selection's chain),
+// Measured: one request of 65536 keys 21 us (two starts and the selection's chain),
 // 678,000 keys of 32 requests 51 us, of which the scores are 39 (4.4 TB/s).
 // Every step is exact and without order effects, so equal calls give equal lists.
 #include <cooperative_groups.h>
@@ -495,13 +495,16 @@ __global__ void __launch_bounds__(kSel, 1)
   // this CTA's piece of the row, a multiple of 4 so that the 16-byte loads stay aligned
   const int piece = ((v + CS - 1) / CS + 3) & ~3;
   const int begin = min(v, rank * piece), end = min(v, begin + piece);
-  const int rounds = (end - begin + kRound - 1) / kRound;
+  // scores of a thread and round, four at a time: a short piece is spread over all threads
+  const int per = min(kPer, (piece + 4 * kSel - 1) / (4 * kSel) * 4), round = per * kSel;
+  const int rounds = (end - begin + round - 1) / round;
   const float* row = scores + (size_t)n * stride;
   uint32_t key[kPer];
   auto load = [&](int r) {
-    const int p0 = begin + r * kRound + tid * kPer;
+    const int p0 = begin + r * round + tid * per;
 #pragma unroll
     for (int j = 0; j < kPer; j += 4) {
+      if (j >= per) continue;
       const int q = p0 + j;
       float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
       if (q < end) f = *reinterpret_cast<const float4*>(row + q);  // (the row's stride is a multiple of 4)
@@ -525,6 +528,7 @@ __global__ void __launch_bounds__(kSel, 1)
     if (rounds > 1) load(r);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
+      if (j / 4 * 4 >= per) continue;
       if (key[j]) mn = min(mn, key[j]);
       mx = max(mx, key[j]);
     }
@@ -561,6 +565,7 @@ __global__ void __launch_bounds__(kSel, 1)
       if (rounds > 1) load(r);
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
+        if (j / 4 * 4 >= per) continue;
         const uint32_t d = key[j] ^ prefix;
         if (key[j] && (bit == 32 || (d >> bit) == 0u)) atomicAdd(&h[(key[j] >> shift) & mask], 1u);
       }
@@ -609,6 +614,7 @@ __global__ void __launch_bounds__(kSel, 1)
     uint32_t c = 0;  // above, and tied from bit 16 (a round holds 16384)
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
+      if (j / 4 * 4 >= per) continue;
       const uint32_t k = key[j] >> bit, q = prefix >> bit;  // (bit < 32: a histogram or equal scores)
       c += k > q ? 1u : (k == q && key[j] ? 0x10000u : 0u);
     }
@@ -617,9 +623,10 @@ __global__ void __launch_bounds__(kSel, 1)
     const uint32_t before = block_scan(c, reinterpret_cast<uint32_t*>(sh[0]) + 32 * (r & 1), sum);
     uint32_t my_tied = tied + (before >> 16);
     uint32_t o = at + (before & 0xffffu) + (min(my_tied, (uint32_t)need) - min(tied, (uint32_t)need));
-    const int p0 = begin + r * kRound + tid * kPer;
+    const int p0 = begin + r * round + tid * per;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
+      if (j / 4 * 4 >= per) continue;
       const uint32_t k = key[j] >> bit, q = prefix >> bit;
       bool take = k > q;
       if (key[j] && k == q) {
@@ -636,12 +643,13 @@ __global__ void __launch_bounds__(kSel, 1)
 
 inline long long stride_of(long long max_len) { return (max_len + 3) / 4 * 4; }
 
-// CTAs per token: a round of 16 scores a thread covers a piece while the row is up to 131072 long; twice that
-// many CTAs while they all fit the card at once.
+// CTAs per token: as many as hold the row in one round, up to 8; and up to 4 while a piece is longer than 8192 and all
+// CTAs fit the card at once (8 x 32768: 25.0 us with 4, 26.8 with 2; 1 x 65536: 20.7 with 4, 21.7 with 8, whose cluster
+// barriers cost more than the shorter pieces save).
 inline int cluster_of(int N, long long max_len) {
   int cs = 1;
   while (cs < 8 && (long long)cs * kRound < max_len) cs *= 2;
-  while (cs < 8 && (long long)cs * 4096 < max_len && (long long)N * cs * 2 <= 152) cs *= 2;
+  while (cs < 4 && (long long)cs * 8192 < max_len && (long long)N * cs * 2 <= 152) cs *= 2;
   return cs;
 }
 
