@@ -30,12 +30,13 @@
 // memory: P^T lies over the tile's last chunk (positions, read only by S^T) and an
 // 8 KiB block that the two tiles share.
 //
-// Measured: 674,000 positions of 64 requests, 64 heads, 175 us (4.4 TB/s); 131072
-// positions, two tokens of 128 heads, 126 us (four groups of rows, each reading the cache,
-// three times of four from L2); 48 lists of 2048 rows 66 us; 1000 positions, 16 heads, 15 us.
+// Measured: 674,000 positions of 64 requests, 64 heads, 170 us (4.6 TB/s); 131072
+// positions, two tokens of 128 heads, 120 us (four groups of rows, each reading the cache,
+// three times of four from L2); 48 lists of 2048 rows 62 us; 1000 positions, 16 heads, 14 us.
 // What bounds it: a tile passes its copy (1350 cycles, as fast as an SM takes one), S^T
 // (1700), the softmax (1600) and P.V (1200) one after the other, and shared memory holds two,
-// so that a tile takes 3650 cycles; the two kernels' starts and the join are 20 us on top.
+// so that a tile takes 3600 cycles; the start (12 us to the first softmax), the end of a group
+// (5 us) and the join (6 to 9 us) come on top.
 #include <cmath>
 
 #include "dsa_f32x2.cuh"
