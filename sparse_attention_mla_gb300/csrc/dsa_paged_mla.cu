@@ -867,17 +867,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
           tmem_ld8(tl, ol);
         }
         tmem_ld_wait();
-        const int c = mt * 128 + qd * 32 + lane;
-        float* part = p.partial + ((size_t)slot * 64 + h0) * kDv + c;
-        __nv_bfloat16* dst = p.out + (size_t)(sg.row0 + h0) * kDv + c;
+        const int c = mt * 128 + qd * 32 + lane, rows = sg.rows - h0;
+        float o[kStep];
 #pragma unroll
-        for (int h = 0; h < kStep; ++h) {
-          const float o = __uint_as_float(oh[h]) + (split ? __uint_as_float(ol[h]) : 0.f);
-          if (h0 + h < sg.rows) {
-            const float f = s_fac[h0 + h];
-            if (whole) dst[h * kDv] = __float2bfloat16_rn(f == 0.f ? 0.f : o * f);
-            else part[h * kDv] = o;
-          }
+        for (int h = 0; h < kStep; ++h) o[h] = __uint_as_float(oh[h]) + (split ? __uint_as_float(ol[h]) : 0.f);
+        // (one branch for all rows: with one for each, every store waits for the one before, 66 cycles in place of 5)
+        if (whole) {
+          __nv_bfloat16* dst = p.out + (size_t)(sg.row0 + h0) * kDv + c;
+          float f[kStep];
+#pragma unroll
+          for (int h = 0; h < kStep; ++h) f[h] = s_fac[h0 + h];
+#pragma unroll
+          for (int h = 0; h < kStep; ++h)
+            if (h < rows) dst[h * kDv] = __float2bfloat16_rn(f[h] == 0.f ? 0.f : o[h] * f[h]);
+        } else {
+          float* part = p.partial + ((size_t)slot * 64 + h0) * kDv + c;
+#pragma unroll
+          for (int h = 0; h < kStep; ++h)
+            if (h < rows) part[h * kDv] = o[h];
         }
       }
       tc_fence_before();
