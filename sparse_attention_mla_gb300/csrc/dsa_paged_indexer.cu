@@ -628,12 +628,10 @@ __global__ void __launch_bounds__(kSel, 1)
     for (int j = 0; j < kPer; ++j) {
       if (j / 4 * 4 >= per) continue;
       const uint32_t k = key[j] >> bit, q = prefix >> bit;
-      bool take = k > q;
-      if (key[j] && k == q) {
-        take = my_tied < (uint32_t)need;
-        ++my_tied;
-      }
-      if (take) out[o++] = p0 + j;
+      const bool tie = key[j] && k == q, take = k > q || (tie && my_tied < (uint32_t)need);
+      my_tied += tie ? 1u : 0u;
+      if (take) out[o] = p0 + j;
+      o += take ? 1u : 0u;
     }
     at += (sum & 0xffffu) + (min(tied + (sum >> 16), (uint32_t)need) - min(tied, (uint32_t)need));
     tied += sum >> 16;
