@@ -559,15 +559,15 @@ __global__ void __launch_bounds__(kSel, 1)
   bool all = false;                         // every score that shares the prefix is taken
   for (int pass = 0; bit > 0 && !all; ++pass) {
     const int shift = max(0, bit - 11);
-    const uint32_t mask = (1u << (bit - shift)) - 1u;
+    const uint32_t span = bit == 32 ? 0xffffffffu : (1u << bit) - 1u;
     uint32_t* h = hist[pass & 1];
     for (int r = 0; r < rounds; ++r) {
       if (rounds > 1) load(r);
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         if (j / 4 * 4 >= per) continue;
-        const uint32_t d = key[j] ^ prefix;
-        if (key[j] && (bit == 32 || (d >> bit) == 0u)) atomicAdd(&h[(key[j] >> shift) & mask], 1u);
+        const uint32_t d = key[j] - prefix;  // (below 2^bit: the prefix is shared)
+        if (key[j] && d <= span) atomicAdd(&h[d >> shift], 1u);
       }
     }
     if constexpr (CS > 1) cl.sync(); else __syncthreads();
@@ -607,28 +607,30 @@ __global__ void __launch_bounds__(kSel, 1)
   }
   // (no CTA leaves while another may still read its shared memory; the last such reads are behind us)
   if constexpr (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  // taken: above the prefix's class, and the first `need` of the class in order of position
+  // taken: above the prefix's class, and the first `need` of the class in order of position (few of a thread's scores:
+  // one bit each, and the bits that are set are walked)
   at += min(tied, (uint32_t)need);
+  const uint32_t low = max(prefix, 1u), top = prefix + ((1u << bit) - 1u);  // (bit < 32: a histogram or equal scores)
   for (int r = 0; r < rounds; ++r) {
     if (rounds > 1) load(r);
-    uint32_t c = 0;  // above, and tied from bit 16 (a round holds 16384)
+    uint32_t above = 0, same = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       if (j / 4 * 4 >= per) continue;
-      const uint32_t k = key[j] >> bit, q = prefix >> bit;  // (bit < 32: a histogram or equal scores)
-      c += k > q ? 1u : (k == q && key[j] ? 0x10000u : 0u);
+      above |= key[j] > top ? 1u << j : 0u;
+      same |= key[j] >= low ? 1u << j : 0u;
     }
-    uint32_t sum;
+    same &= ~above;
+    uint32_t sum;  // above, and tied from bit 16 (a round holds 16384)
     if (r) __syncthreads();
-    const uint32_t before = block_scan(c, reinterpret_cast<uint32_t*>(sh[0]) + 32 * (r & 1), sum);
+    const uint32_t before = block_scan((uint32_t)__popc(above) + ((uint32_t)__popc(same) << 16),
+                                       reinterpret_cast<uint32_t*>(sh[0]) + 32 * (r & 1), sum);
     uint32_t my_tied = tied + (before >> 16);
     uint32_t o = at + (before & 0xffffu) + (min(my_tied, (uint32_t)need) - min(tied, (uint32_t)need));
     const int p0 = begin + r * round + tid * per;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (j / 4 * 4 >= per) continue;
-      const uint32_t k = key[j] >> bit, q = prefix >> bit;
-      const bool tie = key[j] && k == q, take = k > q || (tie && my_tied < (uint32_t)need);
+    for (uint32_t left = above | same; left != 0u; left &= left - 1u) {
+      const int j = __ffs(left) - 1;
+      const bool tie = (same >> j) & 1u, take = !tie || my_tied < (uint32_t)need;
       my_tied += tie ? 1u : 0u;
       if (take) out[o] = p0 + j;
       o += take ? 1u : 0u;
