@@ -10,7 +10,8 @@
 // Split: the (token, head) rows of a request that share its cache are packed into
 // groups of NH = 16 or 64 MMA columns; a group's positions are cut into tiles of 64,
 // and the tiles of all groups, laid end to end, are cut into equal ranges, one per
-// CTA (one CTA per SM).  Every CTA finds its range from the lengths on the device
+// CTA (one CTA per SM); a group's end, in which no tile is copied, counts as some tiles.
+// Every CTA finds its range from the lengths on the device
 // (a sum over the requests), so no plan is made on the host and a captured step
 // follows the lengths.  A group inside one range is finished there; the pieces of
 // a group over several CTAs go to the workspace as (max, sum, unnormalised O) in
@@ -30,13 +31,14 @@
 // memory: P^T lies over the tile's last chunk (positions, read only by S^T) and an
 // 8 KiB block that the two tiles share.
 //
-// Measured: 674,000 positions of 64 requests, 64 heads, 170 us (4.6 TB/s); 131072
-// positions, two tokens of 128 heads, 120 us (four groups of rows, each reading the cache,
-// three times of four from L2); 48 lists of 2048 rows 62 us; 1000 positions, 16 heads, 14 us.
+// Measured: 674,000 positions of 64 requests, 64 heads, 159 us (4.9 TB/s); 131072
+// positions, two tokens of 128 heads, 117 us (four groups of rows, each reading the cache,
+// three times of four from L2); 48 lists of 2048 rows 55 us; 1000 positions, 16 heads, 13 us.
 // What bounds it: a tile passes its copy (1350 cycles, as fast as an SM takes one), S^T
 // (1700), the softmax (1600) and P.V (1200) one after the other, and shared memory holds two,
 // so that a tile takes 3600 cycles; the start (12 us to the first softmax), the end of a group
-// (5 us) and the join (6 to 9 us) come on top.
+// and the join (6 us) come on top.
+#include <climits>
 #include <cmath>
 
 #include "dsa_f32x2.cuh"
@@ -117,6 +119,7 @@ struct Params {
   const int32_t* topk_len;
   int N, B, H, K, num_pages, P, max_pages;
   int G, HB;  // tokens per group, head blocks
+  int extra;  // tiles that the end of a group counts as when the line is cut
   int box;    // rows of a TMA box (32 or a smaller page), 0: every row by cp.async
   float sl2e;
   const float* sink;
@@ -169,7 +172,8 @@ __device__ __forceinline__ Unit unit_of(const Params& p, int u) {
 struct Plan {
   long long w0, w1;  // this CTA's tiles of the whole line
   Unit un;
-  int u, g, t;       // unit, group and tile of tile w0
+  int u, g, t;       // unit, group and tile of the first tile
+  int skip;          // what lies before it: the end of a group
 };
 
 // A run of tiles [t0, t0 + n) of one group, as announced (two int4).
@@ -178,6 +182,7 @@ struct Seg {
   int row0;           // first row (token, head) of q, out and lse
   int rows, head0;    // rows; head of the first row
   bool whole, opens;  // all tiles of the group; its first one among them
+  bool last;          // the CTA's last run
   int b;              // request
   int seen0;          // positions that the group's first token sees (may be <= 0)
   int keys;           // positions looked at by any token, or entries of the list
@@ -192,6 +197,7 @@ __device__ __forceinline__ Seg unpack(const int4 a, const int4 c) {
   s.rows = a.w & 255;
   s.whole = a.w & 256;
   s.opens = a.w & 512;
+  s.last = a.w & 1024;
   s.head0 = c.w;
   s.b = c.x;
   s.seen0 = c.y;
@@ -216,7 +222,7 @@ __device__ __noinline__ bool read_announcement(uint32_t misc, const int4* ring, 
 __device__ __forceinline__ void announce(const Params& p, const Plan& pl, uint32_t full, uint32_t empty, int4* ring,
                                          volatile int* abort) {
   const int lane = threadIdx.x & 31;
-  long long left = pl.w1 - pl.w0;
+  long long left = pl.w1 - pl.w0 - pl.skip;
   int u = pl.u, g = pl.g, t = pl.t;
   Unit un = pl.un;
   bool cut = false;
@@ -235,6 +241,9 @@ __device__ __forceinline__ void announce(const Params& p, const Plan& pl, uint32
     a.z = n0 * p.H + hb * 64;
     a.w = (p.HB > 1 ? min(64, p.H - hb * 64) : min(p.G, un.n - tb * p.G) * p.H) | (t == 0 ? 512 : 0) |
           (t == 0 && a.y == un.tiles ? 256 : 0);
+    t += a.y;
+    left -= a.y + (t >= un.tiles ? p.extra : 0);
+    a.w |= left <= 0 ? 1024 : 0;
     c.x = u;
     c.y = un.len - un.n + tb * p.G + 1;
     c.z = un.keys;
@@ -258,8 +267,6 @@ __device__ __forceinline__ void announce(const Params& p, const Plan& pl, uint32
       ring[2 * at + 1] = c;
       mbar_arrive(full + 8 * at);
     }
-    left -= a.y;
-    t += a.y;
     if (t >= un.tiles) { ++g; t = 0; }
   }
   if (cut && lane == 0) record_error(p.err, DSA_ERR_DEVICE_INDEX);  // the table does not hold a request
@@ -271,22 +278,30 @@ __device__ __forceinline__ void make_plan(const Params& p, Plan* plan, long long
   if (threadIdx.x == 0) p.records[blockIdx.x] = make_int4(0, 0, 0, 0);
   auto tiles_of = [&](int u) -> long long {
     const Unit x = unit_of(p, u);
-    return (long long)x.groups * x.tiles;
+    return (long long)x.groups * (x.tiles + p.extra);
   };
   auto visit = [&](const TileRange& r, int u, long long lo, long long n) {
     const bool starts = lo <= r.w0 && r.w0 < lo + n, ends = lo <= r.w1 - 1 && r.w1 - 1 < lo + n;
     if (!starts && !ends) return;
     const Unit x = unit_of(p, u);
+    const int span = x.tiles + p.extra;
     if (starts) {
       const long long first = r.w0 - lo;
+      int g = (int)(first / span), t = (int)(first - (long long)g * span);
+      plan->skip = 0;
+      if (t >= x.tiles) {
+        plan->skip = span - t;
+        ++g;
+        t = 0;
+      }
       plan->u = u;
       plan->un = x;
-      plan->g = (int)(first / x.tiles);
-      plan->t = (int)(first - (long long)plan->g * x.tiles);
+      plan->g = g;
+      plan->t = t;
     }
     if (ends) {  // the range's last tile
       const long long off = r.w1 - 1 - lo;
-      const int g = (int)(off / x.tiles), tl = (int)(off - (long long)g * x.tiles);
+      const int g = (int)(off / span), tl = (int)(off - (long long)g * span);
       const long long opened = r.w1 - 1 - tl;  // the group's first tile
       if (tl + 1 < x.tiles && opened >= r.w0) {
         const int tb = g / p.HB, hb = g - tb * p.HB;
@@ -372,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
   make_plan(p, s_plan, reinterpret_cast<long long*>(s_red));
   const Plan plan = *s_plan;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the joining kernel waits for this one's end itself)
-  if (plan.w1 <= plan.w0) return;  // (the whole CTA)
+  if (plan.w1 <= plan.w0 || plan.w1 - plan.w0 <= plan.skip) return;  // (the whole CTA)
   if (warp == 0) {
     tmem_alloc(smem_u32(s_tmem), L::TM_COLS);
     tmem_relinquish();
@@ -380,7 +395,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
   __syncthreads();
   const uint32_t tmem = (uint32_t)warp_value((int)*s_tmem);
 
-  const int n_tiles = warp_value((int)(plan.w1 - plan.w0));
   // announcement k, once per warp
   auto read_seg = [&](int k, Seg& s) -> bool {
     return read_announcement(mb, reinterpret_cast<const int4*>(misc + M_SEG), k, s_abort, p.wait_limit, s);
@@ -389,9 +403,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
     // ======================= S^T issuer =======================
     constexpr uint32_t kIdS = idesc_bf16(kTile, NH, false, false);
     int done = 0;
-    for (int seg = 0; done < n_tiles; ++seg) {
+    for (int seg = 0, last = 0; !last; ++seg) {
       Seg sg;
       if (!warp_all(read_seg(seg, sg))) break;
+      last = warp_value(sg.last ? 1 : 0);
       if (!warp_all(wait_for(bar_q, seg & 1, s_abort, p.wait_limit))) break;
       fence_proxy_async_smem();  // (the queries came by cp.async)
       // what the loop needs in registers of the warp (a call does not keep them)
@@ -428,9 +443,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
   } else if (warp == 13) {
     // ======================= P.V issuer =======================
     int done = 0;
-    for (int seg = 0; done < n_tiles; ++seg) {
+    for (int seg = 0, last = 0; !last; ++seg) {
       Seg sg;
       if (!warp_all(read_seg(seg, sg))) break;
+      last = warp_value(sg.last ? 1 : 0);
       const int n = warp_value(sg.n);
       const uint32_t d0 = (uint32_t)warp_value((int)tmem), kv0 = (uint32_t)warp_value((int)sKV);
       int i = warp_value(done);
@@ -483,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
     const int sl = (warp - 9) >> 1, gw = (warp - 9) & 1, uc = lane & 7;
     Seg sg;
     int seg = 0, base = 0, end = 0, limit = 0;  // this CTA's tiles [base, end) are the segment's
+    int n_tiles = INT_MAX;                      // this CTA's tiles, known once one past them has been looked for
     struct Look {
       int pos, b, limit;  // position (then its place in the page), or -1; request; what the position has to stay below
     };
@@ -492,6 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
       if (i < n_tiles && !stop) {
 #pragma unroll 1
         while (i >= end) {
+          if (seg > 0 && sg.last) { n_tiles = end; return k; }
           if (!read_seg(seg, sg)) { stop = true; return k; }
           ++seg;
           base = end;
@@ -683,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
     nx = sg;
     int i = 0;
     for (int seg = 1; !aborted; ++seg) {
-      const bool more = i + sg.n < n_tiles;
+      const bool more = !sg.last;
       bool bad_seg = more && !read_seg(seg, nx);
       // this thread's first row: its token in the group, and how many rows of that token there are from it on
       const int tok0 = (sg.head0 + n0) / p.H, head_left = p.H - ((sg.head0 + n0) - tok0 * p.H);
@@ -1077,6 +1095,9 @@ dsa_status_t launch(Params& p, const CUtensorMap& map, int ctas, cudaStream_t s)
                                           "configuring paged_mla_kernel");
   if (st != DSA_OK) return st;
   p.G = p.topk_idx ? 1 : (p.H <= NH ? NH / p.H : 1);
+  // a group's end takes 15,000 cycles: 4 tiles of whole pages, 2 of listed rows (100 requests of 3000: 72 us, 80 when the
+  // ends count for nothing; 48 lists of 2048: 55.4 and 57.5)
+  p.extra = p.topk_idx ? 2 : 4;
   p.HB = (p.H + NH - 1) / NH;
   paged_mla_kernel<DQK, NH><<<ctas, kThreads, L::TOTAL, s>>>(p, map);
   return cuda_check(cudaGetLastError(), "launching paged_mla_kernel");

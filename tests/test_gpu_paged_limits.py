@@ -104,6 +104,35 @@ def test_two_calls_at_once():
         assert all(dsa.dsa_read_device_status(w) == 0 for w in own[k])
 
 
+@pytest.mark.parametrize("lists", [False, True])
+def test_thousands_of_short_requests(lists):
+    # 20 and more groups of one or two tiles for every CTA, so that many end and open one, or lie between two ends
+    B, H, page = 3200, 3, 8
+    g = torch.Generator().manual_seed(11)
+    lens = torch.randint(0, 90, (B,), generator=g)
+    need = [-(-int(n) // page) for n in lens]
+    pool = 400  # pages that the requests share
+    table = torch.full((B, 12), -1, dtype=I32)
+    for b, k in enumerate(need):
+        table[b, :k] = torch.randint(0, pool, (k,), generator=g, dtype=I32)
+    cache = torch.randn(pool, page, 576, generator=g).bfloat16()
+    q = torch.randn(B, H, 576, generator=g).bfloat16()
+    idx = None
+    if lists:
+        idx = (torch.rand(B, 6, generator=g) * lens.clamp(min=1)[:, None]).to(I32)
+        idx[lens == 0] = -1
+    ws = spaces()[0]
+    out, lse = dsa.dsa_paged_mla(q.to(DEV), cache.to(DEV), table.to(DEV), lens.to(I32).to(DEV), 0.04, workspace=ws,
+                                 topk_idx=None if idx is None else idx.to(DEV))
+    want, want_lse = ref.paged_mla(q, cache, table.tolist(), lens.tolist(), list(range(B + 1)), 0.04, page, None, idx)
+    out, lse = out.cpu().double(), lse.cpu().double()
+    # half a bf16 step for the rounding; scores in fp32 and weights as hi + lo: 2^-13 of the largest value
+    assert bool(((out - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -13 * 5.0).all())
+    seen = ~torch.isinf(want_lse)
+    assert torch.equal(seen, ~torch.isinf(lse)) and bool(((lse - want_lse)[seen].abs() <= 2.0 ** -13).all())
+    assert dsa.dsa_read_device_status(ws) == 0
+
+
 def test_two_graphs_share_a_workspace():
     sets = [step_inputs(s) for s in (3, 4)]
     ws, wt = spaces()
