@@ -835,11 +835,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
         __syncwarp();
         if (lane == 0 && !bad) mbar_arrive(bar_p + 8 * (i & 1));
       }
-      if (!aborted) {
-        const bool got = wait_pv(i - 1, 3);
-        aborted = named_bar_or(bar_id, 128, !got);
-        tc_fence_after();
-      }
       if (aborted) break;
       // ---- the segment's rows: out and lse, or the workspace's partial sums ----
       float sums[NQ];
@@ -868,6 +863,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
         s_fac[n] = fac;
       }
       named_bar(bar_id, 128);
+      const bool got = wait_pv(i - 1, 3);  // (the sums above while the last P.V is under way)
+      aborted = named_bar_or(bar_id, 128, !got);
+      if (aborted) break;
+      tc_fence_after();
       // a few rows of 32 channels at a time, in a loop: unrolled, this code is longer than the time it takes to fetch it
       constexpr int kStep = NHH < 16 ? NHH : 16;
 #pragma unroll 1
