@@ -18,11 +18,12 @@
 // bins through distributed shared memory (one cluster barrier a histogram); then
 // one ordered compaction.  What bounds it is that chain of barriers, not its work;
 // it is launched early and looks its request up while the scores are being made.
-// Measured: one request of 65536 keys 21 us (two starts and the selection's chain),
-// 678,000 keys of 32 requests 51 us, of which the scores are 39 (4.4 TB/s).
+// Measured: one request of 65536 keys 19 us (two starts and the selection's chain),
+// 678,000 keys of 32 requests 48 us, of which the scores are 36 (4.8 TB/s).
 // Every step is exact and without order effects, so equal calls give equal lists.
 #include <cooperative_groups.h>
 
+#include <climits>
 #include <cmath>
 
 #include "dsa_host.h"
@@ -42,6 +43,9 @@ constexpr int kReaders = 14;
 constexpr int kSegs = 8;
 constexpr int kMaxCtas = 160;
 
+// tiles that the end of a group counts as when the tiles are dealt out: the next group's queries are waited for (100
+// requests of 4000: 25.0 us, 27.4 when it counts for nothing; 32 of up to 32k: 48 and 49.6)
+constexpr int kEnd = 3;
 constexpr int kMaxLen = 1 << 30;  // (positions are counted past a row's end by up to a round of the selection)
 constexpr int Q_CHUNK = kCols * 128, K_CHUNK = kTile * 128;
 constexpr int OFF_Q = 0, OFF_K = 2 * Q_CHUNK, OFF_W = OFF_K + kRing * 2 * K_CHUNK, OFF_MISC = OFF_W + 2 * kCols * 4;
@@ -88,12 +92,14 @@ __device__ __forceinline__ Request request_of(const Params& p, int b) {
 
 struct Plan {
   long long w0, w1;
-  int u, g, t, pad;  // request, group and tile of tile w0
+  int u, g, t;  // request, group and tile of the first tile
+  int skip;     // what lies before it: the end of a group
 };
 
 // A run of tiles [t0, t0 + n) of one group of a request's tokens, as announced (two int4).
 struct Seg {
   int t0, n, tok, nt, b, keys;
+  int last;  // the CTA's last run
 };
 
 __device__ __noinline__ bool read_announcement(uint32_t misc, const int4* ring, int k, volatile int* abort, long long limit,
@@ -101,7 +107,7 @@ __device__ __noinline__ bool read_announcement(uint32_t misc, const int4* ring, 
   const int at = k % kSegs;
   if (!__all_sync(0xffffffffu, wait_for(misc + M_ANN + 8 * at, (k / kSegs) & 1, abort, limit))) return false;
   const int4 a = ring[2 * at], c = ring[2 * at + 1];
-  s = Seg{a.x, a.y, a.z, a.w, c.x, c.y};
+  s = Seg{a.x, a.y, a.z, a.w, c.x, c.y, c.z};
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(misc + M_READ + 8 * at);
   return true;
@@ -110,7 +116,7 @@ __device__ __noinline__ bool read_announcement(uint32_t misc, const int4* ring, 
 template <int G>
 __device__ __forceinline__ void announce(const Params& p, const Plan& pl, uint32_t misc, int4* ring, volatile int* abort) {
   const int lane = threadIdx.x & 31;
-  long long left = pl.w1 - pl.w0;
+  long long left = pl.w1 - pl.w0 - pl.skip;
   int u = pl.u, g = pl.g, t = pl.t;
   Request rq = request_of(p, u);
   bool cut = false;
@@ -125,13 +131,13 @@ __device__ __forceinline__ void announce(const Params& p, const Plan& pl, uint32
     }
     cut |= rq.keys < rq.len;
     const int n = (int)min((long long)(tiles - t), left), at = k % kSegs;
+    left -= n + (t + n >= tiles ? kEnd : 0);
     if (k >= kSegs && !wait_for(misc + M_READ + 8 * at, (k / kSegs - 1) & 1, abort, p.wait_limit)) break;
     if (lane == 0) {
       ring[2 * at] = make_int4(t, n, rq.n0 + g * G, min(G, rq.n - g * G));
-      ring[2 * at + 1] = make_int4(u, rq.keys, 0, 0);
+      ring[2 * at + 1] = make_int4(u, rq.keys, left <= 0, 0);
       mbar_arrive(misc + M_ANN + 8 * at);
     }
-    left -= n;
     t += n;
     if (t >= tiles) { ++g; t = 0; }
   }
@@ -174,14 +180,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   auto tiles_of = [&](int u) -> long long {
     const Request r = request_of(p, u);
-    return (long long)((r.n + G - 1) / G) * ((r.keys + kTile - 1) / kTile);
+    return r.keys > 0 ? (long long)((r.n + G - 1) / G) * ((r.keys + kTile - 1) / kTile + kEnd) : 0;
   };
   auto visit = [&](const TileRange& r, int u, long long lo, long long n) {
     if (lo <= r.w0 && r.w0 < lo + n) {
       const int tiles = (request_of(p, u).keys + kTile - 1) / kTile;
+      const int span = tiles + kEnd;
+      int g = (int)((r.w0 - lo) / span), t = (int)((r.w0 - lo) - (long long)g * span);
+      s_plan->skip = 0;
+      if (t >= tiles) {
+        s_plan->skip = span - t;
+        ++g;
+        t = 0;
+      }
       s_plan->u = u;
-      s_plan->g = (int)((r.w0 - lo) / tiles);
-      s_plan->t = (int)((r.w0 - lo) - (long long)s_plan->g * tiles);
+      s_plan->g = g;
+      s_plan->t = t;
     }
   };
   const TileRange rg = split_line<kThreads>(p.B, tiles_of, reinterpret_cast<long long*>(misc + M_SCRATCH), visit);
@@ -192,14 +206,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const Plan plan = *s_plan;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the selection waits for this kernel's end itself)
-  if (plan.w1 <= plan.w0) return;
+  if (plan.w1 <= plan.w0 || plan.w1 - plan.w0 <= plan.skip) return;
   if (warp == 0) {
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
   }
   __syncthreads();
   const uint32_t tmem = (uint32_t)warp_value((int)*s_tmem);
-  const int n_tiles = warp_value((int)(plan.w1 - plan.w0));
   int4* ring = reinterpret_cast<int4*>(misc + M_RING);
   auto read_seg = [&](int k, Seg& s) -> bool { return read_announcement(mb, ring, k, s_abort, p.wait_limit, s); };
   Seg sg;
@@ -207,8 +220,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ======================= MMA issuer =======================
     int done = 0;
-    for (int seg = 0; done < n_tiles; ++seg) {
+    for (int seg = 0, last = 0; !last; ++seg) {
       if (!warp_all(read_seg(seg, sg))) break;
+      last = warp_value(sg.last);
       if (!warp_all(wait_for(mb + M_Q, seg & 1, s_abort, p.wait_limit))) break;
       // what the loop needs in registers of the warp (a call does not keep them)
       const int n = warp_value(sg.n);
@@ -242,10 +256,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     announce<G>(p, plan, mb, ring, s_abort);
   } else if (warp == 13) {
     // ======================= queries of a segment, once the products of the one before are done =======================
-    int done = 0;
-    for (int seg = 0; done < n_tiles; ++seg) {
+    for (int seg = 0, last = 0; !last; ++seg) {
       if (!warp_all(read_seg(seg, sg))) break;
-      done += sg.n;
+      last = sg.last;
       if (seg > 0 && !wait_for(mb + M_SEG, (seg - 1) & 1, s_abort, p.wait_limit)) break;
       const int rows = ((sg.nt * HP + 15) & ~15);
 #pragma unroll 4
@@ -267,12 +280,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // cp.async, zero-filled where there is no key.
     const int sl = warp - 9;
     int seg = 0, base = 0, end = 0;
+    int n_tiles = INT_MAX;  // this CTA's tiles, known once one past them has been looked for
     bool bad = false, stop = false;
     int page[4], at[4];  // of the rows 32 k + lane: page, place in it (-1: no key)
     auto look_up = [&](int i) {
       if (i >= n_tiles) return;
 #pragma unroll 1
       while (i >= end) {
+        if (seg > 0 && sg.last) { n_tiles = end; return; }
         if (!read_seg(seg, sg)) { stop = true; return; }
         ++seg;
         base = end;
@@ -348,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* s_w = reinterpret_cast<float*>(smem + OFF_W) + grp * kCols;
     bool stop = false;
     int i = 0;
-    for (int seg = 0; i < n_tiles; ++seg) {
+    for (int seg = 0; seg == 0 || !sg.last; ++seg) {
       if (!stop && !read_seg(seg, sg)) stop = true;
       // the weights of the segment before have been read; all four warps leave together after a failed wait
       if (named_bar_or(1 + grp, 128, stop)) break;
