@@ -132,7 +132,7 @@ __device__ __forceinline__ void announce(const Params& p, const Plan& pl, uint32
     cut |= rq.keys < rq.len;
     const int n = (int)min((long long)(tiles - t), left), at = k % kSegs;
     left -= n + (t + n >= tiles ? kEnd : 0);
-    if (k >= kSegs && !wait_for(misc + M_READ + 8 * at, (k / kSegs - 1) & 1, abort, p.wait_limit)) break;
+    if (k >= kSegs && !warp_all(wait_for(misc + M_READ + 8 * at, (k / kSegs - 1) & 1, abort, p.wait_limit))) break;
     if (lane == 0) {
       ring[2 * at] = make_int4(t, n, rq.n0 + g * G, min(G, rq.n - g * G));
       ring[2 * at + 1] = make_int4(u, rq.keys, left <= 0, 0);
@@ -211,8 +211,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
   }
-  __syncthreads();
-  const uint32_t tmem = (uint32_t)warp_value((int)*s_tmem);
+  uint32_t tmem = 0;
+  if (warp <= 8) {  // the others neither need it nor wait for it
+    named_bar(3, 288);
+    tmem = (uint32_t)warp_value((int)*s_tmem);
+  }
   int4* ring = reinterpret_cast<int4*>(misc + M_RING);
   auto read_seg = [&](int k, Seg& s) -> bool { return read_announcement(mb, ring, k, s_abort, p.wait_limit, s); };
   Seg sg;
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int seg = 0, last = 0; !last; ++seg) {
       if (!warp_all(read_seg(seg, sg))) break;
       last = sg.last;
-      if (seg > 0 && !wait_for(mb + M_SEG, (seg - 1) & 1, s_abort, p.wait_limit)) break;
+      if (seg > 0 && !warp_all(wait_for(mb + M_SEG, (seg - 1) & 1, s_abort, p.wait_limit))) break;
       const int rows = ((sg.nt * HP + 15) & ~15);
 #pragma unroll 4
       for (int x = lane; x < rows * 16; x += 32) {

@@ -261,7 +261,7 @@ __device__ __forceinline__ void announce(const Params& p, const Plan& pl, uint32
       cut |= un.keys < un.len;
     }
     const int at = k % kSegs;
-    if (k >= kSegs && !wait_for(empty + 8 * at, (k / kSegs - 1) & 1, abort, p.wait_limit)) break;
+    if (k >= kSegs && !warp_all(wait_for(empty + 8 * at, (k / kSegs - 1) & 1, abort, p.wait_limit))) break;
     if (lane == 0) {
       ring[2 * at] = a;
       ring[2 * at + 1] = c;
@@ -392,8 +392,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
     tmem_alloc(smem_u32(s_tmem), L::TM_COLS);
     tmem_relinquish();
   }
-  __syncthreads();
-  const uint32_t tmem = (uint32_t)warp_value((int)*s_tmem);
+  uint32_t tmem = 0;
+  if (warp <= 8 || warp == 13) {  // the others neither need it nor wait for it
+    named_bar(3, 320);
+    tmem = (uint32_t)warp_value((int)*s_tmem);
+  }
 
   // announcement k, once per warp
   auto read_seg = [&](int k, Seg& s) -> bool {
@@ -696,7 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
     };
     const int sum_row = n0 + (((lane >> 1) & 14) | (lane & 1)) % NQ;
     Seg sg, nx;
-    bool aborted = !read_seg(0, sg);
+    // (one answer for the half: its warps meet at barriers from here on)
+    bool aborted = named_bar_or(bar_id, 128, !read_seg(0, sg));
     if (!aborted) load_q(sg);
     nx = sg;
     int i = 0;
