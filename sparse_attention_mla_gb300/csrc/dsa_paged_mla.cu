@@ -844,6 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
       float sums[NQ];
 #pragma unroll
       for (int j = 0; j < NQ / 2; ++j) { sums[2 * j] = l_part[j].x; sums[2 * j + 1] = l_part[j].y; }
+      named_bar(bar_id, 128);  // the factors of a rescale in the last tile have been read (the sums take their place)
       s_red[qd * NH + sum_row] = over_keys(sums, false);
       named_bar(bar_id, 128);
       const bool whole = sg.whole;
