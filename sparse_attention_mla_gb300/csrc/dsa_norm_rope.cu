@@ -215,17 +215,19 @@ struct Turn {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float4 c = q[e];
-        a[e] = in ? make_float2(c.x, c.z) : make_float2(1.f, 1.f);
-        b[e] = in ? make_float2(c.y * sign, c.w * sign) : make_float2(0.f, 0.f);
+        a[e] = make_float2(c.x, c.z);
+        b[e] = make_float2(c.y * sign, c.w * sign);
       }
     }
   }
   __device__ __forceinline__ void apply(float2 (&f)[P], float* stage, const Rows& p, int l, float back) const {
+    // (channels that are not turned are left out, not turned by 0: 0 times a neighbour's infinity is no 0)
     if constexpr (ROT == kPairs) {
 #pragma unroll
       for (int i = 0; i < P; ++i) {
+        const int u0 = ((i / PP) * LPR + l) * VEC - p.r0;
         const float2 x = f[i];
-        f[i] = make_float2(x.x * a[i].x - x.y * a[i].y, x.y * a[i].x + x.x * a[i].y);
+        if (u0 >= 0 && u0 < p.R) f[i] = make_float2(x.x * a[i].x - x.y * a[i].y, x.y * a[i].x + x.x * a[i].y);
       }
     } else if constexpr (ROT == kLanes) {
 #pragma unroll
@@ -235,7 +237,7 @@ struct Turn {
         for (int e = 0; e < 4; ++e) {
           const int i = (k * PP + e) % P;  // (the remainder only keeps the unused scalar shape in range)
           const float2 y = make_float2(__shfl_sync(0xffffffffu, f[i].x, other, LPR), __shfl_sync(0xffffffffu, f[i].y, other, LPR));
-          f[i] = fma2(f[i], a[e], mul2(y, b[e]));
+          if (in) f[i] = fma2(f[i], a[e], mul2(y, b[e]));
         }
       }
     } else {
