@@ -390,6 +390,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t v[32];
           tmem_ld32(tmem_addr(tmem + grp * kCols + c0, qd * 32, 0), v);
           tmem_ld_wait();
+          // the padding's products are left out, not weighed by 0: with an infinite key they are NaN
+          const int real = p.Hi - (c0 & (HP - 1));  // of each token's columns in this chunk
+          if (real < (HP < 32 ? HP : 32)) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if ((j & (HP - 1)) >= real) v[j] = 0u;
+          }
           const float4* w4 = reinterpret_cast<const float4*>(s_w + c0);
           if constexpr (HP >= 32) {
             float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
