@@ -556,6 +556,8 @@ dsa_status_t dsa_rope_frequencies(int32_t rope_dim, double base, double factor, 
  *   z_p = softmax_scale <q[t,h,:], kv_p>,  lse[t,h] = ln(sum_p exp(z_p) [+ exp(attn_sink[h])]),
  *   out[t,h,:] = sum_p exp(z_p - lse) kv_p[0:Dv];
  * a token that sees nothing gets out = 0 and lse = -inf (or attn_sink[h]).
+ * What a position holds, infinities and NaN too, reaches the tokens that see it and no other.  (To one of them whose
+ * score for it is -inf an infinite latent adds NaN, or nothing where another new token of the request does not see it.)
  *  q            device bf16 [N, H, Dqk], Dqk in {512, 576}
  *  cache        device bf16 [num_pages, page_size, Dqk]; rows that no token sees are not read
  *  block_table  device int32 [B, max_pages];  seq_lens device int32 [B]

@@ -139,6 +139,25 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// A latent's 512 channels in shared memory (its 128 bytes of the first chunk at `at`): values that are not finite become 0.
+// (A function of its own, for the same reason as read_announcement.)
+__device__ __noinline__ void zero_not_finite(uint32_t at, uint32_t landed, uint32_t parity) {
+  if (!mbar_test(landed, parity) || !mbar_test(landed + 8, parity)) return;  // (they have long landed: orders what is read here)
+#pragma unroll 1
+  for (int x = 0; x < kDv / 8; ++x, at += (x & 7) ? 16 : kTile * 128 - 112) {
+    uint32_t v[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
+    bool found = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool lo = (v[k] & 0x7f80u) == 0x7f80u, hi = (v[k] & 0x7f800000u) == 0x7f800000u;
+      found |= lo || hi;
+      v[k] &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu);
+    }
+    if (found) st_shared_v4(at, v[0], v[1], v[2], v[3]);
+  }
+}
+
 struct Unit {
   int groups, tiles;  // groups of MMA columns, tiles of each
   int n0, n;          // first token, tokens
@@ -746,6 +765,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_kernel(const __grid_con
 #pragma unroll
           for (int j = 0; j < NQ; ++j) z[j] = -INFINITY;
         } else if (p.topk_idx == nullptr && (t + 1) * (long long)kTile > sg.seen0) {  // some token may not see all of it
+          // The rows share the latent, and a weight of 0 times an infinity is NaN: where a token does not see this position,
+          // what is not finite in its channels becomes 0 before P.V.  (Any row's score tells: with such a latent all are
+          // infinite or NaN.  A row that sees it has NaN for its weight then, unless its score is -inf.)
+          if (pos >= sg.seen0 && !(fabsf(z[0]) < INFINITY))
+            zero_not_finite(L::chunk(sKV, sl, 0) + (uint32_t)r * 128, bar_kv + 8 * (sl * kGroups), (i / R) & 1);
           int seen = sg.seen0 + tok0, left = head_left;
 #pragma unroll
           for (int j = 0; j < NQ; ++j) {
