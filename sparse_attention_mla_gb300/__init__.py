@@ -909,6 +909,8 @@ def dsa_paged_mla(q, cache, block_table, seq_lens, softmax_scale: float, cu_q=No
     if topk_idx is not None:
         p_idx = _dense(topk_idx, "topk_idx", torch.int32, (N, None), dev)
         K = topk_idx.shape[1]
+        if K == 0:  # (an array without entries has no address: the library would take it for no lists at all)
+            raise ValueError("topk_idx must have a column at least (an entry of -1 names no position)")
         if topk_len is not None:
             p_tl = _dense(topk_len, "topk_len", torch.int32, (N,), dev)
     elif topk_len is not None:

@@ -1158,7 +1158,9 @@ extern "C" dsa_status_t dsa_paged_mla(const dsa_bf16_t* q, const dsa_bf16_t* cac
     return fail(DSA_ERR_INVALID_ARGUMENT, "%s: softmax_scale must be finite and > 0", who);
   if (!cu_q && N != B)
     return fail(DSA_ERR_INVALID_ARGUMENT, "%s: without cu_q every request has one token (N = %d, B = %d)", who, N, B);
-  if ((topk_idx != nullptr) != (K > 0)) return fail(DSA_ERR_INVALID_ARGUMENT, "%s: topk_idx and K > 0 go together", who);
+  // (lists of no tokens have no address)
+  if (topk_idx ? K == 0 : K > 0 && N > 0)
+    return fail(DSA_ERR_INVALID_ARGUMENT, "%s: topk_idx and K > 0 go together", who);
   if (topk_len && !topk_idx) return fail(DSA_ERR_INVALID_ARGUMENT, "%s: topk_len needs topk_idx", who);
   if (N > 0 && (!q || !out || !lse)) return fail(DSA_ERR_INVALID_ARGUMENT, "%s: null tensor pointer", who);
   if (B > 0 && (!seq_lens || (max_pages > 0 && !block_table) || (num_pages > 0 && !cache)))
