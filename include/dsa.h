@@ -504,8 +504,8 @@ dsa_status_t dsa_paged_slots(const int32_t* seq_lens, const int32_t* new_lens, i
  *  out          device bf16, row (o, h) at out + o out_stride_t + h out_stride_h, with o = t,
  *               or o = out_rows[t] when out_rows (device int32 [T]) is given: -1 writes no
  *               row, other values outside [0, num_out_rows) are skipped and reported
- *               (DSA_ERR_DEVICE_INDEX); rows named twice get one of the two results.
- *               The rows of out must not overlap; out may equal x with the same strides
+ *               (DSA_ERR_DEVICE_INDEX); a row named twice gets each channel from one of
+ *               the two results, in no order.  The rows of out must not overlap; out may equal x with the same strides
  *               and no out_rows, and must not overlap x otherwise.
  *  workspace    >= 256 bytes (the error word)
  */

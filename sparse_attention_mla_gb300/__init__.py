@@ -797,7 +797,8 @@ def dsa_norm_rope_fwd(x, inv_freq=None, positions=None, norm: str = "none", norm
     """Norm of the first norm_dim channels (default: all) and rotation of 2 * len(inv_freq) channels from rope_start
     (default: the last ones) of bf16 rows x [T, D] or [T, H, D], any strides with contiguous channels -> out, bf16 of
     x's shape (out may be x).  norm: "none", "rms" or "layer"; weight, bias: fp32 [norm_dim]; positions: int32 [T].
-    out_rows: int32 [T], the row of `out` that each token goes to (-1: none); out is then a cache of rows [rows, D],
+    out_rows: int32 [T], the row of `out` that each token goes to (-1: none; a row named twice gets each channel from one of
+    the two results); out is then a cache of rows [rows, D],
     [rows, H, D] or, for x [T, D], pages [num_pages, page_size, D]."""
     lib = _lib or load_library()
     p_x, xt, xh, T, H, D = _rows_of(x, "x", None)
