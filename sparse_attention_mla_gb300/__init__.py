@@ -666,7 +666,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 def paged_workspace_size(kind: str, a: int = 0, b: int = 0) -> int:
     """Workspace bytes of the serving calls: ("slots"), ("norm_rope_fwd"), ("norm_rope_bwd", rows, norm_dim),
-    ("mla", N, H) or ("topk", N, max_len)."""
+    ("mla", N, H) or ("topk", N, max_len).  The first 256 hold the error word, which the calls set and never
+    clear: a workspace is made zeroed (torch.zeros), and dsa_read_device_status clears it."""
     lib = load_library()
     if kind in ("slots", "norm_rope_fwd"):
         return 256
@@ -731,7 +732,9 @@ def dsa_paged_slots(seq_lens, block_table, free_pages, page_size: int, new_lens=
     """Pages and cache rows of a step's new tokens -> (slot_map int32 [N], positions int32 [N], cu_new int32 [B+1],
     seq_lens_out int32 [B], pages_taken int32 [1]); block_table int32 [B, max_pages] gets the fresh pages, taken
     from free_pages int32 [F] in request order.  new_lens: int32 [B], or None for one token each.  N: entries of
-    slot_map and positions (at least the new tokens; -1 beyond them), required with new_lens."""
+    slot_map and positions (at least the new tokens; -1 beyond them), required with new_lens.  A step that does not fit
+    (DSA_ERR_CAPACITY) gives -1 everywhere and cu_new of zeros.  workspace: uint8 [paged_workspace_size("slots")], zeroed
+    once, where errors stay until dsa_read_device_status reads them; None: one that is dropped, and the error with it."""
     lib = _lib or load_library()
     p_len = _dense(seq_lens, "seq_lens", torch.int32, (None,), None)
     dev = seq_lens.device
@@ -798,8 +801,9 @@ def dsa_norm_rope_fwd(x, inv_freq=None, positions=None, norm: str = "none", norm
     (default: the last ones) of bf16 rows x [T, D] or [T, H, D], any strides with contiguous channels -> out, bf16 of
     x's shape (out may be x).  norm: "none", "rms" or "layer"; weight, bias: fp32 [norm_dim]; positions: int32 [T].
     out_rows: int32 [T], the row of `out` that each token goes to (-1: none; a row named twice gets each channel from one of
-    the two results); out is then a cache of rows [rows, D],
-    [rows, H, D] or, for x [T, D], pages [num_pages, page_size, D]."""
+    the two results); out is then a cache of rows [rows, D], [rows, H, D] or, for x [T, D], pages [num_pages, page_size, D].
+    workspace: uint8 [paged_workspace_size("norm_rope_fwd")], zeroed once, where errors (rows outside the cache) stay until
+    dsa_read_device_status reads them; None: one that is dropped, and the error with it."""
     lib = _lib or load_library()
     p_x, xt, xh, T, H, D = _rows_of(x, "x", None)
     dev = x.device
@@ -834,7 +838,8 @@ def dsa_norm_rope_bwd(dout, x=None, inv_freq=None, positions=None, norm: str = "
                       accumulate: bool = False, workspace=None):
     """Gradient of dsa_norm_rope_fwd -> (dx bf16 of dout's shape, dweight fp32 [norm_dim] or None, dbias fp32
     [norm_dim] or None).  With a norm, x is the forward's input and dweight is always formed; with_bias (layer norm)
-    forms dbias too.  accumulate: add to the given dweight / dbias.  dx may be dout or x."""
+    forms dbias too.  accumulate: add to the given dweight / dbias.  dx may be dout or x.  workspace: uint8
+    [paged_workspace_size("norm_rope_bwd", rows, norm_dim)]; this call has no errors for dsa_read_device_status."""
     lib = _lib or load_library()
     p_g, gt, gh, T, H, D = _rows_of(dout, "dout", None)
     dev = dout.device
@@ -900,7 +905,9 @@ def dsa_paged_mla(q, cache, block_table, seq_lens, softmax_scale: float, cu_q=No
     """Attention of new tokens over a paged latent cache -> (out bf16 [N,H,Dv], lse fp32 [N,H]).  q bf16 [N,H,Dqk];
     cache bf16 [num_pages, page_size, Dqk]; block_table int32 [B, max_pages]; seq_lens int32 [B], the new tokens
     included; cu_q int32 [B+1], each request's tokens (None: one each).  topk_idx int32 [N,K] (with topk_len
-    int32 [N] or None): attend only to these positions.  attn_sink: fp32 [H] or None."""
+    int32 [N] or None): attend only to these positions.  attn_sink: fp32 [H] or None.  workspace: uint8
+    [paged_workspace_size("mla", N, H)], zeroed once, where errors (bad pages and positions, waits that ran out) stay until
+    dsa_read_device_status reads them; None: one that is dropped, and the error with it."""
     lib = _lib or load_library()
     p_q = _dense(q, "q", torch.bfloat16, (None, None, None), None)
     dev = q.device
@@ -934,7 +941,9 @@ def dsa_paged_indexer_topk(q_idx, k_cache, head_weights, block_table, seq_lens, 
     """Top-k selection of new tokens over paged index keys -> (topk_idx int32 [N,K], positions ascending with a -1
     suffix, topk_len int32 [N]): the lists of dsa_paged_mla.  q_idx bf16 [N,Hi,128]; k_cache bf16 [num_pages,
     page_size, 128]; head_weights fp32 [N,Hi]; the rest as dsa_paged_mla.  max_len: no request is longer (default:
-    what the table holds), at most 2^30; the workspace is N rows of that many fp32 scores."""
+    what the table holds), at most 2^30; the workspace is N rows of that many fp32 scores.  workspace: uint8
+    [paged_workspace_size("topk", N, max_len)], zeroed once, where errors (bad pages, lengths past max_len, waits that ran
+    out) stay until dsa_read_device_status reads them; None: one that is dropped, and the error with it."""
     lib = _lib or load_library()
     p_q = _dense(q_idx, "q_idx", torch.bfloat16, (None, None, None), None)
     dev = q_idx.device
