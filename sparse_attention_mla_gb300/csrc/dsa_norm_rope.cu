@@ -21,8 +21,8 @@
 // The cosines and sines depend on the token alone: they are formed once per token
 // of a group's run of rows, spread over its lanes, in shared memory.  Measured: the
 // position channels of 16384 x 64 heads (128 of every 1152 bytes) 54 us at 5.0 TB/s,
-// 131104 rows of 128 with the norm 18 us at 3.8 TB/s, the gradient of 32768 rows of
-// 128 with the layer norm 18 us at 1.4 TB/s (four batches of rows a group: latency).
+// 131104 rows of 128 with the norm 18 us at 3.7 TB/s, the gradient of 32768 rows of
+// 128 with the layer norm 16 us at 1.5 TB/s (four batches of rows a group: latency).
 //
 // Angles: positions reach millions, and position times frequency in fp32 is then
 // off by 0.1 rad.  The frequency is held as a 64-bit binary fraction of a turn, so
@@ -640,8 +640,8 @@ struct Shape {
 };
 
 // A forward kernel for each norm where a row's instructions count: the 16-byte path with a rotation in registers.
-// (131104 rows of 128, rms and rotation: 20.4 us, 23.4 us with the norm as an argument; in the backward 1 %, not worth
-// its kernels.)
+// (131104 rows of 128, rms and rotation: 18 us, 25 us with the norm as an argument; in the backward 1 %, not worth its
+// kernels.)
 template <int LPR, int NIT, int ROT, class F>
 dsa_status_t dispatch_norm(const Rows& p, F&& f) {
   if (p.kind == kRms) return f(Shape<8, LPR, NIT, ROT, kRms>{});

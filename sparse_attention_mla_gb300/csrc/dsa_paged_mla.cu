@@ -32,12 +32,13 @@
 // 8 KiB block that the two tiles share.
 //
 // Measured: 674,000 positions of 64 requests, 64 heads, 159 us (4.9 TB/s); 131072
-// positions, two tokens of 128 heads, 117 us (four groups of rows, each reading the cache,
+// positions, two tokens of 128 heads, 116 us (four groups of rows, each reading the cache,
 // three times of four from L2); 48 lists of 2048 rows 55 us; 1000 positions, 16 heads, 13 us.
 // What bounds it: a tile passes its copy (1350 cycles, as fast as an SM takes one), S^T
 // (1700), the softmax (1600) and P.V (1200) one after the other, and shared memory holds two,
-// so that a tile takes 3600 cycles; the start (12 us to the first softmax), the end of a group
-// and the join (6 us) come on top.
+// so that a tile takes 3600 cycles; the start (from the launch to the first softmax 6 us in the call of 1000
+// positions, 9 to 13 in the others), the end of a group and the join (3 us after the last CTA in that call, 6 to 10 in the
+// others) come on top.
 #include <climits>
 #include <cmath>
 
