@@ -487,6 +487,7 @@ dsa_status_t dsa_paged_slots(const int32_t* seq_lens, const int32_t* new_lens, i
  *   norm 1 (rms):   y_c = x_c r weight_c, r = 1 / sqrt(mean x^2 + eps)
  *   norm 2 (layer): y_c = (x_c - mean) r weight_c + bias_c, r = 1 / sqrt(var + eps)
  *   norm 0:         y_c = x_c                          (mean, var over c < norm_dim)
+ * (squares are summed in fp32, so that a norm's rows have |x_c| < 2^57 and, with eps = 0, a largest one above 2^-58)
  * for c < norm_dim, y_c = x_c above; then the rope_dim channels from rope_start are
  * turned in pairs (a, b), number i = 0 .. rope_dim / 2 - 1, by the angle
  * positions[t] * inv_freq[i] (formed exactly, whatever the position):

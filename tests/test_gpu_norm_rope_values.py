@@ -1,10 +1,14 @@
 """dsa_norm_rope_fwd / bwd with values that are not finite: they reach their pair of rotated channels (and, under the norm,
 what the norm covers), and no channel else.  Channels that are neither normalised nor rotated are copied, the sign of a
-zero included."""
+zero included.  And values at both ends of what a norm takes (|x| < 2^57; above 2^-58 with eps = 0): tolerances of
+test_gpu_norm_rope.py, which follow the rows' own magnitudes."""
 import pytest
 import torch
 
 import sparse_attention_mla_gb300 as dsa
+
+import _paged_ref as ref
+from test_gpu_norm_rope import f64, near, near_sum
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -73,3 +77,24 @@ def test_values_reach_their_pair_only(D, n, R, r0, inter, wide, back):
         assert torch.equal(bits(clean[..., wide:][..., plain]), bits(want[..., plain]))
     rot = got[..., r0:r0 + R]
     assert not bool(rot[touched[..., r0:r0 + R]].isfinite().any())  # (0 times an infinity is NaN)
+
+
+@pytest.mark.parametrize("kind,n,D", [("rms", 512, 576), ("layer", 128, 128), ("rms", 97, 97), ("layer", 1024, 1024)])
+@pytest.mark.parametrize("power", [54, -56])
+def test_the_largest_and_smallest_rows_of_a_norm(kind, n, D, power):
+    g = torch.Generator().manual_seed(n)
+    x = (torch.randn(20, 2, D, generator=g).clamp(-7, 7) * 2.0 ** power).bfloat16().to(DEV)
+    x[..., 0] = 7.5 * 2.0 ** power
+    dout = torch.randn(20, 2, D, generator=g).bfloat16().to(DEV)
+    w = (1 + 0.3 * torch.randn(n, generator=g)).to(DEV)
+    kw = dict(norm=kind, norm_dim=n, weight=w, eps=0.0)
+    none = (None, None, D, False)
+    y = dsa.dsa_norm_rope_fwd(x, **kw)
+    near(y[..., :n], ref.norm_rope_fwd(f64(x), kind, n, f64(w), None, 0.0, *none)[..., :n], "y")
+    assert torch.equal(y[..., n:], x[..., n:])
+    dx, dw, _ = dsa.dsa_norm_rope_bwd(dout, x, **kw)
+    # (a gradient is as much smaller as its row is larger: compared with that of the rows at ordinary size)
+    rdx, rdw, _, mw, _, most = ref.norm_rope_bwd(f64(dout), f64(x) / 2.0 ** power, kind, n, f64(w), 0.0, *none)
+    near(dx.double()[..., :n] * 2.0 ** power, rdx[..., :n], "dx", most)
+    assert torch.equal(dx[..., n:], dout[..., n:])
+    near_sum(dw, rdw, mw, "dw")
