@@ -610,6 +610,81 @@ dsa_status_t dsa_paged_indexer_topk(const dsa_bf16_t* q_idx, const dsa_bf16_t* k
                                     void* workspace, size_t workspace_bytes, dsa_stream_t stream);
 
 /*
+ * Rows of a quantised cache.  The first quant_dim channels of a row of D are held as
+ * codes, the others in bf16; a quantised channel's value is code * s (8 bits) or
+ * code * block * s (4 bits).  A row's bytes, for Q = quant_dim (a multiple of 64, D - Q a
+ * multiple of 8, D <= 1024):
+ *   8 bits: Q codes e4m3, s (fp32), zero bytes up to a multiple of 16, 2 (D - Q) bytes of the
+ *           other channels, zero bytes up to a multiple of 16;
+ *   4 bits: Q / 2 bytes of codes e2m1 (channel 2i in the low half of byte i, 2i + 1 in the
+ *           high), Q / 16 block scales e4m3 (one for each 16 channels, >= 0), then s and the
+ *           rest as above.
+ * s is a power of two in [2^-48, 2^48], or NaN: then all Q channels of the row are NaN.
+ * Codes and block scales are finite (no byte 0x7f or 0xff among the e4m3 ones).
+ * For the latents (D = 576, Q = 512) a row has 656 bytes of 8 bits, 432 of 4 bits, in place of 1152.
+ */
+
+/* Bytes of a row (a multiple of 16); 0 when D, quant_dim and bits (8 or 4) are not as above. */
+size_t dsa_paged_quant_row_bytes(int32_t D, int32_t quant_dim, int32_t bits);
+
+/*
+ * dsa_paged_quantize -- rows quantised as they are written to a cache.  For row x with the
+ * largest magnitude a over its first Q channels:
+ *   s = the smallest power of two (at least 2^-48) with a <= 448 s (8 bits), a <= 2688 s (4 bits);
+ *   8 bits: code = e4m3(x / s);
+ *   4 bits: block = e4m3(a_block / (6 s)), code = e2m1(x / (block s)) (0 where block is 0),
+ * rounded to nearest, ties to even, magnitudes past the largest code to that code.  A row with a
+ * channel among the Q that is not finite, or too large for s = 2^48, gets s = NaN.
+ *  x            device bf16, row t at x + t x_stride_t (elements; >= 0), channels contiguous; T >= 0
+ *  cache        device bytes [num_rows, row bytes] (out), 16-byte aligned: the pages' rows laid end to end
+ *  out_rows     device int32 [T] or NULL (row t): as in dsa_norm_rope_fwd (-1 writes no row; other
+ *               values outside [0, num_rows) are skipped and reported, DSA_ERR_DEVICE_INDEX); a row
+ *               named twice holds bytes of both results, in no order
+ *  workspace    >= 256 bytes (the error word)
+ * x and cache must not overlap.  Rows that are not named are left as they are.
+ */
+dsa_status_t dsa_paged_quantize(const dsa_bf16_t* x, int64_t x_stride_t, int32_t T, int32_t D, int32_t quant_dim,
+                                int32_t bits, uint8_t* cache, int64_t num_rows, const int32_t* out_rows,
+                                void* workspace, size_t workspace_bytes, dsa_stream_t stream);
+
+/*
+ * dsa_paged_dequantize -- rows of requests read back: row cu_rows[b] + j of out is the row of
+ * request b's position first[b] + j (j when first is NULL), rounded to bf16 (rows that
+ * dsa_paged_quantize wrote are exact).  Rows named one by one are a request with pages of one row:
+ * the list is then its block table.
+ *  cache        device bytes [num_pages, page_size, row bytes], 16-byte aligned
+ *  block_table  device int32 [B, max_pages];  first device int32 [B] or NULL
+ *  cu_rows      device int32 [B + 1], non-decreasing, within [0, N]; rows of out outside
+ *               [cu_rows[0], cu_rows[B]) are left as they are
+ *  out          device bf16 (out), row t at out + t out_stride_t (>= D), channels contiguous
+ *  workspace    >= 256 bytes (the error word)
+ * Positions that are negative or beyond the table and pages outside [0, num_pages) give rows of
+ * zeros and are reported (DSA_ERR_DEVICE_INDEX).  out must not overlap the cache.
+ */
+dsa_status_t dsa_paged_dequantize(const uint8_t* cache, const int32_t* block_table, const int32_t* first,
+                                  const int32_t* cu_rows, int32_t N, int32_t B, int32_t D, int32_t quant_dim,
+                                  int32_t bits, int32_t num_pages, int32_t page_size, int32_t max_pages,
+                                  dsa_bf16_t* out, int64_t out_stride_t, void* workspace, size_t workspace_bytes,
+                                  dsa_stream_t stream);
+
+/*
+ * dsa_paged_mla_quant -- dsa_paged_mla over a cache of quantised latents (quant_dim = 512): the same
+ * attention, with the rows' values as defined above for kv.  Queries, tables, lists, sink, out and lse
+ * as there; scores are sums in fp32 of exact products, the weights of the latents have 11 bits.
+ *  cache        device bytes [num_pages, page_size, dsa_paged_quant_row_bytes(Dqk, 512, bits)], 16-byte aligned
+ *  bits         8 or 4
+ *  workspace    >= dsa_paged_mla_quant_workspace_size() bytes, whatever the sizes
+ * A row whose s is NaN makes the tokens NaN that see it and no other.
+ */
+size_t dsa_paged_mla_quant_workspace_size(void);
+dsa_status_t dsa_paged_mla_quant(const dsa_bf16_t* q, const uint8_t* cache, const int32_t* block_table,
+                                 const int32_t* seq_lens, const int32_t* cu_q, const int32_t* topk_idx,
+                                 const int32_t* topk_len, int32_t N, int32_t B, int32_t H, int32_t Dqk, int32_t Dv,
+                                 int32_t bits, int32_t K, int32_t num_pages, int32_t page_size, int32_t max_pages,
+                                 float softmax_scale, const float* attn_sink, dsa_bf16_t* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, dsa_stream_t stream);
+
+/*
  * dsa_set_wait_limit_cycles -- the cycle limit of every bounded device-side
  * wait of the kernels launched after the call (process-wide; the default is
  * 2^31 SM cycles, about one second).  A wait that runs past it records

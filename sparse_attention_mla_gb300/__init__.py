@@ -44,10 +44,14 @@ __all__ = [
     "dsa_rope_frequencies",
     "dsa_paged_mla",
     "dsa_paged_indexer_topk",
+    "dsa_paged_quantize",
+    "dsa_paged_dequantize",
+    "dsa_paged_mla_quant",
     "dsa_read_device_status",
     "dsa_set_wait_limit_cycles",
     "workspace_size",
     "paged_workspace_size",
+    "paged_quant_row_bytes",
 ]
 
 DSA_OK = 0
@@ -166,8 +170,16 @@ def load_library(path: str | None = None):
         lib.dsa_paged_indexer_topk_workspace_size.restype = _SZ
         lib.dsa_paged_indexer_topk.argtypes = [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P,
                                                _SZ, _P]
+        lib.dsa_paged_quant_row_bytes.argtypes = [_I, _I, _I]
+        lib.dsa_paged_quant_row_bytes.restype = _SZ
+        lib.dsa_paged_quantize.argtypes = [_P, _L, _I, _I, _I, _I, _P, _L, _P, _P, _SZ, _P]
+        lib.dsa_paged_dequantize.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _L, _P, _SZ, _P]
+        lib.dsa_paged_mla_quant_workspace_size.argtypes = []
+        lib.dsa_paged_mla_quant_workspace_size.restype = _SZ
+        lib.dsa_paged_mla_quant.argtypes = [_P] * 7 + [_I] * 10 + [_F, _P, _P, _P, _P, _SZ, _P]
         for name in ("dsa_paged_slots", "dsa_norm_rope_fwd", "dsa_norm_rope_bwd", "dsa_rope_frequencies",
-                     "dsa_paged_mla", "dsa_paged_indexer_topk"):
+                     "dsa_paged_mla", "dsa_paged_indexer_topk", "dsa_paged_quantize", "dsa_paged_dequantize",
+                     "dsa_paged_mla_quant"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -666,15 +678,17 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 def paged_workspace_size(kind: str, a: int = 0, b: int = 0) -> int:
     """Workspace bytes of the serving calls: ("slots"), ("norm_rope_fwd"), ("norm_rope_bwd", rows, norm_dim),
-    ("mla", N, H) or ("topk", N, max_len).  The first 256 hold the error word, which the calls set and never
+    ("mla", N, H), ("topk", N, max_len), ("quantize"), ("dequantize") or ("mla_quant", N, H).  The first 256 hold the error word, which the calls set and never
     clear: a workspace is made zeroed (torch.zeros), and dsa_read_device_status clears it."""
     lib = load_library()
-    if kind in ("slots", "norm_rope_fwd"):
+    if kind in ("slots", "norm_rope_fwd", "quantize", "dequantize"):
         return 256
     if kind == "norm_rope_bwd":
         return int(lib.dsa_norm_rope_bwd_workspace_size(int(b)))
     if kind == "mla":
         return int(lib.dsa_paged_mla_workspace_size())
+    if kind == "mla_quant":
+        return int(lib.dsa_paged_mla_quant_workspace_size())
     if kind == "topk":
         return int(lib.dsa_paged_indexer_topk_workspace_size(int(a), int(b)))
     raise ValueError(f"unknown workspace kind {kind!r}")
@@ -886,18 +900,31 @@ def dsa_rope_frequencies(rope_dim: int, base: float = 10000.0, factor: float = 1
     return host.to("cuda" if device is None else device), scale.value
 
 
-def _paged(cache, D, block_table, seq_lens, cu_q, N, dev):
+def _paged(cache, D, block_table, seq_lens, cu_q, N, dev, dtype=torch.bfloat16):
     """Pointers and sizes of a paged cache: (cache, table, lengths, cu_q, B, num_pages, page_size, max_pages)."""
     p_len = _dense(seq_lens, "seq_lens", torch.int32, (None,), dev)
     B = seq_lens.shape[0]
     p_tab = _dense(block_table, "block_table", torch.int32, (B, None), dev)
-    p_cache = _dense(cache, "cache", torch.bfloat16, (None, None, D), dev)
+    p_cache = _dense(cache, "cache", dtype, (None, None, D), dev)
     p_cu = None
     if cu_q is not None:
         p_cu = _dense(cu_q, "cu_q", torch.int32, (B + 1,), dev)
     elif N != B:
         raise ValueError(f"without cu_q every request has one token: {N} tokens, {B} requests")
     return p_cache, p_tab, p_len, p_cu, B, cache.shape[0], cache.shape[1], block_table.shape[1]
+
+
+def _lists(topk_idx, topk_len, N, dev):
+    """(K, pointer to the lists, pointer to their lengths), or (0, None, None) without lists."""
+    if topk_idx is None:
+        if topk_len is not None:
+            raise ValueError("topk_len needs topk_idx")
+        return 0, None, None
+    p_idx = _dense(topk_idx, "topk_idx", torch.int32, (N, None), dev)
+    K = topk_idx.shape[1]
+    if K == 0:  # (an array without entries has no address: the library would take it for no lists at all)
+        raise ValueError("topk_idx must have a column at least (an entry of -1 names no position)")
+    return K, p_idx, None if topk_len is None else _dense(topk_len, "topk_len", torch.int32, (N,), dev)
 
 
 def dsa_paged_mla(q, cache, block_table, seq_lens, softmax_scale: float, cu_q=None, topk_idx=None, topk_len=None,
@@ -913,16 +940,7 @@ def dsa_paged_mla(q, cache, block_table, seq_lens, softmax_scale: float, cu_q=No
     dev = q.device
     N, H, D = q.shape
     p_cache, p_tab, p_len, p_cu, B, pages, page, width = _paged(cache, D, block_table, seq_lens, cu_q, N, dev)
-    K, p_idx, p_tl = 0, None, None
-    if topk_idx is not None:
-        p_idx = _dense(topk_idx, "topk_idx", torch.int32, (N, None), dev)
-        K = topk_idx.shape[1]
-        if K == 0:  # (an array without entries has no address: the library would take it for no lists at all)
-            raise ValueError("topk_idx must have a column at least (an entry of -1 names no position)")
-        if topk_len is not None:
-            p_tl = _dense(topk_len, "topk_len", torch.int32, (N,), dev)
-    elif topk_len is not None:
-        raise ValueError("topk_len needs topk_idx")
+    K, p_idx, p_tl = _lists(topk_idx, topk_len, N, dev)
     p_sink = None if attn_sink is None else _dense(attn_sink, "attn_sink", torch.float32, (H,), dev)
     if out is None:
         out = torch.empty(N, H, Dv, dtype=torch.bfloat16, device=dev)
@@ -933,6 +951,103 @@ def dsa_paged_mla(q, cache, block_table, seq_lens, softmax_scale: float, cu_q=No
     ws, p_ws, wsb = _scratch(workspace, 0 if workspace is not None else paged_workspace_size("mla"), dev)
     _call(lib.dsa_paged_mla, "dsa_paged_mla", dev, p_q, p_cache, p_tab, p_len, p_cu, p_idx, p_tl, N, B, H, D, Dv, K,
           pages, page, width, softmax_scale, p_sink, p_out, p_lse, p_ws, wsb)
+    return out, lse
+
+
+def paged_quant_row_bytes(D: int, bits: int, quant_dim: int | None = None) -> int:
+    """Bytes of a row of D channels in a quantised cache (uint8 [num_pages, page_size, row bytes]) whose first quant_dim
+    channels (default: 512, or all of fewer) are held in 8 or 4 bits; the format is described in include/dsa.h."""
+    lib = _lib or load_library()
+    q = min(int(D), 512) if quant_dim is None else int(quant_dim)
+    n = int(lib.dsa_paged_quant_row_bytes(int(D), q, int(bits)))
+    if n == 0:
+        raise ValueError(f"no such rows: D = {D}, quant_dim = {q}, bits = {bits} (bits 8 or 4, quant_dim a multiple of 64, "
+                         "D <= 1024, the other channels a multiple of 8)")
+    return n
+
+
+def dsa_paged_quantize(x, cache, bits: int, quant_dim: int | None = None, out_rows=None, workspace=None):
+    """Rows of bf16 x [T, D] (any token stride, contiguous channels), quantised as they are written to a cache of 8 or 4
+    bits -> cache, uint8 [rows, row bytes] or [num_pages, page_size, row bytes] with row bytes of paged_quant_row_bytes(D,
+    bits, quant_dim).  quant_dim: so many of the first channels are quantised (default: 512, or all of fewer), the others
+    stay bf16.  out_rows: int32 [T], the cache row of each token (-1: none; a row named twice holds bytes of both results),
+    e.g. the slots of dsa_paged_slots; None: row t.  A row whose channels are not all finite reads back as NaN.
+    workspace: uint8 [paged_workspace_size("quantize")], zeroed once, where errors (rows outside the cache) stay until
+    dsa_read_device_status reads them; None: one that is dropped, and the error with it."""
+    lib = _lib or load_library()
+    p_x, xt, _, T, _, D = _rows_of(x, "x", None)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T, D], got shape {tuple(x.shape)}")
+    dev = x.device
+    q = min(D, 512) if quant_dim is None else int(quant_dim)
+    width = paged_quant_row_bytes(D, bits, q)
+    paged = isinstance(cache, torch.Tensor) and cache.dim() == 3
+    p_c = _dense(cache, "cache", torch.uint8, (None, None, width) if paged else (None, width), dev)
+    p_rows = None if out_rows is None else _dense(out_rows, "out_rows", torch.int32, (T,), dev)
+    rows = cache.shape[0] * cache.shape[1] if paged else cache.shape[0]
+    ws, p_ws, wsb = _scratch(workspace, 256, dev)
+    _call(lib.dsa_paged_quantize, "dsa_paged_quantize", dev, p_x, xt, T, D, q, int(bits), p_c, rows, p_rows, p_ws, wsb)
+    return cache
+
+
+def dsa_paged_dequantize(cache, block_table, cu_rows, bits: int, D: int, quant_dim: int | None = None, first=None,
+                         N: int | None = None, out=None, workspace=None):
+    """Rows of requests read back from a quantised cache (uint8 [num_pages, page_size, row bytes], or [rows, row bytes]
+    with pages of one row) -> out bf16 [N, D].  Rows cu_rows[b] .. cu_rows[b+1] - 1 (int32 [B+1]) of out are request b's
+    positions first[b], first[b] + 1, ... (int32 [B]; None: from 0) through block_table int32 [B, max_pages].  Rows named
+    one by one: pages of one row, and the list as the table of one request.  out: any token stride, its other rows are
+    left as they are; None: a new one of N rows (required then).  workspace: uint8 [paged_workspace_size("dequantize")],
+    zeroed once, where errors (bad pages and positions; such rows are zeros) stay until dsa_read_device_status reads them;
+    None: one that is dropped, and the error with it."""
+    lib = _lib or load_library()
+    p_cu = _dense(cu_rows, "cu_rows", torch.int32, (None,), None)
+    dev = cu_rows.device
+    B = cu_rows.shape[0] - 1
+    if B < 0:
+        raise ValueError("cu_rows must have an entry at least")
+    p_tab = _dense(block_table, "block_table", torch.int32, (B, None), dev)
+    p_first = None if first is None else _dense(first, "first", torch.int32, (B,), dev)
+    D = int(D)
+    q = min(D, 512) if quant_dim is None else int(quant_dim)
+    width = paged_quant_row_bytes(D, bits, q)
+    paged = isinstance(cache, torch.Tensor) and cache.dim() == 3
+    p_c = _dense(cache, "cache", torch.uint8, (None, None, width) if paged else (None, width), dev)
+    if out is None:
+        if N is None:
+            raise ValueError("N (rows of the output) must be given without out")
+        out = torch.empty(int(N), D, dtype=torch.bfloat16, device=dev)
+    p_o, ot, _, n, _, oD = _rows_of(out, "out", dev)
+    if out.dim() != 2 or oD != D or (N is not None and n != int(N)):
+        raise ValueError(f"out must be [{'N' if N is None else int(N)}, {D}], got shape {tuple(out.shape)}")
+    ws, p_ws, wsb = _scratch(workspace, 256, dev)
+    _call(lib.dsa_paged_dequantize, "dsa_paged_dequantize", dev, p_c, p_tab, p_first, p_cu, n, B, D, q, int(bits),
+          cache.shape[0], cache.shape[1] if paged else 1, block_table.shape[1], p_o, max(ot, D) if n <= 1 else ot, p_ws, wsb)
+    return out
+
+
+def dsa_paged_mla_quant(q, cache, block_table, seq_lens, softmax_scale: float, bits: int, cu_q=None, topk_idx=None,
+                        topk_len=None, attn_sink=None, out=None, lse=None, workspace=None, Dv: int = 512):
+    """dsa_paged_mla over a cache of latents in 8 or 4 bits (uint8 [num_pages, page_size, paged_quant_row_bytes(Dqk,
+    bits)], rows of dsa_paged_quantize) -> (out bf16 [N,H,Dv], lse fp32 [N,H]); the other arguments as there.  workspace:
+    uint8 [paged_workspace_size("mla_quant", N, H)], zeroed once, where errors (bad pages and positions, waits that ran out)
+    stay until dsa_read_device_status reads them; None: one that is dropped, and the error with it."""
+    lib = _lib or load_library()
+    p_q = _dense(q, "q", torch.bfloat16, (None, None, None), None)
+    dev = q.device
+    N, H, D = q.shape
+    width = paged_quant_row_bytes(D, bits, 512)
+    p_cache, p_tab, p_len, p_cu, B, pages, page, table = _paged(cache, width, block_table, seq_lens, cu_q, N, dev, torch.uint8)
+    K, p_idx, p_tl = _lists(topk_idx, topk_len, N, dev)
+    p_sink = None if attn_sink is None else _dense(attn_sink, "attn_sink", torch.float32, (H,), dev)
+    if out is None:
+        out = torch.empty(N, H, Dv, dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty(N, H, dtype=torch.float32, device=dev)
+    p_out = _dense(out, "out", torch.bfloat16, (N, H, Dv), dev)
+    p_lse = _dense(lse, "lse", torch.float32, (N, H), dev)
+    ws, p_ws, wsb = _scratch(workspace, 0 if workspace is not None else paged_workspace_size("mla_quant"), dev)
+    _call(lib.dsa_paged_mla_quant, "dsa_paged_mla_quant", dev, p_q, p_cache, p_tab, p_len, p_cu, p_idx, p_tl, N, B, H, D,
+          Dv, int(bits), K, pages, page, table, softmax_scale, p_sink, p_out, p_lse, p_ws, wsb)
     return out, lse
 
 
