@@ -104,10 +104,9 @@ __device__ __forceinline__ Seg unpack(const int4 a, const int4 c) {
   return s;
 }
 
-// Announcement k, read by a whole warp; false when the wait ran out.  (A function of its own: called once per segment,
-// and kept out of the roles' loops.)
-__device__ __noinline__ static bool read_announcement(uint32_t full, uint32_t empty, const int4* ring, int k,
-                                                      volatile int* abort, long long limit, Seg& s) {
+// Announcement k, read by a whole warp; false when the wait ran out.
+__device__ __forceinline__ bool read_announcement_here(uint32_t full, uint32_t empty, const int4* ring, int k,
+                                                       volatile int* abort, long long limit, Seg& s) {
   const int at = k % kSegs;
   if (!__all_sync(0xffffffffu, wait_for(full + 8 * at, (k / kSegs) & 1, abort, limit))) return false;
   s = unpack(ring[2 * at], ring[2 * at + 1]);
@@ -115,12 +114,21 @@ __device__ __noinline__ static bool read_announcement(uint32_t full, uint32_t em
   if ((threadIdx.x & 31) == 0) mbar_arrive(empty + 8 * at);
   return true;
 }
+// (As a function of its own: called once per segment, and kept out of the roles' loops.)
+__device__ __noinline__ static bool read_announcement(uint32_t full, uint32_t empty, const int4* ring, int k,
+                                                      volatile int* abort, long long limit, Seg& s) {
+  return read_announcement_here(full, empty, ring, k, abort, limit, s);
+}
 
 // The announcing warp: the segments of the CTA's range, one after the other, into a ring that the other warps read.
 // One copy of this code and of its loads, instead of one per role.
-template <int TILE>
+// after(k) is called when number k has been announced.
+struct Nothing {
+  __device__ __forceinline__ void operator()(int) const {}
+};
+template <int TILE, class F = Nothing>
 __device__ __forceinline__ void announce(const GroupParams& p, const Plan& pl, uint32_t full, uint32_t empty, int4* ring,
-                                         volatile int* abort) {
+                                         volatile int* abort, const F& after = F()) {
   const int lane = threadIdx.x & 31;
   long long left = pl.w1 - pl.w0 - pl.skip;
   int u = pl.u, g = pl.g, t = pl.t;
@@ -168,6 +176,7 @@ __device__ __forceinline__ void announce(const GroupParams& p, const Plan& pl, u
       mbar_arrive(full + 8 * at);
     }
     if (t >= un.tiles) { ++g; t = 0; }
+    after(k);
   }
   if (cut && lane == 0) record_error(p.err, DSA_ERR_DEVICE_INDEX);  // the table does not hold a request
 }

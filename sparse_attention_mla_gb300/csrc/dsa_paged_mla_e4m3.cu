@@ -1,0 +1,733 @@
+// dsa_paged_mla_e4m3.cu -- attention of new tokens over a paged cache of latents in 8 bits (sm_103a).
+//
+// For new token j of request b and head h:  z_p = scale <q, kv_p> over the positions p it sees,
+// lse = ln sum e^{z_p},  out = sum e^{z_p - lse} kv_p[0:512],  kv_p = code_p s_p (e4m3 times the row's power of two) for the
+// first 512 channels, bf16 for the position channels.
+//
+// The codes go into the products as they lie in the cache: nothing is converted, and shared memory holds 640 bytes a
+// position in place of 1152.  s_p stays outside: z_p = s_p <q, code_p> + <q', kv'_p>, the output sums the weights
+// w_p = e^{z_p} s_p, and the running maximum is that of w.  The other operands become sums of 8-bit numbers:
+//  - a query row, divided by a power of two so that its largest channel lies in [2^7, 2^8), is hi + lo, both e4m3: exact
+//    down to 2^-2, and to 2^-10 (2^-17 of the largest channel) below;
+//  - a weight is hi + lo, hi e5m2 (2^15 down to 2^-16) and lo e4m3: 7 to 8 bits above 2^-3 and, where lo runs out, to 2^-10;
+//    the largest weight of a row is between 2^5 and 2^11 (the maximum is raised lazily), so that this is 2^-15 of it.
+// S^T is three sums side by side (hi, lo and the position channels in bf16, which s_p must not reach) that the softmax adds.
+//
+// Split of the work as in dsa_paged_groups.cuh, with tiles of 64 positions and groups of NH = 16 or 64 columns.  A tile:
+// S^T[key, row] = KV Q^T (M = 64 keys; N = hi and lo rows), an online softmax with a lazily raised maximum,
+// O^T[channel, row] += V^T W^T (M = 128 channels, K = 32 keys, hi and then lo into the same columns).  The codes of 128
+// channels of a key are a row of 128 bytes, which is K-major for the first product and M-major for the second.
+//
+// Warps: 0 issues S^T, 1-8 softmax and epilogue, 9-12 copy tiles into a ring of three, 13 issues P.V, 14 announces the
+// runs of tiles that the CTA's range consists of.
+#include <climits>
+#include <cmath>
+
+#include "dsa_f32x2.cuh"
+#include "dsa_paged_groups.cuh"
+#include "dsa_paged_mla_quant.h"
+#include "dsa_paged_quant.cuh"
+
+namespace dsa {
+namespace pmla8 {
+
+using namespace pgroups;
+
+constexpr int kTile = 64;
+constexpr int kWorkers = 256;
+constexpr int kGather = 128;
+constexpr int kThreads = 32 + kWorkers + kGather + 64;
+constexpr int kReaders = 2 + kWorkers / 32 + kGather / 32;  // warps that read an announcement
+constexpr float kRaise = 11.0f;  // log2 units: the running maximum is raised when a weight passes 2^11
+constexpr float kTop = 5.0f;     // a new maximum is 2^5
+constexpr float kLeast = 3.5527136788005009e-15f;  // 2^-48, the least s
+
+template <int DQK, int NH>
+struct Smem {
+  static constexpr bool ROPE = DQK == 576;
+  static constexpr QuantRow LAY = quant_row(DQK, kDv, 8);
+  static constexpr int NCH = ROPE ? 5 : 4;      // 128 codes each, then the position channels
+  static constexpr int CHUNK = kTile * 128;
+  static constexpr int Q_CHUNK = 2 * NH * 128;  // hi rows, lo rows
+  static constexpr int R = 3;                   // tiles in the ring
+  static constexpr int NS = NH == 64 ? 1 : 2;   // S^T buffers in TMEM
+  static constexpr int SW = (ROPE ? 3 : 2) * NH;
+  static constexpr int P_BLOCK = NH == 64 ? kTile * 128 : 2 * NH * 128;
+  static constexpr int OFF_KV = 0;
+  static constexpr int OFF_Q = R * NCH * CHUNK;
+  static constexpr int OFF_P = OFF_Q + 4 * Q_CHUNK + (ROPE ? (NH * 128 + 1023) / 1024 * 1024 : 0);
+  static constexpr int OFF_MISC = OFF_P + 2 * P_BLOCK;
+  static constexpr int MISC = 4096;
+  static constexpr int TOTAL = OFF_MISC + MISC;
+  static_assert(TOTAL <= 232448 && OFF_P % 1024 == 0 && P_BLOCK % 1024 == 0, "shared memory budget");
+  static constexpr int TM_O = (NS * SW + 31) / 32 * 32;
+  static constexpr int TM_COLS = NH == 64 ? 512 : 256;
+  static_assert(TM_O + 4 * NH <= TM_COLS, "TMEM budget");
+};
+
+// misc (bytes).  A tile's channels are given back 128 at a time as P.V reads them.
+constexpr int kSteps = 4, kSlots = 3;
+constexpr int M_KV = 0, M_PV = 48, M_S = 144, M_SF = 160, M_P = 176, M_Q = 192, M_FIN = 200;  // [3] [3][4] [2] [2] [2] 1 [2]
+constexpr int M_SEGF = 216, M_SEGE = M_SEGF + 8 * kSegs;  // [kSegs] each: announced, read by all
+constexpr int M_TMEM = 344, M_ABORT = 348, M_PLAN = 352;  // plan: 56 bytes
+constexpr int M_SEG = 416;                    // int4 [kSegs][2]
+constexpr int M_RED = 672;                    // float [4][64]; the first row also holds the factors of a rescale
+constexpr int M_STAT = M_RED + 1024;          // float [64]
+constexpr int M_COL = M_STAT + 256;           // float [2][64]: a column's factor of the score, by run
+constexpr int M_SCALE = M_COL + 512;          // float [kSlots][64]: s of the rows, -1: masked
+static_assert(M_SEGE + 8 * kSegs <= M_TMEM && M_PLAN + 56 <= M_SEG && M_SCALE + kSlots * 256 <= 4096, "misc layout");
+
+struct Params : GroupParams {
+  const __nv_bfloat16* q;
+  const uint8_t* cache;
+  float sl2e;
+};
+
+// Instruction descriptor for kind::f8f6f4 with fp32 D: formats 0 e4m3, 1 e5m2.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_format, int b_format, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | ((uint32_t)a_format << 7) | ((uint32_t)b_format << 10) | ((a_mn_major ? 1u : 0u) << 15) |
+         ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// As mma4_w, of two or four MMAs of 8-bit operands (32 elements of K each).
+template <int N, int SA, int SB>
+__device__ __forceinline__ void mma_f8_w(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add_first) {
+  static_assert(N == 2 || N == 4, "MMAs");
+  if constexpr (N == 4) {
+    asm volatile(
+        "{\n\t.reg .pred p, q, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 q, 0, 0;\n\t"
+        "add.s64 a1, %1, %5;\n\tadd.s64 a2, %1, %6;\n\tadd.s64 a3, %1, %7;\n\t"
+        "add.s64 b1, %2, %8;\n\tadd.s64 b2, %2, %9;\n\tadd.s64 b3, %2, %10;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, q;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(add_first), "n"(SA), "n"(2 * SA), "n"(3 * SA), "n"(SB), "n"(2 * SB), "n"(3 * SB)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p, q, e;\n\t.reg .b64 a1, b1;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 q, 0, 0;\n\t"
+        "add.s64 a1, %1, %5;\n\tadd.s64 b1, %2, %6;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, q;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(add_first), "n"(SA), "n"(SB)
+        : "memory");
+  }
+}
+
+// Two values to e4m3 or e5m2 (the first in the lower half), and e5m2 back.
+__device__ __forceinline__ uint32_t e4m3x2(float2 v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(v.y), "f"(v.x));
+  return r;
+}
+__device__ __forceinline__ uint32_t e5m2x2(float2 v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(v.y), "f"(v.x));
+  return r;
+}
+__device__ __forceinline__ float2 e5m2x2_floats(uint32_t v) {  // (the upper half of an fp16 number)
+  return f16x2_floats(__byte_perm(v, 0, 0x1404));
+}
+__device__ __forceinline__ float2 e4m3x2_floats(uint32_t v) { return f16x2_floats(e4m3x2_f16x2((uint16_t)v)); }
+__device__ __forceinline__ float2 minus2(float2 a, float2 b) { return add2(a, make_float2(-b.x, -b.y)); }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }  // -126 <= e <= 127
+
+// 16 TMEM lanes x 64 bits, N times: thread t of the warp gets lane base + (t >> 2) + 8 (t & 1) and the columns
+// c + 2j + ((t >> 1) & 1), j = 0..N-1.
+template <int N>
+__device__ __forceinline__ void tmem_ld16x64b(uint32_t a, uint32_t (&r)[N]) {
+  if constexpr (N == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.16x64b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+  } else {
+    static_assert(N == 16, "columns per thread");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x64b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(a));
+  }
+}
+
+template <int DQK, int NH>
+__global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __grid_constant__ Params p) {
+  using L = Smem<DQK, NH>;
+  constexpr bool ROPE = L::ROPE;
+  constexpr int NCH = L::NCH, R = L::R, NS = L::NS;
+  constexpr int NHH = NH / 2, NQ = NHH / 2;  // rows per softmax half, per thread
+  static_assert(R == kSlots, "ring");
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sKV = smem_u32(smem) + L::OFF_KV, sQ = smem_u32(smem) + L::OFF_Q, sP = smem_u32(smem) + L::OFF_P;
+  uint8_t* misc = smem + L::OFF_MISC;
+  const uint32_t mb = smem_u32(misc);
+  const uint32_t bar_kv = mb + M_KV, bar_pv = mb + M_PV, bar_s = mb + M_S, bar_sf = mb + M_SF, bar_p = mb + M_P,
+                 bar_q = mb + M_Q, bar_fin = mb + M_FIN;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc + M_TMEM);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(misc + M_ABORT);
+  Plan* s_plan = reinterpret_cast<Plan*>(misc + M_PLAN);
+  volatile float* s_scale = reinterpret_cast<volatile float*>(misc + M_SCALE);
+  float* s_stat = reinterpret_cast<float*>(misc + M_STAT);
+  float* s_fac = reinterpret_cast<float*>(misc + M_RED);  // a column's factor replaces its first maximum or sum
+  float* s_red = reinterpret_cast<float*>(misc + M_RED);
+  float* s_col = reinterpret_cast<float*>(misc + M_COL);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // tile i has landed; P.V has read 128 of its channels (3: all of it)
+  auto wait_kv = [&](int i) { return wait_for(bar_kv + 8 * (i % R), (i / R) & 1, s_abort, p.wait_limit); };
+  auto wait_pv = [&](int i, int m) {
+    return wait_for(bar_pv + 8 * ((i % R) * kSteps + m), (i / R) & 1, s_abort, p.wait_limit);
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < R; ++s) {
+      mbar_init(bar_kv + 8 * s, 4 * 33);  // four warps: each lane's copies, and what the warp has stored
+      for (int m = 0; m < kSteps; ++m) mbar_init(bar_pv + 8 * (s * kSteps + m), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar_s + 8 * b, 1);
+      mbar_init(bar_sf + 8 * b, 8);
+      mbar_init(bar_p + 8 * b, 8);
+      mbar_init(bar_fin + 8 * b, 1);
+    }
+    mbar_init(bar_q, 8);
+    for (int k = 0; k < kSegs; ++k) {
+      mbar_init(mb + M_SEGF + 8 * k, 1);
+      mbar_init(mb + M_SEGE + 8 * k, kReaders);
+    }
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  make_plan<kTile, kThreads>(p, s_plan, reinterpret_cast<long long*>(s_red));
+  const Plan plan = *s_plan;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the joining kernel waits for this one's end itself)
+  if (plan.w1 <= plan.w0 || plan.w1 - plan.w0 <= plan.skip) return;  // (the whole CTA)
+  if (warp == 0) {
+    tmem_alloc(smem_u32(s_tmem), L::TM_COLS);
+    tmem_relinquish();
+  }
+  uint32_t tmem = 0;
+  if (warp <= 8 || warp == 13) {  // the others neither need it nor wait for it
+    named_bar(3, 320);
+    tmem = (uint32_t)warp_value((int)*s_tmem);
+  }
+  // announcement k, once per warp
+  auto read_seg = [&](int k, Seg& s) -> bool {
+    return read_announcement(mb + M_SEGF, mb + M_SEGE, reinterpret_cast<const int4*>(misc + M_SEG), k, s_abort, p.wait_limit, s);
+  };
+  if (warp == 0) {
+    // ======================= S^T issuer =======================
+    constexpr uint32_t kIdS = idesc_f8(kTile, 2 * NH, 0, 0, false, false), kIdR = idesc_bf16(kTile, NH, false, false);
+    int done = 0;
+    for (int seg = 0, last = 0; !last; ++seg) {
+      Seg sg;
+      if (!warp_all(read_seg(seg, sg))) break;
+      last = warp_value(sg.last ? 1 : 0);
+      if (!warp_all(wait_for(bar_q, seg & 1, s_abort, p.wait_limit))) break;
+      // what the loop needs in registers of the warp (a call does not keep them)
+      const int n = warp_value(sg.n);
+      const uint32_t d0 = (uint32_t)warp_value((int)tmem), q0 = (uint32_t)warp_value((int)sQ), kv0 = (uint32_t)warp_value((int)sKV);
+      int i = warp_value(done);
+      done += n;
+      bool stop = false;
+#pragma unroll 1
+      for (int k0 = 0; k0 < n; ++k0, ++i) {
+        const int sl = i % R, sb = i % NS;
+        if (i >= NS && !warp_all(wait_for(bar_sf + 8 * sb, ((i / NS) - 1) & 1, s_abort, p.wait_limit))) { stop = true; break; }
+        const uint64_t a0 = sdesc_sw128(kv0, 16, 1024) + (uint64_t)(uint32_t)(sl * NCH * (L::CHUNK >> 4));
+        const uint64_t b0 = sdesc_sw128(q0, 16, 1024);
+        if (!warp_all(wait_kv(i))) { stop = true; break; }
+        fence_proxy_async_smem();  // (the rows came by cp.async)
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          mma_f8_w<4, 2, 2>(d0 + sb * L::SW, a0 + c * (L::CHUNK >> 4), b0 + c * (L::Q_CHUNK >> 4), kIdS, c);
+        if (ROPE) mma4_w<2, 2>(d0 + sb * L::SW + 2 * NH, a0 + 4 * (L::CHUNK >> 4), b0 + 4 * (L::Q_CHUNK >> 4), kIdR, 0);
+        mma_commit_w(bar_s + 8 * sb);
+      }
+      if (stop) break;
+    }
+    mma_commit_w(bar_fin);
+    volatile int dummy = 0;
+    mbar_wait(bar_fin, 0, &dummy, p.err);
+    __syncwarp();
+  } else if (warp == 13) {
+    // ======================= P.V issuer =======================
+    int done = 0;
+    for (int seg = 0, last = 0; !last; ++seg) {
+      Seg sg;
+      if (!warp_all(read_seg(seg, sg))) break;
+      last = warp_value(sg.last ? 1 : 0);
+      const int n = warp_value(sg.n);
+      const uint32_t d0 = (uint32_t)warp_value((int)tmem), kv0 = (uint32_t)warp_value((int)sKV), p0 = (uint32_t)warp_value((int)sP);
+      int i = warp_value(done);
+      done += n;
+      bool stop = false;
+#pragma unroll 1
+      for (int k0 = 0; k0 < n; ++k0, ++i) {
+        const int sl = i % R;
+        const uint32_t add = k0 > 0;  // the segment's first tile overwrites O^T
+        if (!warp_all(wait_for(bar_p + 8 * (i & 1), (i >> 1) & 1, s_abort, p.wait_limit))) { stop = true; break; }
+        fence_proxy_async_smem();
+        tc_fence_after();
+        constexpr uint32_t kIdHi = idesc_f8(128, NH, 0, 1, true, NH == 64), kIdLo = idesc_f8(128, NH, 0, 0, true, NH == 64);
+        const uint64_t va = sdesc_sw128(kv0, 16, 1024) + (uint64_t)(uint32_t)(sl * NCH * (L::CHUNK >> 4));
+        // W^T rows are keys, 64 bytes of hi and 64 of lo (NH = 64), or columns: hi rows, then lo rows, keys along K
+        const uint64_t pb = sdesc_sw128(p0, 16, 1024) + (uint64_t)(uint32_t)((i & 1) * (L::P_BLOCK >> 4));
+        constexpr int kLo = NH == 64 ? 64 >> 4 : NH * 128 >> 4, kStep = NH == 64 ? 32 * 128 >> 4 : 2;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const uint64_t a = va + m * (L::CHUNK >> 4);
+          mma_f8_w<2, (32 * 128 >> 4), kStep>(d0 + L::TM_O + m * NH, a, pb, kIdHi, add);
+          mma_f8_w<2, (32 * 128 >> 4), kStep>(d0 + L::TM_O + m * NH, a, pb + kLo, kIdLo, 1);
+          mma_commit_w(bar_pv + 8 * (sl * kSteps + m));
+        }
+      }
+      if (stop) break;
+    }
+    mma_commit_w(bar_fin + 8);
+    volatile int dummy = 0;
+    mbar_wait(bar_fin + 8, 0, &dummy, p.err);
+    __syncwarp();
+  } else if (warp == 14) {
+    announce<kTile>(p, plan, mb + M_SEGF, mb + M_SEGE, reinterpret_cast<int4*>(misc + M_SEG), s_abort);
+  } else if (warp >= 9) {
+    // ======================= gather: 16 rows of every tile each =======================
+    // By cp.async, which takes any row, a warp's instruction the 512 codes of one (8 cycles; boxes of 128 bytes by TMA take as
+    // long as rows of bf16, since a row begins anywhere in a line), and says itself when it has landed; what is masked is
+    // filled with zeros.  A lane looks one row up, in steps whose loads have a tile's time to come back: the list's entry
+    // (three tiles ahead), the page (two ahead), the row number and its s (one ahead).
+    constexpr int kRows = kTile / 4;
+    const int gw = warp - 9;
+    Seg sg;
+    int seg = 0, base = 0, end = 0, limit = 0;  // this CTA's tiles [base, end) are the segment's
+    int n_tiles = INT_MAX;                      // this CTA's tiles, known once one past them has been looked for
+    struct Look {
+      int pos, b, limit;  // position (then its place in the page), or -1; request; what the position has to stay below
+    };
+    bool bad_index = false, stop = false;
+    auto position = [&](int i) -> Look {
+      Look k{-1, 0, 0};
+      if (i < n_tiles && !stop) {
+#pragma unroll 1
+        while (i >= end) {
+          if (seg > 0 && sg.last) { n_tiles = end; return k; }
+          if (!read_seg(seg, sg)) { stop = true; return k; }
+          ++seg;
+          base = end;
+          end += sg.n;
+          limit = (int)min((long long)p.max_pages * p.P, (long long)(p.topk_idx ? sg.seen0 : sg.keys));
+        }
+        k.b = sg.b;
+        k.limit = limit;
+        const int j = (sg.t0 + i - base) * kTile + gw * kRows + lane;
+        if (lane < kRows && j < sg.keys) k.pos = p.topk_idx ? __ldg(p.topk_idx + (size_t)(sg.row0 / p.H) * p.K + j) : j;
+      }
+      return k;
+    };
+    auto page_of = [&](Look& k) -> int {
+      if (k.pos < -1 || k.pos >= k.limit) {
+        bad_index |= k.pos != -1;
+        k.pos = -1;
+      }
+      if (k.pos < 0) return -1;
+      const unsigned at = (unsigned)k.pos / (unsigned)p.P;
+      k.pos -= (int)at * p.P;
+      return __ldg(p.table + (size_t)k.b * p.max_pages + at);
+    };
+    auto row_of = [&](int pos, int page, float& s) -> int {
+      s = -1.f;
+      if (pos < 0) return -1;
+      if (page >= 0 && page < p.num_pages) {
+        const int row = page * p.P + pos;
+        s = __ldg(reinterpret_cast<const float*>(p.cache + (size_t)row * L::LAY.bytes + L::LAY.scale));
+        return row;
+      }
+      bad_index = true;
+      return -1;
+    };
+    Look look[3];
+    int page[2], row[2];  // rows of the next two tiles, and their s
+    float scale[2];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) look[k] = position(k);
+    page[0] = page_of(look[0]);
+    page[1] = page_of(look[1]);
+    row[0] = row_of(look[0].pos, page[0], scale[0]);
+    row[1] = row_of(look[1].pos, page[1], scale[1]);
+    look[0] = look[2];
+    page[0] = page_of(look[0]);
+    look[1] = position(3);
+#pragma unroll 1
+    for (int i = 0; i < n_tiles && !stop; ++i) {
+      const int sl = i % R;
+      if (i >= R && !warp_all(wait_pv(i - R, 3))) { stop = true; break; }
+      if (lane < kRows) s_scale[sl * kTile + gw * kRows + lane] = scale[0] >= 0.f && scale[0] < kLeast ? kLeast : scale[0];
+      const uint32_t to = sKV + sl * NCH * L::CHUNK;
+#pragma unroll
+      for (int x0 = 0; x0 < kRows; x0 += 8) {  // eight rows at a time: a copy's registers are free only when it has been taken
+        const uint8_t* src[8];
+        uint32_t size[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          const int at = __shfl_sync(0xffffffffu, row[0], x0 + y);
+          src[y] = p.cache + (size_t)max(at, 0) * L::LAY.bytes + lane * 16;
+          size[y] = at >= 0 ? 16u : 0u;
+        }
+#pragma unroll
+        for (int y = 0; y < 8; ++y)
+          cp_async16(to + (lane >> 3) * L::CHUNK + sw128_off(gw * kRows + x0 + y, lane & 7), src[y], size[y]);
+      }
+      if constexpr (ROPE) {
+#pragma unroll
+        for (int x0 = 0; x0 < kRows; x0 += 4) {  // four rows' position channels
+          const int at = __shfl_sync(0xffffffffu, row[0], x0 + (lane >> 3));
+          cp_async16(to + 4 * L::CHUNK + sw128_off(gw * kRows + x0 + (lane >> 3), lane & 7),
+                     p.cache + (size_t)max(at, 0) * L::LAY.bytes + L::LAY.tail + (lane & 7) * 16, at >= 0 ? 16u : 0u);
+        }
+      }
+      cp_async_arrive(bar_kv + 8 * sl);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_kv + 8 * sl);
+      row[0] = row[1];
+      scale[0] = scale[1];
+      row[1] = row_of(look[0].pos, page[0], scale[1]);
+      look[0] = look[1];
+      page[0] = page_of(look[0]);
+      look[1] = position(i + 4);
+    }
+    if (bad_index) record_error(p.err, DSA_ERR_DEVICE_INDEX);
+    asm volatile("cp.async.wait_all;" ::: "memory");  // nothing lands after the CTA has left
+  } else {
+    // ======================= softmax + epilogue =======================
+    const int wk = warp - 1, qd = warp & 3, ch = wk >> 2;
+    const int par = (lane >> 1) & 1;
+    const int r = qd * 16 + (lane >> 2) + 8 * (lane & 1);  // key row of the tile
+    const int bar_id = 1 + ch;
+    const int n0 = ch * NHH + par * NQ;  // this thread's rows n0 .. n0 + NQ - 1 of the group
+    // The run's queries: a row a warp, as hi and lo, and what the sums of a column are to be multiplied by.
+    auto load_q = [&](const Seg& s, int run) {
+#pragma unroll 2
+      for (int hh = wk; hh < NH; hh += kWorkers / 32) {
+        constexpr int UNITS = DQK / 8;
+        uint4 v[3];
+        uint32_t top = 0;
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+          const int u = lane + 32 * x;
+          v[x] = make_uint4(0, 0, 0, 0);
+          if (hh < s.rows && u < UNITS) v[x] = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)(s.row0 + hh) * DQK) + u);
+          if (x < 2)
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[x].x & 0x7fff7fffu, v[x].y & 0x7fff7fffu),
+                                         __vmaxu2(v[x].z & 0x7fff7fffu, v[x].w & 0x7fff7fffu)));
+        }
+        const uint32_t most = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+        const int e = max((int)(most >> 7) - 127, -119);
+        const float by = pow2(7 - e);
+        // (a row with a channel that is not finite gives NaN)
+        if (lane == 0) s_col[(run & 1) * 64 + hh] = most >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e - 7) * p.sl2e;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int u = lane + 32 * x;
+          const uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const float2 a = make_float2(__uint_as_float(w[g] << 16) * by, __uint_as_float(w[g] & 0xffff0000u) * by);
+            hi[g] = e4m3x2(a);
+            lo[g] = e4m3x2(minus2(a, e4m3x2_floats(hi[g])));
+          }
+          const uint32_t at = sQ + (u >> 4) * L::Q_CHUNK + (u & 1) * 8;
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + sw128_off(hh, (u & 15) >> 1)), "r"(hi[0] | hi[1] << 16), "r"(hi[2] | hi[3] << 16) : "memory");
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + sw128_off(NH + hh, (u & 15) >> 1)), "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16) : "memory");
+        }
+        if (ROPE && lane < 8) st_shared_v4(sQ + 4 * L::Q_CHUNK + sw128_off(hh, lane), v[2].x, v[2].y, v[2].z, v[2].w);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_q);
+    };
+    // Maxima or sums over the warp's 16 keys of all NQ rows of a thread: the result is that of row sum_row.
+    auto over_keys = [&](float (&v)[NQ], bool is_max) -> float {
+      constexpr int kBit[4] = {16, 8, 4, 1};  // the lanes of one parity
+      int w = 8;
+#pragma unroll
+      for (int s = 0; s < 4; ++s, w >>= 1) {
+        const bool upper = (lane & kBit[s]) != 0;
+        if (w >= NQ) {
+#pragma unroll
+          for (int j = 0; j < NQ; ++j) {
+            const float x = __shfl_xor_sync(0xffffffffu, v[j], kBit[s]);
+            v[j] = is_max ? fmaxf(v[j], x) : v[j] + x;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < w; ++j) {
+            const float send = upper ? v[j] : v[j + w], keep = upper ? v[j + w] : v[j];
+            const float x = __shfl_xor_sync(0xffffffffu, send, kBit[s]);
+            v[j] = is_max ? fmaxf(keep, x) : keep + x;
+          }
+        }
+      }
+      return v[0];
+    };
+    const int sum_row = n0 + (((lane >> 1) & 14) | (lane & 1)) % NQ;
+    Seg sg, nx;
+    // (one answer for the half: its warps meet at barriers from here on)
+    bool aborted = named_bar_or(bar_id, 128, !read_seg(0, sg));
+    if (!aborted) load_q(sg, 0);
+    nx = sg;
+    int i = 0;
+    for (int seg = 1; !aborted; ++seg) {
+      const bool more = !sg.last;
+      bool bad_seg = more && !read_seg(seg, nx);
+      // this thread's first row: its token in the group, and how many rows of that token there are from it on
+      const int tok0 = (sg.head0 + n0) / p.H, head_left = p.H - ((sg.head0 + n0) - tok0 * p.H);
+      // sums and minus the running maxima (log2 units) of this thread's rows, in pairs; a row without a finite score yet
+      // has a maximum of -3e38, which any finite score passes and which leaves e^-inf at 0
+      float2 l_part[NQ / 2], m_neg[NQ / 2];
+#pragma unroll
+      for (int j = 0; j < NQ / 2; ++j) { l_part[j] = make_float2(0.f, 0.f); m_neg[j] = make_float2(3.0e38f, 3.0e38f); }
+      if (qd == 0 && lane < NHH) s_stat[ch * NHH + lane] = -INFINITY;  // (read only after a barrier of the half)
+      const float* col = s_col + ((seg - 1) & 1) * 64 + n0;
+      const int t_end = sg.t0 + sg.n;
+#pragma unroll 1
+      for (int t = sg.t0; t < t_end; ++t, ++i) {
+        const int sl = i % R, sb = i % NS;
+        bool bad = bad_seg || !warp_all(wait_for(bar_s + 8 * sb, (i / NS) & 1, s_abort, p.wait_limit));
+        // (complete since before S^T was issued: order the rows' scales and the columns' factors before their reads below)
+        bad = bad || !warp_all(wait_kv(i));
+        if (t == sg.t0) bad = bad || !warp_all(wait_for(bar_q, (seg - 1) & 1, s_abort, p.wait_limit));
+        // W of tile i overwrites what P.V of tile i - 2 read
+        if (i >= 2) bad = bad || !warp_all(wait_pv(i - 2, 3));
+        tc_fence_after();
+        __syncwarp();
+        uint32_t raw[NQ];
+        float2 z[NQ / 2];  // (alternate columns of the half first)
+        const uint32_t ts = tmem_addr(tmem + sb * L::SW + ch * NHH, qd * 32, 0);
+        {
+          uint32_t lo[NQ], pos[NQ];
+          tmem_ld16x64b<NQ>(ts, raw);
+          tmem_ld16x64b<NQ>(ts + NH, lo);
+          if constexpr (ROPE) tmem_ld16x64b<NQ>(ts + 2 * NH, pos);
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_sf + 8 * sb);
+#pragma unroll
+          for (int j = 0; j < NQ; ++j) raw[j] = __float_as_uint(__uint_as_float(raw[j]) + __uint_as_float(lo[j]));
+          // -> NQ consecutive rows: swap half of them with the key's other thread
+          auto rows_of = [&](uint32_t (&x)[NQ], int j) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, par ? x[j] : x[NQ / 2 + j], 2);
+            return make_float2(__uint_as_float(par ? got : x[j]), __uint_as_float(par ? x[NQ / 2 + j] : got));
+          };
+          const float s = s_scale[sl * kTile + r], log_s0 = s > 0.f ? (float)((int)(__float_as_uint(s) >> 23) - 127) : 0.f;
+#pragma unroll
+          for (int j = 0; j < NQ / 2; ++j) {
+            const float2 f = mul2(*reinterpret_cast<const float2*>(col + 2 * j), make_float2(s, s));
+            float2 c = make_float2(log_s0, log_s0);
+            if constexpr (ROPE) c = fma2(rows_of(pos, j), make_float2(p.sl2e, p.sl2e), c);
+            z[j] = fma2(rows_of(raw, j), f, c);
+          }
+        }
+        if (t + 1 == t_end && more && !bad) load_q(nx, seg);  // S^T of the segment is done: Q is free
+        const float s = s_scale[sl * kTile + r];
+        const float inv_s = s > 0.f ? pow2(127 - (int)(__float_as_uint(s) >> 23)) : 1.f;
+        const int pos = t * kTile + r;
+        if (s < 0.f) {
+#pragma unroll
+          for (int j = 0; j < NQ / 2; ++j) z[j] = make_float2(-INFINITY, -INFINITY);
+        } else if (p.topk_idx == nullptr && (t + 1) * (long long)kTile > sg.seen0) {  // some token may not see all of it
+          int seen = sg.seen0 + tok0, left = head_left;
+#pragma unroll
+          for (int j = 0; j < NQ; ++j) {
+            if (pos >= seen) (j & 1 ? z[j / 2].y : z[j / 2].x) = -INFINITY;
+            if (--left == 0) { left = p.H; ++seen; }
+          }
+        }
+        // the exponents of the weights; one may pass its row's maximum by the threshold
+        float2 e[NQ / 2];
+        bool mine = t == sg.t0;
+#pragma unroll
+        for (int j = 0; j < NQ / 2; ++j) {
+          e[j] = add2(z[j], m_neg[j]);
+          mine |= e[j].x > kRaise || e[j].y > kRaise;
+        }
+        bool raise = false;
+        if (named_bar_or(bar_id, 128, mine || bad)) {
+          if (named_bar_or(bar_id, 128, bad)) { aborted = true; break; }
+          raise = true;
+        }
+        if (raise) {
+          float top[NQ];
+#pragma unroll
+          for (int j = 0; j < NQ / 2; ++j) { top[2 * j] = z[j].x; top[2 * j + 1] = z[j].y; }
+          s_red[qd * NH + sum_row] = over_keys(top, true);
+          named_bar(bar_id, 128);
+          if (qd == 0 && lane < NHH) {
+            const int n = ch * NHH + lane;
+            const float bm = fmaxf(fmaxf(s_red[n], s_red[NH + n]), fmaxf(s_red[2 * NH + n], s_red[3 * NH + n])) - kTop;
+            const float mo = s_stat[n], mn = fmaxf(mo, bm);
+            s_stat[n] = mn;
+            s_fac[n] = mo == -INFINITY ? 0.f : exp2f(mo - mn);
+          }
+          named_bar(bar_id, 128);
+#pragma unroll
+          for (int j = 0; j < NQ / 2; ++j) {
+            l_part[j] = mul2(l_part[j], make_float2(s_fac[n0 + 2 * j], s_fac[n0 + 2 * j + 1]));
+            m_neg[j] = make_float2(-fmaxf(s_stat[n0 + 2 * j], -3.0e38f), -fmaxf(s_stat[n0 + 2 * j + 1], -3.0e38f));
+            e[j] = add2(z[j], m_neg[j]);
+          }
+          if (t > sg.t0) {
+            const bool okw = wait_pv(i - 1, 3);
+            if (named_bar_or(bar_id, 128, !okw)) { aborted = true; break; }
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = 0; x < 4 * (NHH / 8); ++x) {  // 8 columns at a time
+              const int h0 = ch * NHH + (x % (NHH / 8)) * 8;
+              const uint32_t ta = tmem_addr(tmem + L::TM_O + x / (NHH / 8) * NH + h0, qd * 32, 0);
+              uint32_t ov[8];
+              tmem_ld8(ta, ov);
+              tmem_ld_wait();
+#pragma unroll
+              for (int h = 0; h < 8; ++h) ov[h] = __float_as_uint(__uint_as_float(ov[h]) * s_fac[h0 + h]);
+              tmem_st8(ta, ov);
+            }
+            tmem_st_wait();
+          }
+        }
+        uint32_t hi[NQ / 2], lo[NQ / 2];
+#pragma unroll
+        for (int j = 0; j < NQ / 2; ++j) {
+          const float2 w = make_float2(ex2(e[j].x), ex2(e[j].y));
+          l_part[j] = fma2(w, make_float2(inv_s, inv_s), l_part[j]);
+          hi[j] = e5m2x2(w);
+          lo[j] = e4m3x2(minus2(w, e5m2x2_floats(hi[j])));
+        }
+        const uint32_t to = sP + (i & 1) * L::P_BLOCK;
+        if constexpr (NH == 64) {
+          const int u0 = n0 / 16;
+          st_shared_v4(to + sw128_off(r, u0), hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
+          st_shared_v4(to + sw128_off(r, 4 + u0), lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
+        } else {
+#pragma unroll
+          for (int j = 0; j < NQ; ++j) {
+            const int n = n0 + j;
+            const uint32_t at = to + (uint32_t)(n * 128 + (((r >> 4) ^ (n & 7)) << 4) + (r & 15));
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(hi[j / 2] >> (8 * (j & 1))) : "memory");
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + NH * 128), "r"(lo[j / 2] >> (8 * (j & 1))) : "memory");
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && !bad) mbar_arrive(bar_p + 8 * (i & 1));
+      }
+      if (aborted) break;
+      // ---- the segment's rows: out and lse, or the workspace's partial sums ----
+      float sums[NQ];
+#pragma unroll
+      for (int j = 0; j < NQ / 2; ++j) { sums[2 * j] = l_part[j].x; sums[2 * j + 1] = l_part[j].y; }
+      named_bar(bar_id, 128);  // the factors of a rescale in the last tile have been read (the sums take their place)
+      s_red[qd * NH + sum_row] = over_keys(sums, false);
+      named_bar(bar_id, 128);
+      const bool whole = sg.whole;
+      const int slot = 2 * blockIdx.x + (sg.opens ? 1 : 0);
+      if (qd == 0 && lane < NHH) {
+        const int n = ch * NHH + lane;
+        const float l = s_red[n] + s_red[NH + n] + s_red[2 * NH + n] + s_red[3 * NH + n];
+        const float m = s_stat[n];
+        float fac = 1.f;
+        if (whole) {
+          const float s2 = (p.sink && n < sg.rows) ? __ldg(p.sink + (sg.head0 + n) % p.H) * kLog2e : -INFINITY;
+          const float mf = fmaxf(m, s2), base = mf == -INFINITY ? 0.f : mf;
+          const float keep = m == -INFINITY ? 1.f : exp2f(m - base);  // (no finite score: l is 0, or NaN from a NaN)
+          const float lt = l * keep + exp2f(s2 - base);
+          fac = lt == 0.f ? 0.f : keep / lt;
+          if (n < sg.rows) p.lse[sg.row0 + n] = lt == 0.f ? -INFINITY : base * kLn2 + logf(lt);
+        } else {
+          p.stats[(size_t)slot * 128 + n] = m;
+          p.stats[(size_t)slot * 128 + 64 + n] = l;
+        }
+        s_fac[n] = fac;
+      }
+      named_bar(bar_id, 128);
+      const bool got = wait_pv(i - 1, 3);  // (the sums above while the last P.V is under way)
+      aborted = named_bar_or(bar_id, 128, !got);
+      if (aborted) break;
+      tc_fence_after();
+      // a few rows of 32 channels at a time, in a loop: unrolled, this code is longer than the time it takes to fetch it
+      constexpr int kStep = NHH < 16 ? NHH : 16;
+#pragma unroll 1
+      for (int x = 0; x < 4 * NHH / kStep; ++x) {
+        const int mt = x / (NHH / kStep), h0 = ch * NHH + (x % (NHH / kStep)) * kStep;
+        uint32_t o[kStep];
+        const uint32_t ta = tmem_addr(tmem + L::TM_O + mt * NH + h0, qd * 32, 0);
+        if constexpr (kStep == 16) tmem_ld16(ta, o);
+        else tmem_ld8(ta, o);
+        tmem_ld_wait();
+        const int c = mt * 128 + qd * 32 + lane, rows = sg.rows - h0;
+        // (one branch for all rows: with one for each, every store waits for the one before, 66 cycles in place of 5)
+        if (whole) {
+          __nv_bfloat16* dst = p.out + (size_t)(sg.row0 + h0) * kDv + c;
+          float f[kStep];
+#pragma unroll
+          for (int h = 0; h < kStep; ++h) f[h] = s_fac[h0 + h];
+#pragma unroll
+          for (int h = 0; h < kStep; ++h)
+            if (h < rows) dst[h * kDv] = __float2bfloat16_rn(f[h] == 0.f ? 0.f : __uint_as_float(o[h]) * f[h]);
+        } else {
+          float* part = p.partial + ((size_t)slot * 64 + h0) * kDv + c;
+#pragma unroll
+          for (int h = 0; h < kStep; ++h)
+            if (h < rows) part[h * kDv] = __uint_as_float(o[h]);
+        }
+      }
+      tc_fence_before();
+      named_bar(bar_id, 128);  // s_red, s_stat and s_fac have been read
+      if (!more) break;
+      sg = nx;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::TM_COLS);
+    if (lane == 0 && *s_abort) record_error(p.err, DSA_ERR_TIMEOUT);
+  }
+}
+
+template <int DQK, int NH>
+dsa_status_t launch(Params& p, int ctas, cudaStream_t s) {
+  using L = Smem<DQK, NH>;
+  dsa_status_t st = configure_kernel_smem(reinterpret_cast<const void*>(paged_mla_e4m3_kernel<DQK, NH>), L::TOTAL,
+                                          "configuring paged_mla_e4m3_kernel");
+  if (st != DSA_OK) return st;
+  p.G = p.topk_idx ? 1 : (p.H <= NH ? NH / p.H : 1);
+  p.extra = p.topk_idx ? 2 : 4;
+  p.HB = (p.H + NH - 1) / NH;
+  paged_mla_e4m3_kernel<DQK, NH><<<ctas, kThreads, L::TOTAL, s>>>(p);
+  return cuda_check(cudaGetLastError(), "launching paged_mla_e4m3_kernel");
+}
+
+}  // namespace pmla8
+
+dsa_status_t launch_paged_mla_e4m3(const pgroups::GroupParams& g, const __nv_bfloat16* q, const uint8_t* cache, int Dqk,
+                                   float scale_log2e, bool few, int ctas, cudaStream_t s) {
+  pmla8::Params p{};
+  static_cast<pgroups::GroupParams&>(p) = g;
+  p.q = q;
+  p.cache = cache;
+  p.sl2e = scale_log2e;
+  if (few) return Dqk == 576 ? pmla8::launch<576, 16>(p, ctas, s) : pmla8::launch<512, 16>(p, ctas, s);
+  return Dqk == 576 ? pmla8::launch<576, 64>(p, ctas, s) : pmla8::launch<512, 64>(p, ctas, s);
+}
+
+}  // namespace dsa

@@ -11,20 +11,20 @@
 // rows' scales are.  The denominator adds w_p / s_p in fp32.  A query row is divided by a power of two so that its
 // largest channel lies in [2^14, 2^15): the channels that this takes out of fp16 are below 2^-38 of that one.
 //
-// Split of the work as in dsa_paged_groups.cuh, with tiles of 128 positions and groups of NH = 16 or 64 columns.
-// A tile: 16 warps take the codes from global memory to registers (their loads run a tile ahead of them), form fp16
-// and write it twice: to TMEM, position by lane, as the A operand of S^T[position, column] = V Q^T, and to shared memory
-// as the A operand of O^T[channel, column] += V^T W^T, 128 channels at a time as P.V of the tile before is done
-// with them.  Then the same warps do the softmax, a position a thread.  In this way shared memory, whose 128 bytes a
-// cycle are what the whole thing runs into, sees a latent written once and read once: 131 KB each for a tile, and 74 KB
-// of Q, 66 KB of W, 131 KB / 4 ... of codes not at all.
+// Split of the work as in dsa_paged_groups.cuh, with tiles of 96 positions and groups of NH = 16 or 64 columns.
+// A tile: two warps copy its rows as they are to shared memory; 12 warps take the codes from there to registers, form
+// fp16 and write it twice: to TMEM, position by lane, as the A operand of S^T[position, column] = V Q^T, and to shared
+// memory as the A operand of O^T[channel, column] += V^T W^T, 128 channels at a time as P.V of the tile before is done
+// with them.  Then the same warps do the softmax, a position a thread.
 //
-// Warps: 0-15 convert, softmax, epilogue; 16 issues S^T, 17 P.V, 18 announces the runs of tiles, 19 looks rows up.
+// Warps: three of four convert and do softmax and epilogue (they reach the TMEM lanes 0-95); of the others one issues the
+// products, one announces the runs of tiles, two copy.
 #include <climits>
 #include <cmath>
 
 #include "dsa_f32x2.cuh"
 #include "dsa_paged_groups.cuh"
+#include "dsa_paged_mla_quant.h"
 #include "dsa_paged_quant.cuh"
 
 namespace dsa {
@@ -32,48 +32,58 @@ namespace pmlaq {
 
 using namespace pgroups;
 
-constexpr int kTile = 128;
-constexpr int kWarps = 16;  // that convert and do the softmax
-constexpr int kThreads = 32 * (kWarps + 4);
-constexpr int kReaders = kWarps + 3;  // warps that read an announcement
-constexpr int kRing = 4;              // tiles whose rows are looked up ahead
-constexpr float kRaise = 15.0f;       // log2 units: the running maximum is raised when a weight passes 2^15
-constexpr float kTop = 7.0f;          // a new maximum is 2^7
+constexpr int kTile = 96;
+constexpr int kThreads = 512;
+constexpr int kWorkers = 12;              // warps that convert and do the softmax: number w with w % 4 < 3
+constexpr int kReaders = kWorkers + 6;    // readings of an announcement: two copying warps' two each, the announcing warp's own
+constexpr int kTeam = 96;                 // threads of a column group
+constexpr float kRaise = 15.0f;           // log2 units: the running maximum is raised when a weight passes 2^15
+constexpr float kTop = 7.0f;              // a new maximum is 2^7
 constexpr float kLeast = 3.5527136788005009e-15f;  // 2^-48, the least s
 
-template <int DQK, int NH>
+template <int DQK, int NH, int BITS>
 struct Smem {
   static constexpr bool kRope = DQK == 576;
-  static constexpr int CHUNK = kTile * 128;    // 64 channels of a tile
+  static constexpr QuantRow LAY = quant_row(DQK, kDv, BITS);
+  static constexpr int CHUNK = kTile * 128;  // 64 channels of a tile
   static constexpr int Q_CHUNK = NH * 128;
+  static constexpr int P_BYTES = NH == 64 || kRope ? kTile * 128 : 2 * NH * 128;  // (position channels lie there before W)
+  // With 8 bits, 64 columns and position channels there is no room for whole rows: the last 128 channels' codes come late,
+  // to where they will be written as fp16, the position channels to the place of W.
+  static constexpr bool LATE = BITS == 8 && NH == 64 && kRope;
+  static constexpr int PITCH = LATE ? 400 : LAY.bytes;  // of a row as it comes: an odd number of 16 bytes
+  static constexpr int SCALE_AT = LATE ? 384 : LAY.scale;
   static constexpr int OFF_Q = 8 * CHUNK;
   static constexpr int OFF_P = OFF_Q + (kRope ? 9 : 8) * Q_CHUNK;
-  static constexpr int OFF_MISC = OFF_P + kTile * NH * 2;
-  static constexpr int MISC = 8192;
-  static constexpr int TOTAL = OFF_MISC + MISC + 1024;  // + alignment slack
-  static_assert(TOTAL <= 232448, "shared memory budget");
-  // TMEM columns: O^T, S^T, the position channels and the slots of 128 channels of the A operand
-  static constexpr int TM_S = 4 * NH, TM_R = TM_S + (NH < 32 ? 32 : NH), TM_A = TM_R + 32;
-  static constexpr int SLOTS = NH == 64 ? 2 : 4;
-  static_assert(TM_A + SLOTS * 64 <= 512, "TMEM budget");
+  static constexpr int OFF_MISC = OFF_P + P_BYTES;
+  static constexpr int MISC = 3584;
+  static constexpr int OFF_RAW = OFF_MISC + MISC;
+  static constexpr int TOTAL = OFF_RAW + kTile * PITCH;
+  static_assert(TOTAL <= 232448 && PITCH % 32 == 16, "shared memory budget");
+  // TMEM columns: O^T, S^T and three slots of 128 channels of the A operand
+  static constexpr int TM_S = 4 * NH, TM_A = TM_S + (NH < 32 ? 32 : NH);
+  static_assert(TM_A + 3 * 64 <= 512, "TMEM budget");
 };
 
 // misc (bytes)
-constexpr int M_LAND = 0;      // [5]: position channels, then 128 channels each: converted by all warps
+constexpr int M_LAND = 0;      // [2]: S^T's operand is there: 384 channels, the others
 constexpr int M_PV = 40;       // [4]: P.V is done with 128 channels
-constexpr int M_A = 72;        // [2]: S^T is done with a slot
-constexpr int M_S = 88, M_P = 96, M_Q = 104, M_FIN = 112;  // 1, 1, 1, [2]
-constexpr int M_ROWF = 128, M_ROWE = 160;                   // [kRing] each
-constexpr int M_SEGF = 192, M_SEGE = 256;                   // [kSegs] each
-constexpr int M_TMEM = 320, M_ABORT = 324, M_PLAN = 328;    // plan: 56 bytes
-constexpr int M_SEG = 384;                                  // int4 [kSegs][2]
-constexpr int M_COL = 640;                                  // float [2][64]: a column's factor of the score, by run
-constexpr int M_NEG = 1152;                                 // float [64]: minus the running maxima
-constexpr int M_RED = 1408;                                 // float [4][64]; the first row also holds the factors of a rescale
-constexpr int M_STAT = 2432;                                // float [64]
-constexpr int M_SCALE = 2688;                               // float [2][128]: s of a tile's rows, -1: masked
-constexpr int M_ROW = 3712;                                 // long long [kRing][128]: where the rows lie, -1: masked
-static_assert(M_SEGE + 8 * kSegs <= M_TMEM && M_PLAN + 56 <= M_SEG && M_ROW + kRing * kTile * 8 <= 8192, "misc layout");
+constexpr int M_A = 72;        // S^T is done with the first slot
+constexpr int M_S = 88, M_P = 96, M_Q = 104, M_FIN = 112;
+constexpr int M_RAW = 120, M_READ = 128, M_LATE = 136;     // a tile's rows have come, have been read; what comes late has
+constexpr int M_SEGF = 144, M_SEGE = 208;                   // [kSegs] each
+constexpr int M_TMEM = 272, M_ABORT = 276, M_PLAN = 280;    // plan: 56 bytes
+constexpr int M_FAC = 3192, M_EPI = 3200;                   // a run's factors are there; its lanes 96-127 are stored
+constexpr int M_FLAG = 3208;                                // uint8 [2][4]: a tile's raise, by column group
+constexpr int M_VALID = 3240;                               // uint8 [96]: rows that are not masked
+constexpr int M_SEG = 336;                                  // int4 [kSegs][2]
+constexpr int M_COL = 592;                                  // float [2][64]: a column's factor of the score, by run
+constexpr int M_NEG = 1104;                                 // float [64]: minus the running maxima
+constexpr int M_RED = 1360;                                 // float [3][64]
+constexpr int M_STAT = 2128;                                // float [64]
+constexpr int M_SCL = 2384;                                 // float [64]: factors of a rescale
+constexpr int M_OUT = 2640;                                 // float [2][64]: factors of the output, by run
+static_assert(M_SEGE + 8 * kSegs <= M_TMEM && M_PLAN + 56 <= M_SEG && M_OUT + 512 <= M_FAC && M_FLAG + 32 <= M_VALID && M_VALID + kTile <= 3584, "misc layout");
 
 struct Params : GroupParams {
   const __nv_bfloat16* q;
@@ -93,11 +103,6 @@ __device__ __forceinline__ void tmem_st16x256b(uint32_t a, const uint32_t (&r)[1
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
-}
-__device__ __forceinline__ void tmem_st16x256b(uint32_t a, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
 }
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&r)[N]) {
@@ -133,6 +138,20 @@ __device__ __forceinline__ void mma4_ts_w(uint32_t d_tmem, uint32_t a, uint64_t 
       : "memory");
 }
 
+// Two MMAs on consecutive steps, added to D (as mma4_w).
+template <int SA, int SB>
+__device__ __forceinline__ void mma2_w(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred q, e;\n\t.reg .b64 a1, b1;\n\t"
+      "setp.eq.b32 q, 0, 0;\n\t"
+      "add.s64 a1, %1, %4;\n\tadd.s64 b1, %2, %5;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "n"(SA), "n"(SB)
+      : "memory");
+}
+
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -145,47 +164,99 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }  // -126 <= e <= 127
 
-// What a thread holds of a tile between its loads and its conversion: 16 channels of every 64 of half the chunks, of two rows.
-template <int BITS, bool ROPE>
-struct Raw {
-  uint32_t code[4][2][BITS / 2];  // step (128 channels), row
-  uint32_t block[2];              // the scales of two blocks of four (4 bits)
-  uint32_t rope[2][ROPE ? 4 : 1];
-  float s[2];                     // -1: masked
-};
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds4(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds1(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// A quarter (32 lanes of TMEM) of the channels of NC columns from n0 on: out, or the workspace's partial sums.
+template <int NH>
+__device__ __noinline__ void store_quarter(const Params& p, const Seg& sg, uint32_t tmem, int qd, int n0, const float* fac) {
+  constexpr int NC = NH / 4;
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int m = 0; m < 4; ++m) {
+    uint32_t ov[NC];
+    tmem_ld<NC>(tmem_addr(tmem, qd * 32, m * NH + n0), ov);
+    tmem_ld_wait();
+    const int c = m * 128 + qd * 32 + lane, rows = sg.rows - n0;
+    // (one branch for all rows: with one for each, every store waits for the one before)
+    if (sg.whole) {
+      __nv_bfloat16* dst = p.out + (size_t)(sg.row0 + n0) * kDv + c;
+      float f[NC];
+#pragma unroll
+      for (int h = 0; h < NC; ++h) f[h] = fac[n0 + h];
+#pragma unroll
+      for (int h = 0; h < NC; ++h)
+        if (h < rows) dst[h * kDv] = __float2bfloat16_rn(f[h] == 0.f ? 0.f : __uint_as_float(ov[h]) * f[h]);
+    } else {
+      float* part = p.partial + ((size_t)(2 * blockIdx.x + (sg.opens ? 1 : 0)) * 64 + n0) * kDv + c;
+#pragma unroll
+      for (int h = 0; h < NC; ++h)
+        if (h < rows) part[h * kDv] = __uint_as_float(ov[h]);
+    }
+  }
+}
 
 template <int DQK, int NH, int BITS>
 __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __grid_constant__ Params p) {
-  using L = Smem<DQK, NH>;
-  constexpr bool ROPE = L::kRope;
+  using L = Smem<DQK, NH, BITS>;
+  constexpr bool ROPE = L::kRope, LATE = L::LATE;
   constexpr int NC = NH / 4;  // columns of a softmax thread
-  constexpr QuantRow LAY = quant_row(DQK, kDv, BITS);
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t sV = smem_u32(smem), sQ = sV + L::OFF_Q, sP = sV + L::OFF_P;
+  constexpr QuantRow LAY = L::LAY;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sV = smem_u32(smem), sQ = sV + L::OFF_Q, sP = sV + L::OFF_P, sRaw = sV + L::OFF_RAW;
   uint8_t* misc = smem + L::OFF_MISC;
   const uint32_t mb = smem_u32(misc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(misc + M_ABORT);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc + M_TMEM);
   Plan* s_plan = reinterpret_cast<Plan*>(misc + M_PLAN);
-  long long* s_row = reinterpret_cast<long long*>(misc + M_ROW);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto wait = [&](int off, uint32_t parity) { return wait_for(mb + off, parity, s_abort, p.wait_limit); };
+  auto wait = [&](int off, uint32_t parity) -> bool {
+    return warp_all(wait_for(mb + off, parity, s_abort, p.wait_limit));
+  };
 
+  // rows that follow one another in pages of some size come by copies of whole runs, others one by one
+  const bool runs = !LATE && p.topk_idx == nullptr && p.P >= 16;
   if (threadIdx.x == 0) {
-    for (int k = 0; k < 5; ++k) mbar_init(mb + M_LAND + 8 * k, kWarps);
+    for (int k = 0; k < 2; ++k) mbar_init(mb + M_LAND + 8 * k, kWorkers);
     for (int k = 0; k < 4; ++k) mbar_init(mb + M_PV + 8 * k, 1);
-    for (int k = 0; k < 2; ++k) {
-      mbar_init(mb + M_A + 8 * k, 1);
-      mbar_init(mb + M_FIN + 8 * k, 1);
-    }
+    mbar_init(mb + M_A, 1);
+    mbar_init(mb + M_FIN, 1);
     mbar_init(mb + M_S, 1);
-    mbar_init(mb + M_P, kWarps);
-    mbar_init(mb + M_Q, kWarps);
-    for (int k = 0; k < kRing; ++k) {
-      mbar_init(mb + M_ROWF + 8 * k, 1);
-      mbar_init(mb + M_ROWE + 8 * k, kWarps);
-    }
+    mbar_init(mb + M_P, kWorkers);
+    mbar_init(mb + M_Q, kWorkers);
+    mbar_init(mb + M_RAW, runs ? 2 : 2 * 33);  // two warps' copies, and their stores
+    mbar_init(mb + M_LATE, 2 * 33);
+    mbar_init(mb + M_READ, kWorkers);
+    mbar_init(mb + M_FAC, 4);
+    mbar_init(mb + M_EPI, 3);
     for (int k = 0; k < kSegs; ++k) {
       mbar_init(mb + M_SEGF + 8 * k, 1);
       mbar_init(mb + M_SEGE + 8 * k, kReaders);
@@ -197,240 +268,353 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
   const Plan plan = *s_plan;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the joining kernel waits for this one's end itself)
   if (plan.w1 <= plan.w0 || plan.w1 - plan.w0 <= plan.skip) return;  // (the whole CTA)
-  if (warp == 16) {
+  if (warp == 3) {
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
   }
-  uint32_t tmem = 0;
-  if (warp < 18) {  // the others neither need it nor wait for it
-    named_bar(5, 32 * 18);
-    tmem = (uint32_t)warp_value((int)*s_tmem);
-  }
+  __syncthreads();
+  const uint32_t tmem = (uint32_t)warp_value((int)*s_tmem);
   auto read_seg = [&](int k, Seg& s) -> bool {
-    return read_announcement(mb + M_SEGF, mb + M_SEGE, reinterpret_cast<const int4*>(misc + M_SEG), k, s_abort, p.wait_limit, s);
+    return read_announcement_here(mb + M_SEGF, mb + M_SEGE, reinterpret_cast<const int4*>(misc + M_SEG), k, s_abort, p.wait_limit, s);
   };
-  if (warp == 16) {
-    // ======================= S^T issuer =======================
-    constexpr uint32_t kIdR = idesc_bf16(kTile, NH, false, false), kId = idesc_f16(kTile, NH, false, false);
+  // The lanes 96-127 of TMEM hold no positions, but channels of O^T: the four warps that reach them store them, a column
+  // group each (the one that issues the products rescales them too).  Run k, whose last tile is number i - 1 of the CTA's.
+  const float* s_out = reinterpret_cast<const float*>(misc + M_OUT);
+  auto last_quarter = [&](int k, int& i) -> bool {
+    Seg sg;
+    if (!warp_all(read_seg(k, sg))) return false;
+    i += sg.n;
+    if (!(wait(M_FAC, k & 1) && wait(M_PV + 24, (i - 1) & 1))) return false;
+    tc_fence_after();
+    store_quarter<NH>(p, sg, tmem, 3, (warp >> 2) * NC, s_out + (k & 1) * 64);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(mb + M_EPI);
+    return true;
+  };
+  if (warp == 3) {
+    // ======================= the products: S^T of a tile as its steps are converted, then P.V =======================
+    constexpr uint32_t kIdR = idesc_bf16(128, NH, false, false), kIdS = idesc_f16(128, NH, false, false);
+    constexpr uint32_t kIdV = idesc_f16(128, NH, true, NH == 64);
     int done = 0;
     for (int seg = 0, last = 0; !last; ++seg) {
       Seg sg;
       if (!warp_all(read_seg(seg, sg))) break;
       last = warp_value(sg.last ? 1 : 0);
-      if (!warp_all(wait(M_Q, seg & 1))) break;
+      if (!wait(M_Q, seg & 1)) break;
       const int n = warp_value(sg.n);
-      const uint32_t t0 = (uint32_t)warp_value((int)tmem), q0 = (uint32_t)warp_value((int)sQ);
+      const uint32_t t0 = (uint32_t)warp_value((int)tmem), q0 = (uint32_t)warp_value((int)sQ), v0 = (uint32_t)warp_value((int)sV),
+                     w0 = (uint32_t)warp_value((int)sP);
       int i = warp_value(done);
       done += n;
       bool stop = false;
 #pragma unroll 1
       for (int k0 = 0; k0 < n; ++k0, ++i) {
         const uint64_t b0 = sdesc_sw128(q0, 16, 1024);
-        if (ROPE) {
-          if (!warp_all(wait(M_LAND, i & 1))) { stop = true; break; }
-          tc_fence_after();
-          mma4_ts_w<2>(t0 + L::TM_S, t0 + L::TM_R, b0 + (8 * L::Q_CHUNK >> 4), kIdR, 0);
-        }
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          if (!warp_all(wait(M_LAND + 8 * (1 + m), i & 1))) { stop = true; break; }
-          tc_fence_after();
-          const uint32_t a = t0 + L::TM_A + (m % L::SLOTS) * 64;
-          mma4_ts_w<2>(t0 + L::TM_S, a, b0 + (2 * m * L::Q_CHUNK >> 4), kId, ROPE || m > 0);
-          mma4_ts_w<2>(t0 + L::TM_S, a + 32, b0 + ((2 * m + 1) * L::Q_CHUNK >> 4), kId, 1);
-          if (L::SLOTS == 2 && m < 2) mma_commit_w(mb + M_A + 8 * m);
+          if (m == 0 || m == 3) {
+            if (!wait(M_LAND + (m ? 8 : 0), i & 1)) { stop = true; break; }
+            tc_fence_after();
+          }
+          const uint32_t a = t0 + L::TM_A + (m % 3) * 64;
+          mma4_ts_w<2>(t0 + L::TM_S, a, b0 + (2 * m * L::Q_CHUNK >> 4), kIdS, m > 0);
+          mma4_ts_w<2>(t0 + L::TM_S, a + 32, b0 + ((2 * m + 1) * L::Q_CHUNK >> 4), kIdS, 1);
+          if (m == 0) mma_commit_w(mb + M_A);
         }
+        if (!stop && ROPE) mma4_w<2, 2>(t0 + L::TM_S, sdesc_sw128(w0, 16, 1024), b0 + (8 * L::Q_CHUNK >> 4), kIdR, 1);
         if (stop) break;
         mma_commit_w(mb + M_S);
-      }
-      if (stop) break;
-    }
-    mma_commit_w(mb + M_FIN);
-    volatile int dummy = 0;
-    mbar_wait(mb + M_FIN, 0, &dummy, p.err);
-    __syncwarp();
-  } else if (warp == 17) {
-    // ======================= P.V issuer =======================
-    constexpr uint32_t kId = idesc_f16(128, NH, true, NH == 64);
-    int done = 0;
-    for (int seg = 0, last = 0; !last; ++seg) {
-      Seg sg;
-      if (!warp_all(read_seg(seg, sg))) break;
-      last = warp_value(sg.last ? 1 : 0);
-      const int n = warp_value(sg.n);
-      const uint32_t t0 = (uint32_t)warp_value((int)tmem), v0 = (uint32_t)warp_value((int)sV), w0 = (uint32_t)warp_value((int)sP);
-      int i = warp_value(done);
-      done += n;
-      bool stop = false;
-#pragma unroll 1
-      for (int k0 = 0; k0 < n; ++k0, ++i) {
-        if (!warp_all(wait(M_P, i & 1))) { stop = true; break; }
+        if (!wait(M_P, i & 1)) { stop = true; break; }
         tc_fence_after();
+        if (k0 == 0) {  // the run before has left O^T
+          if (seg > 0 && !wait(M_EPI, (seg - 1) & 1)) { stop = true; break; }
+          tc_fence_after();
+        } else {
+          const uint32_t flags = lds32(mb + M_FLAG + (i & 1) * 4);
+          const float* scl = reinterpret_cast<const float*>(misc + M_SCL);
+#pragma unroll 1
+          for (int g = 0; flags != 0 && g < 4; ++g) {
+            if (!((flags >> (8 * g)) & 1u)) continue;
+#pragma unroll 1
+            for (int m = 0; m < 4; ++m) {
+              const uint32_t ta = tmem_addr(tmem, 96, m * NH + g * NC);
+              uint32_t ov[NC];
+              tmem_ld<NC>(ta, ov);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < NC; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * scl[g * NC + j]);
+              tmem_st<NC>(ta, ov);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            tc_fence_after();
+          }
+        }
         const uint64_t va = sdesc_sw128(v0, L::CHUNK, 1024), wb = sdesc_sw128(w0, 16, 1024);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const uint64_t a = va + m * (2 * L::CHUNK >> 4);
           if constexpr (NH == 64) {  // W^T rows are positions (MN-major)
-            mma4_w<128, 128>(t0 + m * NH, a, wb, kId, k0 > 0);
-            mma4_w<128, 128>(t0 + m * NH, a + 512, wb + 512, kId, 1);
-          } else {  // W^T rows are columns, 64 positions along K, then the other 64
-            mma4_w<128, 2>(t0 + m * NH, a, wb, kId, k0 > 0);
-            mma4_w<128, 2>(t0 + m * NH, a + 512, wb + (NH * 128 >> 4), kId, 1);
+            mma4_w<128, 128>(t0 + m * NH, a, wb, kIdV, k0 > 0);
+            mma2_w<128, 128>(t0 + m * NH, a + 512, wb + 512, kIdV);
+          } else {  // W^T rows are columns, 64 positions along K, then the other 32
+            mma4_w<128, 2>(t0 + m * NH, a, wb, kIdV, k0 > 0);
+            mma2_w<128, 2>(t0 + m * NH, a + 512, wb + (NH * 128 >> 4), kIdV);
           }
           mma_commit_w(mb + M_PV + 8 * m);
         }
       }
       if (stop) break;
+      // (as last_quarter, of the first column group)
+      if (!(wait(M_FAC, seg & 1) && wait(M_PV + 24, (i - 1) & 1))) break;
+      tc_fence_after();
+      store_quarter<NH>(p, sg, tmem, 3, 0, s_out + (seg & 1) * 64);
+      tc_fence_before();
+      __syncwarp();
     }
-    mma_commit_w(mb + M_FIN + 8);
+    mma_commit_w(mb + M_FIN);
     volatile int dummy = 0;
-    mbar_wait(mb + M_FIN + 8, 0, &dummy, p.err);
+    mbar_wait(mb + M_FIN, 0, &dummy, p.err);
     __syncwarp();
-  } else if (warp == 18) {
-    announce<kTile>(p, plan, mb + M_SEGF, mb + M_SEGE, reinterpret_cast<int4*>(misc + M_SEG), s_abort);
-  } else if (warp == 19) {
-    // ======================= rows of the tiles =======================
-    bool bad_index = false;
-    int i = 0;
-    for (int seg = 0, last = 0; !last; ++seg) {
-      Seg sg;
-      if (!read_seg(seg, sg)) break;
-      last = sg.last;
-      const int limit = (int)min((long long)p.max_pages * p.P, (long long)(p.topk_idx ? sg.seen0 : sg.keys));
-      const int32_t* table = p.table + (size_t)sg.b * p.max_pages;
-      const int32_t* list = p.topk_idx ? p.topk_idx + (size_t)(sg.row0 / p.H) * p.K : nullptr;
-      bool stop = false;
+  } else if (warp == 7) {
+    int told = 0, stored = 0, i = 0;
+    bool ok = true;
+    auto store = [&](int upto) {
+      while (ok && stored < upto) ok = last_quarter(stored++, i);
+    };
+    announce<kTile>(p, plan, mb + M_SEGF, mb + M_SEGE, reinterpret_cast<int4*>(misc + M_SEG), s_abort, [&](int k) {
+      told = k + 1;
+      store(told - 4);  // (runs are announced some ahead)
+    });
+    store(told);
+  } else if ((warp & 3) == 3) {
+    // ======================= copies: 48 rows of every tile each =======================
+    // Rows that follow one another by bulk copies; lists and small pages by cp.async, a warp's instruction up to 512 bytes of
+    // one row.  Not the converting warps' own loads: their fences before the tensor core's reads would wait for all that
+    // they have under way, and loads to registers need lines of L1, of which there are few beside 227 KB of shared memory.
+    // A lane looks up to two rows up, in steps whose loads have a tile's time to come back: the list's entry (three tiles
+    // ahead), the page (two), the row number (one).
+    constexpr int kHalf = kTile / 2;
+    const int gw = warp == 15;
+    Seg sg;
+    int seg = 0, base = 0, end = 0, limit = 0, n_tiles = INT_MAX;
+    bool bad_index = false, stop = false;
+    struct Look {
+      int pos[2], b, limit;  // positions (then their places in the page), or -1; request; what they have to stay below
+    };
+    auto position = [&](int i) -> Look {
+      Look k{{-1, -1}, 0, 0};
+      if (i < n_tiles && !stop) {
 #pragma unroll 1
-      for (int t = sg.t0; t < sg.t0 + sg.n; ++t, ++i) {
-        int pos[4], page[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int j = t * kTile + 32 * k + lane;
-          pos[k] = j >= sg.keys ? -1 : list ? __ldg(list + j) : j;
+        while (i >= end) {
+          if (seg > 0 && sg.last) { n_tiles = end; return k; }
+          if (!read_seg(seg, sg)) { stop = true; return k; }
+          ++seg;
+          base = end;
+          end += sg.n;
+          limit = (int)min((long long)p.max_pages * p.P, (long long)(p.topk_idx ? sg.seen0 : sg.keys));
         }
+        k.b = sg.b;
+        k.limit = limit;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (pos[k] < -1 || pos[k] >= limit) {
-            bad_index |= pos[k] != -1;
-            pos[k] = -1;
-          }
-          page[k] = -1;
-          if (pos[k] >= 0) {
-            const unsigned at = (unsigned)pos[k] / (unsigned)p.P;
-            pos[k] -= (int)at * p.P;
-            page[k] = __ldg(table + at);
-          }
+        for (int e = 0; e < 2; ++e) {
+          const int j = (sg.t0 + i - base) * kTile + gw * kHalf + e * 32 + lane;
+          if (j < sg.keys && (e == 0 || lane < kHalf - 32))
+            k.pos[e] = p.topk_idx ? __ldg(p.topk_idx + (size_t)(sg.row0 / p.H) * p.K + j) : j;
         }
-        const int slot = i % kRing;
-        if (i >= kRing && !warp_all(wait(M_ROWE + 8 * slot, (i / kRing - 1) & 1))) { stop = true; break; }
+      }
+      return k;
+    };
+    auto page_of = [&](Look& k, int (&page)[2]) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          long long at = -1;
-          if (pos[k] >= 0) {
-            if (page[k] >= 0 && page[k] < p.num_pages) at = ((long long)page[k] * p.P + pos[k]) * LAY.bytes;
-            else bad_index = true;
+      for (int e = 0; e < 2; ++e) {
+        page[e] = -1;
+        if (k.pos[e] < -1 || k.pos[e] >= k.limit) {
+          bad_index |= k.pos[e] != -1;
+          k.pos[e] = -1;
+        }
+        if (k.pos[e] < 0) continue;
+        const unsigned at = (unsigned)k.pos[e] / (unsigned)p.P;
+        k.pos[e] -= (int)at * p.P;
+        page[e] = __ldg(p.table + (size_t)k.b * p.max_pages + at);
+      }
+    };
+    auto row_of = [&](const Look& k, const int (&page)[2], int (&row)[2]) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        row[e] = -1;
+        if (k.pos[e] >= 0) {
+          if (page[e] >= 0 && page[e] < p.num_pages) row[e] = page[e] * p.P + k.pos[e];
+          else bad_index = true;
+        }
+      }
+    };
+    auto given = [&](int bar) {
+      cp_async_arrive(mb + bar);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(mb + bar);
+    };
+    // units of 16 bytes of a staged row: a lane's first (and, of the widest rows, second), and where they come from
+    constexpr int kUnits = L::PITCH / 16;
+    const uint8_t* lane_src = p.cache + (LATE && lane == L::SCALE_AT / 16 ? LAY.scale : lane * 16);
+    const uint32_t stage = sRaw + gw * kHalf * L::PITCH;
+    volatile uint8_t* s_valid = misc + M_VALID + gw * kHalf;
+    int armed = -1;                // the last tile that this warp's bulk copies belong to
+    int stored = 0, store_at = 0;  // runs whose last quarter is stored, and the tiles before the next one
+    bool ok = true;
+    Look ahead = position(0), next = position(1);
+    int page[2], row[2], row_next[2];
+    int in_page[2], in_page_next[2];
+    page_of(ahead, page);
+    row_of(ahead, page, row_next);
+    in_page_next[0] = ahead.pos[0];
+    in_page_next[1] = ahead.pos[1];
+    page_of(next, page);
+    ahead = next;
+    next = position(2);
+#pragma unroll 1
+    for (int i = 0; i < n_tiles && !stop; ++i) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        row[e] = row_next[e];
+        in_page[e] = in_page_next[e];
+        in_page_next[e] = ahead.pos[e];
+      }
+      row_of(ahead, page, row_next);
+      ahead = next;
+      page_of(ahead, page);
+      next = position(i + 3);
+      if (i > 0 && !wait(M_READ, (i - 1) & 1)) { stop = true; break; }
+      s_valid[lane] = row[0] >= 0;
+      if (lane < kHalf - 32) s_valid[32 + lane] = row[1] >= 0;
+      if (runs) {
+        // a run's first lane copies it (up to where the warp's first 32 rows or its others end)
+        unsigned on[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) on[e] = __ballot_sync(0xffffffffu, row[e] >= 0);
+        armed = i;
+        if (lane == 0) mbar_expect_tx(mb + M_RAW, (__popc(on[0]) + __popc(on[1])) * LAY.bytes);
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (row[e] >= 0 && (lane == 0 || in_page[e] == 0 || !((on[e] >> ((lane + 31) & 31)) & 1u))) {
+            const unsigned stop_at = ~(on[e] >> lane);  // (its lowest set bit: the first row after this one that is masked)
+            const int n = min(min(p.P - in_page[e], 32 - lane), stop_at ? __ffs(stop_at) - 1 : 32);
+            bulk_copy(stage + (e * 32 + lane) * L::PITCH, p.cache + (size_t)row[e] * LAY.bytes, n * LAY.bytes, mb + M_RAW);
           }
-          s_row[slot * kTile + 32 * k + lane] = at;
-          if (at >= 0)
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.cache + at), "n"(LAY.bytes) : "memory");
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(mb + M_ROWF + 8 * slot);
+      } else {
+        // eight rows at a time: what a copy reads from registers is free only when it has been taken
+#pragma unroll 1
+        for (int x0 = 0; x0 < kHalf; x0 += 8) {
+          const uint8_t* src[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const int at = __shfl_sync(0xffffffffu, x0 < 32 ? row[0] : row[1], (x0 + y) & 31);
+            src[y] = at >= 0 ? lane_src + (size_t)at * LAY.bytes : nullptr;
+          }
+          const uint32_t dst = stage + x0 * L::PITCH + lane * 16;
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            if (src[y] && lane < kUnits) cp_async16(dst + y * L::PITCH, src[y], 16);
+            if (src[y] && lane + 32 < kUnits) cp_async16(dst + y * L::PITCH + 512, src[y] + 512, 16);
+          }
+        }
+        given(M_RAW);
       }
-      if (stop) break;
+      if constexpr (LATE) {
+        if (i > 0 && !wait(M_PV + 24, (i - 1) & 1)) { stop = true; break; }
+        const int quad = lane & 3;
+#pragma unroll
+        for (int x = 0; x < kHalf / 8; ++x) {  // rows 8 x + lane / 4 of this warp's
+          const int at = __shfl_sync(0xffffffffu, x < 4 ? row[0] : row[1], (8 * x + (lane >> 2)) & 31);
+          const uint8_t* src = p.cache + (size_t)max(at, 0) * LAY.bytes + quad * 16;
+          const uint32_t size = at >= 0 ? 16u : 0u, r = gw * kHalf + 8 * x + (lane >> 2);
+          cp_async16(sV + 6 * L::CHUNK + sw128_off(r, 2 * quad), src + 384, size);
+          cp_async16(sV + 7 * L::CHUNK + sw128_off(r, 2 * quad), src + 448, size);
+          cp_async16(sP + sw128_off(r, quad), src + LAY.tail, size);
+          cp_async16(sP + sw128_off(r, 4 + quad), src + LAY.tail + 64, size);
+        }
+        given(M_LATE);
+      }
+      // a run that ended before this tile (its announcement stays until it is read for the second time)
+      if (ok && store_at + reinterpret_cast<const volatile int*>(misc + M_SEG)[8 * (stored % kSegs) + 1] <= i)
+        ok = last_quarter(stored++, store_at);
     }
+    if (!stop)
+      while (ok && stored < seg) ok = last_quarter(stored++, store_at);
     if (bad_index) record_error(p.err, DSA_ERR_DEVICE_INDEX);
+    // Nothing lands after the CTA has left: bulk copies are waited for too, and where a wait ran out, the other warp, which may
+    // have begun the next tile, gets this warp's part of it.
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    volatile int dummy = 0;
+    if (armed >= 0) mbar_wait(mb + M_RAW, armed & 1, &dummy, p.err);
+    __syncwarp();
+    if (runs && stop && lane == 0) mbar_arrive(mb + M_RAW);
   } else {
     // ======================= conversion, softmax, epilogue =======================
     float* s_col = reinterpret_cast<float*>(misc + M_COL);
     float* s_neg = reinterpret_cast<float*>(misc + M_NEG);
     float* s_red = reinterpret_cast<float*>(misc + M_RED);
-    float* s_fac = s_red;  // a column's factor replaces its first maximum or sum
+    float* s_fac = reinterpret_cast<float*>(misc + M_SCL);
+    float* s_fin = reinterpret_cast<float*>(misc + M_OUT);
+    volatile uint8_t* s_flag = misc + M_FLAG;
     float* s_stat = reinterpret_cast<float*>(misc + M_STAT);
-    volatile float* s_scale = reinterpret_cast<volatile float*>(misc + M_SCALE);
-    // conversion: rows r0 and r0 + 8 of the tile, 16 channels of chunk 2m + half in step m
-    const int qd = warp & 3, half = warp >> 3, quad = lane & 3;
-    const int r0 = qd * 32 + ((warp >> 2) & 1) * 16 + (lane >> 2);
+    // conversion: rows r0 and r0 + 8 of the tile, of every 128 channels 16 (16 quad and on) of 64 (half)
+    const int qd = warp & 3, cg = warp >> 2, half = cg & 1, quad = lane & 3;
+    const int r0 = qd * 32 + (cg >> 1) * 16 + (lane >> 2);
     const uint32_t to0 = sV + half * L::CHUNK + sw128_off(r0, 2 * quad), to1 = sV + half * L::CHUNK + sw128_off(r0, 2 * quad + 1);
-    const uint32_t tm_a = tmem_addr(tmem, (r0 & ~15) & 127, 0);
-    // softmax: position `row` of the tile, columns n0 .. n0 + NC - 1, together with the other warps of the column group
-    const int cg = warp >> 2, n0 = cg * NC, row = qd * 32 + lane, bar_id = 1 + cg;
-    Raw<BITS, ROPE> raw;
-    auto load_tile = [&](int i) -> bool {
-      const int slot = i % kRing;
-      if (!warp_all(wait(M_ROWF + 8 * slot, (i / kRing) & 1))) return false;
-      long long at[2] = {s_row[slot * kTile + r0], s_row[slot * kTile + r0 + 8]};
-      __syncwarp();
-      if (lane == 0) mbar_arrive(mb + M_ROWE + 8 * slot);
+    const uint32_t raw0 = sRaw + r0 * L::PITCH;
+    const uint32_t tm_a = tmem_addr(tmem, qd * 32 + (cg >> 1) * 16, 0);
+    // softmax: position `row` of the tile, columns n0 .. n0 + NC - 1, together with the two other warps of the column group
+    const int n0 = cg * NC, row = qd * 32 + lane, bar_id = 1 + cg;
+    auto scale_of = [&](int r) {  // (a row that was never written, of zero bytes, holds zeros; -1: masked)
+      const float s = lds4(sRaw + r * L::PITCH + L::SCALE_AT);
+      return !lds1(mb + M_VALID + r) ? -1.f : s < kLeast ? kLeast : s;
+    };
+    // Tile i from its rows to TMEM and shared memory, and s of this thread's position; false when a wait ran out.
+    auto convert = [&](int i, float& s_mine) -> bool {
+      if (!wait(M_RAW, i & 1)) return false;
+      // all that has come, to registers: the copies of the next tile take its place
+      constexpr int kNow = LATE ? 3 : 4;
+      uint32_t code[4][2][BITS / 2], blk[4][2];
+      uint4 rope[2];
+      float sc[2];
+      s_mine = scale_of(row);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const bool on = at[k] >= 0;
-        const uint8_t* src = p.cache + (on ? at[k] : 0);
-        raw.s[k] = -1.f;
-        if (on) {  // (a row that was never written, of zero bytes, holds zeros)
-          const float v = __ldg(reinterpret_cast<const float*>(src + LAY.scale));
-          raw.s[k] = v < kLeast ? kLeast : v;
-        }
-        if constexpr (ROPE) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (on) v = __ldg(reinterpret_cast<const uint4*>(src + LAY.tail + half * 64 + quad * 16));
-          raw.rope[k][0] = v.x; raw.rope[k][1] = v.y; raw.rope[k][2] = v.z; raw.rope[k][3] = v.w;
-        }
-        if constexpr (BITS == 4)  // of chunk 2 quad + half; the lanes exchange them
-          raw.block[k] = on ? __ldg(reinterpret_cast<const uint32_t*>(src + LAY.blocks) + 2 * quad + half) : 0u;
+        const uint32_t at = raw0 + k * 8 * L::PITCH;
+        sc[k] = scale_of(r0 + 8 * k);
+        const bool on = !(sc[k] < 0.f);  // (what lies in a masked row's place may be anything)
+        if (ROPE && !LATE) rope[k] = on ? lds16(at + LAY.tail + half * 64 + quad * 16) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
+        for (int m = 0; m < kNow; ++m) {
           if constexpr (BITS == 4) {
-            uint2 v = make_uint2(0, 0);
-            if (on) v = __ldg(reinterpret_cast<const uint2*>(src + (2 * m + half) * 32) + quad);
-            raw.code[m][k][0] = v.x; raw.code[m][k][1] = v.y;
+            const uint2 v = on ? lds8(at + m * 64 + half * 32 + quad * 8) : make_uint2(0, 0);
+            code[m][k][0] = v.x; code[m][k][1] = v.y;
+            blk[m][k] = on ? lds1(at + LAY.blocks + m * 8 + half * 4 + quad) : 0u;
           } else {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (on) v = __ldg(reinterpret_cast<const uint4*>(src + (2 * m + half) * 64) + quad);
-            raw.code[m][k][0] = v.x; raw.code[m][k][1] = v.y; raw.code[m][k][2] = v.z; raw.code[m][k][3] = v.w;
+            const uint4 v = on ? lds16(at + m * 128 + half * 64 + quad * 16) : make_uint4(0, 0, 0, 0);
+            code[m][k][0] = v.x; code[m][k][1] = v.y; code[m][k][2] = v.z; code[m][k][3] = v.w;
           }
         }
       }
-      return true;
-    };
-    auto landed = [&](int step) {
-      tmem_st_wait();
-      fence_proxy_async_smem();
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(mb + M_LAND + 8 * step);
-    };
-    // Tile i from registers to TMEM and shared memory; false when a wait ran out.
-    auto convert = [&](int i) -> bool {
-      if (half == 0 && quad == 0) {
-        s_scale[(i & 1) * kTile + r0] = raw.s[0];
-        s_scale[(i & 1) * kTile + r0 + 8] = raw.s[1];
-      }
-      tc_fence_after();  // (the tile before has left S^T's operands: its scores have been waited for)
-      if constexpr (ROPE) {
-        uint32_t v[8];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float inv = raw.s[k] < 0.f ? 1.f : __frcp_rn(raw.s[k]);
-          const uint32_t by = pack_bf16x2(inv, inv);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[(j >> 1) * 4 + 2 * k + (j & 1)] = mul_bf16x2(raw.rope[k][j], by);
-        }
-        tmem_st16x256b(tm_a + L::TM_R + half * 16, v);
-        landed(0);
-      }
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        uint32_t v[16];
+      if (lane == 0) mbar_arrive(mb + M_READ);
+      tc_fence_after();  // (TMEM: S^T of the tile before is done)
+      // 128 channels' codes as fp16, the halves of a row's four channels side by side as TMEM takes them
+      auto to_fp16 = [&](int m, uint32_t (&v)[16]) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t h[8];
           if constexpr (BITS == 4) {
-            const uint32_t b4 = __shfl_sync(0xffffffffu, raw.block[k], (lane & 28) | m);
-            const uint32_t by = e4m3x2_f16x2((uint16_t)__byte_perm(b4, 0, quad * 0x11));
+            const uint32_t by = e4m3x2_f16x2((uint16_t)(blk[m][k] * 0x101u));
             uint32_t lo[4], hi[4];
-            e2m1x8_f16x2(raw.code[m][k][0], lo);
-            e2m1x8_f16x2(raw.code[m][k][1], hi);
+            e2m1x8_f16x2(code[m][k][0], lo);
+            e2m1x8_f16x2(code[m][k][1], hi);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               h[j] = mul_f16x2(lo[j], by);
@@ -439,33 +623,78 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
           } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              h[2 * j] = e4m3x2_f16x2((uint16_t)raw.code[m][k][j]);
-              h[2 * j + 1] = e4m3x2_f16x2((uint16_t)(raw.code[m][k][j] >> 16));
+              h[2 * j] = e4m3x2_f16x2((uint16_t)code[m][k][j]);
+              h[2 * j + 1] = e4m3x2_f16x2((uint16_t)(code[m][k][j] >> 16));
             }
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[(j >> 1) * 4 + 2 * k + (j & 1)] = h[j];
         }
-        if (i > 0 && !warp_all(wait(M_PV + 8 * m, (i - 1) & 1))) return false;
-        if (L::SLOTS == 2 && m >= 2) {
-          if (!warp_all(wait(M_A + 8 * (m - 2), i & 1))) return false;
-          tc_fence_after();
-        }
+      };
+      auto to_tmem = [&](int m, const uint32_t (&v)[16]) { tmem_st16x256b(tm_a + L::TM_A + (m % 3) * 64 + half * 32, v); };
+      auto in_tmem = [&](int bar) {
+        tmem_st_wait();
+        tc_fence_before();
         __syncwarp();
-        tmem_st16x256b(tm_a + L::TM_A + (m % L::SLOTS) * 64 + half * 32, v);
+        if (lane == 0) mbar_arrive(mb + bar);
+      };
+      // (seen by the tensor core with the weights, which every thread stores after this)
+      auto to_shared = [&](int m, const uint32_t (&v)[16]) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          st_shared_v4(to0 + m * 2 * L::CHUNK + k * 1024, v[2 * k], v[2 * k + 1], v[4 + 2 * k], v[5 + 2 * k]);
-          st_shared_v4(to1 + m * 2 * L::CHUNK + k * 1024, v[8 + 2 * k], v[9 + 2 * k], v[12 + 2 * k], v[13 + 2 * k]);
+          const uint32_t at = m * 2 * L::CHUNK + k * 1024;
+          st_shared_v4(to0 + at, v[2 * k], v[2 * k + 1], v[4 + 2 * k], v[5 + 2 * k]);
+          st_shared_v4(to1 + at, v[8 + 2 * k], v[9 + 2 * k], v[12 + 2 * k], v[13 + 2 * k]);
         }
-        landed(1 + m);
+      };
+      // S^T's operand, as far as there is room: while P.V of the tile before is under way
+      uint32_t v[3][16];
+#pragma unroll
+      for (int m = 0; m < 3; ++m) {
+        to_fp16(m, v[m]);
+        to_tmem(m, v[m]);
       }
+      in_tmem(M_LAND);
+      // P.V's, as it leaves the places
+#pragma unroll
+      for (int m = 0; m < 3; ++m) {
+        if (i > 0 && !wait(M_PV + 8 * m, (i - 1) & 1)) return false;
+        to_shared(m, v[m]);
+      }
+      if (LATE) {
+        if (!wait(M_LATE, i & 1)) return false;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          rope[k] = lds16(sP + sw128_off(r0 + 8 * k, 4 * half + quad));
+          const uint4 x = lds16(to0 + 6 * L::CHUNK + k * 1024);
+          code[3][k][0] = x.x; code[3][k][1] = x.y; code[3][k][BITS / 2 - 2] = x.z; code[3][k][BITS / 2 - 1] = x.w;
+          if (sc[k] < 0.f) rope[k] = make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+      }
+      to_fp16(3, v[0]);
+      if (!wait(M_A, i & 1)) return false;
+      tc_fence_after();
+      to_tmem(3, v[0]);
+      if (!LATE && i > 0 && !wait(M_PV + 24, (i - 1) & 1)) return false;
+      if constexpr (ROPE) {  // P.V has read all of W: the position channels take its place
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float inv = sc[k] < 0.f ? 1.f : __frcp_rn(sc[k]);
+          const uint32_t by = pack_bf16x2(inv, inv);
+          st_shared_v4(sP + sw128_off(r0 + 8 * k, 4 * half + quad), mul_bf16x2(rope[k].x, by), mul_bf16x2(rope[k].y, by),
+                       mul_bf16x2(rope[k].z, by), mul_bf16x2(rope[k].w, by));
+        }
+        fence_proxy_async_smem();
+      }
+      in_tmem(M_LAND + 8);
+      to_shared(3, v[0]);
       return true;
     };
     // The run's queries: a row a warp, divided by a power of two, its channels in the order in which they lie in TMEM.
     auto load_q = [&](const Seg& s, int run) {
 #pragma unroll 1
-      for (int hh = warp; hh < NH; hh += kWarps) {
+      for (int hh = cg * 3 + qd; hh < NH; hh += kWorkers) {
         constexpr int UNITS = DQK / 8;
         uint4 v[3];
         uint32_t top = 0;
@@ -499,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
               const uint32_t by2 = pack_bf16x2(by, by);
               a = mul_bf16x2(w[2 * g], by2);
               b = mul_bf16x2(w[2 * g + 1], by2);
-              at = ((u - 64) >> 2) * 8 + g * 4 + ((u - 64) & 3);
+              at = 2 * (u - 64) + g;  // (these are read from shared memory, as they lie)
             }
             const uint32_t dst = sQ + (u >> 3) * L::Q_CHUNK + sw128_off(hh, at >> 1) + (at & 1) * 8;
             asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(a), "r"(b) : "memory");
@@ -510,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
       __syncwarp();
       if (lane == 0) mbar_arrive(mb + M_Q);
     };
-    // Maxima or sums over the warp's 32 positions of a thread's columns: the result is that of column n0 + lane / (32 / NC).
+    // Maxima or sums over the warp's 32 positions of a thread's columns: the result is that of column own_col.
     auto over_lanes = [&](float (&v)[NC], bool is_max) -> float {
       int w = NC / 2;
 #pragma unroll
@@ -532,58 +761,57 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
     };
     const int own_col = n0 + lane / (32 / NC);
     Seg sg;
-    bool aborted = named_bar_or(bar_id, 128, !read_seg(0, sg));
+    bool aborted = named_bar_or(bar_id, kTeam, !read_seg(0, sg));
     bool bad = false;
-    if (!aborted) {
-      load_q(sg, 0);
-      bad = !load_tile(0);
-    }
+    if (!aborted) load_q(sg, 0);
     int i = 0;
     for (int seg = 0; !aborted; ++seg) {
       const bool more = !sg.last;
-      // this thread's first row: its token in the group, and how many rows of that token there are from it on
-      const int tok0 = (sg.head0 + n0) / p.H, head_left = p.H - ((sg.head0 + n0) - tok0 * p.H);
-      float2 l_part[NC / 2];
+      float2 l_part[NC / 2], neg[NC / 2];
 #pragma unroll
-      for (int j = 0; j < NC / 2; ++j) l_part[j] = make_float2(0.f, 0.f);
-      // a column without a finite score yet has a maximum of -3e38, which any finite score passes and which leaves e^-inf at 0
-      if (qd == 0 && lane < NC) {
-        s_stat[n0 + lane] = -INFINITY;
-        s_neg[n0 + lane] = 3.0e38f;
+      for (int j = 0; j < NC / 2; ++j) {
+        l_part[j] = make_float2(0.f, 0.f);
+        neg[j] = make_float2(3.0e38f, 3.0e38f);
       }
-      named_bar(bar_id, 128);
+      // a column without a finite score yet has a maximum of -3e38, which any finite score passes and which leaves e^-inf at 0
+      if (qd == 0 && lane < NC) s_stat[n0 + lane] = -INFINITY;
+      named_bar(bar_id, kTeam);
       const float* col = s_col + (seg & 1) * 64 + n0;
       const int t_end = sg.t0 + sg.n;
 #pragma unroll 1
       for (int t = sg.t0; t < t_end; ++t, ++i) {
-        const bool end = t + 1 == t_end;
-        bad = bad || !convert(i);
-        if ((!end || more) && !bad) bad = !load_tile(i + 1);
-        bad = bad || !warp_all(wait(M_S, i & 1));
-        // (complete since before S^T was issued: orders the columns' factors and the rows' scales before their reads below)
-        bad = bad || !warp_all(wait(M_Q, seg & 1) && wait(M_LAND + 32, i & 1));
+        float s = -1.f;
+        bad = bad || !convert(i, s);
+        bad = bad || !wait(M_S, i & 1);
+        // (complete since before S^T was issued: orders the columns' factors before their reads below)
+        if (t == sg.t0) bad = bad || !wait(M_Q, seg & 1);
         tc_fence_after();
         __syncwarp();
-        uint32_t zr[NC];
-        tmem_ld<NC>(tmem_addr(tmem, qd * 32, L::TM_S + n0), zr);
-        const float s = s_scale[(i & 1) * kTile + row];
         const bool plain = s > 0.f;  // neither masked nor NaN
         const int ls = plain ? (int)(__float_as_uint(s) >> 23) - 127 : 0;
         const float log_s = (float)ls, inv_s = pow2(-ls);
-        tmem_ld_wait();
-        // scores in log2 units; the exponents of the weights: with s, above the running maximum
-        float2 z[NC / 2], e[NC / 2];
-#pragma unroll
-        for (int j = 0; j < NC / 2; ++j) {
-          const float2 f = mul2(*reinterpret_cast<const float2*>(col + 2 * j), make_float2(s, s));
-          z[j] = fma2(make_float2(__uint_as_float(zr[2 * j]), __uint_as_float(zr[2 * j + 1])), f, make_float2(log_s, log_s));
-        }
         const int pos = t * kTile + row;
+        const bool partly = p.topk_idx == nullptr && (t + 1) * (long long)kTile > sg.seen0;  // some token may not see all of it
+        // scores in log2 units, with s
+        float2 z[NC / 2];
+        {
+          uint32_t zr[NC];
+          tmem_ld<NC>(tmem_addr(tmem, qd * 32, L::TM_S + n0), zr);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < NC / 4; ++j) {
+            const float4 c = *reinterpret_cast<const float4*>(col + 4 * j);
+            const float2 f0 = mul2(make_float2(c.x, c.y), make_float2(s, s)), f1 = mul2(make_float2(c.z, c.w), make_float2(s, s));
+            z[2 * j] = fma2(make_float2(__uint_as_float(zr[4 * j]), __uint_as_float(zr[4 * j + 1])), f0, make_float2(log_s, log_s));
+            z[2 * j + 1] = fma2(make_float2(__uint_as_float(zr[4 * j + 2]), __uint_as_float(zr[4 * j + 3])), f1, make_float2(log_s, log_s));
+          }
+        }
         if (s < 0.f) {
 #pragma unroll
           for (int j = 0; j < NC / 2; ++j) z[j] = make_float2(-INFINITY, -INFINITY);
-        } else if (p.topk_idx == nullptr && (t + 1) * (long long)kTile > sg.seen0) {  // some token may not see all of it
-          int seen = sg.seen0 + tok0, left = head_left;
+        } else if (partly) {
+          const int tok0 = (sg.head0 + n0) / p.H;
+          int seen = sg.seen0 + tok0, left = p.H - ((sg.head0 + n0) - tok0 * p.H);
 #pragma unroll
           for (int j = 0; j < NC; ++j) {
             if (pos >= seen) (j & 1 ? z[j / 2].y : z[j / 2].x) = -INFINITY;
@@ -593,12 +821,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
         bool mine = t == sg.t0;
 #pragma unroll
         for (int j = 0; j < NC / 2; ++j) {
-          e[j] = add2(z[j], *reinterpret_cast<const float2*>(s_neg + n0 + 2 * j));
-          mine |= e[j].x > kRaise || e[j].y > kRaise;
+          const float2 e = add2(z[j], neg[j]);
+          mine |= fmaxf(e.x, e.y) > kRaise;
         }
         bool raise = false;
-        if (named_bar_or(bar_id, 128, mine || bad)) {
-          if (named_bar_or(bar_id, 128, bad)) { aborted = true; break; }
+        if (named_bar_or(bar_id, kTeam, mine || bad)) {
+          if (named_bar_or(bar_id, kTeam, bad)) { aborted = true; break; }
           raise = true;
         }
         if (raise) {
@@ -606,20 +834,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
 #pragma unroll
           for (int j = 0; j < NC / 2; ++j) { top[2 * j] = z[j].x; top[2 * j + 1] = z[j].y; }
           s_red[qd * 64 + own_col] = over_lanes(top, true);
-          named_bar(bar_id, 128);
+          named_bar(bar_id, kTeam);
           if (qd == 0 && lane < NC) {
             const int n = n0 + lane;
-            const float bm = fmaxf(fmaxf(s_red[n], s_red[64 + n]), fmaxf(s_red[128 + n], s_red[192 + n])) - kTop;
+            const float bm = fmaxf(fmaxf(s_red[n], s_red[64 + n]), s_red[128 + n]) - kTop;
             const float mo = s_stat[n], mn = fmaxf(mo, bm);
             s_stat[n] = mn;
             s_neg[n] = -fmaxf(mn, -3.0e38f);
             s_fac[n] = mo == -INFINITY ? 0.f : exp2f(mo - mn);
           }
-          named_bar(bar_id, 128);
+          named_bar(bar_id, kTeam);
 #pragma unroll
           for (int j = 0; j < NC / 2; ++j) {
             l_part[j] = mul2(l_part[j], *reinterpret_cast<const float2*>(s_fac + n0 + 2 * j));
-            e[j] = add2(z[j], *reinterpret_cast<const float2*>(s_neg + n0 + 2 * j));
+            neg[j] = *reinterpret_cast<const float2*>(s_neg + n0 + 2 * j);
           }
           if (t > sg.t0) {  // (P.V of the tile before has been waited for)
 #pragma unroll 1
@@ -634,12 +862,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
             }
             tmem_st_wait();
           }
-          named_bar(bar_id, 128);  // the factors have been read
+          named_bar(bar_id, kTeam);  // the factors have been read
         }
+        if (qd == 0 && lane == 0) s_flag[(i & 1) * 4 + cg] = raise;
         uint32_t w[NC / 2];
 #pragma unroll
         for (int j = 0; j < NC / 2; ++j) {
-          const float2 x = make_float2(ex2(e[j].x), ex2(e[j].y));
+          const float2 e = add2(z[j], neg[j]);
+          const float2 x = make_float2(ex2(e.x), ex2(e.y));
           l_part[j] = fma2(x, make_float2(inv_s, inv_s), l_part[j]);
           w[j] = pack_f16x2(x.x, x.y);
         }
@@ -665,17 +895,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
         if (!read_seg(seg + 1, nx)) bad = true;
         else load_q(nx, seg + 1);  // (S^T of the run is done: Q is free)
       }
+      if (seg > 0 && !wait(M_EPI, (seg - 1) & 1)) bad = true;  // (its factors have been read)
       // ---- the run's rows: out and lse, or the workspace's partial sums ----
       float sums[NC];
 #pragma unroll
       for (int j = 0; j < NC / 2; ++j) { sums[2 * j] = l_part[j].x; sums[2 * j + 1] = l_part[j].y; }
       s_red[qd * 64 + own_col] = over_lanes(sums, false);
-      named_bar(bar_id, 128);
+      named_bar(bar_id, kTeam);
       const bool whole = sg.whole;
       const int slot = 2 * blockIdx.x + (sg.opens ? 1 : 0);
       if (qd == 0 && lane < NC) {
         const int n = n0 + lane;
-        const float l = s_red[n] + s_red[64 + n] + s_red[128 + n] + s_red[192 + n];
+        const float l = s_red[n] + s_red[64 + n] + s_red[128 + n];
         const float m = s_stat[n];
         float fac = 1.f;
         if (whole) {
@@ -689,37 +920,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
           p.stats[(size_t)slot * 128 + n] = m;
           p.stats[(size_t)slot * 128 + 64 + n] = l;
         }
-        s_fac[n] = fac;
+        s_fin[(seg & 1) * 64 + n] = fac;
       }
-      named_bar(bar_id, 128);
+      if (qd == 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(mb + M_FAC);
+      }
+      named_bar(bar_id, kTeam);
       const bool got = wait(M_PV + 24, (i - 1) & 1);
-      aborted = named_bar_or(bar_id, 128, !got || bad);
+      aborted = named_bar_or(bar_id, kTeam, !got || bad);
       if (aborted) break;
       tc_fence_after();
-#pragma unroll 1
-      for (int m = 0; m < 4; ++m) {
-        uint32_t ov[NC];
-        tmem_ld<NC>(tmem_addr(tmem, qd * 32, m * NH + n0), ov);
-        tmem_ld_wait();
-        const int c = m * 128 + qd * 32 + lane, rows = sg.rows - n0;
-        // (one branch for all rows: with one for each, every store waits for the one before)
-        if (whole) {
-          __nv_bfloat16* dst = p.out + (size_t)(sg.row0 + n0) * kDv + c;
-          float f[NC];
-#pragma unroll
-          for (int h = 0; h < NC; ++h) f[h] = s_fac[n0 + h];
-#pragma unroll
-          for (int h = 0; h < NC; ++h)
-            if (h < rows) dst[h * kDv] = __float2bfloat16_rn(f[h] == 0.f ? 0.f : __uint_as_float(ov[h]) * f[h]);
-        } else {
-          float* part = p.partial + ((size_t)slot * 64 + n0) * kDv + c;
-#pragma unroll
-          for (int h = 0; h < NC; ++h)
-            if (h < rows) part[h * kDv] = __uint_as_float(ov[h]);
-        }
-      }
+      store_quarter<NH>(p, sg, tmem, qd, n0, s_out + (seg & 1) * 64);
       tc_fence_before();
-      named_bar(bar_id, 128);  // s_red, s_stat and s_fac have been read
+      named_bar(bar_id, kTeam);  // s_red, s_stat and s_fac have been read
       if (!more) break;
       sg = nx;
     }
@@ -727,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == 3) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
     if (lane == 0 && *s_abort) record_error(p.err, DSA_ERR_TIMEOUT);
@@ -736,9 +950,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
 
 constexpr size_t kRecordOff = kErrorWordBytes, kStatOff = kRecordOff + kRecordBytes, kPartialOff = kStatOff + kStatBytes;
 
-template <int DQK, int NH, int BITS>
+template <int DQK, int NH, int BITS = 4>
 dsa_status_t launch(Params& p, int ctas, cudaStream_t s) {
-  using L = Smem<DQK, NH>;
+  using L = Smem<DQK, NH, BITS>;
   dsa_status_t st = configure_kernel_smem(reinterpret_cast<const void*>(paged_mla_quant_kernel<DQK, NH, BITS>), L::TOTAL,
                                           "configuring paged_mla_quant_kernel");
   if (st != DSA_OK) return st;
@@ -748,11 +962,6 @@ dsa_status_t launch(Params& p, int ctas, cudaStream_t s) {
   paged_mla_quant_kernel<DQK, NH, BITS><<<ctas, kThreads, L::TOTAL, s>>>(p);
   return cuda_check(cudaGetLastError(), "launching paged_mla_quant_kernel");
 }
-template <int DQK, int NH>
-dsa_status_t launch(Params& p, int bits, int ctas, cudaStream_t s) {
-  return bits == 8 ? launch<DQK, NH, 8>(p, ctas, s) : launch<DQK, NH, 4>(p, ctas, s);
-}
-
 }  // namespace pmlaq
 }  // namespace dsa
 
@@ -778,6 +987,8 @@ extern "C" dsa_status_t dsa_paged_mla_quant(const dsa_bf16_t* q, const uint8_t* 
   if (Dv != 512) return fail(DSA_ERR_INVALID_ARGUMENT, "%s: Dv must be 512 (got %d)", who, Dv);
   if (bits != 8 && bits != 4) return fail(DSA_ERR_INVALID_ARGUMENT, "%s: bits must be 8 or 4 (got %d)", who, bits);
   if ((int64_t)N * H > 0x7fffffffll) return fail(DSA_ERR_INVALID_ARGUMENT, "%s: N * H must be below 2^31", who);
+  if ((int64_t)num_pages * page_size > 0x7fffffffll)
+    return fail(DSA_ERR_INVALID_ARGUMENT, "%s: num_pages * page_size must be below 2^31", who);
   if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f))
     return fail(DSA_ERR_INVALID_ARGUMENT, "%s: softmax_scale must be finite and > 0", who);
   if (!cu_q && N != B)
@@ -825,8 +1036,9 @@ extern "C" dsa_status_t dsa_paged_mla_quant(const dsa_bf16_t* q, const uint8_t* 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // 16 columns while all rows of a request (or of a list) fit
   const int64_t rows = (int64_t)H * (topk_idx ? 1 : (N + B - 1) / B);
-  if (rows <= 16) st = Dqk == 576 ? pmlaq::launch<576, 16>(p, bits, ctas, s) : pmlaq::launch<512, 16>(p, bits, ctas, s);
-  else st = Dqk == 576 ? pmlaq::launch<576, 64>(p, bits, ctas, s) : pmlaq::launch<512, 64>(p, bits, ctas, s);
+  if (bits == 8) st = launch_paged_mla_e4m3(p, p.q, cache, Dqk, p.sl2e, rows <= 16, ctas, s);
+  else if (rows <= 16) st = Dqk == 576 ? pmlaq::launch<576, 16>(p, ctas, s) : pmlaq::launch<512, 16>(p, ctas, s);
+  else st = Dqk == 576 ? pmlaq::launch<576, 64>(p, ctas, s) : pmlaq::launch<512, 64>(p, ctas, s);
   if (st != DSA_OK) return st;
   st = pgroups::launch_join(p, ctas, s);
   return st == DSA_OK ? ok() : st;

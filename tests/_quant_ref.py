@@ -67,14 +67,15 @@ def decode(rows, D, Q, bits):
 def attention(q, cache, bits, table, seq_lens, cu_q, scale, sink=None, topk=None, topk_len=None):
     """out [N, H, 512], lse [N, H] in 64 bits (NaN outside the requests), and per row what bounds a kernel's error:
     size [N, H] = the largest scale * sum |q k| over the positions seen, mass [N, H, 512] = sum of weights * |kv|,
-    top [N, H, 512] = (the largest weight times its row's s) * sum of |kv| / s."""
+    top [N, H, 512] = (the largest weight times its row's s) * sum of |kv| / s, and most [N, H] = the largest scale * (largest
+    |q| of the first 512 channels) * sum of their |k|."""
     N, H, D = q.shape
     page = cache.shape[1]
     flat = cache.cpu().reshape(-1, cache.shape[2])
     nan = float("nan")
     out, mass = torch.full((N, H, 512), nan, dtype=torch.float64), torch.zeros(N, H, 512, dtype=torch.float64)
     lse, size = torch.full((N, H), nan, dtype=torch.float64), torch.zeros(N, H, dtype=torch.float64)
-    top, at_s = torch.zeros_like(mass), layout(D, 512, bits)[1]
+    top, most, at_s = torch.zeros_like(mass), torch.zeros_like(size), layout(D, 512, bits)[1]
     for b in range(len(seq_lens)):
         lo, hi = cu_q[b], cu_q[b + 1]
         for n in range(lo, hi):
@@ -97,24 +98,32 @@ def attention(q, cache, bits, table, seq_lens, cu_q, scale, sink=None, topk=None
                 size[n] = (q[n].double().abs() @ kv.abs().T).max(1).values * scale
                 s = flat[rows][:, at_s:at_s + 4].contiguous().view(torch.float32).double()[:, 0]
                 top[n] = (p * s).max(1, keepdim=True).values * (kv[:, :512].abs() / s[:, None]).sum(0)
-    return out, lse, size, mass, top
+                most[n] = q[n, :, :512].double().abs().max(1).values * float(kv[:, :512].abs().sum(1).max()) * scale
+    return out, lse, size, mass, top, most
 
 
-def check_attention(got, want):
+def check_attention(got, want, bits):
     """out and lse of a kernel against attention()'s answer; rows that are NaN there are not looked at.
 
     A score is a sum of 576 exact products in fp32.  Whether they are added one by one, by sixteens or in a tree, and by
-    truncation or to nearest, its error is at most 80 * 2^-23 times the sum of magnitudes, times the scale: dz.  Forming
-    2^x from it adds 2^-21 of a weight, and 2^-23 of x, |x| being at most twice size.  A weight is rounded to 11 bits
-    (2^-11), and where it is below 2^-14 to a multiple of 2^-24, the largest weight times its row's s being 2^7 at least: that
-    is 2^-32 of it times |kv| / s of each position at most.  A sum of weights or products in fp32 adds less than 2^-13 of its mass at the lengths tested; the output is
-    rounded to bf16 (2^-8 of it)."""
-    out, lse, size, mass, top = want
+    truncation or to nearest, its error is at most 80 * 2^-23 times the sum of magnitudes, times the scale: dz.  With 8 bits
+    a query is two numbers of 4 bits, which leaves up to 2^-17 of its row's largest channel of each channel.  Forming 2^x
+    from a score adds 2^-21 of a weight, and 2^-23 of x, |x| being at most twice size.
+
+    4 bits: a weight is rounded to 11 bits (2^-11), and where it is below 2^-14 to a multiple of 2^-24, the largest weight
+    times its row's s being 2^7 at least: that is 2^-32 of it times |kv| / s of each position at most.
+    8 bits: to 3 bits, which leaves 2^-3 of its power of two at most, and what is left to 4 bits (2^-7 of the weight) or,
+    below 2^-6, to a multiple of 2^-9 (2^-10), the largest weight times its row's s being 2^5 at least: 2^-15 of it.
+
+    A sum of weights or products in fp32 adds less than 2^-13 of its mass at the lengths tested; the output is rounded to
+    bf16 (2^-8 of it)."""
+    out, lse, size, mass, top, most = want
     o, l = got[0].cpu().double(), got[1].cpu().double()
     seen = ~torch.isnan(lse)
-    dz = 84 * 2.0 ** -23 * size + 2.0 ** -20
+    dz = 84 * 2.0 ** -23 * size + 2.0 ** -20 + (2.0 ** -17 * most if bits == 8 else 0.0)
     fin = seen & torch.isfinite(lse)
     assert torch.equal(torch.isinf(l) & seen, torch.isinf(lse) & seen)
     assert bool(((l - lse).abs() <= dz + 2.0 ** -13 + 2.0 ** -22 * lse.abs())[fin].all())
-    tol = 2.0 ** -8 * out.abs() + (2.0 ** -11 + 2.0 ** -13 + 2 * dz)[..., None] * mass + 2.0 ** -32 * top + 2.0 ** -133
+    w, floor = (2.0 ** -7, 2.0 ** -15) if bits == 8 else (2.0 ** -11, 2.0 ** -32)
+    tol = 2.0 ** -8 * out.abs() + (w + 2.0 ** -13 + 2 * dz)[..., None] * mass + floor * top + 2.0 ** -133
     assert bool((o - out).abs()[seen].le(tol[seen]).all()), float(((o - out).abs() / tol)[seen].max())

@@ -57,7 +57,7 @@ def compare(bits, D, H, page, lens, news, seed=0, sink=False, scale=None, **kw):
     ws = workspace()
     got = run(bits, cache, table, q, lens, cu, scale, sink=s, ws=ws)
     assert dsa.dsa_read_device_status(ws) == 0
-    ref.check_attention(got, ref.attention(q, cache, bits, table, lens, cu, scale, s))
+    ref.check_attention(got, ref.attention(q, cache, bits, table, lens, cu, scale, s), bits)
     return got
 
 
@@ -108,7 +108,7 @@ def test_lists(bits, H, K, sink):
     ws = workspace()
     got = run(bits, cache, table, q, lens, cu, 0.04, idx, length, s, ws)
     assert dsa.dsa_read_device_status(ws) == 0
-    ref.check_attention(got, ref.attention(q, cache, bits, table, lens, cu, 0.04, s, idx, length))
+    ref.check_attention(got, ref.attention(q, cache, bits, table, lens, cu, 0.04, s, idx, length), bits)
 
 
 @pytest.mark.parametrize("bits", [8, 4])
@@ -125,7 +125,7 @@ def test_rows_and_queries_of_every_size(bits, kw, H):
 def test_heads_of_very_different_size(bits, H):
     g, cache, table, q, cu = make(bits, 576, H, 64, [300], [2])
     q = (q.float() * torch.exp2(torch.randint(-40, 3, (2, H, 1), generator=g).float())).bfloat16()
-    ref.check_attention(run(bits, cache, table, q, [300], cu, 0.1), ref.attention(q, cache, bits, table, [300], cu, 0.1))
+    ref.check_attention(run(bits, cache, table, q, [300], cu, 0.1), ref.attention(q, cache, bits, table, [300], cu, 0.1), bits)
 
 
 @pytest.mark.parametrize("bits", [8, 4])
@@ -138,7 +138,7 @@ def test_a_maximum_that_rises_late_and_one_that_comes_first(bits, H):
         slots = torch.tensor([int(table[0, p // 64]) * 64 + p % 64 for p in range(700)], dtype=I32, device=DEV)
         dsa.dsa_paged_quantize(x.bfloat16().to(DEV), cache, bits, out_rows=slots)
         qq = (q.float().abs() * 0.3).bfloat16()
-        ref.check_attention(run(bits, cache, table, qq, lens, cu, 0.05), ref.attention(qq, cache, bits, table, lens, cu, 0.05))
+        ref.check_attention(run(bits, cache, table, qq, lens, cu, 0.05), ref.attention(qq, cache, bits, table, lens, cu, 0.05), bits)
 
 
 @pytest.mark.parametrize("bits", [8, 4])
@@ -153,7 +153,7 @@ def test_a_nan_row_reaches_the_tokens_that_see_it(bits, H):
     out, lse = run(bits, cache, table, q, lens, cu, 0.04)
     assert bool(torch.isnan(out[1:]).all()) and bool(torch.isnan(lse[1:]).all())
     want = ref.attention(q[:1], cache, bits, table, [198], [0, 1], 0.04)
-    ref.check_attention((out[:1], lse[:1]), want)
+    ref.check_attention((out[:1], lse[:1]), want, bits)
 
 
 @pytest.mark.parametrize("bits", [8, 4])
@@ -165,7 +165,7 @@ def test_rows_outside_the_requests_are_left(bits):
     run(bits, cache, table, q, [30, 40], [2, 4, 5], 0.04, out=out, lse=lse)
     assert bool((out[:2] == 5).all()) and bool((out[5:] == 5).all()) and bool((lse[5:] == 5).all())
     want = ref.attention(q, cache, bits, table, [30, 40], [2, 4, 5], 0.04)
-    ref.check_attention((out, lse), want)
+    ref.check_attention((out, lse), want, bits)
 
 
 @pytest.mark.parametrize("bits", [8, 4])
@@ -181,17 +181,17 @@ def test_bad_pages_and_positions_are_masked_and_reported(bits, lists):
         got = run(bits, cache, t, q, lens, cu, 0.04, idx, ws=ws)
         assert dsa.dsa_read_device_status(ws) == 6
         keep = torch.tensor([[p for p in range(200) if p // 32 != 2]], dtype=I32)
-        ref.check_attention(got, ref.attention(q, cache, bits, table, lens, cu, 0.04, None, keep))
+        ref.check_attention(got, ref.attention(q, cache, bits, table, lens, cu, 0.04, None, keep), bits)
     if lists:
         idx = torch.tensor([[0, 200, -7, 5, 2 ** 31 - 1, -2 ** 31]], dtype=I32)
         got = run(bits, cache, table, q, lens, cu, 0.04, idx, ws=ws)
         assert dsa.dsa_read_device_status(ws) == 6
-        ref.check_attention(got, ref.attention(q, cache, bits, table, lens, cu, 0.04, None, torch.tensor([[0, 5]], dtype=I32)))
+        ref.check_attention(got, ref.attention(q, cache, bits, table, lens, cu, 0.04, None, torch.tensor([[0, 5]], dtype=I32)), bits)
     else:  # a request longer than its table
         got = run(bits, cache, table[:, :3].contiguous(), q, lens, cu, 0.04, ws=ws)
         assert dsa.dsa_read_device_status(ws) == 6
         keep = torch.arange(96, dtype=I32)[None]
-        ref.check_attention(got, ref.attention(q, cache, bits, table, lens, cu, 0.04, None, keep))
+        ref.check_attention(got, ref.attention(q, cache, bits, table, lens, cu, 0.04, None, keep), bits)
 
 
 @pytest.mark.parametrize("bits", [8, 4])
@@ -200,7 +200,7 @@ def test_many_requests_and_equal_bits(bits):
     news = [1 + i % 3 for i in range(70)]
     g, cache, table, q, cu = make(bits, 576, 16, 16, lens, news, 9)
     first = run(bits, cache, table, q, lens, cu, 0.04)
-    ref.check_attention(first, ref.attention(q, cache, bits, table, lens, cu, 0.04))
+    ref.check_attention(first, ref.attention(q, cache, bits, table, lens, cu, 0.04), bits)
     ws = workspace()
     for _ in range(3):
         again = run(bits, cache, table, q, lens, cu, 0.04, ws=ws)
