@@ -49,7 +49,7 @@ struct Smem {
   static constexpr int NCH = ROPE ? 5 : 4;      // 128 codes each, then the position channels
   static constexpr int CHUNK = kTile * 128;
   static constexpr int Q_CHUNK = 2 * NH * 128;  // hi rows, lo rows
-  static constexpr int R = 3;                   // tiles in the ring
+  static constexpr int R = NH == 64 ? 3 : 4;    // tiles in the ring
   static constexpr int NS = NH == 64 ? 1 : 2;   // S^T buffers in TMEM
   static constexpr int SW = (ROPE ? 3 : 2) * NH;
   static constexpr int P_BLOCK = NH == 64 ? kTile * 128 : 2 * NH * 128;
@@ -66,12 +66,12 @@ struct Smem {
 };
 
 // misc (bytes).  A tile's channels are given back 128 at a time as P.V reads them.
-constexpr int kSteps = 4, kSlots = 3;
-constexpr int M_KV = 0, M_PV = 48, M_S = 144, M_SF = 160, M_P = 176, M_Q = 192, M_FIN = 200;  // [3] [3][4] [2] [2] [2] 1 [2]
-constexpr int M_SEGF = 216, M_SEGE = M_SEGF + 8 * kSegs;  // [kSegs] each: announced, read by all
-constexpr int M_TMEM = 344, M_ABORT = 348, M_PLAN = 352;  // plan: 56 bytes
-constexpr int M_SEG = 416;                    // int4 [kSegs][2]
-constexpr int M_RED = 672;                    // float [4][64]; the first row also holds the factors of a rescale
+constexpr int kSteps = 4, kSlots = 4;
+constexpr int M_KV = 0, M_PV = 32, M_S = 160, M_SF = 176, M_P = 192, M_Q = 208, M_FIN = 216;  // [4] [4][4] [2] [2] [2] 1 [2]
+constexpr int M_SEGF = 232, M_SEGE = M_SEGF + 8 * kSegs;  // [kSegs] each: announced, read by all
+constexpr int M_TMEM = 360, M_ABORT = 364, M_PLAN = 368;  // plan: 56 bytes
+constexpr int M_SEG = 432;                    // int4 [kSegs][2]
+constexpr int M_RED = 688;                    // float [4][64]; the first row also holds the factors of a rescale
 constexpr int M_STAT = M_RED + 1024;          // float [64]
 constexpr int M_COL = M_STAT + 256;           // float [2][64]: a column's factor of the score, by run
 constexpr int M_SCALE = M_COL + 512;          // float [kSlots][64]: s of the rows, -1: masked
@@ -121,6 +121,10 @@ __device__ __forceinline__ void mma_f8_w(uint32_t d_tmem, uint64_t a, uint64_t b
   }
 }
 
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // Two values to e4m3 or e5m2 (the first in the lower half), and e5m2 back.
 __device__ __forceinline__ uint32_t e4m3x2(float2 v) {
   uint16_t r;
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
   constexpr bool ROPE = L::ROPE;
   constexpr int NCH = L::NCH, R = L::R, NS = L::NS;
   constexpr int NHH = NH / 2, NQ = NHH / 2;  // rows per softmax half, per thread
-  static_assert(R == kSlots, "ring");
+  static_assert(R <= kSlots, "ring");
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sKV = smem_u32(smem) + L::OFF_KV, sQ = smem_u32(smem) + L::OFF_Q, sP = smem_u32(smem) + L::OFF_P;
   uint8_t* misc = smem + L::OFF_MISC;
@@ -172,7 +176,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc + M_TMEM);
   volatile int* s_abort = reinterpret_cast<volatile int*>(misc + M_ABORT);
   Plan* s_plan = reinterpret_cast<Plan*>(misc + M_PLAN);
+  const uint32_t sScale = smem_u32(misc + M_SCALE);
   volatile float* s_scale = reinterpret_cast<volatile float*>(misc + M_SCALE);
+  auto scale_of = [&](int at) {  // (a row that was never written, of zero bytes, holds zeros; -1: masked)
+    const float s = s_scale[at];
+    return s >= 0.f && s < kLeast ? kLeast : s;
+  };
   float* s_stat = reinterpret_cast<float*>(misc + M_STAT);
   float* s_fac = reinterpret_cast<float*>(misc + M_RED);  // a column's factor replaces its first maximum or sum
   float* s_red = reinterpret_cast<float*>(misc + M_RED);
@@ -340,34 +349,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
       k.pos -= (int)at * p.P;
       return __ldg(p.table + (size_t)k.b * p.max_pages + at);
     };
-    auto row_of = [&](int pos, int page, float& s) -> int {
-      s = -1.f;
+    auto row_of = [&](int pos, int page) -> int {
       if (pos < 0) return -1;
-      if (page >= 0 && page < p.num_pages) {
-        const int row = page * p.P + pos;
-        s = __ldg(reinterpret_cast<const float*>(p.cache + (size_t)row * L::LAY.bytes + L::LAY.scale));
-        return row;
-      }
+      if (page >= 0 && page < p.num_pages) return page * p.P + pos;
       bad_index = true;
       return -1;
     };
+    auto to_l2 = [&](int row) {
+#pragma unroll
+      for (int x = 0; x < kRows; x += 4) {  // four rows, eight lanes each
+        const int at = __shfl_sync(0xffffffffu, row, x + (lane >> 3));
+        if (at >= 0 && (lane & 7) * 128 < L::LAY.bytes)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.cache + (size_t)at * L::LAY.bytes + (lane & 7) * 128));
+      }
+    };
     Look look[3];
-    int page[2], row[2];  // rows of the next two tiles, and their s
-    float scale[2];
+    int page[2], row[2];  // rows of the next two tiles
 #pragma unroll
     for (int k = 0; k < 3; ++k) look[k] = position(k);
     page[0] = page_of(look[0]);
     page[1] = page_of(look[1]);
-    row[0] = row_of(look[0].pos, page[0], scale[0]);
-    row[1] = row_of(look[1].pos, page[1], scale[1]);
+    row[0] = row_of(look[0].pos, page[0]);
+    row[1] = row_of(look[1].pos, page[1]);
     look[0] = look[2];
     page[0] = page_of(look[0]);
     look[1] = position(3);
+    to_l2(row[1]);
 #pragma unroll 1
     for (int i = 0; i < n_tiles && !stop; ++i) {
       const int sl = i % R;
       if (i >= R && !warp_all(wait_pv(i - R, 3))) { stop = true; break; }
-      if (lane < kRows) s_scale[sl * kTile + gw * kRows + lane] = scale[0] >= 0.f && scale[0] < kLeast ? kLeast : scale[0];
+      if (lane < kRows) {
+        const int r = sl * kTile + gw * kRows + lane;
+        if (row[0] < 0) s_scale[r] = -1.f;
+        else cp_async4(sScale + 4 * r, p.cache + (size_t)row[0] * L::LAY.bytes + L::LAY.scale);
+      }
       const uint32_t to = sKV + sl * NCH * L::CHUNK;
 #pragma unroll
       for (int x0 = 0; x0 < kRows; x0 += 8) {  // eight rows at a time: a copy's registers are free only when it has been taken
@@ -395,11 +411,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_kv + 8 * sl);
       row[0] = row[1];
-      scale[0] = scale[1];
-      row[1] = row_of(look[0].pos, page[0], scale[1]);
+      row[1] = row_of(look[0].pos, page[0]);
       look[0] = look[1];
       page[0] = page_of(look[0]);
       look[1] = position(i + 4);
+      to_l2(row[1]);
     }
     if (bad_index) record_error(p.err, DSA_ERR_DEVICE_INDEX);
     asm volatile("cp.async.wait_all;" ::: "memory");  // nothing lands after the CTA has left
@@ -526,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
             const uint32_t got = __shfl_xor_sync(0xffffffffu, par ? x[j] : x[NQ / 2 + j], 2);
             return make_float2(__uint_as_float(par ? got : x[j]), __uint_as_float(par ? x[NQ / 2 + j] : got));
           };
-          const float s = s_scale[sl * kTile + r], log_s0 = s > 0.f ? (float)((int)(__float_as_uint(s) >> 23) - 127) : 0.f;
+          const float s = scale_of(sl * kTile + r), log_s0 = s > 0.f ? (float)((int)(__float_as_uint(s) >> 23) - 127) : 0.f;
 #pragma unroll
           for (int j = 0; j < NQ / 2; ++j) {
             const float2 f = mul2(*reinterpret_cast<const float2*>(col + 2 * j), make_float2(s, s));
@@ -536,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
           }
         }
         if (t + 1 == t_end && more && !bad) load_q(nx, seg);  // S^T of the segment is done: Q is free
-        const float s = s_scale[sl * kTile + r];
+        const float s = scale_of(sl * kTile + r);
         const float inv_s = s > 0.f ? pow2(127 - (int)(__float_as_uint(s) >> 23)) : 1.f;
         const int pos = t * kTile + r;
         if (s < 0.f) {
