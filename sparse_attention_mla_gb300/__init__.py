@@ -9,6 +9,7 @@ the library is missing or the device is not sm_103, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import re
@@ -954,12 +955,16 @@ def dsa_paged_mla(q, cache, block_table, seq_lens, softmax_scale: float, cu_q=No
     return out, lse
 
 
+@functools.lru_cache(maxsize=64)
+def _quant_row_bytes(D: int, quant_dim: int, bits: int) -> int:  # (a property of the format)
+    return int((_lib or load_library()).dsa_paged_quant_row_bytes(D, quant_dim, bits))
+
+
 def paged_quant_row_bytes(D: int, bits: int, quant_dim: int | None = None) -> int:
     """Bytes of a row of D channels in a quantised cache (uint8 [num_pages, page_size, row bytes]) whose first quant_dim
     channels (default: 512, or all of fewer) are held in 8 or 4 bits; the format is described in include/dsa.h."""
-    lib = _lib or load_library()
     q = min(int(D), 512) if quant_dim is None else int(quant_dim)
-    n = int(lib.dsa_paged_quant_row_bytes(int(D), q, int(bits)))
+    n = _quant_row_bytes(int(D), q, int(bits))
     if n == 0:
         raise ValueError(f"no such rows: D = {D}, quant_dim = {q}, bits = {bits} (bits 8 or 4, quant_dim a multiple of 64, "
                          "D <= 1024, the other channels a multiple of 8)")

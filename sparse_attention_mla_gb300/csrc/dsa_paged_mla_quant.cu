@@ -1,10 +1,11 @@
-// dsa_paged_mla_quant.cu -- attention of new tokens over a paged cache of quantised latents (sm_103a).
+// dsa_paged_mla_quant.cu -- attention of new tokens over a paged cache of quantised latents (sm_103a): the kernel for rows of
+// 4 bits, and the entry point for both (8 bits: dsa_paged_mla_e4m3.cu).
 //
 // For new token j of request b and head h:  z_p = scale <q, kv_p> over the positions p it sees,
-// lse = ln sum e^{z_p},  out = sum e^{z_p - lse} kv_p[0:512],  kv_p = v_p s_p with v_p = code (8 bits) or code * block
-// (4 bits) for the first 512 channels and s_p the row's scale.
+// lse = ln sum e^{z_p},  out = sum e^{z_p - lse} kv_p[0:512],  kv_p = v_p s_p with v_p = code * block (e2m1 times
+// e4m3) for the first 512 channels and s_p the row's scale, a power of two.
 //
-// What a code stands for without s is exact in fp16 (4 or 6 bits between 2^-10 and 2688), so the products run in fp16
+// v is exact in fp16 (6 bits between 2^-10 and 2688), so the products run in fp16
 // and s stays outside of them: z_p = s_p <q, v_p> + <q', kv'_p>, with the position channels' part in bf16, divided by
 // s_p (a power of two); and the output sums the weights w_p = e^{z_p} s_p.  The running maximum is that of w, not of
 // e^{z}: w in fp16 (11 bits, 2^15 down to 2^-24 around a maximum of 2^7) then loses nothing that counts, whatever the
@@ -41,25 +42,20 @@ constexpr float kRaise = 15.0f;           // log2 units: the running maximum is 
 constexpr float kTop = 7.0f;              // a new maximum is 2^7
 constexpr float kLeast = 3.5527136788005009e-15f;  // 2^-48, the least s
 
-template <int DQK, int NH, int BITS>
+template <int DQK, int NH>
 struct Smem {
   static constexpr bool kRope = DQK == 576;
-  static constexpr QuantRow LAY = quant_row(DQK, kDv, BITS);
+  static constexpr QuantRow LAY = quant_row(DQK, kDv, 4);
   static constexpr int CHUNK = kTile * 128;  // 64 channels of a tile
   static constexpr int Q_CHUNK = NH * 128;
   static constexpr int P_BYTES = NH == 64 || kRope ? kTile * 128 : 2 * NH * 128;  // (position channels lie there before W)
-  // With 8 bits, 64 columns and position channels there is no room for whole rows: the last 128 channels' codes come late,
-  // to where they will be written as fp16, the position channels to the place of W.
-  static constexpr bool LATE = BITS == 8 && NH == 64 && kRope;
-  static constexpr int PITCH = LATE ? 400 : LAY.bytes;  // of a row as it comes: an odd number of 16 bytes
-  static constexpr int SCALE_AT = LATE ? 384 : LAY.scale;
   static constexpr int OFF_Q = 8 * CHUNK;
   static constexpr int OFF_P = OFF_Q + (kRope ? 9 : 8) * Q_CHUNK;
   static constexpr int OFF_MISC = OFF_P + P_BYTES;
   static constexpr int MISC = 3584;
   static constexpr int OFF_RAW = OFF_MISC + MISC;
-  static constexpr int TOTAL = OFF_RAW + kTile * PITCH;
-  static_assert(TOTAL <= 232448 && PITCH % 32 == 16, "shared memory budget");
+  static constexpr int TOTAL = OFF_RAW + kTile * LAY.bytes;
+  static_assert(TOTAL <= 232448 && LAY.bytes % 32 == 16, "shared memory budget");
   // TMEM columns: O^T, S^T and three slots of 128 channels of the A operand
   static constexpr int TM_S = 4 * NH, TM_A = TM_S + (NH < 32 ? 32 : NH);
   static_assert(TM_A + 3 * 64 <= 512, "TMEM budget");
@@ -70,7 +66,7 @@ constexpr int M_LAND = 0;      // [2]: S^T's operand is there: 384 channels, the
 constexpr int M_PV = 40;       // [4]: P.V is done with 128 channels
 constexpr int M_A = 72;        // S^T is done with the first slot
 constexpr int M_S = 88, M_P = 96, M_Q = 104, M_FIN = 112;
-constexpr int M_RAW = 120, M_READ = 128, M_LATE = 136;     // a tile's rows have come, have been read; what comes late has
+constexpr int M_RAW = 120, M_READ = 128;                    // a tile's rows have come, have been read
 constexpr int M_SEGF = 144, M_SEGE = 208;                   // [kSegs] each
 constexpr int M_TMEM = 272, M_ABORT = 276, M_PLAN = 280;    // plan: 56 bytes
 constexpr int M_FAC = 3192, M_EPI = 3200;                   // a run's factors are there; its lanes 96-127 are stored
@@ -224,10 +220,10 @@ __device__ __noinline__ void store_quarter(const Params& p, const Seg& sg, uint3
   }
 }
 
-template <int DQK, int NH, int BITS>
+template <int DQK, int NH>
 __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __grid_constant__ Params p) {
-  using L = Smem<DQK, NH, BITS>;
-  constexpr bool ROPE = L::kRope, LATE = L::LATE;
+  using L = Smem<DQK, NH>;
+  constexpr bool ROPE = L::kRope;
   constexpr int NC = NH / 4;  // columns of a softmax thread
   constexpr QuantRow LAY = L::LAY;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -243,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
   };
 
   // rows that follow one another in pages of some size come by copies of whole runs, others one by one
-  const bool runs = !LATE && p.topk_idx == nullptr && p.P >= 16;
+  const bool runs = p.topk_idx == nullptr && p.P >= 16;
   if (threadIdx.x == 0) {
     for (int k = 0; k < 2; ++k) mbar_init(mb + M_LAND + 8 * k, kWorkers);
     for (int k = 0; k < 4; ++k) mbar_init(mb + M_PV + 8 * k, 1);
@@ -253,7 +249,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
     mbar_init(mb + M_P, kWorkers);
     mbar_init(mb + M_Q, kWorkers);
     mbar_init(mb + M_RAW, runs ? 2 : 2 * 33);  // two warps' copies, and their stores
-    mbar_init(mb + M_LATE, 2 * 33);
     mbar_init(mb + M_READ, kWorkers);
     mbar_init(mb + M_FAC, 4);
     mbar_init(mb + M_EPI, 3);
@@ -451,15 +446,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
         }
       }
     };
-    auto given = [&](int bar) {
-      cp_async_arrive(mb + bar);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(mb + bar);
-    };
-    // units of 16 bytes of a staged row: a lane's first (and, of the widest rows, second), and where they come from
-    constexpr int kUnits = L::PITCH / 16;
-    const uint8_t* lane_src = p.cache + (LATE && lane == L::SCALE_AT / 16 ? LAY.scale : lane * 16);
-    const uint32_t stage = sRaw + gw * kHalf * L::PITCH;
+    constexpr int kUnits = LAY.bytes / 16;  // of a row: a lane copies one
+    static_assert(kUnits <= 32, "a row by one instruction");
+    const uint32_t stage = sRaw + gw * kHalf * LAY.bytes;
     volatile uint8_t* s_valid = misc + M_VALID + gw * kHalf;
     int armed = -1;                // the last tile that this warp's bulk copies belong to
     int stored = 0, store_at = 0;  // runs whose last quarter is stored, and the tiles before the next one
@@ -502,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
           if (row[e] >= 0 && (lane == 0 || in_page[e] == 0 || !((on[e] >> ((lane + 31) & 31)) & 1u))) {
             const unsigned stop_at = ~(on[e] >> lane);  // (its lowest set bit: the first row after this one that is masked)
             const int n = min(min(p.P - in_page[e], 32 - lane), stop_at ? __ffs(stop_at) - 1 : 32);
-            bulk_copy(stage + (e * 32 + lane) * L::PITCH, p.cache + (size_t)row[e] * LAY.bytes, n * LAY.bytes, mb + M_RAW);
+            bulk_copy(stage + (e * 32 + lane) * LAY.bytes, p.cache + (size_t)row[e] * LAY.bytes, n * LAY.bytes, mb + M_RAW);
           }
         }
         __syncwarp();
@@ -514,31 +503,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
 #pragma unroll
           for (int y = 0; y < 8; ++y) {
             const int at = __shfl_sync(0xffffffffu, x0 < 32 ? row[0] : row[1], (x0 + y) & 31);
-            src[y] = at >= 0 ? lane_src + (size_t)at * LAY.bytes : nullptr;
+            src[y] = at >= 0 ? p.cache + (size_t)at * LAY.bytes + lane * 16 : nullptr;
           }
-          const uint32_t dst = stage + x0 * L::PITCH + lane * 16;
+          const uint32_t dst = stage + x0 * LAY.bytes + lane * 16;
 #pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            if (src[y] && lane < kUnits) cp_async16(dst + y * L::PITCH, src[y], 16);
-            if (src[y] && lane + 32 < kUnits) cp_async16(dst + y * L::PITCH + 512, src[y] + 512, 16);
-          }
+          for (int y = 0; y < 8; ++y)
+            if (src[y] && lane < kUnits) cp_async16(dst + y * LAY.bytes, src[y], 16);
         }
-        given(M_RAW);
-      }
-      if constexpr (LATE) {
-        if (i > 0 && !wait(M_PV + 24, (i - 1) & 1)) { stop = true; break; }
-        const int quad = lane & 3;
-#pragma unroll
-        for (int x = 0; x < kHalf / 8; ++x) {  // rows 8 x + lane / 4 of this warp's
-          const int at = __shfl_sync(0xffffffffu, x < 4 ? row[0] : row[1], (8 * x + (lane >> 2)) & 31);
-          const uint8_t* src = p.cache + (size_t)max(at, 0) * LAY.bytes + quad * 16;
-          const uint32_t size = at >= 0 ? 16u : 0u, r = gw * kHalf + 8 * x + (lane >> 2);
-          cp_async16(sV + 6 * L::CHUNK + sw128_off(r, 2 * quad), src + 384, size);
-          cp_async16(sV + 7 * L::CHUNK + sw128_off(r, 2 * quad), src + 448, size);
-          cp_async16(sP + sw128_off(r, quad), src + LAY.tail, size);
-          cp_async16(sP + sw128_off(r, 4 + quad), src + LAY.tail + 64, size);
-        }
-        given(M_LATE);
+        cp_async_arrive(mb + M_RAW);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(mb + M_RAW);
       }
       // a run that ended before this tile (its announcement stays until it is read for the second time)
       if (ok && store_at + reinterpret_cast<const volatile int*>(misc + M_SEG)[8 * (stored % kSegs) + 1] <= i)
@@ -567,39 +541,33 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
     const int qd = warp & 3, cg = warp >> 2, half = cg & 1, quad = lane & 3;
     const int r0 = qd * 32 + (cg >> 1) * 16 + (lane >> 2);
     const uint32_t to0 = sV + half * L::CHUNK + sw128_off(r0, 2 * quad), to1 = sV + half * L::CHUNK + sw128_off(r0, 2 * quad + 1);
-    const uint32_t raw0 = sRaw + r0 * L::PITCH;
+    const uint32_t raw0 = sRaw + r0 * LAY.bytes;
     const uint32_t tm_a = tmem_addr(tmem, qd * 32 + (cg >> 1) * 16, 0);
     // softmax: position `row` of the tile, columns n0 .. n0 + NC - 1, together with the two other warps of the column group
     const int n0 = cg * NC, row = qd * 32 + lane, bar_id = 1 + cg;
     auto scale_of = [&](int r) {  // (a row that was never written, of zero bytes, holds zeros; -1: masked)
-      const float s = lds4(sRaw + r * L::PITCH + L::SCALE_AT);
+      const float s = lds4(sRaw + r * LAY.bytes + LAY.scale);
       return !lds1(mb + M_VALID + r) ? -1.f : s < kLeast ? kLeast : s;
     };
     // Tile i from its rows to TMEM and shared memory, and s of this thread's position; false when a wait ran out.
     auto convert = [&](int i, float& s_mine) -> bool {
       if (!wait(M_RAW, i & 1)) return false;
       // all that has come, to registers: the copies of the next tile take its place
-      constexpr int kNow = LATE ? 3 : 4;
-      uint32_t code[4][2][BITS / 2], blk[4][2];
+      uint32_t code[4][2][2], blk[4][2];
       uint4 rope[2];
       float sc[2];
       s_mine = scale_of(row);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const uint32_t at = raw0 + k * 8 * L::PITCH;
+        const uint32_t at = raw0 + k * 8 * LAY.bytes;
         sc[k] = scale_of(r0 + 8 * k);
         const bool on = !(sc[k] < 0.f);  // (what lies in a masked row's place may be anything)
-        if (ROPE && !LATE) rope[k] = on ? lds16(at + LAY.tail + half * 64 + quad * 16) : make_uint4(0, 0, 0, 0);
+        if (ROPE) rope[k] = on ? lds16(at + LAY.tail + half * 64 + quad * 16) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int m = 0; m < kNow; ++m) {
-          if constexpr (BITS == 4) {
-            const uint2 v = on ? lds8(at + m * 64 + half * 32 + quad * 8) : make_uint2(0, 0);
-            code[m][k][0] = v.x; code[m][k][1] = v.y;
-            blk[m][k] = on ? lds1(at + LAY.blocks + m * 8 + half * 4 + quad) : 0u;
-          } else {
-            const uint4 v = on ? lds16(at + m * 128 + half * 64 + quad * 16) : make_uint4(0, 0, 0, 0);
-            code[m][k][0] = v.x; code[m][k][1] = v.y; code[m][k][2] = v.z; code[m][k][3] = v.w;
-          }
+        for (int m = 0; m < 4; ++m) {
+          const uint2 v = on ? lds8(at + m * 64 + half * 32 + quad * 8) : make_uint2(0, 0);
+          code[m][k][0] = v.x; code[m][k][1] = v.y;
+          blk[m][k] = on ? lds1(at + LAY.blocks + m * 8 + half * 4 + quad) : 0u;
         }
       }
       __syncwarp();
@@ -609,23 +577,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
       auto to_fp16 = [&](int m, uint32_t (&v)[16]) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          uint32_t h[8];
-          if constexpr (BITS == 4) {
-            const uint32_t by = e4m3x2_f16x2((uint16_t)(blk[m][k] * 0x101u));
-            uint32_t lo[4], hi[4];
-            e2m1x8_f16x2(code[m][k][0], lo);
-            e2m1x8_f16x2(code[m][k][1], hi);
+          uint32_t h[8], lo[4], hi[4];
+          const uint32_t by = e4m3x2_f16x2((uint16_t)(blk[m][k] * 0x101u));
+          e2m1x8_f16x2(code[m][k][0], lo);
+          e2m1x8_f16x2(code[m][k][1], hi);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              h[j] = mul_f16x2(lo[j], by);
-              h[4 + j] = mul_f16x2(hi[j], by);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              h[2 * j] = e4m3x2_f16x2((uint16_t)code[m][k][j]);
-              h[2 * j + 1] = e4m3x2_f16x2((uint16_t)(code[m][k][j] >> 16));
-            }
+          for (int j = 0; j < 4; ++j) {
+            h[j] = mul_f16x2(lo[j], by);
+            h[4 + j] = mul_f16x2(hi[j], by);
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[(j >> 1) * 4 + 2 * k + (j & 1)] = h[j];
@@ -661,22 +620,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
         if (i > 0 && !wait(M_PV + 8 * m, (i - 1) & 1)) return false;
         to_shared(m, v[m]);
       }
-      if (LATE) {
-        if (!wait(M_LATE, i & 1)) return false;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          rope[k] = lds16(sP + sw128_off(r0 + 8 * k, 4 * half + quad));
-          const uint4 x = lds16(to0 + 6 * L::CHUNK + k * 1024);
-          code[3][k][0] = x.x; code[3][k][1] = x.y; code[3][k][BITS / 2 - 2] = x.z; code[3][k][BITS / 2 - 1] = x.w;
-          if (sc[k] < 0.f) rope[k] = make_uint4(0, 0, 0, 0);
-        }
-        __syncwarp();
-      }
       to_fp16(3, v[0]);
       if (!wait(M_A, i & 1)) return false;
       tc_fence_after();
       to_tmem(3, v[0]);
-      if (!LATE && i > 0 && !wait(M_PV + 24, (i - 1) & 1)) return false;
+      if (i > 0 && !wait(M_PV + 24, (i - 1) & 1)) return false;
       if constexpr (ROPE) {  // P.V has read all of W: the position channels take its place
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -950,16 +898,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
 
 constexpr size_t kRecordOff = kErrorWordBytes, kStatOff = kRecordOff + kRecordBytes, kPartialOff = kStatOff + kStatBytes;
 
-template <int DQK, int NH, int BITS = 4>
+template <int DQK, int NH>
 dsa_status_t launch(Params& p, int ctas, cudaStream_t s) {
-  using L = Smem<DQK, NH, BITS>;
-  dsa_status_t st = configure_kernel_smem(reinterpret_cast<const void*>(paged_mla_quant_kernel<DQK, NH, BITS>), L::TOTAL,
+  using L = Smem<DQK, NH>;
+  dsa_status_t st = configure_kernel_smem(reinterpret_cast<const void*>(paged_mla_quant_kernel<DQK, NH>), L::TOTAL,
                                           "configuring paged_mla_quant_kernel");
   if (st != DSA_OK) return st;
   p.G = p.topk_idx ? 1 : (p.H <= NH ? NH / p.H : 1);
   p.extra = 2;
   p.HB = (p.H + NH - 1) / NH;
-  paged_mla_quant_kernel<DQK, NH, BITS><<<ctas, kThreads, L::TOTAL, s>>>(p);
+  paged_mla_quant_kernel<DQK, NH><<<ctas, kThreads, L::TOTAL, s>>>(p);
   return cuda_check(cudaGetLastError(), "launching paged_mla_quant_kernel");
 }
 }  // namespace pmlaq
