@@ -415,9 +415,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
         k.limit = limit;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int j = (sg.t0 + i - base) * kTile + gw * kHalf + e * 32 + lane;
-          if (j < sg.keys && (e == 0 || lane < kHalf - 32))
-            k.pos[e] = p.topk_idx ? __ldg(p.topk_idx + (size_t)(sg.row0 / p.H) * p.K + j) : j;
+          const unsigned j = (unsigned)(sg.t0 + i - base) * kTile + gw * kHalf + e * 32 + lane;  // (may pass 2^31)
+          if (j < (unsigned)sg.keys && (e == 0 || lane < kHalf - 32))
+            k.pos[e] = p.topk_idx ? __ldg(p.topk_idx + (size_t)(sg.row0 / p.H) * p.K + j) : (int)j;
         }
       }
       return k;
@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
         const bool plain = s > 0.f;  // neither masked nor NaN
         const int ls = plain ? (int)(__float_as_uint(s) >> 23) - 127 : 0;
         const float log_s = (float)ls, inv_s = pow2(-ls);
-        const int pos = t * kTile + row;
+        const int pos = (int)((unsigned)t * kTile + row);  // (past 2^31: masked by its s)
         const bool partly = p.topk_idx == nullptr && (t + 1) * (long long)kTile > sg.seen0;  // some token may not see all of it
         // scores in log2 units, with s
         float2 z[NC / 2];
@@ -885,6 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
       if (!more) break;
       sg = nx;
     }
+    tmem_st_wait();  // (a wait that ran out may have left one under way)
   }
 
   tc_fence_before();

@@ -97,6 +97,7 @@ def attention(q, cache, bits, table, seq_lens, cu_q, scale, sink=None, topk=None
             if rows:
                 size[n] = (q[n].double().abs() @ kv.abs().T).max(1).values * scale
                 s = flat[rows][:, at_s:at_s + 4].contiguous().view(torch.float32).double()[:, 0]
+                s = torch.where(s < 2.0 ** -48, 2.0 ** -48, s)  # (a row that was never written)
                 top[n] = (p * s).max(1, keepdim=True).values * (kv[:, :512].abs() / s[:, None]).sum(0)
                 most[n] = q[n, :, :512].double().abs().max(1).values * float(kv[:, :512].abs().sum(1).max()) * scale
     return out, lse, size, mass, top, most

@@ -1,6 +1,7 @@
 """CPU checks of the calls over a quantised cache: what the library and the binding refuse before anything is launched,
 and the tests' own form of a row."""
 import ctypes
+import inspect
 
 import pytest
 import torch
@@ -140,3 +141,11 @@ def test_the_reference_rows(bits):
     else:  # half a step is amax / 6 of a block at most, a block's scale is off by 1/16 of itself
         top = v.reshape(-1, 4, 16).abs().amax(2).repeat_interleave(16, 1)
         assert bool(((w - v).abs() <= top / 6 * 17 / 16).all())
+
+
+@pytest.mark.parametrize("name", ["dsa_paged_quantize", "dsa_paged_dequantize", "dsa_paged_mla_quant"])
+def test_a_call_with_a_workspace_says_how_its_errors_are_read(name):
+    call = getattr(dsa, name)
+    doc = " ".join(call.__doc__.split())
+    assert inspect.signature(call).parameters["workspace"].default is None
+    assert all(w in doc for w in ("dsa_read_device_status", "paged_workspace_size", "zeroed once", "dropped"))
