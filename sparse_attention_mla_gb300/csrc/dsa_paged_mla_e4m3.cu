@@ -426,22 +426,33 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
     const int r = qd * 16 + (lane >> 2) + 8 * (lane & 1);  // key row of the tile
     const int bar_id = 1 + ch;
     const int n0 = ch * NHH + par * NQ;  // this thread's rows n0 .. n0 + NQ - 1 of the group
-    // The run's queries: a row a warp, as hi and lo, and what the sums of a column are to be multiplied by.
+    // The run's queries: a row a warp, as hi and lo, and what the sums of a column are to be multiplied by.  A warp asks for
+    // all its rows at once (one or two at a time, each with the time of a read from DRAM: 16000 cycles in place of 4000) and
+    // has them come to where their hi and lo will lie, which are as large together; each is then read before it is written.
     auto load_q = [&](const Seg& s, int run) {
+      auto raw_at = [&](int hh, int u) { return sQ + (u >> 4) * L::Q_CHUNK + sw128_off((u >> 3 & 1) * NH + hh, u & 7); };
+#pragma unroll 1
+      for (int hh = wk; hh < NH; hh += kWorkers / 32) {
+        const __nv_bfloat16* src = p.q + (size_t)(hh < s.rows ? s.row0 + hh : s.row0) * DQK + lane * 8;
+        const uint32_t size = hh < s.rows ? 16 : 0;
+        cp_async16(raw_at(hh, lane), src, size);
+        cp_async16(raw_at(hh, lane + 32), src + 256, size);
+        if (ROPE && lane < 8) cp_async16(sQ + 4 * L::Q_CHUNK + sw128_off(hh, lane), src + 512, size);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
 #pragma unroll 2
       for (int hh = wk; hh < NH; hh += kWorkers / 32) {
-        constexpr int UNITS = DQK / 8;
-        uint4 v[3];
+        uint4 v[2];
         uint32_t top = 0;
 #pragma unroll
-        for (int x = 0; x < 3; ++x) {
-          const int u = lane + 32 * x;
-          v[x] = make_uint4(0, 0, 0, 0);
-          if (hh < s.rows && u < UNITS) v[x] = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)(s.row0 + hh) * DQK) + u);
-          if (x < 2)
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[x].x & 0x7fff7fffu, v[x].y & 0x7fff7fffu),
-                                         __vmaxu2(v[x].z & 0x7fff7fffu, v[x].w & 0x7fff7fffu)));
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t at = raw_at(hh, lane + 32 * x);
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[x].x), "=r"(v[x].y), "=r"(v[x].z), "=r"(v[x].w) : "r"(at) : "memory");
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[x].x & 0x7fff7fffu, v[x].y & 0x7fff7fffu),
+                                       __vmaxu2(v[x].z & 0x7fff7fffu, v[x].w & 0x7fff7fffu)));
         }
+        __syncwarp();
         const uint32_t most = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
         const int e = max((int)(most >> 7) - 127, -119);
         const float by = pow2(7 - e);
@@ -462,7 +473,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
           asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + sw128_off(hh, (u & 15) >> 1)), "r"(hi[0] | hi[1] << 16), "r"(hi[2] | hi[3] << 16) : "memory");
           asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + sw128_off(NH + hh, (u & 15) >> 1)), "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16) : "memory");
         }
-        if (ROPE && lane < 8) st_shared_v4(sQ + 4 * L::Q_CHUNK + sw128_off(hh, lane), v[2].x, v[2].y, v[2].z, v[2].w);
       }
       fence_proxy_async_smem();
       __syncwarp();

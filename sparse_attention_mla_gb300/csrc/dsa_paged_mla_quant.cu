@@ -639,21 +639,33 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
       to_shared(3, v[0]);
       return true;
     };
-    // The run's queries: a row a warp, divided by a power of two, its channels in the order in which they lie in TMEM.
+    // The run's queries: a row a warp, divided by a power of two, its channels in the order in which they lie in TMEM.  A warp
+    // asks for all its rows at once and has them come to where they will lie; each is then read before it is written.
     auto load_q = [&](const Seg& s, int run) {
+      constexpr int UNITS = DQK / 8;
+      auto raw_at = [&](int hh, int u) { return sQ + (u >> 3) * L::Q_CHUNK + sw128_off(hh, u & 7); };
 #pragma unroll 1
       for (int hh = cg * 3 + qd; hh < NH; hh += kWorkers) {
-        constexpr int UNITS = DQK / 8;
+        const __nv_bfloat16* src = p.q + (size_t)(hh < s.rows ? s.row0 + hh : s.row0) * DQK + lane * 8;
+        const uint32_t size = hh < s.rows ? 16 : 0;
+        cp_async16(raw_at(hh, lane), src, size);
+        cp_async16(raw_at(hh, lane + 32), src + 256, size);
+        if (ROPE && lane < UNITS - 64) cp_async16(raw_at(hh, lane + 64), src + 512, size);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+#pragma unroll 1
+      for (int hh = cg * 3 + qd; hh < NH; hh += kWorkers) {
         uint4 v[3];
         uint32_t top = 0;
 #pragma unroll
         for (int x = 0; x < 3; ++x) {
           const int u = lane + 32 * x;
-          v[x] = make_uint4(0, 0, 0, 0);
-          if (hh < s.rows && u < UNITS) v[x] = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)(s.row0 + hh) * DQK) + u);
+          v[x] = u < UNITS ? lds16(raw_at(hh, u)) : make_uint4(0, 0, 0, 0);
           top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[x].x & 0x7fff7fffu, v[x].y & 0x7fff7fffu),
                                        __vmaxu2(v[x].z & 0x7fff7fffu, v[x].w & 0x7fff7fffu)));
         }
+        __syncwarp();
         const uint32_t most = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
         const int e = max((int)(most >> 7) - 127, -112);
         const float by = pow2(14 - e);
