@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
-#pragma unroll 2
+#pragma unroll 1
       for (int hh = wk; hh < NH; hh += kWorkers / 32) {
         uint4 v[2];
         uint32_t top = 0;
