@@ -62,9 +62,8 @@ struct Smem {
 };
 
 // misc (bytes)
-constexpr int M_LAND = 0;      // [2]: S^T's operand is there: 384 channels, the others
-constexpr int M_PV = 40;       // [4]: P.V is done with 128 channels
-constexpr int M_A = 72;        // S^T is done with the first slot
+constexpr int M_LAND = 0;      // [2]: S^T's operand is there: 384 channels in TMEM, the others in shared memory
+constexpr int M_PV = 40;       // P.V is done
 constexpr int M_S = 88, M_P = 96, M_Q = 104, M_FIN = 112;
 constexpr int M_RAW = 120, M_READ = 128;                    // a tile's rows have come, have been read
 constexpr int M_SEGF = 144, M_SEGE = 208;                   // [kSegs] each
@@ -201,7 +200,7 @@ __device__ __noinline__ void store_quarter(const Params& p, const Seg& sg, uint3
     uint32_t ov[NC];
     tmem_ld<NC>(tmem_addr(tmem, qd * 32, m * NH + n0), ov);
     tmem_ld_wait();
-    const int c = m * 128 + qd * 32 + lane, rows = sg.rows - n0;
+    const int c = (qd * 32 + lane) / 16 * 64 + m * 16 + lane % 16, rows = sg.rows - n0;
     // (one branch for all rows: with one for each, every store waits for the one before)
     if (sg.whole) {
       __nv_bfloat16* dst = p.out + (size_t)(sg.row0 + n0) * kDv + c;
@@ -242,8 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
   const bool runs = p.topk_idx == nullptr && p.P >= 16;
   if (threadIdx.x == 0) {
     for (int k = 0; k < 2; ++k) mbar_init(mb + M_LAND + 8 * k, kWorkers);
-    for (int k = 0; k < 4; ++k) mbar_init(mb + M_PV + 8 * k, 1);
-    mbar_init(mb + M_A, 1);
+    mbar_init(mb + M_PV, 1);
     mbar_init(mb + M_FIN, 1);
     mbar_init(mb + M_S, 1);
     mbar_init(mb + M_P, kWorkers);
@@ -279,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
     Seg sg;
     if (!warp_all(read_seg(k, sg))) return false;
     i += sg.n;
-    if (!(wait(M_FAC, k & 1) && wait(M_PV + 24, (i - 1) & 1))) return false;
+    if (!(wait(M_FAC, k & 1) && wait(M_PV, (i - 1) & 1))) return false;
     tc_fence_after();
     store_quarter<NH>(p, sg, tmem, 3, (warp >> 2) * NC, s_out + (k & 1) * 64);
     tc_fence_before();
@@ -306,19 +304,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
 #pragma unroll 1
       for (int k0 = 0; k0 < n; ++k0, ++i) {
         const uint64_t b0 = sdesc_sw128(q0, 16, 1024);
+        if (!wait(M_LAND, i & 1)) { stop = true; break; }
+        tc_fence_after();
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          if (m == 0 || m == 3) {
-            if (!wait(M_LAND + (m ? 8 : 0), i & 1)) { stop = true; break; }
-            tc_fence_after();
-          }
-          const uint32_t a = t0 + L::TM_A + (m % 3) * 64;
+        for (int m = 0; m < 3; ++m) {
+          const uint32_t a = t0 + L::TM_A + m * 64;
           mma4_ts_w<2>(t0 + L::TM_S, a, b0 + (2 * m * L::Q_CHUNK >> 4), kIdS, m > 0);
           mma4_ts_w<2>(t0 + L::TM_S, a + 32, b0 + ((2 * m + 1) * L::Q_CHUNK >> 4), kIdS, 1);
-          if (m == 0) mma_commit_w(mb + M_A);
         }
-        if (!stop && ROPE) mma4_w<2, 2>(t0 + L::TM_S, sdesc_sw128(w0, 16, 1024), b0 + (8 * L::Q_CHUNK >> 4), kIdR, 1);
-        if (stop) break;
+        // the other channels from where P.V will read them (of its 128 rows those past 96 are anything: no one looks at them)
+        if (!wait(M_LAND + 8, i & 1)) { stop = true; break; }
+        tc_fence_after();
+        const uint64_t a0 = sdesc_sw128(v0, 16, 1024);
+        mma4_w<2, 2>(t0 + L::TM_S, a0 + (6 * L::CHUNK >> 4), b0 + (6 * L::Q_CHUNK >> 4), kIdS, 1);
+        mma4_w<2, 2>(t0 + L::TM_S, a0 + (7 * L::CHUNK >> 4), b0 + (7 * L::Q_CHUNK >> 4), kIdS, 1);
+        if (ROPE) mma4_w<2, 2>(t0 + L::TM_S, sdesc_sw128(w0, 16, 1024), b0 + (8 * L::Q_CHUNK >> 4), kIdR, 1);
         mma_commit_w(mb + M_S);
         if (!wait(M_P, i & 1)) { stop = true; break; }
         tc_fence_after();
@@ -358,12 +358,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
             mma4_w<128, 2>(t0 + m * NH, a, wb, kIdV, k0 > 0);
             mma2_w<128, 2>(t0 + m * NH, a + 512, wb + (NH * 128 >> 4), kIdV);
           }
-          mma_commit_w(mb + M_PV + 8 * m);
         }
+        mma_commit_w(mb + M_PV);
       }
       if (stop) break;
       // (as last_quarter, of the first column group)
-      if (!(wait(M_FAC, seg & 1) && wait(M_PV + 24, (i - 1) & 1))) break;
+      if (!(wait(M_FAC, seg & 1) && wait(M_PV, (i - 1) & 1))) break;
       tc_fence_after();
       store_quarter<NH>(p, sg, tmem, 3, 0, s_out + (seg & 1) * 64);
       tc_fence_before();
@@ -553,21 +553,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
     auto convert = [&](int i, float& s_mine) -> bool {
       if (!wait(M_RAW, i & 1)) return false;
       // all that has come, to registers: the copies of the next tile take its place
-      uint32_t code[4][2][2], blk[4][2];
-      uint4 rope[2];
+      uint4 code[2][2], rope[2];
+      uint32_t blk[2];
       float sc[2];
       s_mine = scale_of(row);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint32_t at = raw0 + k * 8 * LAY.bytes;
+        code[k][0] = lds16(at + (half * 4 + quad) * 32);
+        code[k][1] = lds16(at + (half * 4 + quad) * 32 + 16);
+        blk[k] = lds32(at + LAY.blocks + (half * 4 + quad) * 4);
+        if (ROPE) rope[k] = lds16(at + LAY.tail + half * 64 + quad * 16);
         sc[k] = scale_of(r0 + 8 * k);
-        const bool on = !(sc[k] < 0.f);  // (what lies in a masked row's place may be anything)
-        if (ROPE) rope[k] = on ? lds16(at + LAY.tail + half * 64 + quad * 16) : make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const uint2 v = on ? lds8(at + m * 64 + half * 32 + quad * 8) : make_uint2(0, 0);
-          code[m][k][0] = v.x; code[m][k][1] = v.y;
-          blk[m][k] = on ? lds1(at + LAY.blocks + m * 8 + half * 4 + quad) : 0u;
+      for (int k = 0; k < 2; ++k) {
+        if (sc[k] < 0.f) {  // (what lies in a masked row's place may be anything; codes are numbers, and zeros times a zero)
+          blk[k] = 0;
+          rope[k] = make_uint4(0, 0, 0, 0);
         }
       }
       __syncwarp();
@@ -578,9 +581,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t h[8], lo[4], hi[4];
-          const uint32_t by = e4m3x2_f16x2((uint16_t)(blk[m][k] * 0x101u));
-          e2m1x8_f16x2(code[m][k][0], lo);
-          e2m1x8_f16x2(code[m][k][1], hi);
+          const uint32_t by = e4m3x2_f16x2((uint16_t)(((blk[k] >> (8 * m)) & 255u) * 0x101u));
+          const uint4 c = code[k][m >> 1];
+          e2m1x8_f16x2(m & 1 ? c.z : c.x, lo);
+          e2m1x8_f16x2(m & 1 ? c.w : c.y, hi);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             h[j] = mul_f16x2(lo[j], by);
@@ -590,13 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
           for (int j = 0; j < 8; ++j) v[(j >> 1) * 4 + 2 * k + (j & 1)] = h[j];
         }
       };
-      auto to_tmem = [&](int m, const uint32_t (&v)[16]) { tmem_st16x256b(tm_a + L::TM_A + (m % 3) * 64 + half * 32, v); };
-      auto in_tmem = [&](int bar) {
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(mb + bar);
-      };
+      auto to_tmem = [&](int m, const uint32_t (&v)[16]) { tmem_st16x256b(tm_a + L::TM_A + m * 64 + half * 32, v); };
       // (seen by the tensor core with the weights, which every thread stores after this)
       auto to_shared = [&](int m, const uint32_t (&v)[16]) {
 #pragma unroll
@@ -613,18 +611,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
         to_fp16(m, v[m]);
         to_tmem(m, v[m]);
       }
-      in_tmem(M_LAND);
-      // P.V's, as it leaves the places
-#pragma unroll
-      for (int m = 0; m < 3; ++m) {
-        if (i > 0 && !wait(M_PV + 8 * m, (i - 1) & 1)) return false;
-        to_shared(m, v[m]);
-      }
-      to_fp16(3, v[0]);
-      if (!wait(M_A, i & 1)) return false;
-      tc_fence_after();
-      to_tmem(3, v[0]);
-      if (i > 0 && !wait(M_PV + 24, (i - 1) & 1)) return false;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(mb + M_LAND);
+      // the rest of it; the other channels, which only P.V reads from there, while S^T is under way
+      if (i > 0 && !wait(M_PV, (i - 1) & 1)) return false;
+      uint32_t rest[16];
+      to_fp16(3, rest);
+      to_shared(3, rest);
       if constexpr (ROPE) {  // P.V has read all of W: the position channels take its place
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -633,10 +628,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
           st_shared_v4(sP + sw128_off(r0 + 8 * k, 4 * half + quad), mul_bf16x2(rope[k].x, by), mul_bf16x2(rope[k].y, by),
                        mul_bf16x2(rope[k].z, by), mul_bf16x2(rope[k].w, by));
         }
-        fence_proxy_async_smem();
       }
-      in_tmem(M_LAND + 8);
-      to_shared(3, v[0]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(mb + M_LAND + 8);
+#pragma unroll
+      for (int m = 0; m < 3; ++m) to_shared(m, v[m]);
       return true;
     };
     // The run's queries: a row a warp, divided by a power of two, its channels in the order in which they lie in TMEM.  A warp
@@ -678,19 +675,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
 #pragma unroll
           for (int g = 0; g < 2; ++g) {  // four channels, and their place among the 64
             uint32_t a, b;
-            int at;
+            int at, chunk = 8;
             if (u < 64) {
               a = pack_f16x2(__uint_as_float(w[2 * g] << 16) * by, __uint_as_float(w[2 * g] & 0xffff0000u) * by);
               b = pack_f16x2(__uint_as_float(w[2 * g + 1] << 16) * by, __uint_as_float(w[2 * g + 1] & 0xffff0000u) * by);
-              const int c4 = 2 * (u & 7) + g;
-              at = (c4 & 3) * 4 + (c4 >> 2);
+              const int c4 = (u >> 3 & 3) * 4 + 2 * (u & 1) + g;
+              chunk = (u >> 1 & 3) * 2 + (u >> 5);
+              at = chunk < 6 ? (c4 & 3) * 4 + (c4 >> 2) : c4;
             } else {
               const uint32_t by2 = pack_bf16x2(by, by);
               a = mul_bf16x2(w[2 * g], by2);
               b = mul_bf16x2(w[2 * g + 1], by2);
               at = 2 * (u - 64) + g;  // (these are read from shared memory, as they lie)
             }
-            const uint32_t dst = sQ + (u >> 3) * L::Q_CHUNK + sw128_off(hh, at >> 1) + (at & 1) * 8;
+            const uint32_t dst = sQ + chunk * L::Q_CHUNK + sw128_off(hh, at >> 1) + (at & 1) * 8;
             asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(a), "r"(b) : "memory");
           }
         }
@@ -887,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
         if (lane == 0) mbar_arrive(mb + M_FAC);
       }
       named_bar(bar_id, kTeam);
-      const bool got = wait(M_PV + 24, (i - 1) & 1);
+      const bool got = wait(M_PV, (i - 1) & 1);
       aborted = named_bar_or(bar_id, kTeam, !got || bad);
       if (aborted) break;
       tc_fence_after();
