@@ -549,14 +549,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
       const float s = lds4(sRaw + r * LAY.bytes + LAY.scale);
       return !lds1(mb + M_VALID + r) ? -1.f : s < kLeast ? kLeast : s;
     };
-    // Tile i from its rows to TMEM and shared memory, and s of this thread's position; false when a wait ran out.
-    auto convert = [&](int i, float& s_mine) -> bool {
+    // Tile i's rows to registers (the copies of the next tile take their place), and s of this thread's position; false when
+    // a wait ran out.  Done while S^T of the tile before is under way.
+    uint4 code[2][2], rope[2];
+    uint32_t blk[2];
+    float sc[2], s_row;
+    auto read = [&](int i) -> bool {
       if (!wait(M_RAW, i & 1)) return false;
-      // all that has come, to registers: the copies of the next tile take its place
-      uint4 code[2][2], rope[2];
-      uint32_t blk[2];
-      float sc[2];
-      s_mine = scale_of(row);
+      s_row = scale_of(row);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint32_t at = raw0 + k * 8 * LAY.bytes;
@@ -575,6 +575,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(mb + M_READ);
+      return true;
+    };
+    // ... and to TMEM and shared memory.
+    auto convert = [&](int i) -> bool {
       tc_fence_after();  // (TMEM: S^T of the tile before is done)
       // 128 channels' codes as fp16, the halves of a row's four channels side by side as TMEM takes them
       auto to_fp16 = [&](int m, uint32_t (&v)[16]) {
@@ -738,59 +742,60 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
       const int t_end = sg.t0 + sg.n;
 #pragma unroll 1
       for (int t = sg.t0; t < t_end; ++t, ++i) {
-        float s = -1.f;
-        bad = bad || !convert(i, s);
+        bad = bad || !read(i);
+        bad = bad || !convert(i);
+        // the weights without s are 2^(S f - m), m the running maximum of those with it
+        if (t == sg.t0) bad = bad || !wait(M_Q, seg & 1);  // (orders the columns' factors before their reads)
+        const float s = bad ? -1.f : s_row;
+        const float log_s = s > 0.f ? (float)((int)(__float_as_uint(s) >> 23) - 127) : 0.f;  // (masked, or NaN: 0)
+        float2 f[NC / 2];
+#pragma unroll
+        for (int j = 0; j < NC / 4; ++j) {
+          const float4 c = *reinterpret_cast<const float4*>(col + 4 * j);
+          f[2 * j] = mul2(make_float2(c.x, c.y), make_float2(s, s));
+          f[2 * j + 1] = mul2(make_float2(c.z, c.w), make_float2(s, s));
+        }
         bad = bad || !wait(M_S, i & 1);
-        // (complete since before S^T was issued: orders the columns' factors before their reads below)
-        if (t == sg.t0) bad = bad || !wait(M_Q, seg & 1);
         tc_fence_after();
         __syncwarp();
-        const bool plain = s > 0.f;  // neither masked nor NaN
-        const int ls = plain ? (int)(__float_as_uint(s) >> 23) - 127 : 0;
-        const float log_s = (float)ls, inv_s = pow2(-ls);
         const int pos = (int)((unsigned)t * kTile + row);  // (past 2^31: masked by its s)
         const bool partly = p.topk_idx == nullptr && (t + 1) * (long long)kTile > sg.seen0;  // some token may not see all of it
-        // scores in log2 units, with s
-        float2 z[NC / 2];
-        {
+        float2 e[NC / 2];
+        auto exponents = [&](auto&& add) {
           uint32_t zr[NC];
           tmem_ld<NC>(tmem_addr(tmem, qd * 32, L::TM_S + n0), zr);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < NC / 4; ++j) {
-            const float4 c = *reinterpret_cast<const float4*>(col + 4 * j);
-            const float2 f0 = mul2(make_float2(c.x, c.y), make_float2(s, s)), f1 = mul2(make_float2(c.z, c.w), make_float2(s, s));
-            z[2 * j] = fma2(make_float2(__uint_as_float(zr[4 * j]), __uint_as_float(zr[4 * j + 1])), f0, make_float2(log_s, log_s));
-            z[2 * j + 1] = fma2(make_float2(__uint_as_float(zr[4 * j + 2]), __uint_as_float(zr[4 * j + 3])), f1, make_float2(log_s, log_s));
+          for (int j = 0; j < NC / 2; ++j)
+            e[j] = fma2(make_float2(__uint_as_float(zr[2 * j]), __uint_as_float(zr[2 * j + 1])), f[j], add(j));
+          if (s < 0.f) {
+#pragma unroll
+            for (int j = 0; j < NC / 2; ++j) e[j] = make_float2(-INFINITY, -INFINITY);
+          } else if (partly) {
+            const int tok0 = (sg.head0 + n0) / p.H;
+            int seen = sg.seen0 + tok0, left = p.H - ((sg.head0 + n0) - tok0 * p.H);
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {
+              if (pos >= seen) (j & 1 ? e[j / 2].y : e[j / 2].x) = -INFINITY;
+              if (--left == 0) { left = p.H; ++seen; }
+            }
           }
-        }
-        if (s < 0.f) {
+        };
+        exponents([&](int j) { return neg[j]; });
+        float most = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < NC / 2; ++j) z[j] = make_float2(-INFINITY, -INFINITY);
-        } else if (partly) {
-          const int tok0 = (sg.head0 + n0) / p.H;
-          int seen = sg.seen0 + tok0, left = p.H - ((sg.head0 + n0) - tok0 * p.H);
-#pragma unroll
-          for (int j = 0; j < NC; ++j) {
-            if (pos >= seen) (j & 1 ? z[j / 2].y : z[j / 2].x) = -INFINITY;
-            if (--left == 0) { left = p.H; ++seen; }
-          }
-        }
-        bool mine = t == sg.t0;
-#pragma unroll
-        for (int j = 0; j < NC / 2; ++j) {
-          const float2 e = add2(z[j], neg[j]);
-          mine |= fmaxf(e.x, e.y) > kRaise;
-        }
+        for (int j = 0; j < NC / 2; ++j) most = fmaxf(most, fmaxf(e[j].x, e[j].y));
+        const bool mine = t == sg.t0 || most > kRaise - log_s;
         bool raise = false;
         if (named_bar_or(bar_id, kTeam, mine || bad)) {
           if (named_bar_or(bar_id, kTeam, bad)) { aborted = true; break; }
           raise = true;
         }
         if (raise) {
+          exponents([&](int) { return make_float2(log_s, log_s); });
           float top[NC];
 #pragma unroll
-          for (int j = 0; j < NC / 2; ++j) { top[2 * j] = z[j].x; top[2 * j + 1] = z[j].y; }
+          for (int j = 0; j < NC / 2; ++j) { top[2 * j] = e[j].x; top[2 * j + 1] = e[j].y; }
           s_red[qd * 64 + own_col] = over_lanes(top, true);
           named_bar(bar_id, kTeam);
           if (qd == 0 && lane < NC) {
@@ -806,6 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
           for (int j = 0; j < NC / 2; ++j) {
             l_part[j] = mul2(l_part[j], *reinterpret_cast<const float2*>(s_fac + n0 + 2 * j));
             neg[j] = *reinterpret_cast<const float2*>(s_neg + n0 + 2 * j);
+            e[j] = add2(e[j], add2(neg[j], make_float2(-log_s, -log_s)));
           }
           if (t > sg.t0) {  // (P.V of the tile before has been waited for)
 #pragma unroll 1
@@ -823,13 +829,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
           named_bar(bar_id, kTeam);  // the factors have been read
         }
         if (qd == 0 && lane == 0) s_flag[(i & 1) * 4 + cg] = raise;
+        const float times = s > 0.f ? s : 1.f;  // (a NaN is in x where the row is seen, and only there)
         uint32_t w[NC / 2];
 #pragma unroll
         for (int j = 0; j < NC / 2; ++j) {
-          const float2 e = add2(z[j], neg[j]);
-          const float2 x = make_float2(ex2(e.x), ex2(e.y));
-          l_part[j] = fma2(x, make_float2(inv_s, inv_s), l_part[j]);
-          w[j] = pack_f16x2(x.x, x.y);
+          const float2 x = make_float2(ex2(e[j].x), ex2(e[j].y));
+          l_part[j] = add2(l_part[j], x);
+          const float2 ws = mul2(x, make_float2(times, times));
+          w[j] = pack_f16x2(ws.x, ws.y);
         }
         if constexpr (NH == 64) {
           st_shared_v4(sP + sw128_off(row, 2 * cg), w[0], w[1], w[2], w[3]);
