@@ -40,6 +40,7 @@ constexpr int kThreads = 32 + kWorkers + kGather + 64;
 constexpr int kReaders = 2 + kWorkers / 32 + kGather / 32;  // warps that read an announcement
 constexpr float kRaise = 11.0f;  // log2 units: the running maximum is raised when a weight passes 2^11
 constexpr float kTop = 5.0f;     // a new maximum is 2^5
+constexpr float kMost = 2048.0f;
 constexpr float kLeast = 3.5527136788005009e-15f;  // 2^-48, the least s
 
 template <int DQK, int NH>
@@ -50,17 +51,20 @@ struct Smem {
   static constexpr int CHUNK = kTile * 128;
   static constexpr int Q_CHUNK = 2 * NH * 128;  // hi rows, lo rows
   static constexpr int R = NH == 64 ? 3 : 4;    // tiles in the ring
-  static constexpr int NS = NH == 64 ? 1 : 2;   // S^T buffers in TMEM
-  static constexpr int SW = (ROPE ? 3 : 2) * NH;
-  static constexpr int P_BLOCK = NH == 64 ? kTile * 128 : 2 * NH * 128;
+  // 64 rows: S[row, key], hi and lo rows as M = 128 (of each warp's 32 lanes the first 16 hi, the others lo);
+  // 16 rows: S^T[key, row], M = 64 keys, hi and lo side by side.
+  static constexpr bool ROWS = NH == 64;
+  static constexpr int SW = ROWS ? (ROPE ? 2 : 1) * kTile : (ROPE ? 3 : 2) * NH;  // TMEM columns of S
+  static constexpr int P_BLOCK = NH * 128 * (ROWS ? 1 : 2);
+  static constexpr int QR_CHUNK = (ROWS ? 2 : 1) * NH * 128;  // position channels (rows as the hi rows)
   static constexpr int OFF_KV = 0;
   static constexpr int OFF_Q = R * NCH * CHUNK;
-  static constexpr int OFF_P = OFF_Q + 4 * Q_CHUNK + (ROPE ? (NH * 128 + 1023) / 1024 * 1024 : 0);
+  static constexpr int OFF_P = OFF_Q + 4 * Q_CHUNK + (ROPE ? QR_CHUNK : 0);
   static constexpr int OFF_MISC = OFF_P + 2 * P_BLOCK;
   static constexpr int MISC = 4096;
   static constexpr int TOTAL = OFF_MISC + MISC;
   static_assert(TOTAL <= 232448 && OFF_P % 1024 == 0 && P_BLOCK % 1024 == 0, "shared memory budget");
-  static constexpr int TM_O = (NS * SW + 31) / 32 * 32;
+  static constexpr int TM_O = (2 * SW + 31) / 32 * 32;
   static constexpr int TM_COLS = NH == 64 ? 512 : 256;
   static_assert(TM_O + 4 * NH <= TM_COLS, "TMEM budget");
 };
@@ -75,7 +79,8 @@ constexpr int M_RED = 688;                    // float [4][64]; the first row al
 constexpr int M_STAT = M_RED + 1024;          // float [64]
 constexpr int M_COL = M_STAT + 256;           // float [2][64]: a column's factor of the score, by run
 constexpr int M_SCALE = M_COL + 512;          // float [kSlots][64]: s of the rows, -1: masked
-static_assert(M_SEGE + 8 * kSegs <= M_TMEM && M_PLAN + 56 <= M_SEG && M_SCALE + kSlots * 256 <= 4096, "misc layout");
+constexpr int M_MASKED = M_SCALE + kSlots * 256;  // uint8 [kSlots]: some row of a tile is masked
+static_assert(M_SEGE + 8 * kSegs <= M_TMEM && M_PLAN + 56 <= M_SEG && M_SEG % 16 == 0 && M_SCALE % 16 == 0 && M_MASKED + kSlots <= 4096, "misc layout");
 
 struct Params : GroupParams {
   const __nv_bfloat16* q;
@@ -143,28 +148,32 @@ __device__ __forceinline__ float2 e4m3x2_floats(uint32_t v) { return f16x2_float
 __device__ __forceinline__ float2 minus2(float2 a, float2 b) { return add2(a, make_float2(-b.x, -b.y)); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }  // -126 <= e <= 127
 
-// 16 TMEM lanes x 64 bits, N times: thread t of the warp gets lane base + (t >> 2) + 8 (t & 1) and the columns
-// c + 2j + ((t >> 1) & 1), j = 0..N-1.
-template <int N>
-__device__ __forceinline__ void tmem_ld16x64b(uint32_t a, uint32_t (&r)[N]) {
-  if constexpr (N == 4) {
-    asm volatile("tcgen05.ld.sync.aligned.16x64b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
-  } else {
-    static_assert(N == 16, "columns per thread");
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x64b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(a));
-  }
+// 16 TMEM lanes x 64 bits, four times: thread t of the warp gets lane base + (t >> 2) + 8 (t & 1) and the columns
+// c + 2j + ((t >> 1) & 1), j = 0..3.
+__device__ __forceinline__ void tmem_ld16x64b(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x64b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+// 16 TMEM lanes, a thread 16 columns of one: threads 0-15 from column c, 16-31 from column c + 16.
+__device__ __forceinline__ void tmem_ld16x32bx2(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 16;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a));
+}
+__device__ __forceinline__ float4 lds4f(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
 }
 
 template <int DQK, int NH>
 __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __grid_constant__ Params p) {
   using L = Smem<DQK, NH>;
   constexpr bool ROPE = L::ROPE;
-  constexpr int NCH = L::NCH, R = L::R, NS = L::NS;
+  constexpr int NCH = L::NCH, R = L::R;
+  constexpr bool ROWS = L::ROWS;
   constexpr int NHH = NH / 2, NQ = NHH / 2;  // rows per softmax half, per thread
   static_assert(R <= kSlots, "ring");
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -182,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
     const float s = s_scale[at];
     return s >= 0.f && s < kLeast ? kLeast : s;
   };
+  volatile uint8_t* s_masked = misc + M_MASKED;
   float* s_stat = reinterpret_cast<float*>(misc + M_STAT);
   float* s_fac = reinterpret_cast<float*>(misc + M_RED);  // a column's factor replaces its first maximum or sum
   float* s_red = reinterpret_cast<float*>(misc + M_RED);
@@ -199,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
       for (int m = 0; m < kSteps; ++m) mbar_init(bar_pv + 8 * (s * kSteps + m), 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(bar_s + 8 * b, 1);
+      mbar_init(bar_s + 8 * b, ROWS ? 2 : 1);
       mbar_init(bar_sf + 8 * b, 8);
       mbar_init(bar_p + 8 * b, 8);
       mbar_init(bar_fin + 8 * b, 1);
@@ -231,7 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
   };
   if (warp == 0) {
     // ======================= S^T issuer =======================
-    constexpr uint32_t kIdS = idesc_f8(kTile, 2 * NH, 0, 0, false, false), kIdR = idesc_bf16(kTile, NH, false, false);
+    constexpr uint32_t kIdS = ROWS ? idesc_f8(128, kTile, 0, 0, false, false) : idesc_f8(kTile, 2 * NH, 0, 0, false, false);
+    constexpr uint32_t kIdR = ROWS ? idesc_bf16(128, kTile, false, false) : idesc_bf16(kTile, NH, false, false);
     int done = 0;
     for (int seg = 0, last = 0; !last; ++seg) {
       Seg sg;
@@ -246,17 +257,37 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
       bool stop = false;
 #pragma unroll 1
       for (int k0 = 0; k0 < n; ++k0, ++i) {
-        const int sl = i % R, sb = i % NS;
-        if (i >= NS && !warp_all(wait_for(bar_sf + 8 * sb, ((i / NS) - 1) & 1, s_abort, p.wait_limit))) { stop = true; break; }
+        const int sl = i % R, sb = i & 1;
+        if (i >= 2 && !warp_all(wait_for(bar_sf + 8 * sb, ((i >> 1) - 1) & 1, s_abort, p.wait_limit))) { stop = true; break; }
         const uint64_t a0 = sdesc_sw128(kv0, 16, 1024) + (uint64_t)(uint32_t)(sl * NCH * (L::CHUNK >> 4));
         const uint64_t b0 = sdesc_sw128(q0, 16, 1024);
         if (!warp_all(wait_kv(i))) { stop = true; break; }
         fence_proxy_async_smem();  // (the rows came by cp.async)
         tc_fence_after();
+        if constexpr (ROWS) {
+          // (hi rows of position channels are the first 16 of every 32; the others are anything: no one looks at those sums)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          mma_f8_w<4, 2, 2>(d0 + sb * L::SW, a0 + c * (L::CHUNK >> 4), b0 + c * (L::Q_CHUNK >> 4), kIdS, c);
-        if (ROPE) mma4_w<2, 2>(d0 + sb * L::SW + 2 * NH, a0 + 4 * (L::CHUNK >> 4), b0 + 4 * (L::Q_CHUNK >> 4), kIdR, 0);
+          for (int c = 0; c < 4; ++c)
+            mma_f8_w<4, 2, 2>(d0 + sb * L::SW, b0 + c * (L::Q_CHUNK >> 4), a0 + c * (L::CHUNK >> 4), kIdS, c);
+          if (ROPE) mma4_w<2, 2>(d0 + sb * L::SW + kTile, b0 + 4 * (L::Q_CHUNK >> 4), a0 + 4 * (L::CHUNK >> 4), kIdR, 0);
+          // what the softmax needs of s, once for all rows: -1: masked; whether there are such
+          bool masked = false;
+#pragma unroll
+          for (int x = 0; x < kTile; x += 32) {
+            const float v = scale_of(sl * kTile + x + lane);
+            s_scale[sl * kTile + x + lane] = v;
+            masked |= v < 0.f;
+          }
+          masked = __any_sync(0xffffffffu, masked);
+          if (lane == 0) s_masked[sl] = masked;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_s + 8 * sb);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            mma_f8_w<4, 2, 2>(d0 + sb * L::SW, a0 + c * (L::CHUNK >> 4), b0 + c * (L::Q_CHUNK >> 4), kIdS, c);
+          if (ROPE) mma4_w<2, 2>(d0 + sb * L::SW + 2 * NH, a0 + 4 * (L::CHUNK >> 4), b0 + 4 * (L::Q_CHUNK >> 4), kIdR, 0);
+        }
         mma_commit_w(bar_s + 8 * sb);
       }
       if (stop) break;
@@ -284,11 +315,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
         if (!warp_all(wait_for(bar_p + 8 * (i & 1), (i >> 1) & 1, s_abort, p.wait_limit))) { stop = true; break; }
         fence_proxy_async_smem();
         tc_fence_after();
-        constexpr uint32_t kIdHi = idesc_f8(128, NH, 0, 1, true, NH == 64), kIdLo = idesc_f8(128, NH, 0, 0, true, NH == 64);
+        constexpr uint32_t kIdHi = idesc_f8(128, NH, 0, 1, true, false), kIdLo = idesc_f8(128, NH, 0, 0, true, false);
         const uint64_t va = sdesc_sw128(kv0, 16, 1024) + (uint64_t)(uint32_t)(sl * NCH * (L::CHUNK >> 4));
-        // W^T rows are keys, 64 bytes of hi and 64 of lo (NH = 64), or columns: hi rows, then lo rows, keys along K
+        // W: a row for each row of the group, 64 bytes of hi and 64 of lo, or hi rows, then lo rows; keys along K
         const uint64_t pb = sdesc_sw128(p0, 16, 1024) + (uint64_t)(uint32_t)((i & 1) * (L::P_BLOCK >> 4));
-        constexpr int kLo = NH == 64 ? 64 >> 4 : NH * 128 >> 4, kStep = NH == 64 ? 32 * 128 >> 4 : 2;
+        constexpr int kLo = ROWS ? 64 >> 4 : NH * 128 >> 4, kStep = 2;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const uint64_t a = va + m * (L::CHUNK >> 4);
@@ -424,20 +455,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
     const int wk = warp - 1, qd = warp & 3, ch = wk >> 2;
     const int par = (lane >> 1) & 1;
     const int r = qd * 16 + (lane >> 2) + 8 * (lane & 1);  // key row of the tile
-    const int bar_id = 1 + ch;
     const int n0 = ch * NHH + par * NQ;  // this thread's rows n0 .. n0 + NQ - 1 of the group
+    // or (ROWS) its row of the group, and its 16 keys of the tile
+    const int my_row = qd * 16 + (lane & 15), k0 = ch * 32 + (lane >> 4) * 16;
+    // warps that share rows, and meet at barriers
+    const int bar_id = ROWS ? 1 : 1 + ch;
+    constexpr int kTeam = ROWS ? kWorkers : kWorkers / 2;
+    // row hh of the group in Q, its hi or its lo
+    auto q_row = [&](int hh, int lo) { return ROWS ? (hh >> 4) * 32 + (hh & 15) + 16 * lo : hh + NH * lo; };
     // The run's queries: a row a warp, as hi and lo, and what the sums of a column are to be multiplied by.  A warp asks for
     // all its rows at once (one or two at a time, each with the time of a read from DRAM: 16000 cycles in place of 4000) and
     // has them come to where their hi and lo will lie, which are as large together; each is then read before it is written.
     auto load_q = [&](const Seg& s, int run) {
-      auto raw_at = [&](int hh, int u) { return sQ + (u >> 4) * L::Q_CHUNK + sw128_off((u >> 3 & 1) * NH + hh, u & 7); };
+      auto raw_at = [&](int hh, int u) { return sQ + (u >> 4) * L::Q_CHUNK + sw128_off(q_row(hh, u >> 3 & 1), u & 7); };
 #pragma unroll 1
       for (int hh = wk; hh < NH; hh += kWorkers / 32) {
         const __nv_bfloat16* src = p.q + (size_t)(hh < s.rows ? s.row0 + hh : s.row0) * DQK + lane * 8;
         const uint32_t size = hh < s.rows ? 16 : 0;
         cp_async16(raw_at(hh, lane), src, size);
         cp_async16(raw_at(hh, lane + 32), src + 256, size);
-        if (ROPE && lane < 8) cp_async16(sQ + 4 * L::Q_CHUNK + sw128_off(hh, lane), src + 512, size);
+        if (ROPE && lane < 8) cp_async16(sQ + 4 * L::Q_CHUNK + sw128_off(q_row(hh, 0), lane), src + 512, size);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
@@ -457,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
         const int e = max((int)(most >> 7) - 127, -119);
         const float by = pow2(7 - e);
         // (a row with a channel that is not finite gives NaN)
-        if (lane == 0) s_col[(run & 1) * 64 + hh] = most >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e - 7) * p.sl2e;
+        if (lane == 0) s_col[(run & 1) * 64 + hh] = most >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e - 7) * (ROWS ? 1.f : p.sl2e);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int u = lane + 32 * x;
@@ -470,8 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
             lo[g] = e4m3x2(minus2(a, e4m3x2_floats(hi[g])));
           }
           const uint32_t at = sQ + (u >> 4) * L::Q_CHUNK + (u & 1) * 8;
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + sw128_off(hh, (u & 15) >> 1)), "r"(hi[0] | hi[1] << 16), "r"(hi[2] | hi[3] << 16) : "memory");
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + sw128_off(NH + hh, (u & 15) >> 1)), "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16) : "memory");
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + sw128_off(q_row(hh, 0), (u & 15) >> 1)), "r"(hi[0] | hi[1] << 16), "r"(hi[2] | hi[3] << 16) : "memory");
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + sw128_off(q_row(hh, 1), (u & 15) >> 1)), "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16) : "memory");
         }
       }
       fence_proxy_async_smem();
@@ -503,9 +540,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
       return v[0];
     };
     const int sum_row = n0 + (((lane >> 1) & 14) | (lane & 1)) % NQ;
+    // the running maxima of the half's rows, from those of the tile in s_red, and the factors of what has been summed so far
+    auto new_maxima = [&]() {
+      if (qd == 0 && lane < NHH) {
+        const int n = ch * NHH + lane;
+        float bm = fmaxf(s_red[n], s_red[NH + n]);
+        if constexpr (!ROWS) bm = fmaxf(bm, fmaxf(s_red[2 * NH + n], s_red[3 * NH + n]));
+        const float mo = s_stat[n], mn = fmaxf(mo, bm - kTop);
+        s_stat[n] = mn;
+        s_fac[n] = mo == -INFINITY ? 0.f : exp2f(mo - mn);
+      }
+    };
+    auto rescale = [&]() {
+#pragma unroll 1
+      for (int x = 0; x < 4 * (NHH / 8); ++x) {  // 8 columns at a time
+        const int h0 = ch * NHH + (x % (NHH / 8)) * 8;
+        const uint32_t ta = tmem_addr(tmem + L::TM_O + x / (NHH / 8) * NH + h0, qd * 32, 0);
+        uint32_t ov[8];
+        tmem_ld8(ta, ov);
+        tmem_ld_wait();
+#pragma unroll
+        for (int h = 0; h < 8; ++h) ov[h] = __float_as_uint(__uint_as_float(ov[h]) * s_fac[h0 + h]);
+        tmem_st8(ta, ov);
+      }
+      tmem_st_wait();
+    };
     Seg sg, nx;
-    // (one answer for the half: its warps meet at barriers from here on)
-    bool aborted = named_bar_or(bar_id, 128, !read_seg(0, sg));
+    // (one answer for the team: its warps meet at barriers from here on)
+    bool aborted = named_bar_or(bar_id, kTeam, !read_seg(0, sg));
     if (!aborted) load_q(sg, 0);
     nx = sg;
     int i = 0;
@@ -521,11 +583,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
       for (int j = 0; j < NQ / 2; ++j) { l_part[j] = make_float2(0.f, 0.f); m_neg[j] = make_float2(3.0e38f, 3.0e38f); }
       if (qd == 0 && lane < NHH) s_stat[ch * NHH + lane] = -INFINITY;  // (read only after a barrier of the half)
       const float* col = s_col + ((seg - 1) & 1) * 64 + n0;
+      float2 l_row = make_float2(0.f, 0.f);
+      float neg = 3.0e38f, factor = 0.f;
+      const int seen = sg.seen0 + (sg.head0 + my_row) / p.H;
       const int t_end = sg.t0 + sg.n;
 #pragma unroll 1
       for (int t = sg.t0; t < t_end; ++t, ++i) {
-        const int sl = i % R, sb = i % NS;
-        bool bad = bad_seg || !warp_all(wait_for(bar_s + 8 * sb, (i / NS) & 1, s_abort, p.wait_limit));
+        const int sl = i % R, sb = i & 1;
+        bool bad = bad_seg || !warp_all(wait_for(bar_s + 8 * sb, (i >> 1) & 1, s_abort, p.wait_limit));
         // (complete since before S^T was issued: order the rows' scales and the columns' factors before their reads below)
         bad = bad || !warp_all(wait_kv(i));
         if (t == sg.t0) bad = bad || !warp_all(wait_for(bar_q, (seg - 1) & 1, s_abort, p.wait_limit));
@@ -533,14 +598,100 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
         if (i >= 2) bad = bad || !warp_all(wait_pv(i - 2, 3));
         tc_fence_after();
         __syncwarp();
+        if constexpr (ROWS) {
+        if (t == sg.t0) factor = s_col[((seg - 1) & 1) * 64 + my_row];
+        uint32_t v[16], x[16], w[16];  // scores before softmax_scale; e^z; the weights
+        const uint32_t ts = tmem_addr(tmem + sb * L::SW + ch * 32, qd * 32, 0);
+        tmem_ld16x32bx2(ts, v);
+        tmem_ld16x32bx2(ts + (16u << 16), x);
+        if constexpr (ROPE) tmem_ld16x32bx2(ts + kTile, w);
+        const uint32_t scales = sScale + (sl * kTile + k0) * 4;
+        const bool some = s_masked[sl] || (p.topk_idx == nullptr && (t + 1) * (long long)kTile > sg.seen0);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_sf + 8 * sb);
+        auto at2 = [](const uint32_t (&a)[16], int j) { return make_float2(__uint_as_float(a[j]), __uint_as_float(a[j + 1])); };
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 s4 = lds4f(scales + 4 * j);
+#pragma unroll
+          for (int h = 0; h < 4; h += 2) {
+            const float2 s2 = h ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y), sum = add2(at2(v, j + h), at2(x, j + h));
+            const float2 by = make_float2(factor, factor);
+            const float2 c = ROPE ? fma2(mul2(sum, s2), by, at2(w, j + h)) : mul2(mul2(sum, s2), by);
+            v[j + h] = __float_as_uint(c.x);
+            v[j + h + 1] = __float_as_uint(c.y);
+          }
+        }
+        if (t + 1 == t_end && more && !bad) load_q(nx, seg);  // S of the segment is done: Q is free
+        auto hidden = [&](int j, float s) { return s < 0.f || (p.topk_idx == nullptr && t * kTile + k0 + j >= seen); };
+        auto weights = [&]() -> float {
+          float most = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 s4 = lds4f(scales + 4 * j);
+#pragma unroll
+            for (int h = 0; h < 4; h += 2) {
+              const float2 s2 = h ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y);
+              const float2 e = fma2(at2(v, j + h), make_float2(p.sl2e, p.sl2e), make_float2(neg, neg));
+              float2 y = make_float2(ex2(e.x), ex2(e.y)), z = mul2(y, s2);
+              if (some) {
+                if (hidden(j + h, s2.x)) y.x = z.x = 0.f;
+                if (hidden(j + h + 1, s2.y)) y.y = z.y = 0.f;
+              }
+              most = fmaxf(most, fmaxf(z.x, z.y));
+              x[j + h] = __float_as_uint(y.x); x[j + h + 1] = __float_as_uint(y.y);
+              w[j + h] = __float_as_uint(z.x); w[j + h + 1] = __float_as_uint(z.y);
+            }
+          }
+          return most;
+        };
+        const bool mine = !(weights() <= kMost) || t == sg.t0;
+        if (named_bar_or(bar_id, kTeam, mine || bad)) {
+          if (named_bar_or(bar_id, kTeam, bad)) { aborted = true; break; }
+          float top = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float s = s_scale[sl * kTile + k0 + j];
+            const float z = __uint_as_float(v[j]) * p.sl2e + (float)((int)(__float_as_uint(s) >> 23) - 127);
+            if (s > 0.f && !(some && hidden(j, s))) top = fmaxf(top, z);
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          if (lane < 16) s_red[ch * NH + my_row] = top;
+          named_bar(bar_id, kTeam);
+          new_maxima();
+          named_bar(bar_id, kTeam);
+          l_row = mul2(l_row, make_float2(s_fac[my_row], s_fac[my_row]));
+          neg = -fmaxf(s_stat[my_row], -3.0e38f);
+          weights();
+          if (t > sg.t0) {
+            const bool okw = wait_pv(i - 1, 3);
+            if (named_bar_or(bar_id, kTeam, !okw)) { aborted = true; break; }
+            tc_fence_after();
+            rescale();
+          }
+        }
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          l_row = add2(l_row, add2(at2(x, j), at2(x, j + 2)));
+          const uint32_t h0 = e5m2x2(at2(w, j)), h1 = e5m2x2(at2(w, j + 2));
+          hi[j / 4] = h0 | h1 << 16;
+          lo[j / 4] = e4m3x2(minus2(at2(w, j), e5m2x2_floats(h0))) | e4m3x2(minus2(at2(w, j + 2), e5m2x2_floats(h1))) << 16;
+        }
+        const uint32_t to = sP + (i & 1) * L::P_BLOCK;
+        st_shared_v4(to + sw128_off(my_row, k0 / 16), hi[0], hi[1], hi[2], hi[3]);
+        st_shared_v4(to + sw128_off(my_row, 4 + k0 / 16), lo[0], lo[1], lo[2], lo[3]);
+        } else {
         uint32_t raw[NQ];
         float2 z[NQ / 2];  // (alternate columns of the half first)
         const uint32_t ts = tmem_addr(tmem + sb * L::SW + ch * NHH, qd * 32, 0);
         {
           uint32_t lo[NQ], pos[NQ];
-          tmem_ld16x64b<NQ>(ts, raw);
-          tmem_ld16x64b<NQ>(ts + NH, lo);
-          if constexpr (ROPE) tmem_ld16x64b<NQ>(ts + 2 * NH, pos);
+          tmem_ld16x64b(ts, raw);
+          tmem_ld16x64b(ts + NH, lo);
+          if constexpr (ROPE) tmem_ld16x64b(ts + 2 * NH, pos);
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
@@ -585,8 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
           mine |= e[j].x > kRaise || e[j].y > kRaise;
         }
         bool raise = false;
-        if (named_bar_or(bar_id, 128, mine || bad)) {
-          if (named_bar_or(bar_id, 128, bad)) { aborted = true; break; }
+        if (named_bar_or(bar_id, kTeam, mine || bad)) {
+          if (named_bar_or(bar_id, kTeam, bad)) { aborted = true; break; }
           raise = true;
         }
         if (raise) {
@@ -594,15 +745,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
 #pragma unroll
           for (int j = 0; j < NQ / 2; ++j) { top[2 * j] = z[j].x; top[2 * j + 1] = z[j].y; }
           s_red[qd * NH + sum_row] = over_keys(top, true);
-          named_bar(bar_id, 128);
-          if (qd == 0 && lane < NHH) {
-            const int n = ch * NHH + lane;
-            const float bm = fmaxf(fmaxf(s_red[n], s_red[NH + n]), fmaxf(s_red[2 * NH + n], s_red[3 * NH + n])) - kTop;
-            const float mo = s_stat[n], mn = fmaxf(mo, bm);
-            s_stat[n] = mn;
-            s_fac[n] = mo == -INFINITY ? 0.f : exp2f(mo - mn);
-          }
-          named_bar(bar_id, 128);
+          named_bar(bar_id, kTeam);
+          new_maxima();
+          named_bar(bar_id, kTeam);
 #pragma unroll
           for (int j = 0; j < NQ / 2; ++j) {
             l_part[j] = mul2(l_part[j], make_float2(s_fac[n0 + 2 * j], s_fac[n0 + 2 * j + 1]));
@@ -611,20 +756,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
           }
           if (t > sg.t0) {
             const bool okw = wait_pv(i - 1, 3);
-            if (named_bar_or(bar_id, 128, !okw)) { aborted = true; break; }
+            if (named_bar_or(bar_id, kTeam, !okw)) { aborted = true; break; }
             tc_fence_after();
-#pragma unroll 1
-            for (int x = 0; x < 4 * (NHH / 8); ++x) {  // 8 columns at a time
-              const int h0 = ch * NHH + (x % (NHH / 8)) * 8;
-              const uint32_t ta = tmem_addr(tmem + L::TM_O + x / (NHH / 8) * NH + h0, qd * 32, 0);
-              uint32_t ov[8];
-              tmem_ld8(ta, ov);
-              tmem_ld_wait();
-#pragma unroll
-              for (int h = 0; h < 8; ++h) ov[h] = __float_as_uint(__uint_as_float(ov[h]) * s_fac[h0 + h]);
-              tmem_st8(ta, ov);
-            }
-            tmem_st_wait();
+            rescale();
           }
         }
         uint32_t hi[NQ / 2], lo[NQ / 2];
@@ -636,18 +770,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
           lo[j] = e4m3x2(minus2(w, e5m2x2_floats(hi[j])));
         }
         const uint32_t to = sP + (i & 1) * L::P_BLOCK;
-        if constexpr (NH == 64) {
-          const int u0 = n0 / 16;
-          st_shared_v4(to + sw128_off(r, u0), hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
-          st_shared_v4(to + sw128_off(r, 4 + u0), lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
-        } else {
 #pragma unroll
-          for (int j = 0; j < NQ; ++j) {
-            const int n = n0 + j;
-            const uint32_t at = to + (uint32_t)(n * 128 + (((r >> 4) ^ (n & 7)) << 4) + (r & 15));
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(hi[j / 2] >> (8 * (j & 1))) : "memory");
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + NH * 128), "r"(lo[j / 2] >> (8 * (j & 1))) : "memory");
-          }
+        for (int j = 0; j < NQ; ++j) {
+          const int n = n0 + j;
+          const uint32_t at = to + (uint32_t)(n * 128 + (((r >> 4) ^ (n & 7)) << 4) + (r & 15));
+          asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(hi[j / 2] >> (8 * (j & 1))) : "memory");
+          asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + NH * 128), "r"(lo[j / 2] >> (8 * (j & 1))) : "memory");
+        }
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -656,17 +785,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
       }
       if (aborted) break;
       // ---- the segment's rows: out and lse, or the workspace's partial sums ----
-      float sums[NQ];
+      named_bar(bar_id, kTeam);  // the factors of a rescale in the last tile have been read (the sums take their place)
+      if constexpr (ROWS) {
+        float sum = l_row.x + l_row.y;
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        if (lane < 16) s_red[ch * NH + my_row] = sum;
+      } else {
+        float sums[NQ];
 #pragma unroll
-      for (int j = 0; j < NQ / 2; ++j) { sums[2 * j] = l_part[j].x; sums[2 * j + 1] = l_part[j].y; }
-      named_bar(bar_id, 128);  // the factors of a rescale in the last tile have been read (the sums take their place)
-      s_red[qd * NH + sum_row] = over_keys(sums, false);
-      named_bar(bar_id, 128);
+        for (int j = 0; j < NQ / 2; ++j) { sums[2 * j] = l_part[j].x; sums[2 * j + 1] = l_part[j].y; }
+        s_red[qd * NH + sum_row] = over_keys(sums, false);
+      }
+      named_bar(bar_id, kTeam);
       const bool whole = sg.whole;
       const int slot = 2 * blockIdx.x + (sg.opens ? 1 : 0);
       if (qd == 0 && lane < NHH) {
         const int n = ch * NHH + lane;
-        const float l = s_red[n] + s_red[NH + n] + s_red[2 * NH + n] + s_red[3 * NH + n];
+        float l = s_red[n] + s_red[NH + n];
+        if constexpr (!ROWS) l = l + s_red[2 * NH + n] + s_red[3 * NH + n];
         const float m = s_stat[n];
         float fac = 1.f;
         if (whole) {
@@ -682,9 +818,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
         }
         s_fac[n] = fac;
       }
-      named_bar(bar_id, 128);
+      named_bar(bar_id, kTeam);
       const bool got = wait_pv(i - 1, 3);  // (the sums above while the last P.V is under way)
-      aborted = named_bar_or(bar_id, 128, !got);
+      aborted = named_bar_or(bar_id, kTeam, !got);
       if (aborted) break;
       tc_fence_after();
       // a few rows of 32 channels at a time, in a loop: unrolled, this code is longer than the time it takes to fetch it
@@ -715,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
         }
       }
       tc_fence_before();
-      named_bar(bar_id, 128);  // s_red, s_stat and s_fac have been read
+      named_bar(bar_id, kTeam);  // s_red, s_stat and s_fac have been read
       if (!more) break;
       sg = nx;
     }
