@@ -34,10 +34,7 @@ namespace pmla8 {
 using namespace pgroups;
 
 constexpr int kTile = 64;
-constexpr int kWorkers = 256;
-constexpr int kGather = 128;
-constexpr int kThreads = 32 + kWorkers + kGather + 64;
-constexpr int kReaders = 2 + kWorkers / 32 + kGather / 32;  // warps that read an announcement
+constexpr int kGather = 4;  // warps that copy
 constexpr float kRaise = 11.0f;  // log2 units: the running maximum is raised when a weight passes 2^11
 constexpr float kTop = 5.0f;     // a new maximum is 2^5
 constexpr float kMost = 2048.0f;
@@ -54,6 +51,9 @@ struct Smem {
   // 64 rows: S[row, key], hi and lo rows as M = 128 (of each warp's 32 lanes the first 16 hi, the others lo);
   // 16 rows: S^T[key, row], M = 64 keys, hi and lo side by side.
   static constexpr bool ROWS = NH == 64;
+  static constexpr int W = ROWS ? 16 : 8;       // softmax warps
+  static constexpr int THREADS = 32 * (W + kGather + 3);
+  static constexpr int READERS = W + kGather + 2;  // warps that read an announcement
   static constexpr int SW = ROWS ? (ROPE ? 2 : 1) * kTile : (ROPE ? 3 : 2) * NH;  // TMEM columns of S
   static constexpr int P_BLOCK = NH * 128 * (ROWS ? 1 : 2);
   static constexpr int QR_CHUNK = (ROWS ? 2 : 1) * NH * 128;  // position channels (rows as the hi rows)
@@ -154,13 +154,13 @@ __device__ __forceinline__ void tmem_ld16x64b(uint32_t a, uint32_t (&r)[4]) {
   asm volatile("tcgen05.ld.sync.aligned.16x64b.x4.b32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
-// 16 TMEM lanes, a thread 16 columns of one: threads 0-15 from column c, 16-31 from column c + 16.
-__device__ __forceinline__ void tmem_ld16x32bx2(uint32_t a, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 16;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(a));
+// 16 TMEM lanes, a thread 8 columns of one: threads 0-15 from column c, 16-31 from column c + 8.
+__device__ __forceinline__ void tmem_ld16x32bx2(uint32_t a, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], 8;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(a));
+}
+__device__ __forceinline__ void st_shared_v2(uint32_t at, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(a), "r"(b) : "memory");
 }
 __device__ __forceinline__ float4 lds4f(uint32_t at) {
   float4 v;
@@ -169,12 +169,13 @@ __device__ __forceinline__ float4 lds4f(uint32_t at) {
 }
 
 template <int DQK, int NH>
-__global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kernel(const __grid_constant__ Params p) {
   using L = Smem<DQK, NH>;
   constexpr bool ROPE = L::ROPE;
   constexpr int NCH = L::NCH, R = L::R;
   constexpr bool ROWS = L::ROWS;
-  constexpr int NHH = NH / 2, NQ = NHH / 2;  // rows per softmax half, per thread
+  constexpr int W = L::W, NHH = NH / (W / 4), NQ = 4;  // columns of O^T of four softmax warps; rows of a thread (16 rows)
+  constexpr int kKeys = 8;  // keys of a thread (64 rows)
   static_assert(R <= kSlots, "ring");
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sKV = smem_u32(smem) + L::OFF_KV, sQ = smem_u32(smem) + L::OFF_Q, sP = smem_u32(smem) + L::OFF_P;
@@ -210,19 +211,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar_s + 8 * b, ROWS ? 2 : 1);
-      mbar_init(bar_sf + 8 * b, 8);
-      mbar_init(bar_p + 8 * b, 8);
+      mbar_init(bar_sf + 8 * b, W);
+      mbar_init(bar_p + 8 * b, W);
       mbar_init(bar_fin + 8 * b, 1);
     }
-    mbar_init(bar_q, 8);
+    mbar_init(bar_q, W);
     for (int k = 0; k < kSegs; ++k) {
       mbar_init(mb + M_SEGF + 8 * k, 1);
-      mbar_init(mb + M_SEGE + 8 * k, kReaders);
+      mbar_init(mb + M_SEGE + 8 * k, L::READERS);
     }
     *s_abort = 0;
     fence_mbar_init();
   }
-  make_plan<kTile, kThreads>(p, s_plan, reinterpret_cast<long long*>(s_red));
+  make_plan<kTile, L::THREADS>(p, s_plan, reinterpret_cast<long long*>(s_red));
   const Plan plan = *s_plan;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the joining kernel waits for this one's end itself)
   if (plan.w1 <= plan.w0 || plan.w1 - plan.w0 <= plan.skip) return;  // (the whole CTA)
@@ -231,8 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
     tmem_relinquish();
   }
   uint32_t tmem = 0;
-  if (warp <= 8 || warp == 13) {  // the others neither need it nor wait for it
-    named_bar(3, 320);
+  if (warp <= W || warp == W + 5) {  // the others neither need it nor wait for it
+    named_bar(3, 32 * (W + 2));
     tmem = (uint32_t)warp_value((int)*s_tmem);
   }
   // announcement k, once per warp
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
     volatile int dummy = 0;
     mbar_wait(bar_fin, 0, &dummy, p.err);
     __syncwarp();
-  } else if (warp == 13) {
+  } else if (warp == W + 5) {
     // ======================= P.V issuer =======================
     int done = 0;
     for (int seg = 0, last = 0; !last; ++seg) {
@@ -334,16 +335,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
     volatile int dummy = 0;
     mbar_wait(bar_fin + 8, 0, &dummy, p.err);
     __syncwarp();
-  } else if (warp == 14) {
+  } else if (warp == W + 6) {
     announce<kTile>(p, plan, mb + M_SEGF, mb + M_SEGE, reinterpret_cast<int4*>(misc + M_SEG), s_abort);
-  } else if (warp >= 9) {
+  } else if (warp > W) {
     // ======================= gather: 16 rows of every tile each =======================
     // By cp.async, which takes any row, a warp's instruction the 512 codes of one (8 cycles; boxes of 128 bytes by TMA take as
     // long as rows of bf16, since a row begins anywhere in a line), and says itself when it has landed; what is masked is
     // filled with zeros.  A lane looks one row up, in steps whose loads have a tile's time to come back: the list's entry
     // (three tiles ahead), the page (two ahead), the row number and its s (one ahead).
     constexpr int kRows = kTile / 4;
-    const int gw = warp - 9;
+    const int gw = warp - W - 1;
     Seg sg;
     int seg = 0, base = 0, end = 0, limit = 0;  // this CTA's tiles [base, end) are the segment's
     int n_tiles = INT_MAX;                      // this CTA's tiles, known once one past them has been looked for
@@ -456,11 +457,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
     const int par = (lane >> 1) & 1;
     const int r = qd * 16 + (lane >> 2) + 8 * (lane & 1);  // key row of the tile
     const int n0 = ch * NHH + par * NQ;  // this thread's rows n0 .. n0 + NQ - 1 of the group
-    // or (ROWS) its row of the group, and its 16 keys of the tile
-    const int my_row = qd * 16 + (lane & 15), k0 = ch * 32 + (lane >> 4) * 16;
+    // or (ROWS) its row of the group, and its keys of the tile
+    const int my_row = qd * 16 + (lane & 15), k0 = ch * 16 + (lane >> 4) * kKeys;
     // warps that share rows, and meet at barriers
     const int bar_id = ROWS ? 1 : 1 + ch;
-    constexpr int kTeam = ROWS ? kWorkers : kWorkers / 2;
+    constexpr int kTeam = ROWS ? 32 * W : 128;
     // row hh of the group in Q, its hi or its lo
     auto q_row = [&](int hh, int lo) { return ROWS ? (hh >> 4) * 32 + (hh & 15) + 16 * lo : hh + NH * lo; };
     // The run's queries: a row a warp, as hi and lo, and what the sums of a column are to be multiplied by.  A warp asks for
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
     auto load_q = [&](const Seg& s, int run) {
       auto raw_at = [&](int hh, int u) { return sQ + (u >> 4) * L::Q_CHUNK + sw128_off(q_row(hh, u >> 3 & 1), u & 7); };
 #pragma unroll 1
-      for (int hh = wk; hh < NH; hh += kWorkers / 32) {
+      for (int hh = wk; hh < NH; hh += W) {
         const __nv_bfloat16* src = p.q + (size_t)(hh < s.rows ? s.row0 + hh : s.row0) * DQK + lane * 8;
         const uint32_t size = hh < s.rows ? 16 : 0;
         cp_async16(raw_at(hh, lane), src, size);
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
 #pragma unroll 1
-      for (int hh = wk; hh < NH; hh += kWorkers / 32) {
+      for (int hh = wk; hh < NH; hh += W) {
         uint4 v[2];
         uint32_t top = 0;
 #pragma unroll
@@ -544,8 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
     auto new_maxima = [&]() {
       if (qd == 0 && lane < NHH) {
         const int n = ch * NHH + lane;
-        float bm = fmaxf(s_red[n], s_red[NH + n]);
-        if constexpr (!ROWS) bm = fmaxf(bm, fmaxf(s_red[2 * NH + n], s_red[3 * NH + n]));
+        const float bm = fmaxf(fmaxf(s_red[n], s_red[NH + n]), fmaxf(s_red[2 * NH + n], s_red[3 * NH + n]));
         const float mo = s_stat[n], mn = fmaxf(mo, bm - kTop);
         s_stat[n] = mn;
         s_fac[n] = mo == -INFINITY ? 0.f : exp2f(mo - mn);
@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
         const int sl = i % R, sb = i & 1;
         bool bad = bad_seg || !warp_all(wait_for(bar_s + 8 * sb, (i >> 1) & 1, s_abort, p.wait_limit));
         // (complete since before S^T was issued: order the rows' scales and the columns' factors before their reads below)
-        bad = bad || !warp_all(wait_kv(i));
+        if (!ROWS) bad = bad || !warp_all(wait_kv(i));
         if (t == sg.t0) bad = bad || !warp_all(wait_for(bar_q, (seg - 1) & 1, s_abort, p.wait_limit));
         // W of tile i overwrites what P.V of tile i - 2 read
         if (i >= 2) bad = bad || !warp_all(wait_pv(i - 2, 3));
@@ -600,62 +600,56 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
         __syncwarp();
         if constexpr (ROWS) {
         if (t == sg.t0) factor = s_col[((seg - 1) & 1) * 64 + my_row];
-        uint32_t v[16], x[16], w[16];  // scores before softmax_scale; e^z; the weights
-        const uint32_t ts = tmem_addr(tmem + sb * L::SW + ch * 32, qd * 32, 0);
+        uint32_t v[kKeys], x[kKeys], w[kKeys];  // scores before softmax_scale; e^z; the weights
+        const uint32_t ts = tmem_addr(tmem + sb * L::SW + ch * 16, qd * 32, 0);
         tmem_ld16x32bx2(ts, v);
         tmem_ld16x32bx2(ts + (16u << 16), x);
         if constexpr (ROPE) tmem_ld16x32bx2(ts + kTile, w);
-        const uint32_t scales = sScale + (sl * kTile + k0) * 4;
+        const float4 sa = lds4f(sScale + (sl * kTile + k0) * 4), sb4 = lds4f(sScale + (sl * kTile + k0) * 4 + 16);
+        const float2 s2[4] = {make_float2(sa.x, sa.y), make_float2(sa.z, sa.w), make_float2(sb4.x, sb4.y), make_float2(sb4.z, sb4.w)};
         const bool some = s_masked[sl] || (p.topk_idx == nullptr && (t + 1) * (long long)kTile > sg.seen0);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_sf + 8 * sb);
-        auto at2 = [](const uint32_t (&a)[16], int j) { return make_float2(__uint_as_float(a[j]), __uint_as_float(a[j + 1])); };
+        auto at2 = [](const uint32_t (&a)[kKeys], int j) { return make_float2(__uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1])); };
+        auto set2 = [](uint32_t (&a)[kKeys], int j, float2 y) { a[2 * j] = __float_as_uint(y.x); a[2 * j + 1] = __float_as_uint(y.y); };
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 s4 = lds4f(scales + 4 * j);
-#pragma unroll
-          for (int h = 0; h < 4; h += 2) {
-            const float2 s2 = h ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y), sum = add2(at2(v, j + h), at2(x, j + h));
-            const float2 by = make_float2(factor, factor);
-            const float2 c = ROPE ? fma2(mul2(sum, s2), by, at2(w, j + h)) : mul2(mul2(sum, s2), by);
-            v[j + h] = __float_as_uint(c.x);
-            v[j + h + 1] = __float_as_uint(c.y);
-          }
+        for (int j = 0; j < kKeys / 2; ++j) {
+          const float2 sum = mul2(add2(at2(v, j), at2(x, j)), s2[j]), by = make_float2(factor, factor);
+          set2(v, j, ROPE ? fma2(sum, by, at2(w, j)) : mul2(sum, by));
         }
         if (t + 1 == t_end && more && !bad) load_q(nx, seg);  // S of the segment is done: Q is free
-        auto hidden = [&](int j, float s) { return s < 0.f || (p.topk_idx == nullptr && t * kTile + k0 + j >= seen); };
+        auto hidden = [&](int j) {
+          return (j & 1 ? s2[j / 2].y : s2[j / 2].x) < 0.f || (p.topk_idx == nullptr && t * kTile + k0 + j >= seen);
+        };
         auto weights = [&]() -> float {
+#pragma unroll
+          for (int j = 0; j < kKeys / 2; ++j) {
+            const float2 e = fma2(at2(v, j), make_float2(p.sl2e, p.sl2e), make_float2(neg, neg));
+            const float2 y = make_float2(ex2(e.x), ex2(e.y));
+            set2(x, j, y);
+            set2(w, j, mul2(y, s2[j]));
+          }
+          if (some) {
+#pragma unroll
+            for (int j = 0; j < kKeys; ++j)
+              if (hidden(j)) x[j] = w[j] = 0;
+          }
           float most = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 s4 = lds4f(scales + 4 * j);
-#pragma unroll
-            for (int h = 0; h < 4; h += 2) {
-              const float2 s2 = h ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y);
-              const float2 e = fma2(at2(v, j + h), make_float2(p.sl2e, p.sl2e), make_float2(neg, neg));
-              float2 y = make_float2(ex2(e.x), ex2(e.y)), z = mul2(y, s2);
-              if (some) {
-                if (hidden(j + h, s2.x)) y.x = z.x = 0.f;
-                if (hidden(j + h + 1, s2.y)) y.y = z.y = 0.f;
-              }
-              most = fmaxf(most, fmaxf(z.x, z.y));
-              x[j + h] = __float_as_uint(y.x); x[j + h + 1] = __float_as_uint(y.y);
-              w[j + h] = __float_as_uint(z.x); w[j + h + 1] = __float_as_uint(z.y);
-            }
-          }
+          for (int j = 0; j < kKeys; ++j) most = fmaxf(most, __uint_as_float(w[j]));
           return most;
         };
-        const bool mine = !(weights() <= kMost) || t == sg.t0;
+        const bool mine = weights() > kMost || t == sg.t0;
         if (named_bar_or(bar_id, kTeam, mine || bad)) {
           if (named_bar_or(bar_id, kTeam, bad)) { aborted = true; break; }
           float top = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float s = s_scale[sl * kTile + k0 + j];
+          for (int j = 0; j < kKeys; ++j) {
+            const float s = j & 1 ? s2[j / 2].y : s2[j / 2].x;
             const float z = __uint_as_float(v[j]) * p.sl2e + (float)((int)(__float_as_uint(s) >> 23) - 127);
-            if (s > 0.f && !(some && hidden(j, s))) top = fmaxf(top, z);
+            if (s > 0.f && !(some && hidden(j))) top = fmaxf(top, z);
           }
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
           if (lane < 16) s_red[ch * NH + my_row] = top;
@@ -672,17 +666,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
             rescale();
           }
         }
-        uint32_t hi[4], lo[4];
+        uint32_t hi[2], lo[2];
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          l_row = add2(l_row, add2(at2(x, j), at2(x, j + 2)));
-          const uint32_t h0 = e5m2x2(at2(w, j)), h1 = e5m2x2(at2(w, j + 2));
-          hi[j / 4] = h0 | h1 << 16;
-          lo[j / 4] = e4m3x2(minus2(at2(w, j), e5m2x2_floats(h0))) | e4m3x2(minus2(at2(w, j + 2), e5m2x2_floats(h1))) << 16;
+        for (int j = 0; j < kKeys / 2; j += 2) {
+          l_row = add2(l_row, add2(at2(x, j), at2(x, j + 1)));
+          const uint32_t h0 = e5m2x2(at2(w, j)), h1 = e5m2x2(at2(w, j + 1));
+          hi[j / 2] = h0 | h1 << 16;
+          lo[j / 2] = e4m3x2(minus2(at2(w, j), e5m2x2_floats(h0))) | e4m3x2(minus2(at2(w, j + 1), e5m2x2_floats(h1))) << 16;
         }
-        const uint32_t to = sP + (i & 1) * L::P_BLOCK;
-        st_shared_v4(to + sw128_off(my_row, k0 / 16), hi[0], hi[1], hi[2], hi[3]);
-        st_shared_v4(to + sw128_off(my_row, 4 + k0 / 16), lo[0], lo[1], lo[2], lo[3]);
+        const uint32_t to = sP + (i & 1) * L::P_BLOCK + (k0 & 8);
+        st_shared_v2(to + sw128_off(my_row, ch), hi[0], hi[1]);
+        st_shared_v2(to + sw128_off(my_row, 4 + ch), lo[0], lo[1]);
         } else {
         uint32_t raw[NQ];
         float2 z[NQ / 2];  // (alternate columns of the half first)
@@ -801,8 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_e4m3_kernel(const __gri
       const int slot = 2 * blockIdx.x + (sg.opens ? 1 : 0);
       if (qd == 0 && lane < NHH) {
         const int n = ch * NHH + lane;
-        float l = s_red[n] + s_red[NH + n];
-        if constexpr (!ROWS) l = l + s_red[2 * NH + n] + s_red[3 * NH + n];
+        const float l = s_red[n] + s_red[NH + n] + s_red[2 * NH + n] + s_red[3 * NH + n];
         const float m = s_stat[n];
         float fac = 1.f;
         if (whole) {
@@ -875,7 +868,7 @@ dsa_status_t launch(Params& p, int ctas, cudaStream_t s) {
   p.G = p.topk_idx ? 1 : (p.H <= NH ? NH / p.H : 1);
   p.extra = p.topk_idx ? 2 : 4;
   p.HB = (p.H + NH - 1) / NH;
-  paged_mla_e4m3_kernel<DQK, NH><<<ctas, kThreads, L::TOTAL, s>>>(p);
+  paged_mla_e4m3_kernel<DQK, NH><<<ctas, L::THREADS, L::TOTAL, s>>>(p);
   return cuda_check(cudaGetLastError(), "launching paged_mla_e4m3_kernel");
 }
 
