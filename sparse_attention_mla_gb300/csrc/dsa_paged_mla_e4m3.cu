@@ -11,14 +11,25 @@
 //    down to 2^-2, and to 2^-10 (2^-17 of the largest channel) below;
 //  - a weight is hi + lo, hi e5m2 (2^15 down to 2^-16) and lo e4m3: 7 to 8 bits above 2^-3 and, where lo runs out, to 2^-10;
 //    the largest weight of a row is between 2^5 and 2^11 (the maximum is raised lazily), so that this is 2^-15 of it.
-// S^T is three sums side by side (hi, lo and the position channels in bf16, which s_p must not reach) that the softmax adds.
+// Position channels are multiplied in bf16 and added by the softmax, since s_p must not reach them.
 //
-// Split of the work as in dsa_paged_groups.cuh, with tiles of 64 positions and groups of NH = 16 or 64 columns.  A tile:
-// S^T[key, row] = KV Q^T (M = 64 keys; N = hi and lo rows), an online softmax with a lazily raised maximum,
-// O^T[channel, row] += V^T W^T (M = 128 channels, K = 32 keys, hi and then lo into the same columns).  The codes of 128
-// channels of a key are a row of 128 bytes, which is K-major for the first product and M-major for the second.
+// Split of the work as in dsa_paged_groups.cuh, with tiles of 64 positions and groups of 64 rows, or of 16 while all rows of a
+// request (or a list) fit.  A tile:
+//  - 64 rows: S[row, key] = Q K^T with hi and lo of the queries as the 128 lanes (M = 128, N = 64 keys), so that a thread of
+//    the softmax has keys of one row.  16 rows: S^T[key, row] = K Q^T (M = 64), hi and lo side by side, which keeps all warps
+//    busy; with 64 rows it took the tensor core, whose M = 64 runs at half its rate, 2000 cycles a tile in place of 1300.
+//  - an online softmax with a lazily raised maximum;
+//  - O^T[channel, row] += V^T W^T (M = 128 channels, K = 32 keys, hi and then lo into the same columns).  The codes of 128
+//    channels of a key are a row of 128 bytes, which is K-major for the first product and M-major for the second.
 //
-// Warps: 0 issues S^T, 1-8 softmax and epilogue, 9-12 copy tiles into a ring of three, 13 issues P.V, 14 announces the
+// What bounds it: 64 requests of 4000 to 16384 positions, 64 heads: 125 us, of which 10 pass before the first scores (cutting
+// the line, the queries), 15 with the launches and the joining; the 430 MB of rows are read at 4.3 TB/s in between, where a copy
+// reaches 6.8.  A tile's place in the ring (three tiles of 40 KB beside 64 KB of queries) is in use for 6900 cycles: 1700 for
+// its copies, 1700 for S, 2200 for the softmax, 1000 for P.V, the two products sharing shared memory's 128 bytes a cycle (216
+// KB a tile).  Measured beside it: the same rows converted to fp16 as the 4-bit kernel does, 220 us; queries in TMEM and four
+// tiles in the ring, 136 (queries that a thread loads by its row cost 13 us a run); copies by TMA boxes, 206.
+//
+// Warps: 0 issues S, the next 16 (or 8) softmax and epilogue, four copy tiles into the ring, one issues P.V, one announces the
 // runs of tiles that the CTA's range consists of.
 #include <climits>
 #include <cmath>
@@ -34,10 +45,10 @@ namespace pmla8 {
 using namespace pgroups;
 
 constexpr int kTile = 64;
-constexpr int kGather = 4;  // warps that copy
+constexpr int kGather = 4;       // warps that copy
 constexpr float kRaise = 11.0f;  // log2 units: the running maximum is raised when a weight passes 2^11
 constexpr float kTop = 5.0f;     // a new maximum is 2^5
-constexpr float kMost = 2048.0f;
+constexpr float kMost = 2048.0f; // 2^kRaise
 constexpr float kLeast = 3.5527136788005009e-15f;  // 2^-48, the least s
 
 template <int DQK, int NH>
@@ -80,7 +91,8 @@ constexpr int M_STAT = M_RED + 1024;          // float [64]
 constexpr int M_COL = M_STAT + 256;           // float [2][64]: a column's factor of the score, by run
 constexpr int M_SCALE = M_COL + 512;          // float [kSlots][64]: s of the rows, -1: masked
 constexpr int M_MASKED = M_SCALE + kSlots * 256;  // uint8 [kSlots]: some row of a tile is masked
-static_assert(M_SEGE + 8 * kSegs <= M_TMEM && M_PLAN + 56 <= M_SEG && M_SEG % 16 == 0 && M_SCALE % 16 == 0 && M_MASKED + kSlots <= 4096, "misc layout");
+static_assert(M_SEGE + 8 * kSegs <= M_TMEM && M_PLAN + 56 <= M_SEG && M_SEG % 16 == 0 && M_SCALE % 16 == 0 &&
+                  M_MASKED + kSlots <= 4096, "misc layout");
 
 struct Params : GroupParams {
   const __nv_bfloat16* q;
@@ -241,7 +253,7 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
     return read_announcement(mb + M_SEGF, mb + M_SEGE, reinterpret_cast<const int4*>(misc + M_SEG), k, s_abort, p.wait_limit, s);
   };
   if (warp == 0) {
-    // ======================= S^T issuer =======================
+    // ======================= S issuer =======================
     constexpr uint32_t kIdS = ROWS ? idesc_f8(128, kTile, 0, 0, false, false) : idesc_f8(kTile, 2 * NH, 0, 0, false, false);
     constexpr uint32_t kIdR = ROWS ? idesc_bf16(128, kTile, false, false) : idesc_bf16(kTile, NH, false, false);
     int done = 0;
@@ -339,10 +351,11 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
     announce<kTile>(p, plan, mb + M_SEGF, mb + M_SEGE, reinterpret_cast<int4*>(misc + M_SEG), s_abort);
   } else if (warp > W) {
     // ======================= gather: 16 rows of every tile each =======================
-    // By cp.async, which takes any row, a warp's instruction the 512 codes of one (8 cycles; boxes of 128 bytes by TMA take as
-    // long as rows of bf16, since a row begins anywhere in a line), and says itself when it has landed; what is masked is
-    // filled with zeros.  A lane looks one row up, in steps whose loads have a tile's time to come back: the list's entry
-    // (three tiles ahead), the page (two ahead), the row number and its s (one ahead).
+    // By cp.async, which takes any row, a warp's instruction the 512 codes of one, and says itself when it has landed; what is
+    // masked is filled with zeros.  A lane looks one row up, in steps whose loads have a tile's time to come back: the list's
+    // entry (three tiles ahead), the page (two ahead), the row number (one ahead, and its lines are asked for in L2: without,
+    // 132 us in place of 125; runs of rows by bulk prefetch, 126).  s comes as a copy too: a load whose value moves from one
+    // register to another in the loop holds the warp up until it is there.
     constexpr int kRows = kTile / 4;
     const int gw = warp - W - 1;
     Seg sg;
@@ -486,7 +499,8 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const uint32_t at = raw_at(hh, lane + 32 * x);
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[x].x), "=r"(v[x].y), "=r"(v[x].z), "=r"(v[x].w) : "r"(at) : "memory");
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v[x].x), "=r"(v[x].y), "=r"(v[x].z), "=r"(v[x].w) : "r"(at) : "memory");
           top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[x].x & 0x7fff7fffu, v[x].y & 0x7fff7fffu),
                                        __vmaxu2(v[x].z & 0x7fff7fffu, v[x].w & 0x7fff7fffu)));
         }
@@ -508,8 +522,8 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
             lo[g] = e4m3x2(minus2(a, e4m3x2_floats(hi[g])));
           }
           const uint32_t at = sQ + (u >> 4) * L::Q_CHUNK + (u & 1) * 8;
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + sw128_off(q_row(hh, 0), (u & 15) >> 1)), "r"(hi[0] | hi[1] << 16), "r"(hi[2] | hi[3] << 16) : "memory");
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + sw128_off(q_row(hh, 1), (u & 15) >> 1)), "r"(lo[0] | lo[1] << 16), "r"(lo[2] | lo[3] << 16) : "memory");
+          st_shared_v2(at + sw128_off(q_row(hh, 0), (u & 15) >> 1), hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+          st_shared_v2(at + sw128_off(q_row(hh, 1), (u & 15) >> 1), lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
         }
       }
       fence_proxy_async_smem();
@@ -541,7 +555,7 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
       return v[0];
     };
     const int sum_row = n0 + (((lane >> 1) & 14) | (lane & 1)) % NQ;
-    // the running maxima of the half's rows, from those of the tile in s_red, and the factors of what has been summed so far
+    // the running maxima of the team's rows, from those of the tile in s_red, and the factors of what has been summed so far
     auto new_maxima = [&]() {
       if (qd == 0 && lane < NHH) {
         const int n = ch * NHH + lane;
@@ -581,7 +595,7 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
       float2 l_part[NQ / 2], m_neg[NQ / 2];
 #pragma unroll
       for (int j = 0; j < NQ / 2; ++j) { l_part[j] = make_float2(0.f, 0.f); m_neg[j] = make_float2(3.0e38f, 3.0e38f); }
-      if (qd == 0 && lane < NHH) s_stat[ch * NHH + lane] = -INFINITY;  // (read only after a barrier of the half)
+      if (qd == 0 && lane < NHH) s_stat[ch * NHH + lane] = -INFINITY;  // (read only after a barrier of the team)
       const float* col = s_col + ((seg - 1) & 1) * 64 + n0;
       float2 l_row = make_float2(0.f, 0.f);
       float neg = 3.0e38f, factor = 0.f;
@@ -599,178 +613,186 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
         tc_fence_after();
         __syncwarp();
         if constexpr (ROWS) {
-        if (t == sg.t0) factor = s_col[((seg - 1) & 1) * 64 + my_row];
-        uint32_t v[kKeys], x[kKeys], w[kKeys];  // scores before softmax_scale; e^z; the weights
-        const uint32_t ts = tmem_addr(tmem + sb * L::SW + ch * 16, qd * 32, 0);
-        tmem_ld16x32bx2(ts, v);
-        tmem_ld16x32bx2(ts + (16u << 16), x);
-        if constexpr (ROPE) tmem_ld16x32bx2(ts + kTile, w);
-        const float4 sa = lds4f(sScale + (sl * kTile + k0) * 4), sb4 = lds4f(sScale + (sl * kTile + k0) * 4 + 16);
-        const float2 s2[4] = {make_float2(sa.x, sa.y), make_float2(sa.z, sa.w), make_float2(sb4.x, sb4.y), make_float2(sb4.z, sb4.w)};
-        const bool some = s_masked[sl] || (p.topk_idx == nullptr && (t + 1) * (long long)kTile > sg.seen0);
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_sf + 8 * sb);
-        auto at2 = [](const uint32_t (&a)[kKeys], int j) { return make_float2(__uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1])); };
-        auto set2 = [](uint32_t (&a)[kKeys], int j, float2 y) { a[2 * j] = __float_as_uint(y.x); a[2 * j + 1] = __float_as_uint(y.y); };
-#pragma unroll
-        for (int j = 0; j < kKeys / 2; ++j) {
-          const float2 sum = mul2(add2(at2(v, j), at2(x, j)), s2[j]), by = make_float2(factor, factor);
-          set2(v, j, ROPE ? fma2(sum, by, at2(w, j)) : mul2(sum, by));
-        }
-        if (t + 1 == t_end && more && !bad) load_q(nx, seg);  // S of the segment is done: Q is free
-        auto hidden = [&](int j) {
-          return (j & 1 ? s2[j / 2].y : s2[j / 2].x) < 0.f || (p.topk_idx == nullptr && t * kTile + k0 + j >= seen);
-        };
-        auto weights = [&]() -> float {
-#pragma unroll
-          for (int j = 0; j < kKeys / 2; ++j) {
-            const float2 e = fma2(at2(v, j), make_float2(p.sl2e, p.sl2e), make_float2(neg, neg));
-            const float2 y = make_float2(ex2(e.x), ex2(e.y));
-            set2(x, j, y);
-            set2(w, j, mul2(y, s2[j]));
-          }
-          if (some) {
-#pragma unroll
-            for (int j = 0; j < kKeys; ++j)
-              if (hidden(j)) x[j] = w[j] = 0;
-          }
-          float most = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < kKeys; ++j) most = fmaxf(most, __uint_as_float(w[j]));
-          return most;
-        };
-        const bool mine = weights() > kMost || t == sg.t0;
-        if (named_bar_or(bar_id, kTeam, mine || bad)) {
-          if (named_bar_or(bar_id, kTeam, bad)) { aborted = true; break; }
-          float top = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < kKeys; ++j) {
-            const float s = j & 1 ? s2[j / 2].y : s2[j / 2].x;
-            const float z = __uint_as_float(v[j]) * p.sl2e + (float)((int)(__float_as_uint(s) >> 23) - 127);
-            if (s > 0.f && !(some && hidden(j))) top = fmaxf(top, z);
-          }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          if (lane < 16) s_red[ch * NH + my_row] = top;
-          named_bar(bar_id, kTeam);
-          new_maxima();
-          named_bar(bar_id, kTeam);
-          l_row = mul2(l_row, make_float2(s_fac[my_row], s_fac[my_row]));
-          neg = -fmaxf(s_stat[my_row], -3.0e38f);
-          weights();
-          if (t > sg.t0) {
-            const bool okw = wait_pv(i - 1, 3);
-            if (named_bar_or(bar_id, kTeam, !okw)) { aborted = true; break; }
-            tc_fence_after();
-            rescale();
-          }
-        }
-        uint32_t hi[2], lo[2];
-#pragma unroll
-        for (int j = 0; j < kKeys / 2; j += 2) {
-          l_row = add2(l_row, add2(at2(x, j), at2(x, j + 1)));
-          const uint32_t h0 = e5m2x2(at2(w, j)), h1 = e5m2x2(at2(w, j + 1));
-          hi[j / 2] = h0 | h1 << 16;
-          lo[j / 2] = e4m3x2(minus2(at2(w, j), e5m2x2_floats(h0))) | e4m3x2(minus2(at2(w, j + 1), e5m2x2_floats(h1))) << 16;
-        }
-        const uint32_t to = sP + (i & 1) * L::P_BLOCK + (k0 & 8);
-        st_shared_v2(to + sw128_off(my_row, ch), hi[0], hi[1]);
-        st_shared_v2(to + sw128_off(my_row, 4 + ch), lo[0], lo[1]);
-        } else {
-        uint32_t raw[NQ];
-        float2 z[NQ / 2];  // (alternate columns of the half first)
-        const uint32_t ts = tmem_addr(tmem + sb * L::SW + ch * NHH, qd * 32, 0);
-        {
-          uint32_t lo[NQ], pos[NQ];
-          tmem_ld16x64b(ts, raw);
-          tmem_ld16x64b(ts + NH, lo);
-          if constexpr (ROPE) tmem_ld16x64b(ts + 2 * NH, pos);
+          if (t == sg.t0) factor = s_col[((seg - 1) & 1) * 64 + my_row];
+          uint32_t v[kKeys], x[kKeys], w[kKeys];  // scores before softmax_scale; e^z; the weights
+          const uint32_t ts = tmem_addr(tmem + sb * L::SW + ch * 16, qd * 32, 0);
+          tmem_ld16x32bx2(ts, v);
+          tmem_ld16x32bx2(ts + (16u << 16), x);
+          if constexpr (ROPE) tmem_ld16x32bx2(ts + kTile, w);
+          const uint32_t scales = sScale + (sl * kTile + k0) * 4;
+          const float4 sx = lds4f(scales), sy = lds4f(scales + 16);
+          const float2 s2[kKeys / 2] = {{sx.x, sx.y}, {sx.z, sx.w}, {sy.x, sy.y}, {sy.z, sy.w}};
+          const bool some = s_masked[sl] || (p.topk_idx == nullptr && (t + 1) * (long long)kTile > sg.seen0);
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_sf + 8 * sb);
-#pragma unroll
-          for (int j = 0; j < NQ; ++j) raw[j] = __float_as_uint(__uint_as_float(raw[j]) + __uint_as_float(lo[j]));
-          // -> NQ consecutive rows: swap half of them with the key's other thread
-          auto rows_of = [&](uint32_t (&x)[NQ], int j) {
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, par ? x[j] : x[NQ / 2 + j], 2);
-            return make_float2(__uint_as_float(par ? got : x[j]), __uint_as_float(par ? x[NQ / 2 + j] : got));
+          auto at2 = [](const uint32_t (&a)[kKeys], int j) {
+            return make_float2(__uint_as_float(a[2 * j]), __uint_as_float(a[2 * j + 1]));
           };
-          const float s = scale_of(sl * kTile + r), log_s0 = s > 0.f ? (float)((int)(__float_as_uint(s) >> 23) - 127) : 0.f;
+          auto set2 = [](uint32_t (&a)[kKeys], int j, float2 y) {
+            a[2 * j] = __float_as_uint(y.x);
+            a[2 * j + 1] = __float_as_uint(y.y);
+          };
+#pragma unroll
+          for (int j = 0; j < kKeys / 2; ++j) {
+            const float2 sum = mul2(add2(at2(v, j), at2(x, j)), s2[j]), by = make_float2(factor, factor);
+            set2(v, j, ROPE ? fma2(sum, by, at2(w, j)) : mul2(sum, by));
+          }
+          if (t + 1 == t_end && more && !bad) load_q(nx, seg);  // S of the segment is done: Q is free
+          auto hidden = [&](int j) {
+            return (j & 1 ? s2[j / 2].y : s2[j / 2].x) < 0.f || (p.topk_idx == nullptr && t * kTile + k0 + j >= seen);
+          };
+          auto weights = [&]() -> float {
+#pragma unroll
+            for (int j = 0; j < kKeys / 2; ++j) {
+              const float2 e = fma2(at2(v, j), make_float2(p.sl2e, p.sl2e), make_float2(neg, neg));
+              const float2 y = make_float2(ex2(e.x), ex2(e.y));
+              set2(x, j, y);
+              set2(w, j, mul2(y, s2[j]));
+            }
+            if (some) {
+#pragma unroll
+              for (int j = 0; j < kKeys; ++j)
+                if (hidden(j)) x[j] = w[j] = 0;
+            }
+            float most = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < kKeys; ++j) most = fmaxf(most, __uint_as_float(w[j]));
+            return most;
+          };
+          const bool mine = weights() > kMost || t == sg.t0;
+          if (named_bar_or(bar_id, kTeam, mine || bad)) {
+            if (named_bar_or(bar_id, kTeam, bad)) { aborted = true; break; }
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < kKeys; ++j) {
+              const float s = j & 1 ? s2[j / 2].y : s2[j / 2].x;
+              const float z = __uint_as_float(v[j]) * p.sl2e + (float)((int)(__float_as_uint(s) >> 23) - 127);
+              if (s > 0.f && !(some && hidden(j))) top = fmaxf(top, z);
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            if (lane < 16) s_red[ch * NH + my_row] = top;
+            named_bar(bar_id, kTeam);
+            new_maxima();
+            named_bar(bar_id, kTeam);
+            l_row = mul2(l_row, make_float2(s_fac[my_row], s_fac[my_row]));
+            neg = -fmaxf(s_stat[my_row], -3.0e38f);
+            weights();
+            if (t > sg.t0) {
+              const bool okw = wait_pv(i - 1, 3);
+              if (named_bar_or(bar_id, kTeam, !okw)) { aborted = true; break; }
+              tc_fence_after();
+              rescale();
+            }
+          }
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int j = 0; j < kKeys / 2; j += 2) {
+            l_row = add2(l_row, add2(at2(x, j), at2(x, j + 1)));
+            const uint32_t h0 = e5m2x2(at2(w, j)), h1 = e5m2x2(at2(w, j + 1));
+            hi[j / 2] = h0 | h1 << 16;
+            lo[j / 2] = e4m3x2(minus2(at2(w, j), e5m2x2_floats(h0))) |
+                        e4m3x2(minus2(at2(w, j + 1), e5m2x2_floats(h1))) << 16;
+          }
+          const uint32_t to = sP + (i & 1) * L::P_BLOCK + (k0 & 8);
+          st_shared_v2(to + sw128_off(my_row, ch), hi[0], hi[1]);
+          st_shared_v2(to + sw128_off(my_row, 4 + ch), lo[0], lo[1]);
+        } else {
+          uint32_t raw[NQ];
+          float2 z[NQ / 2];  // (alternate columns of the half first)
+          const uint32_t ts = tmem_addr(tmem + sb * L::SW + ch * NHH, qd * 32, 0);
+          {
+            uint32_t lo[NQ], pos[NQ];
+            tmem_ld16x64b(ts, raw);
+            tmem_ld16x64b(ts + NH, lo);
+            if constexpr (ROPE) tmem_ld16x64b(ts + 2 * NH, pos);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_sf + 8 * sb);
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) raw[j] = __float_as_uint(__uint_as_float(raw[j]) + __uint_as_float(lo[j]));
+            // -> NQ consecutive rows: swap half of them with the key's other thread
+            auto rows_of = [&](uint32_t (&x)[NQ], int j) {
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, par ? x[j] : x[NQ / 2 + j], 2);
+              return make_float2(__uint_as_float(par ? got : x[j]), __uint_as_float(par ? x[NQ / 2 + j] : got));
+            };
+            const float s = scale_of(sl * kTile + r);
+            const float log_s0 = s > 0.f ? (float)((int)(__float_as_uint(s) >> 23) - 127) : 0.f;
+#pragma unroll
+            for (int j = 0; j < NQ / 2; ++j) {
+              const float2 f = mul2(*reinterpret_cast<const float2*>(col + 2 * j), make_float2(s, s));
+              float2 c = make_float2(log_s0, log_s0);
+              if constexpr (ROPE) c = fma2(rows_of(pos, j), make_float2(p.sl2e, p.sl2e), c);
+              z[j] = fma2(rows_of(raw, j), f, c);
+            }
+          }
+          if (t + 1 == t_end && more && !bad) load_q(nx, seg);  // S^T of the segment is done: Q is free
+          const float s = scale_of(sl * kTile + r);
+          const float inv_s = s > 0.f ? pow2(127 - (int)(__float_as_uint(s) >> 23)) : 1.f;
+          const int pos = t * kTile + r;
+          if (s < 0.f) {
+#pragma unroll
+            for (int j = 0; j < NQ / 2; ++j) z[j] = make_float2(-INFINITY, -INFINITY);
+          } else if (p.topk_idx == nullptr && (t + 1) * (long long)kTile > sg.seen0) {  // some token may not see all of it
+            int seen = sg.seen0 + tok0, left = head_left;
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) {
+              if (pos >= seen) (j & 1 ? z[j / 2].y : z[j / 2].x) = -INFINITY;
+              if (--left == 0) { left = p.H; ++seen; }
+            }
+          }
+          // the exponents of the weights; one may pass its row's maximum by the threshold
+          float2 e[NQ / 2];
+          bool mine = t == sg.t0;
 #pragma unroll
           for (int j = 0; j < NQ / 2; ++j) {
-            const float2 f = mul2(*reinterpret_cast<const float2*>(col + 2 * j), make_float2(s, s));
-            float2 c = make_float2(log_s0, log_s0);
-            if constexpr (ROPE) c = fma2(rows_of(pos, j), make_float2(p.sl2e, p.sl2e), c);
-            z[j] = fma2(rows_of(raw, j), f, c);
+            e[j] = add2(z[j], m_neg[j]);
+            mine |= e[j].x > kRaise || e[j].y > kRaise;
           }
-        }
-        if (t + 1 == t_end && more && !bad) load_q(nx, seg);  // S^T of the segment is done: Q is free
-        const float s = scale_of(sl * kTile + r);
-        const float inv_s = s > 0.f ? pow2(127 - (int)(__float_as_uint(s) >> 23)) : 1.f;
-        const int pos = t * kTile + r;
-        if (s < 0.f) {
+          bool raise = false;
+          if (named_bar_or(bar_id, kTeam, mine || bad)) {
+            if (named_bar_or(bar_id, kTeam, bad)) { aborted = true; break; }
+            raise = true;
+          }
+          if (raise) {
+            float top[NQ];
 #pragma unroll
-          for (int j = 0; j < NQ / 2; ++j) z[j] = make_float2(-INFINITY, -INFINITY);
-        } else if (p.topk_idx == nullptr && (t + 1) * (long long)kTile > sg.seen0) {  // some token may not see all of it
-          int seen = sg.seen0 + tok0, left = head_left;
+            for (int j = 0; j < NQ / 2; ++j) { top[2 * j] = z[j].x; top[2 * j + 1] = z[j].y; }
+            s_red[qd * NH + sum_row] = over_keys(top, true);
+            named_bar(bar_id, kTeam);
+            new_maxima();
+            named_bar(bar_id, kTeam);
+#pragma unroll
+            for (int j = 0; j < NQ / 2; ++j) {
+              l_part[j] = mul2(l_part[j], make_float2(s_fac[n0 + 2 * j], s_fac[n0 + 2 * j + 1]));
+              m_neg[j] = make_float2(-fmaxf(s_stat[n0 + 2 * j], -3.0e38f), -fmaxf(s_stat[n0 + 2 * j + 1], -3.0e38f));
+              e[j] = add2(z[j], m_neg[j]);
+            }
+            if (t > sg.t0) {
+              const bool okw = wait_pv(i - 1, 3);
+              if (named_bar_or(bar_id, kTeam, !okw)) { aborted = true; break; }
+              tc_fence_after();
+              rescale();
+            }
+          }
+          uint32_t hi[NQ / 2], lo[NQ / 2];
+#pragma unroll
+          for (int j = 0; j < NQ / 2; ++j) {
+            const float2 w = make_float2(ex2(e[j].x), ex2(e[j].y));
+            l_part[j] = fma2(w, make_float2(inv_s, inv_s), l_part[j]);
+            hi[j] = e5m2x2(w);
+            lo[j] = e4m3x2(minus2(w, e5m2x2_floats(hi[j])));
+          }
+          const uint32_t to = sP + (i & 1) * L::P_BLOCK;
 #pragma unroll
           for (int j = 0; j < NQ; ++j) {
-            if (pos >= seen) (j & 1 ? z[j / 2].y : z[j / 2].x) = -INFINITY;
-            if (--left == 0) { left = p.H; ++seen; }
+            const int n = n0 + j;
+            const uint32_t at = to + (uint32_t)(n * 128 + (((r >> 4) ^ (n & 7)) << 4) + (r & 15));
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(hi[j / 2] >> (8 * (j & 1))) : "memory");
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + NH * 128), "r"(lo[j / 2] >> (8 * (j & 1))) : "memory");
           }
-        }
-        // the exponents of the weights; one may pass its row's maximum by the threshold
-        float2 e[NQ / 2];
-        bool mine = t == sg.t0;
-#pragma unroll
-        for (int j = 0; j < NQ / 2; ++j) {
-          e[j] = add2(z[j], m_neg[j]);
-          mine |= e[j].x > kRaise || e[j].y > kRaise;
-        }
-        bool raise = false;
-        if (named_bar_or(bar_id, kTeam, mine || bad)) {
-          if (named_bar_or(bar_id, kTeam, bad)) { aborted = true; break; }
-          raise = true;
-        }
-        if (raise) {
-          float top[NQ];
-#pragma unroll
-          for (int j = 0; j < NQ / 2; ++j) { top[2 * j] = z[j].x; top[2 * j + 1] = z[j].y; }
-          s_red[qd * NH + sum_row] = over_keys(top, true);
-          named_bar(bar_id, kTeam);
-          new_maxima();
-          named_bar(bar_id, kTeam);
-#pragma unroll
-          for (int j = 0; j < NQ / 2; ++j) {
-            l_part[j] = mul2(l_part[j], make_float2(s_fac[n0 + 2 * j], s_fac[n0 + 2 * j + 1]));
-            m_neg[j] = make_float2(-fmaxf(s_stat[n0 + 2 * j], -3.0e38f), -fmaxf(s_stat[n0 + 2 * j + 1], -3.0e38f));
-            e[j] = add2(z[j], m_neg[j]);
-          }
-          if (t > sg.t0) {
-            const bool okw = wait_pv(i - 1, 3);
-            if (named_bar_or(bar_id, kTeam, !okw)) { aborted = true; break; }
-            tc_fence_after();
-            rescale();
-          }
-        }
-        uint32_t hi[NQ / 2], lo[NQ / 2];
-#pragma unroll
-        for (int j = 0; j < NQ / 2; ++j) {
-          const float2 w = make_float2(ex2(e[j].x), ex2(e[j].y));
-          l_part[j] = fma2(w, make_float2(inv_s, inv_s), l_part[j]);
-          hi[j] = e5m2x2(w);
-          lo[j] = e4m3x2(minus2(w, e5m2x2_floats(hi[j])));
-        }
-        const uint32_t to = sP + (i & 1) * L::P_BLOCK;
-#pragma unroll
-        for (int j = 0; j < NQ; ++j) {
-          const int n = n0 + j;
-          const uint32_t at = to + (uint32_t)(n * 128 + (((r >> 4) ^ (n & 7)) << 4) + (r & 15));
-          asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(hi[j / 2] >> (8 * (j & 1))) : "memory");
-          asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + NH * 128), "r"(lo[j / 2] >> (8 * (j & 1))) : "memory");
-        }
         }
         fence_proxy_async_smem();
         tc_fence_before();

@@ -12,11 +12,23 @@
 // rows' scales are.  The denominator adds w_p / s_p in fp32.  A query row is divided by a power of two so that its
 // largest channel lies in [2^14, 2^15): the channels that this takes out of fp16 are below 2^-38 of that one.
 //
-// Split of the work as in dsa_paged_groups.cuh, with tiles of 96 positions and groups of NH = 16 or 64 columns.
-// A tile: two warps copy its rows as they are to shared memory; 12 warps take the codes from there to registers, form
-// fp16 and write it twice: to TMEM, position by lane, as the A operand of S^T[position, column] = V Q^T, and to shared
-// memory as the A operand of O^T[channel, column] += V^T W^T, 128 channels at a time as P.V of the tile before is done
-// with them.  Then the same warps do the softmax, a position a thread.
+// Split of the work as in dsa_paged_groups.cuh, with tiles of 96 positions and groups of NH = 64 columns, or of 16 while all
+// rows of a request (or a list) fit.  A tile: two warps copy its rows as they are to shared memory; 12 warps take the codes from
+// there to registers and form fp16, which is the A operand of S^T[position, column] = V Q^T and, as V^T, of O^T[channel, column]
+// += V^T W^T.  Three quarters of the channels are written to TMEM, position by lane, before P.V of the tile before has left
+// shared memory; the last quarter to shared memory, from where both products read it; then the three quarters there too, while
+// S^T is under way.  Then the same warps do the softmax, a position a thread.  96 positions, since an fp16 tile of 128, its
+// queries and W leave no room for the next tile's rows as they come.
+//
+// A thread's four blocks of 16 channels lie side by side in a row (one load for four scales), but 16 channels apart in every
+// 128 of the products: O^T's row 128 m + 16 y + e is channel 64 y + 16 m + e, and the queries' channels follow.
+//
+// What bounds it: 64 requests of 4000 to 16384 positions, 64 heads: 161 us, where the same over bf16 rows of 2.7 times the
+// bytes takes 159 and over 8 bits (dsa_paged_mla_e4m3.cu, which converts nothing) 125.  A tile takes about 5700 cycles, of which
+// the warps convert for 3300 and do the softmax for 1500; shared memory moves 424 KB (rows in and out 84, V in and out 192, W
+// 60, queries 88), 3400 cycles at 128 bytes each.  One group after the other costs what overlap would save: with 64 registers
+// a thread and twice the warps 209 us, the next tile's rows in registers during the softmax 171, loads by the converting
+// warps themselves 190 and more.
 //
 // Warps: three of four convert and do softmax and epilogue (they reach the TMEM lanes 0-95); of the others one issues the
 // products, one announces the runs of tiles, two copy.
@@ -78,7 +90,8 @@ constexpr int M_RED = 1360;                                 // float [3][64]
 constexpr int M_STAT = 2128;                                // float [64]
 constexpr int M_SCL = 2384;                                 // float [64]: factors of a rescale
 constexpr int M_OUT = 2640;                                 // float [2][64]: factors of the output, by run
-static_assert(M_SEGE + 8 * kSegs <= M_TMEM && M_PLAN + 56 <= M_SEG && M_OUT + 512 <= M_FAC && M_FLAG + 32 <= M_VALID && M_VALID + kTile <= 3584, "misc layout");
+static_assert(M_SEGE + 8 * kSegs <= M_TMEM && M_PLAN + 56 <= M_SEG && M_OUT + 512 <= M_FAC && M_FLAG + 32 <= M_VALID &&
+                  M_VALID + kTile <= 3584, "misc layout");
 
 struct Params : GroupParams {
   const __nv_bfloat16* q;
@@ -112,7 +125,9 @@ __device__ __forceinline__ void tmem_ld(uint32_t a, uint32_t (&r)[N]) {
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t a, const uint32_t (&r)[N]) {
   if constexpr (N == 16) tmem_st16(a, r);
-  else asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+  else
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]) : "memory");
 }
 
 // Four MMAs on consecutive 16-element steps of K, A in TMEM (8 columns a step), issued by one elected lane (as mma4_w).
