@@ -164,3 +164,39 @@ def test_the_binding_refuses_other_shapes():
             bad()
     with pytest.raises(dsa.DsaError):
         dsa.dsa_paged_quantize(x, c[:3], 8)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_many_rows_of_many_requests_are_read_back(bits):
+    # enough rows for the wider blocks, requests of none in between, and rows of out that are no request's
+    D, Q, page = 72, 64, 16
+    g = torch.Generator().manual_seed(bits)
+    lens = torch.randint(0, 290, (420,), generator=g)
+    lens[torch.rand(420, generator=g) < 0.2] = 0
+    lens[100:140] = 0
+    need = (lens + page - 1) // page
+    pages = int(need.sum())
+    perm = torch.randperm(pages, generator=g).to(torch.int32)
+    table = torch.full((420, int(need.max())), -1, dtype=torch.int32)
+    at = 0
+    for b in range(420):
+        table[b, :need[b]] = perm[at:at + int(need[b])]
+        at += int(need[b])
+    cache = torch.zeros(pages, page, dsa.paged_quant_row_bytes(D, bits, Q), dtype=torch.uint8, device=DEV)
+    x = torch.randn(pages * page, D, generator=g).bfloat16().to(DEV)
+    dsa.dsa_paged_quantize(x, cache, bits, quant_dim=Q)
+    cu = torch.zeros(421, dtype=torch.int32)
+    cu[1:] = lens.cumsum(0)
+    cu += 7
+    N = int(cu[-1]) + 9
+    assert N > 64 * 4 * 152
+    out = torch.full((N, D), 5.0, dtype=torch.bfloat16, device=DEV)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    dsa.dsa_paged_dequantize(cache, table.to(DEV), cu.to(DEV), bits, D, quant_dim=Q, out=out, workspace=ws)
+    assert dsa.dsa_read_device_status(ws) == 0
+    rows = torch.cat([table[b, torch.arange(int(lens[b])) // page].long() * page + torch.arange(int(lens[b])) % page
+                      for b in range(420)])
+    want = ref.decode(cache.view(-1, cache.shape[2])[rows.to(DEV)], D, Q, bits)
+    got = out.cpu().double()
+    assert bool((got[:7] == 5).all()) and bool((got[N - 9:] == 5).all())
+    assert torch.equal(got[7:N - 9], want)
