@@ -22,7 +22,7 @@
 //  - O^T[channel, row] += V^T W^T (M = 128 channels, K = 32 keys, hi and then lo into the same columns).  The codes of 128
 //    channels of a key are a row of 128 bytes, which is K-major for the first product and M-major for the second.
 //
-// What bounds it: 64 requests of 4000 to 16384 positions, 64 heads: 125 us, of which 10 pass before the first scores (cutting
+// What bounds it: 64 requests of 4000 to 16384 positions, 64 heads: 122 us, of which 10 pass before the first scores (cutting
 // the line, the queries), 15 with the launches and the joining; the 430 MB of rows are read at 4.3 TB/s in between, where a copy
 // reaches 6.8.  A tile's place in the ring (three tiles of 40 KB beside 64 KB of queries) is in use for 6900 cycles: 1700 for
 // its copies, 1700 for S, 2200 for the softmax, 1000 for P.V, the two products sharing shared memory's 128 bytes a cycle (216
@@ -888,7 +888,9 @@ dsa_status_t launch(Params& p, int ctas, cudaStream_t s) {
                                           "configuring paged_mla_e4m3_kernel");
   if (st != DSA_OK) return st;
   p.G = p.topk_idx ? 1 : (p.H <= NH ? NH / p.H : 1);
-  p.extra = p.topk_idx ? 2 : 4;
+  // (queries, a pipeline that runs dry and the sums: as long as six tiles.  64 x 16384: 122.5 us, with 4 124.4, with 2 125.5; 48
+  // lists of 2048: 42.9, with 4 43.4, with 2 47.1)
+  p.extra = 6;
   p.HB = (p.H + NH - 1) / NH;
   paged_mla_e4m3_kernel<DQK, NH><<<ctas, L::THREADS, L::TOTAL, s>>>(p);
   return cuda_check(cudaGetLastError(), "launching paged_mla_e4m3_kernel");

@@ -24,7 +24,7 @@
 // 128 of the products: O^T's row 128 m + 16 y + e is channel 64 y + 16 m + e, and the queries' channels follow.
 //
 // What bounds it: 64 requests of 4000 to 16384 positions, 64 heads: 161 us, where the same over bf16 rows of 2.7 times the
-// bytes takes 159 and over 8 bits (dsa_paged_mla_e4m3.cu, which converts nothing) 125.  A tile takes about 5700 cycles, of which
+// bytes takes 159 and over 8 bits (dsa_paged_mla_e4m3.cu, which converts nothing) 122.  A tile takes about 5700 cycles, of which
 // the warps convert for 3300 and do the softmax for 1500; shared memory moves 424 KB (rows in and out 84, V in and out 192, W
 // 60, queries 88), 3400 cycles at 128 bytes each.  One group after the other costs what overlap would save: with 64 registers
 // a thread and twice the warps 209 us, the next tile's rows in registers during the softmax 171, loads by the converting
@@ -938,7 +938,8 @@ dsa_status_t launch(Params& p, int ctas, cudaStream_t s) {
                                           "configuring paged_mla_quant_kernel");
   if (st != DSA_OK) return st;
   p.G = p.topk_idx ? 1 : (p.H <= NH ? NH / p.H : 1);
-  p.extra = 2;
+  // (64 x 16384, 64 heads: 161 us with 2 to 4, 164 with 1; 96 x 4097, 8 heads: 61.9 with 1, 62.7 with 2, 65 with 4)
+  p.extra = NH == 16 ? 1 : 2;
   p.HB = (p.H + NH - 1) / NH;
   paged_mla_quant_kernel<DQK, NH><<<ctas, kThreads, L::TOTAL, s>>>(p);
   return cuda_check(cudaGetLastError(), "launching paged_mla_quant_kernel");
