@@ -22,9 +22,9 @@
 //  - O^T[channel, row] += V^T W^T (M = 128 channels, K = 32 keys, hi and then lo into the same columns).  The codes of 128
 //    channels of a key are a row of 128 bytes, which is K-major for the first product and M-major for the second.
 //
-// What bounds it: 64 requests of 4000 to 16384 positions, 64 heads: 122 us, of which 10 pass before the first scores (cutting
+// What bounds it: 64 requests of 4000 to 16384 positions, 64 heads: 121 us, of which 10 pass before the first scores (cutting
 // the line, the queries), 15 with the launches and the joining; the 430 MB of rows are read at 4.3 TB/s in between, where a copy
-// reaches 6.8.  A tile's place in the ring (three tiles of 40 KB beside 64 KB of queries) is in use for 6900 cycles: 1700 for
+// reaches 6.8.  A tile's place in the ring (three tiles of 40 KB beside 80 KB of queries) is in use for 6900 cycles: 1700 for
 // its copies, 1700 for S, 2200 for the softmax, 1000 for P.V, the two products sharing shared memory's 128 bytes a cycle (216
 // KB a tile).  Measured beside it: the same rows converted to fp16 as the 4-bit kernel does, 220 us; queries in TMEM and four
 // tiles in the ring, 136 (queries that a thread loads by its row cost 13 us a run); copies by TMA boxes, 206.
@@ -72,7 +72,7 @@ struct Smem {
   static constexpr int OFF_Q = R * NCH * CHUNK;
   static constexpr int OFF_P = OFF_Q + 4 * Q_CHUNK + (ROPE ? QR_CHUNK : 0);
   static constexpr int OFF_MISC = OFF_P + 2 * P_BLOCK;
-  static constexpr int MISC = 4096;
+  static constexpr int MISC = 8192;
   static constexpr int TOTAL = OFF_MISC + MISC;
   static_assert(TOTAL <= 232448 && OFF_P % 1024 == 0 && P_BLOCK % 1024 == 0, "shared memory budget");
   static constexpr int TM_O = (2 * SW + 31) / 32 * 32;
@@ -90,9 +90,10 @@ constexpr int M_RED = 688;                    // float [4][64]; the first row al
 constexpr int M_STAT = M_RED + 1024;          // float [64]
 constexpr int M_COL = M_STAT + 256;           // float [2][64]: a column's factor of the score, by run
 constexpr int M_SCALE = M_COL + 512;          // float [kSlots][64]: s of the rows, -1: masked
+constexpr int M_RAW = 4096;                   // float4 [kSlots][64]: s of the rows as it comes, -1: masked
 constexpr int M_MASKED = M_SCALE + kSlots * 256;  // uint8 [kSlots]: some row of a tile is masked
 static_assert(M_SEGE + 8 * kSegs <= M_TMEM && M_PLAN + 56 <= M_SEG && M_SEG % 16 == 0 && M_SCALE % 16 == 0 &&
-                  M_MASKED + kSlots <= 4096, "misc layout");
+                  M_MASKED + kSlots <= M_RAW, "misc layout");
 
 struct Params : GroupParams {
   const __nv_bfloat16* q;
@@ -136,10 +137,6 @@ __device__ __forceinline__ void mma_f8_w(uint32_t d_tmem, uint64_t a, uint64_t b
         "l"(a), "l"(b), "r"(idesc), "r"(add_first), "n"(SA), "n"(SB)
         : "memory");
   }
-}
-
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // Two values to e4m3 or e5m2 (the first in the lower half), and e5m2 back.
@@ -198,10 +195,11 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc + M_TMEM);
   volatile int* s_abort = reinterpret_cast<volatile int*>(misc + M_ABORT);
   Plan* s_plan = reinterpret_cast<Plan*>(misc + M_PLAN);
-  const uint32_t sScale = smem_u32(misc + M_SCALE);
+  const uint32_t sScale = smem_u32(misc + M_SCALE), sRaw = smem_u32(misc + M_RAW);
+  volatile float* s_raw = reinterpret_cast<volatile float*>(misc + M_RAW);
   volatile float* s_scale = reinterpret_cast<volatile float*>(misc + M_SCALE);
   auto scale_of = [&](int at) {  // (a row that was never written, of zero bytes, holds zeros; -1: masked)
-    const float s = s_scale[at];
+    const float s = s_raw[4 * at];
     return s >= 0.f && s < kLeast ? kLeast : s;
   };
   volatile uint8_t* s_masked = misc + M_MASKED;
@@ -354,8 +352,10 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
     // By cp.async, which takes any row, a warp's instruction the 512 codes of one, and says itself when it has landed; what is
     // masked is filled with zeros.  A lane looks one row up, in steps whose loads have a tile's time to come back: the list's
     // entry (three tiles ahead), the page (two ahead), the row number (one ahead, and its lines are asked for in L2: without,
-    // 132 us in place of 125; runs of rows by bulk prefetch, 126).  s comes as a copy too: a load whose value moves from one
-    // register to another in the loop holds the warp up until it is there.
+    // 132 us in place of 125; runs of rows by bulk prefetch, 126).  s comes as a copy too, of its 16 bytes (four would go through
+    // L1: 122.5 us in place of 121): a load whose value moves from one register to another in the loop holds the warp up until it
+    // is there.  L2 gives 995 bytes a row, since eight lanes' 128 bytes begin anywhere in a line; eight lanes a line of their own
+    // took 124.
     constexpr int kRows = kTile / 4;
     const int gw = warp - W - 1;
     Seg sg;
@@ -426,8 +426,8 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
       if (i >= R && !warp_all(wait_pv(i - R, 3))) { stop = true; break; }
       if (lane < kRows) {
         const int r = sl * kTile + gw * kRows + lane;
-        if (row[0] < 0) s_scale[r] = -1.f;
-        else cp_async4(sScale + 4 * r, p.cache + (size_t)row[0] * L::LAY.bytes + L::LAY.scale);
+        if (row[0] < 0) s_raw[4 * r] = -1.f;
+        else cp_async16(sRaw + 16 * r, p.cache + (size_t)row[0] * L::LAY.bytes + L::LAY.scale, 16);
       }
       const uint32_t to = sKV + sl * NCH * L::CHUNK;
 #pragma unroll

@@ -24,7 +24,7 @@
 // 128 of the products: O^T's row 128 m + 16 y + e is channel 64 y + 16 m + e, and the queries' channels follow.
 //
 // What bounds it: 64 requests of 4000 to 16384 positions, 64 heads: 161 us, where the same over bf16 rows of 2.7 times the
-// bytes takes 159 and over 8 bits (dsa_paged_mla_e4m3.cu, which converts nothing) 122.  A tile takes about 5700 cycles, of which
+// bytes takes 159 and over 8 bits (dsa_paged_mla_e4m3.cu, which converts nothing) 121.  A tile takes about 5700 cycles, of which
 // the warps convert for 3300 and do the softmax for 1500; shared memory moves 424 KB (rows in and out 84, V in and out 192, W
 // 60, queries 88), 3400 cycles at 128 bytes each.  One group after the other costs what overlap would save: with 64 registers
 // a thread and twice the warps 209 us, the next tile's rows in registers during the softmax 171, loads by the converting
