@@ -677,8 +677,9 @@ dsa_status_t dsa_paged_dequantize(const uint8_t* cache, const int32_t* block_tab
  *  bits         8 or 4
  *  workspace    >= dsa_paged_mla_quant_workspace_size() bytes, whatever the sizes
  * A row whose s is NaN makes the tokens NaN that see it and no other; a row of zero bytes, which nothing
- * was written to, holds zeros.  A query with a channel that is not finite gives its row of out and lse
- * values that are not finite, and touches no other.  num_pages * page_size < 2^31.  The result does not
+ * was written to, holds zeros.  A query with a channel that is not finite touches no row of out and lse
+ * but its own (8 bits: that becomes NaN if the channel is among the first 512).  4 bits: position channels
+ * count divided by s, and overflow above 2^127 s.  num_pages * page_size < 2^31.  The result does not
  * depend on timing: equal calls on equal devices give equal bits.
  */
 size_t dsa_paged_mla_quant_workspace_size(void);
