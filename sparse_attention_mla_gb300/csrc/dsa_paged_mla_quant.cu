@@ -74,7 +74,7 @@ struct Smem {
 };
 
 // misc (bytes)
-constexpr int M_LAND = 0;      // [2]: S^T's operand is there: 384 channels in TMEM, the others in shared memory
+constexpr int M_LAND = 0;      // [3]: S^T's operand is there: 256 channels in TMEM, the last 128 in shared memory, the others in TMEM
 constexpr int M_PV = 40;       // P.V is done
 constexpr int M_S = 88, M_P = 96, M_Q = 104, M_FIN = 112;
 constexpr int M_RAW = 120, M_READ = 128;                    // a tile's rows have come, have been read
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
   // rows that follow one another in pages of some size come by copies of whole runs, others one by one
   const bool runs = p.topk_idx == nullptr && p.P >= 16;
   if (threadIdx.x == 0) {
-    for (int k = 0; k < 2; ++k) mbar_init(mb + M_LAND + 8 * k, kWorkers);
+    for (int k = 0; k < 3; ++k) mbar_init(mb + M_LAND + 8 * k, kWorkers);
     mbar_init(mb + M_PV, 1);
     mbar_init(mb + M_FIN, 1);
     mbar_init(mb + M_S, 1);
@@ -319,21 +319,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
 #pragma unroll 1
       for (int k0 = 0; k0 < n; ++k0, ++i) {
         const uint64_t b0 = sdesc_sw128(q0, 16, 1024);
-        if (!wait(M_LAND, i & 1)) { stop = true; break; }
-        tc_fence_after();
-#pragma unroll
-        for (int m = 0; m < 3; ++m) {
+        auto from_tmem = [&](int m) {
           const uint32_t a = t0 + L::TM_A + m * 64;
           mma4_ts_w<2>(t0 + L::TM_S, a, b0 + (2 * m * L::Q_CHUNK >> 4), kIdS, m > 0);
           mma4_ts_w<2>(t0 + L::TM_S, a + 32, b0 + ((2 * m + 1) * L::Q_CHUNK >> 4), kIdS, 1);
-        }
-        // the other channels from where P.V will read them (of its 128 rows those past 96 are anything: no one looks at them)
+        };
+        if (!wait(M_LAND, i & 1)) { stop = true; break; }
+        tc_fence_after();
+        from_tmem(0);
+        from_tmem(1);
+        // a quarter from where P.V will read it (of its 128 rows those past 96 are anything: no one looks at them)
         if (!wait(M_LAND + 8, i & 1)) { stop = true; break; }
         tc_fence_after();
         const uint64_t a0 = sdesc_sw128(v0, 16, 1024);
         mma4_w<2, 2>(t0 + L::TM_S, a0 + (6 * L::CHUNK >> 4), b0 + (6 * L::Q_CHUNK >> 4), kIdS, 1);
         mma4_w<2, 2>(t0 + L::TM_S, a0 + (7 * L::CHUNK >> 4), b0 + (7 * L::Q_CHUNK >> 4), kIdS, 1);
         if (ROPE) mma4_w<2, 2>(t0 + L::TM_S, sdesc_sw128(w0, 16, 1024), b0 + (8 * L::Q_CHUNK >> 4), kIdR, 1);
+        if (!wait(M_LAND + 16, i & 1)) { stop = true; break; }
+        tc_fence_after();
+        from_tmem(2);
         mma_commit_w(mb + M_S);
         if (!wait(M_P, i & 1)) { stop = true; break; }
         tc_fence_after();
@@ -623,22 +627,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
           st_shared_v4(to1 + at, v[8 + 2 * k], v[9 + 2 * k], v[12 + 2 * k], v[13 + 2 * k]);
         }
       };
-      // S^T's operand, as far as there is room: while P.V of the tile before is under way
+      // S^T's operand: two quarters while P.V of the tile before is under way, one to where P.V will read it, and the last
       uint32_t v[3][16];
-#pragma unroll
-      for (int m = 0; m < 3; ++m) {
+      auto quarter = [&](int m) {
         to_fp16(m, v[m]);
         to_tmem(m, v[m]);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(mb + M_LAND);
-      // the rest of it; the other channels, which only P.V reads from there, while S^T is under way
+      };
+      auto in_tmem = [&](int bar) {
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(mb + bar);
+      };
+      quarter(0);
+      quarter(1);
+      in_tmem(M_LAND);
       if (i > 0 && !wait(M_PV, (i - 1) & 1)) return false;
-      uint32_t rest[16];
-      to_fp16(3, rest);
-      to_shared(3, rest);
+      to_fp16(3, v[2]);
+      to_shared(3, v[2]);
       if constexpr (ROPE) {  // P.V has read all of W: the position channels take its place
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -651,6 +657,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(mb + M_LAND + 8);
+      quarter(2);
+      in_tmem(M_LAND + 16);
+      // the channels that only P.V reads from shared memory, while S^T is under way
 #pragma unroll
       for (int m = 0; m < 3; ++m) to_shared(m, v[m]);
       return true;
