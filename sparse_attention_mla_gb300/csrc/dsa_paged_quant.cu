@@ -3,9 +3,8 @@
 // A row's scale s is a power of two (codes that have an exponent of their own lose nothing by that), a block's scale
 // e4m3, a code the nearest of e4m3 or e2m1: x / s and every value read back are exact, and a code does not depend on
 // how a quotient was rounded (see nearest_side).  Both directions are bound by memory: a row is read once and written
-// once, 1152 + 420 bytes for a latent in 4 bits.  Reading 12 requests of 7500 to 30000 latents of 4 bits back: 73 us, 5.1
-// TB/s, where a copy reaches 6.8 (each value costs a load of its 4 codes' word, its block's scale and s, and their
-// conversion); writing 8191 latents of 4 bits and reading them: 11 us, two kernels of little more than their launch.
+// once, 1152 + 420 bytes for a latent in 4 bits.  Reading 12 requests of 7500 to 30000 latents of 4 bits back: 66 us, 5.7
+// TB/s, where a copy reaches 6.8 (8 channels a thread in place of 16, and stores of 16 bytes in place of 32: 73.7); writing 8191 latents of 4 bits and reading them: 10.6 us, two kernels of little more than their launch.
 #include <climits>
 
 #include "dsa_host.h"
@@ -150,17 +149,17 @@ struct Back {
   const int32_t *table, *first, *cu;
   int N, B, D, Q, num_pages, P, max_pages;
   int rows;                  // of a CTA: 32 a warp that looks them up
-  unsigned inv_q, inv_tail;  // ceil(2^21 / units of 8 channels) of both parts: a unit's row is (i inv) >> 21 for i < 64 * 128
+  unsigned inv_q, inv_tail;  // ceil(2^21 / units) of both parts, of 16 and 8 channels: a unit's row is (i inv) >> 21 for i < 64 * 128
   __nv_bfloat16* out;
   long long stride;
   int* err;
-  bool vec;  // 16-byte aligned rows of out
+  int align;  // of the rows of out: 32, 16 or 2 bytes
 };
 constexpr int kBackRows = 64;  // at most
 
 // A CTA reads rows that follow one another in the output: a warp finds where 32 of them lie (together: a search of its own
-// for each row is a chain of loads, and a CTA has little else to do), then all threads take units of 8 channels, so
-// that a warp writes 512 bytes that follow one another; four units at a time, loads before stores.
+// for each row is a chain of loads, and a CTA has little else to do), then all threads take units of 16 channels (a
+// block), so that a warp writes 1024 bytes that follow one another; two units at a time, loads before stores.
 template <int BITS>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const Back p) {
   __shared__ long long s_row[kBackRows];  // row of the cache; -1: zeros, -2: not to be written
@@ -195,10 +194,9 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const Back p) {
   }
   __syncthreads();
   const QuantRow lay = quant_row(p.D, p.Q, BITS);
-  const int rows = (int)min((long long)p.rows, p.N - t0), q8 = p.Q / 8, tail8 = (p.D - p.Q) / 8;
-  auto store = [&](int r, int u, uint4 v) {
-    __nv_bfloat16* dst = p.out + (t0 + r) * p.stride + u * 8;
-    if (p.vec) {
+  const int rows = (int)min((long long)p.rows, p.N - t0), q16 = p.Q / 16, tail8 = (p.D - p.Q) / 8;
+  auto store8 = [&](__nv_bfloat16* dst, uint4 v) {
+    if (p.align >= 16) {
       *reinterpret_cast<uint4*>(dst) = v;
     } else {
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -206,57 +204,73 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const Back p) {
       for (int k = 0; k < 8; ++k) reinterpret_cast<uint16_t*>(dst)[k] = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
     }
   };
-  constexpr int kAtOnce = 4;
+  constexpr int kAtOnce = 2;
 #pragma unroll 1
-  for (int i0 = threadIdx.x; i0 < rows * q8; i0 += kThreads * kAtOnce) {
+  for (int i0 = threadIdx.x; i0 < rows * q16; i0 += kThreads * kAtOnce) {
     int r[kAtOnce];
     bool zero[kAtOnce];
-    uint2 code[kAtOnce];
+    uint4 code[kAtOnce];
     uint32_t block[kAtOnce];
     float scale[kAtOnce];
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       const int i = i0 + k * kThreads;
       r[k] = (int)(((unsigned)i * p.inv_q) >> 21);
-      const long long at = i < rows * q8 ? s_row[r[k]] : -2;
-      const int u = i - r[k] * q8;
+      const long long at = i < rows * q16 ? s_row[r[k]] : -2;
+      const int u = i - r[k] * q16;
       const uint8_t* row = p.cache + (size_t)(at < 0 ? 0 : at) * lay.bytes;
       zero[k] = at == -1;
       if (at == -2) r[k] = -1;
-      code[k] = make_uint2(0, 0);
+      code[k] = make_uint4(0, 0, 0, 0);
       block[k] = 0;
       scale[k] = 0.f;
       if (at >= 0) {
         scale[k] = __ldg(reinterpret_cast<const float*>(row + lay.scale));
         if constexpr (BITS == 8) {
-          code[k] = __ldg(reinterpret_cast<const uint2*>(row) + u);
+          code[k] = __ldg(reinterpret_cast<const uint4*>(row) + u);
         } else {
-          block[k] = __ldg(row + lay.blocks + u / 2);
-          code[k].x = __ldg(reinterpret_cast<const uint32_t*>(row) + u);
+          block[k] = __ldg(row + lay.blocks + u);
+          const uint2 c = __ldg(reinterpret_cast<const uint2*>(row) + u);
+          code[k].x = c.x;
+          code[k].y = c.y;
         }
       }
     }
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       if (r[k] < 0) continue;
-      uint32_t h[4], o[4];
+      uint32_t h[8], o[8];
       if constexpr (BITS == 8) {
-        h[0] = e4m3x2_f16x2((uint16_t)code[k].x);
-        h[1] = e4m3x2_f16x2((uint16_t)(code[k].x >> 16));
-        h[2] = e4m3x2_f16x2((uint16_t)code[k].y);
-        h[3] = e4m3x2_f16x2((uint16_t)(code[k].y >> 16));
+        const uint32_t c[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          h[2 * x] = e4m3x2_f16x2((uint16_t)c[x]);
+          h[2 * x + 1] = e4m3x2_f16x2((uint16_t)(c[x] >> 16));
+        }
       } else {
         const uint32_t by = e4m3x2_f16x2((uint16_t)(block[k] | block[k] << 8));
-        e2m1x8_f16x2(code[k].x, h);
+        uint32_t lo[4], hi[4];
+        e2m1x8_f16x2(code[k].x, lo);
+        e2m1x8_f16x2(code[k].y, hi);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) h[x] = mul_f16x2(h[x], by);
+        for (int x = 0; x < 4; ++x) {
+          h[x] = mul_f16x2(lo[x], by);
+          h[4 + x] = mul_f16x2(hi[x], by);
+        }
       }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
+      for (int x = 0; x < 8; ++x) {
         const float2 f = f16x2_floats(h[x]);
-        o[x] = pack_bf16x2(f.x * scale[k], f.y * scale[k]);
+        o[x] = zero[k] ? 0u : pack_bf16x2(f.x * scale[k], f.y * scale[k]);
       }
-      store(r[k], i0 + k * kThreads - r[k] * q8, zero[k] ? make_uint4(0, 0, 0, 0) : make_uint4(o[0], o[1], o[2], o[3]));
+      __nv_bfloat16* dst = p.out + (t0 + r[k]) * p.stride + (i0 + k * kThreads - r[k] * q16) * 16;
+      if (p.align == 32) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]),
+                     "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
+      } else {
+        store8(dst, make_uint4(o[0], o[1], o[2], o[3]));
+        store8(dst + 8, make_uint4(o[4], o[5], o[6], o[7]));
+      }
     }
   }
 #pragma unroll 1
@@ -265,7 +279,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const Back p) {
     const long long at = s_row[r];
     if (at == -2) continue;
     const uint4* src = reinterpret_cast<const uint4*>(p.cache + (size_t)(at < 0 ? 0 : at) * lay.bytes + lay.tail) + u;
-    store(r, q8 + u, at < 0 ? make_uint4(0, 0, 0, 0) : __ldg(src));
+    store8(p.out + (t0 + r) * p.stride + p.Q + u * 8, at < 0 ? make_uint4(0, 0, 0, 0) : __ldg(src));
   }
 }
 
@@ -374,15 +388,16 @@ extern "C" dsa_status_t dsa_paged_dequantize(const uint8_t* cache, const int32_t
   p.num_pages = num_pages;
   p.P = page_size;
   p.max_pages = max_pages;
-  const unsigned q8 = quant_dim / 8, tail8 = (D - quant_dim) / 8;
-  p.inv_q = ((1u << 21) + q8 - 1) / q8;
+  const unsigned q16 = quant_dim / 16, tail8 = (D - quant_dim) / 8;
+  p.inv_q = ((1u << 21) + q16 - 1) / q16;
   p.inv_tail = tail8 ? ((1u << 21) + tail8 - 1) / tail8 : 0;
   p.out = reinterpret_cast<__nv_bfloat16*>(out);
   p.stride = out_stride_t;
   p.err = reinterpret_cast<int*>(workspace);
-  p.vec = aligned16(out) && (out_stride_t % 8 == 0 || N == 1);
-  // 64 rows a CTA while that leaves four CTAs an SM (131104 rows of 128 channels, written and read: 24.8 us, with 32 28.1;
-  // 12 x 30000 of 576 read: 73 and 74, with 128 78, with 256 90)
+  const uintptr_t lie = reinterpret_cast<uintptr_t>(out) | (N == 1 ? 0 : (uintptr_t)out_stride_t * 2);
+  p.align = lie % 32 == 0 ? 32 : lie % 16 == 0 ? 16 : 2;
+  // 64 rows a CTA while that leaves four CTAs an SM (units of 8 channels: 131104 rows of 128, written and read, 24.8 us, with 32 28.1;
+  // 12 x 30000 of 576 read 73 and 74, with 128 78, with 256 90)
   p.rows = N / 64 >= 4 * pquant::kSms ? 64 : 32;
   const unsigned blocks = (unsigned)(((int64_t)N + p.rows - 1) / p.rows);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

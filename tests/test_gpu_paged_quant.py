@@ -200,3 +200,22 @@ def test_many_rows_of_many_requests_are_read_back(bits):
     got = out.cpu().double()
     assert bool((got[:7] == 5).all()) and bool((got[N - 9:] == 5).all())
     assert torch.equal(got[7:N - 9], want)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("D,Q", [(576, 512), (72, 64)])
+@pytest.mark.parametrize("stride,shift", [(0, 0), (16, 16), (8, 0), (16, 8), (1, 0), (3, 5)])
+def test_strides_of_the_output(bits, D, Q, stride, shift):
+    # rows that begin at multiples of 32, 16 and 2 bytes; what lies between them is left as it was
+    g = torch.Generator().manual_seed(D + stride)
+    cache = torch.zeros(70, 1, dsa.paged_quant_row_bytes(D, bits, Q), dtype=torch.uint8, device=DEV)
+    dsa.dsa_paged_quantize(torch.randn(70, D, generator=g).bfloat16().to(DEV), cache, bits, quant_dim=Q)
+    rows = torch.randperm(70, generator=g).to(I32)
+    flat = torch.full((70 * (D + stride) + shift,), 9.0, dtype=torch.bfloat16, device=DEV)
+    out = flat[shift:].view(70, D + stride)[:, :D]
+    cu = torch.tensor([0, 70], dtype=I32, device=DEV)
+    dsa.dsa_paged_dequantize(cache, rows[None].to(DEV), cu, bits, D, quant_dim=Q, out=out)
+    want = ref.decode(cache.view(70, -1).cpu()[rows.long()], D, Q, bits)
+    assert torch.equal(out.cpu().double(), want)
+    rest = flat[shift:].view(70, D + stride)[:, D:]
+    assert bool((rest == 9).all()) and bool((flat[:shift] == 9).all())
