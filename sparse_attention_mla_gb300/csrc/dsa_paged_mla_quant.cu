@@ -5,30 +5,29 @@
 // lse = ln sum e^{z_p},  out = sum e^{z_p - lse} kv_p[0:512],  kv_p = v_p s_p with v_p = code * block (e2m1 times
 // e4m3) for the first 512 channels and s_p the row's scale, a power of two.
 //
-// v is exact in fp16 (6 bits between 2^-10 and 2688), so the products run in fp16
-// and s stays outside of them: z_p = s_p <q, v_p> + <q', kv'_p>, with the position channels' part in bf16, divided by
+// v is exact in fp16 (6 bits between 2^-10 and 2688), so the products run in fp16 and s stays outside of them: z_p = s_p <q, v_p> + <q', kv'_p>, with the position channels' part in bf16, divided by
 // s_p (a power of two); and the output sums the weights w_p = e^{z_p} s_p.  The running maximum is that of w, not of
 // e^{z}: w in fp16 (11 bits, 2^15 down to 2^-24 around a maximum of 2^7) then loses nothing that counts, whatever the
-// rows' scales are.  The denominator adds w_p / s_p in fp32.  A query row is divided by a power of two so that its
+// rows' scales are.  The denominator adds e^{z_p} in fp32.  A query row is divided by a power of two so that its
 // largest channel lies in [2^14, 2^15): the channels that this takes out of fp16 are below 2^-38 of that one.
 //
 // Split of the work as in dsa_paged_groups.cuh, with tiles of 96 positions and groups of NH = 64 columns, or of 16 while all
 // rows of a request (or a list) fit.  A tile: two warps copy its rows as they are to shared memory; 12 warps take the codes from
 // there to registers and form fp16, which is the A operand of S^T[position, column] = V Q^T and, as V^T, of O^T[channel, column]
-// += V^T W^T.  Three quarters of the channels are written to TMEM, position by lane, before P.V of the tile before has left
-// shared memory; the last quarter to shared memory, from where both products read it; then the three quarters there too, while
-// S^T is under way.  Then the same warps do the softmax, a position a thread.  96 positions, since an fp16 tile of 128, its
-// queries and W leave no room for the next tile's rows as they come.
+// += V^T W^T.  Two quarters of the channels are written to TMEM, position by lane, before P.V of the tile before has left
+// shared memory; one quarter to shared memory, from where both products read it, and the last to TMEM; then the three quarters
+// in TMEM to shared memory too, while S^T is under way.  Then the same warps do the softmax, a position a thread.  96
+// positions, since an fp16 tile of 128, its queries and W leave no room for the next tile's rows as they come.
 //
 // A thread's four blocks of 16 channels lie side by side in a row (one load for four scales), but 16 channels apart in every
 // 128 of the products: O^T's row 128 m + 16 y + e is channel 64 y + 16 m + e, and the queries' channels follow.
 //
-// What bounds it: 64 requests of 4000 to 16384 positions, 64 heads: 161 us, where the same over bf16 rows of 2.7 times the
-// bytes takes 159 and over 8 bits (dsa_paged_mla_e4m3.cu, which converts nothing) 121.  A tile takes about 5700 cycles, of which
-// the warps convert for 3300 and do the softmax for 1500; shared memory moves 424 KB (rows in and out 84, V in and out 192, W
-// 60, queries 88), 3400 cycles at 128 bytes each.  One group after the other costs what overlap would save: with 64 registers
-// a thread and twice the warps 209 us, the next tile's rows in registers during the softmax 171, loads by the converting
-// warps themselves 190 and more.
+// What bounds it: 64 requests of 4000 to 16384 positions, 64 heads: 158 us, where the same over bf16 rows of 2.7 times the
+// bytes takes 159 and over 8 bits (dsa_paged_mla_e4m3.cu, which converts nothing) 121.  A tile takes about 5500 cycles, of which
+// the warps convert for 3900 and do the softmax for 1400, never waiting for a product; shared memory moves 424 KB (rows in
+// and out 84, V in and out 192, W 60, queries 88), 3400 cycles at 128 bytes each.  Measured beside it: with 64 registers
+// a thread and twice the warps 209 us, the next tile's rows in registers during the softmax 171 (half of them: 163), loads by the
+// converting warps themselves 190 and more, three quarters in TMEM before the one in shared memory 161.5.
 //
 // Warps: three of four convert and do softmax and epilogue (they reach the TMEM lanes 0-95); of the others one issues the
 // products, one announces the runs of tiles, two copy.
@@ -947,7 +946,7 @@ dsa_status_t launch(Params& p, int ctas, cudaStream_t s) {
                                           "configuring paged_mla_quant_kernel");
   if (st != DSA_OK) return st;
   p.G = p.topk_idx ? 1 : (p.H <= NH ? NH / p.H : 1);
-  // (64 x 16384, 64 heads: 161 us with 2 to 4, 164 with 1; 96 x 4097, 8 heads: 61.9 with 1, 62.7 with 2, 65 with 4)
+  // (64 x 16384, 64 heads, in the state then: 161 us with 2 to 4, 164 with 1; 96 x 4097, 8 heads: 61.9 with 1, 62.7 with 2, 65 with 4)
   p.extra = NH == 16 ? 1 : 2;
   p.HB = (p.H + NH - 1) / NH;
   paged_mla_quant_kernel<DQK, NH><<<ctas, kThreads, L::TOTAL, s>>>(p);

@@ -4,7 +4,8 @@
 // e4m3, a code the nearest of e4m3 or e2m1: x / s and every value read back are exact, and a code does not depend on
 // how a quotient was rounded (see nearest_side).  Both directions are bound by memory: a row is read once and written
 // once, 1152 + 420 bytes for a latent in 4 bits.  Reading 12 requests of 7500 to 30000 latents of 4 bits back: 66 us, 5.7
-// TB/s, where a copy reaches 6.8 (8 channels a thread in place of 16, and stores of 16 bytes in place of 32: 73.7); writing 8191 latents of 4 bits and reading them: 10.6 us, two kernels of little more than their launch.
+// TB/s, where a copy reaches 6.8 (8 channels a thread in place of 16, and stores of 16 bytes in place of 32: 73.7); writing
+// 8191 latents of 4 bits and reading them: 10.6 us, two kernels of little more than their launch.
 #include <climits>
 
 #include "dsa_host.h"
