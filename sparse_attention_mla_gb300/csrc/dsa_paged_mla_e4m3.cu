@@ -80,13 +80,13 @@ struct Smem {
   static_assert(TM_O + 4 * NH <= TM_COLS, "TMEM budget");
 };
 
-// misc (bytes).  A tile's channels are given back 128 at a time as P.V reads them.
-constexpr int kSteps = 4, kSlots = 4;
-constexpr int M_KV = 0, M_PV = 32, M_S = 160, M_SF = 176, M_P = 192, M_Q = 208, M_FIN = 216;  // [4] [4][4] [2] [2] [2] 1 [2]
-constexpr int M_SEGF = 232, M_SEGE = M_SEGF + 8 * kSegs;  // [kSegs] each: announced, read by all
-constexpr int M_TMEM = 360, M_ABORT = 364, M_PLAN = 368;  // plan: 56 bytes
-constexpr int M_SEG = 432;                    // int4 [kSegs][2]
-constexpr int M_RED = 688;                    // float [4][64]; the first row also holds the factors of a rescale
+// misc (bytes)
+constexpr int kSlots = 4;
+constexpr int M_KV = 0, M_PV = 32, M_S = 64, M_SF = 80, M_P = 96, M_Q = 112, M_FIN = 120;  // [4] [4] [2] [2] [2] 1 [2]
+constexpr int M_SEGF = 136, M_SEGE = M_SEGF + 8 * kSegs;  // [kSegs] each: announced, read by all
+constexpr int M_TMEM = 264, M_ABORT = 268, M_PLAN = 272;  // plan: 56 bytes
+constexpr int M_SEG = 336;                    // int4 [kSegs][2]
+constexpr int M_RED = 592;                    // float [4][64]; the first row also holds the factors of a rescale
 constexpr int M_STAT = M_RED + 1024;          // float [64]
 constexpr int M_COL = M_STAT + 256;           // float [2][64]: a column's factor of the score, by run
 constexpr int M_SCALE = M_COL + 512;          // float [kSlots][64]: s of the rows, -1: masked
@@ -208,16 +208,14 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
   float* s_red = reinterpret_cast<float*>(misc + M_RED);
   float* s_col = reinterpret_cast<float*>(misc + M_COL);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // tile i has landed; P.V has read 128 of its channels (3: all of it)
+  // tile i has landed; P.V has read it
   auto wait_kv = [&](int i) { return wait_for(bar_kv + 8 * (i % R), (i / R) & 1, s_abort, p.wait_limit); };
-  auto wait_pv = [&](int i, int m) {
-    return wait_for(bar_pv + 8 * ((i % R) * kSteps + m), (i / R) & 1, s_abort, p.wait_limit);
-  };
+  auto wait_pv = [&](int i) { return wait_for(bar_pv + 8 * (i % R), (i / R) & 1, s_abort, p.wait_limit); };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < R; ++s) {
       mbar_init(bar_kv + 8 * s, 4 * 33);  // four warps: each lane's copies, and what the warp has stored
-      for (int m = 0; m < kSteps; ++m) mbar_init(bar_pv + 8 * (s * kSteps + m), 1);
+      mbar_init(bar_pv + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar_s + 8 * b, ROWS ? 2 : 1);
@@ -336,8 +334,8 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
           const uint64_t a = va + m * (L::CHUNK >> 4);
           mma_f8_w<2, (32 * 128 >> 4), kStep>(d0 + L::TM_O + m * NH, a, pb, kIdHi, add);
           mma_f8_w<2, (32 * 128 >> 4), kStep>(d0 + L::TM_O + m * NH, a, pb + kLo, kIdLo, 1);
-          mma_commit_w(bar_pv + 8 * (sl * kSteps + m));
         }
+        mma_commit_w(bar_pv + 8 * sl);
       }
       if (stop) break;
     }
@@ -423,7 +421,7 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
 #pragma unroll 1
     for (int i = 0; i < n_tiles && !stop; ++i) {
       const int sl = i % R;
-      if (i >= R && !warp_all(wait_pv(i - R, 3))) { stop = true; break; }
+      if (i >= R && !warp_all(wait_pv(i - R))) { stop = true; break; }
       if (lane < kRows) {
         const int r = sl * kTile + gw * kRows + lane;
         if (row[0] < 0) s_raw[4 * r] = -1.f;
@@ -609,7 +607,7 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
         if (!ROWS) bad = bad || !warp_all(wait_kv(i));
         if (t == sg.t0) bad = bad || !warp_all(wait_for(bar_q, (seg - 1) & 1, s_abort, p.wait_limit));
         // W of tile i overwrites what P.V of tile i - 2 read
-        if (i >= 2) bad = bad || !warp_all(wait_pv(i - 2, 3));
+        if (i >= 2) bad = bad || !warp_all(wait_pv(i - 2));
         tc_fence_after();
         __syncwarp();
         if constexpr (ROWS) {
@@ -680,7 +678,7 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
             neg = -fmaxf(s_stat[my_row], -3.0e38f);
             weights();
             if (t > sg.t0) {
-              const bool okw = wait_pv(i - 1, 3);
+              const bool okw = wait_pv(i - 1);
               if (named_bar_or(bar_id, kTeam, !okw)) { aborted = true; break; }
               tc_fence_after();
               rescale();
@@ -771,7 +769,7 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
               e[j] = add2(z[j], m_neg[j]);
             }
             if (t > sg.t0) {
-              const bool okw = wait_pv(i - 1, 3);
+              const bool okw = wait_pv(i - 1);
               if (named_bar_or(bar_id, kTeam, !okw)) { aborted = true; break; }
               tc_fence_after();
               rescale();
@@ -834,7 +832,7 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
         s_fac[n] = fac;
       }
       named_bar(bar_id, kTeam);
-      const bool got = wait_pv(i - 1, 3);  // (the sums above while the last P.V is under way)
+      const bool got = wait_pv(i - 1);  // (the sums above while the last P.V is under way)
       aborted = named_bar_or(bar_id, kTeam, !got);
       if (aborted) break;
       tc_fence_after();

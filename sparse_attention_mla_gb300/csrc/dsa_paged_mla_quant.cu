@@ -5,9 +5,9 @@
 // lse = ln sum e^{z_p},  out = sum e^{z_p - lse} kv_p[0:512],  kv_p = v_p s_p with v_p = code * block (e2m1 times
 // e4m3) for the first 512 channels and s_p the row's scale, a power of two.
 //
-// v is exact in fp16 (6 bits between 2^-10 and 2688), so the products run in fp16 and s stays outside of them: z_p = s_p <q, v_p> + <q', kv'_p>, with the position channels' part in bf16, divided by
-// s_p (a power of two); and the output sums the weights w_p = e^{z_p} s_p.  The running maximum is that of w, not of
-// e^{z}: w in fp16 (11 bits, 2^15 down to 2^-24 around a maximum of 2^7) then loses nothing that counts, whatever the
+// v is exact in fp16 (6 bits between 2^-10 and 2688), so the products run in fp16 and s stays outside of them:
+// z_p = s_p <q, v_p> + <q', kv'_p>, with the position channels' part in bf16, divided by s_p (a power of two); and the
+// output sums the weights w_p = e^{z_p} s_p.  The running maximum is that of w, not of e^{z}: w in fp16 (11 bits, 2^15 down to 2^-24 around a maximum of 2^7) then loses nothing that counts, whatever the
 // rows' scales are.  The denominator adds e^{z_p} in fp32.  A query row is divided by a power of two so that its
 // largest channel lies in [2^14, 2^15): the channels that this takes out of fp16 are below 2^-38 of that one.
 //
@@ -181,11 +181,6 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
 __device__ __forceinline__ uint4 lds16(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds8(uint32_t at) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
   return v;
 }
 __device__ __forceinline__ float lds4(uint32_t at) {
