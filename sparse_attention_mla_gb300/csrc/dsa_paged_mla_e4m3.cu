@@ -507,7 +507,8 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
         const int e = max((int)(most >> 7) - 127, -119);
         const float by = pow2(7 - e);
         // (a row with a channel that is not finite gives NaN)
-        if (lane == 0) s_col[(run & 1) * 64 + hh] = most >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e - 7) * (ROWS ? 1.f : p.sl2e);
+        const float factor = most >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2(e - 7) * (ROWS ? 1.f : p.sl2e);
+        if (lane == 0) s_col[(run & 1) * 64 + hh] = factor;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int u = lane + 32 * x;

@@ -7,9 +7,10 @@
 //
 // v is exact in fp16 (6 bits between 2^-10 and 2688), so the products run in fp16 and s stays outside of them:
 // z_p = s_p <q, v_p> + <q', kv'_p>, with the position channels' part in bf16, divided by s_p (a power of two); and the
-// output sums the weights w_p = e^{z_p} s_p.  The running maximum is that of w, not of e^{z}: w in fp16 (11 bits, 2^15 down to 2^-24 around a maximum of 2^7) then loses nothing that counts, whatever the
-// rows' scales are.  The denominator adds e^{z_p} in fp32.  A query row is divided by a power of two so that its
-// largest channel lies in [2^14, 2^15): the channels that this takes out of fp16 are below 2^-38 of that one.
+// output sums the weights w_p = e^{z_p} s_p.  The running maximum is that of w, not of e^{z}: w in fp16 (11 bits, 2^15 down
+// to 2^-24 around a maximum of 2^7) then loses nothing that counts, whatever the rows' scales are.  The denominator adds
+// e^{z_p} in fp32.  A query row is divided by a power of two so that its largest channel lies in [2^14, 2^15): the channels
+// that this takes out of fp16 are below 2^-38 of that one.
 //
 // Split of the work as in dsa_paged_groups.cuh, with tiles of 96 positions and groups of NH = 64 columns, or of 16 while all
 // rows of a request (or a list) fit.  A tile: two warps copy its rows as they are to shared memory; 12 warps take the codes from
@@ -73,7 +74,7 @@ struct Smem {
 };
 
 // misc (bytes)
-constexpr int M_LAND = 0;      // [3]: S^T's operand is there: 256 channels in TMEM, the last 128 in shared memory, the others in TMEM
+constexpr int M_LAND = 0;      // [3]: S^T's operand is there: 256 channels in TMEM, the last 128 in shared memory, the others
 constexpr int M_PV = 40;       // P.V is done
 constexpr int M_S = 88, M_P = 96, M_Q = 104, M_FIN = 112;
 constexpr int M_RAW = 120, M_READ = 128;                    // a tile's rows have come, have been read
@@ -277,7 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
   __syncthreads();
   const uint32_t tmem = (uint32_t)warp_value((int)*s_tmem);
   auto read_seg = [&](int k, Seg& s) -> bool {
-    return read_announcement_here(mb + M_SEGF, mb + M_SEGE, reinterpret_cast<const int4*>(misc + M_SEG), k, s_abort, p.wait_limit, s);
+    const int4* ring = reinterpret_cast<const int4*>(misc + M_SEG);
+    return read_announcement_here(mb + M_SEGF, mb + M_SEGE, ring, k, s_abort, p.wait_limit, s);
   };
   // The lanes 96-127 of TMEM hold no positions, but channels of O^T: the four warps that reach them store them, a column
   // group each (the one that issues the products rescales them too).  Run k, whose last tile is number i - 1 of the CTA's.
@@ -941,7 +943,7 @@ dsa_status_t launch(Params& p, int ctas, cudaStream_t s) {
                                           "configuring paged_mla_quant_kernel");
   if (st != DSA_OK) return st;
   p.G = p.topk_idx ? 1 : (p.H <= NH ? NH / p.H : 1);
-  // (64 x 16384, 64 heads, in the state then: 161 us with 2 to 4, 164 with 1; 96 x 4097, 8 heads: 61.9 with 1, 62.7 with 2, 65 with 4)
+  // (64 x 16384, 64 heads, in the state then: 161 us with 2 to 4, 164 with 1; 96 x 4097, 8 heads: 61.9 with 1, 62.7 with 2)
   p.extra = NH == 16 ? 1 : 2;
   p.HB = (p.H + NH - 1) / NH;
   paged_mla_quant_kernel<DQK, NH><<<ctas, kThreads, L::TOTAL, s>>>(p);

@@ -150,7 +150,8 @@ struct Back {
   const int32_t *table, *first, *cu;
   int N, B, D, Q, num_pages, P, max_pages;
   int rows;                  // of a CTA: 32 a warp that looks them up
-  unsigned inv_q, inv_tail;  // ceil(2^21 / units) of both parts, of 16 and 8 channels: a unit's row is (i inv) >> 21 for i < 64 * 128
+  // ceil(2^21 / units) of both parts, of 16 and 8 channels: a unit's row is (i inv) >> 21 for i < 64 * 128
+  unsigned inv_q, inv_tail;
   __nv_bfloat16* out;
   long long stride;
   int* err;
@@ -397,7 +398,7 @@ extern "C" dsa_status_t dsa_paged_dequantize(const uint8_t* cache, const int32_t
   p.err = reinterpret_cast<int*>(workspace);
   const uintptr_t lie = reinterpret_cast<uintptr_t>(out) | (N == 1 ? 0 : (uintptr_t)out_stride_t * 2);
   p.align = lie % 32 == 0 ? 32 : lie % 16 == 0 ? 16 : 2;
-  // 64 rows a CTA while that leaves four CTAs an SM (units of 8 channels: 131104 rows of 128, written and read, 24.8 us, with 32 28.1;
+  // 64 rows a CTA while that leaves four an SM (units of 8 channels: 131104 rows of 128, written and read, 24.8 us, 28.1 with 32;
   // 12 x 30000 of 576 read 73 and 74, with 128 78, with 256 90)
   p.rows = N / 64 >= 4 * pquant::kSms ? 64 : 32;
   const unsigned blocks = (unsigned)(((int64_t)N + p.rows - 1) / p.rows);
