@@ -677,6 +677,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
       __syncwarp();
 #pragma unroll 1
       for (int hh = cg * 3 + qd; hh < NH; hh += kWorkers) {
+        if (hh >= s.rows) {  // (zeros, as they have come)
+          if (lane == 0) s_col[(run & 1) * 64 + hh] = 0.f;
+          continue;
+        }
         uint4 v[3];
         uint32_t top = 0;
 #pragma unroll
