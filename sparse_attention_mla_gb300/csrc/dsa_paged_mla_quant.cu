@@ -499,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
 #pragma unroll
         for (int e = 0; e < 2; ++e) on[e] = __ballot_sync(0xffffffffu, row[e] >= 0);
         armed = i;
+        __syncwarp();  // (all lanes' flags come before the arrival that gives them to the other warps: votes order no memory)
         if (lane == 0) mbar_expect_tx(mb + M_RAW, (__popc(on[0]) + __popc(on[1])) * LAY.bytes);
         __syncwarp();
 #pragma unroll
