@@ -672,7 +672,7 @@ dsa_status_t dsa_paged_dequantize(const uint8_t* cache, const int32_t* block_tab
  * attention, with the rows' values as defined above for kv.  Queries, tables, lists, sink, out and lse
  * as there.  Scores and sums are fp32.  4 bits: products of the scores are exact, a weight has 11 bits
  * (down to 2^-32 of the largest weight times s).  8 bits: a query row counts to 2^-17 of its largest
- * channel among the first 512, a weight to 2^-7 of itself (2^-15 of the largest weight times s).
+ * channel among the first 512, a weight to 2^-11 of itself (2^-28 of the largest weight times s).
  *  cache        device bytes [num_pages, page_size, dsa_paged_quant_row_bytes(Dqk, 512, bits)], 16-byte aligned
  *  bits         8 or 4
  *  workspace    >= dsa_paged_mla_quant_workspace_size() bytes, whatever the sizes

@@ -9,8 +9,9 @@
 // w_p = e^{z_p} s_p, and the running maximum is that of w.  The other operands become sums of 8-bit numbers:
 //  - a query row, divided by a power of two so that its largest channel lies in [2^7, 2^8), is hi + lo, both e4m3: exact
 //    down to 2^-2, and to 2^-10 (2^-17 of the largest channel) below;
-//  - a weight is hi + lo, hi e5m2 (2^15 down to 2^-16) and lo e4m3: 7 to 8 bits above 2^-3 and, where lo runs out, to 2^-10;
-//    the largest weight of a row is between 2^5 and 2^11 (the maximum is raised lazily), so that this is 2^-15 of it.
+//  - a weight is the sum of three e5m2 (2^15 down to 2^-16, 3 bits each): within 2^-11 of itself and, where they run out, to
+//    2^-17; the largest weight of a row is between 2^11 and 2^15 (the maximum is raised lazily), so that this is 2^-28 of it.
+//    With less a long tail far below one position is off as a whole: its weights are alike, and so are their errors.
 // Position channels are multiplied in bf16 and added by the softmax, since s_p must not reach them.
 //
 // Split of the work as in dsa_paged_groups.cuh, with tiles of 64 positions and groups of 64 rows, or of 16 while all rows of a
@@ -19,15 +20,17 @@
 //    the softmax has keys of one row.  16 rows: S^T[key, row] = K Q^T (M = 64), hi and lo side by side, which keeps all warps
 //    busy; with 64 rows it took the tensor core, whose M = 64 runs at half its rate, 2000 cycles a tile in place of 1300.
 //  - an online softmax with a lazily raised maximum;
-//  - O^T[channel, row] += V^T W^T (M = 128 channels, K = 32 keys, hi and then lo into the same columns).  The codes of 128
+//  - O^T[channel, row] += V^T W^T (M = 128 channels, K = 32 keys, the weights' parts one after the other into the same columns).  The codes of 128
 //    channels of a key are a row of 128 bytes, which is K-major for the first product and M-major for the second.
 //
-// What bounds it: 64 requests of 4000 to 16384 positions, 64 heads: 121 us, of which 10 pass before the first scores (cutting
-// the line, the queries), 15 with the launches and the joining; the 430 MB of rows are read at 4.3 TB/s in between, where a copy
-// reaches 6.8.  A tile's place in the ring (three tiles of 40 KB beside 80 KB of queries) is in use for 6900 cycles: 1700 for
-// its copies, 1700 for S, 2200 for the softmax, 1000 for P.V, the two products sharing shared memory's 128 bytes a cycle (216
-// KB a tile).  Measured beside it: the same rows converted to fp16 as the 4-bit kernel does, 220 us; queries in TMEM and four
-// tiles in the ring, 136 (queries that a thread loads by its row cost 13 us a run); copies by TMA boxes, 206.
+// What bounds it: 64 requests of 4000 to 16384 positions, 64 heads: 136 us (122 with weights of two parts, e5m2 and e4m3,
+// which held 2^-15 of the largest), of which 10 pass before the first scores (cutting the line, the queries), 15 with the
+// launches and the joining; the 430 MB of rows are read at 3.9 TB/s in between, where a copy reaches 6.8.  A tile takes 2700
+// cycles, and its place in the ring (three tiles of 40 KB beside 72 KB of queries) is in use for 9200: 2000 for its copies, 1900
+// for S, 2300 for the softmax, 3000 for P.V, which is issued behind the next tiles' S; the products share shared memory's 128
+// bytes a cycle (260 KB a tile).  Measured beside it, with weights of two parts: the same rows converted to fp16 as the 4-bit
+// kernel does, 220 us; queries in TMEM and four tiles in the ring, 136 (queries that a thread loads by its row cost 13 us a run);
+// copies by TMA boxes, 206.
 //
 // Warps: 0 issues S, the next 16 (or 8) softmax and epilogue, four copy tiles into the ring, one issues P.V, one announces the
 // runs of tiles that the CTA's range consists of.
@@ -46,9 +49,9 @@ using namespace pgroups;
 
 constexpr int kTile = 64;
 constexpr int kGather = 4;       // warps that copy
-constexpr float kRaise = 11.0f;  // log2 units: the running maximum is raised when a weight passes 2^11
-constexpr float kTop = 5.0f;     // a new maximum is 2^5
-constexpr float kMost = 2048.0f; // 2^kRaise
+constexpr float kRaise = 15.0f;    // log2 units: the running maximum is raised when a weight passes 2^15 (e5m2 ends at 1.75 2^15)
+constexpr float kTop = 11.0f;      // a new maximum is 2^11 (2^9: fewer rescales, 133 us in place of 136, and four times the floor)
+constexpr float kMost = 32768.0f;  // 2^kRaise
 constexpr float kLeast = 3.5527136788005009e-15f;  // 2^-48, the least s
 
 template <int DQK, int NH>
@@ -66,12 +69,15 @@ struct Smem {
   static constexpr int THREADS = 32 * (W + kGather + 3);
   static constexpr int READERS = W + kGather + 2;  // warps that read an announcement
   static constexpr int SW = ROWS ? (ROPE ? 2 : 1) * kTile : (ROPE ? 3 : 2) * NH;  // TMEM columns of S
+  // W, two buffers.  64 rows: a row's 64 keys of the first part and of the second side by side, and the third parts of both
+  // buffers so in a block of their own; 16 rows: the first part beside the third, then rows of the second.
   static constexpr int P_BLOCK = NH * 128 * (ROWS ? 1 : 2);
-  static constexpr int QR_CHUNK = (ROWS ? 2 : 1) * NH * 128;  // position channels (rows as the hi rows)
+  static constexpr int P_BYTES = (ROWS ? 3 : 2) * P_BLOCK;
+  static constexpr int QR_CHUNK = NH * 128;  // position channels
   static constexpr int OFF_KV = 0;
   static constexpr int OFF_Q = R * NCH * CHUNK;
   static constexpr int OFF_P = OFF_Q + 4 * Q_CHUNK + (ROPE ? QR_CHUNK : 0);
-  static constexpr int OFF_MISC = OFF_P + 2 * P_BLOCK;
+  static constexpr int OFF_MISC = OFF_P + P_BYTES;
   static constexpr int MISC = 8192;
   static constexpr int TOTAL = OFF_MISC + MISC;
   static_assert(TOTAL <= 232448 && OFF_P % 1024 == 0 && P_BLOCK % 1024 == 0, "shared memory budget");
@@ -155,6 +161,13 @@ __device__ __forceinline__ float2 e5m2x2_floats(uint32_t v) {  // (the upper hal
 }
 __device__ __forceinline__ float2 e4m3x2_floats(uint32_t v) { return f16x2_floats(e4m3x2_f16x2((uint16_t)v)); }
 __device__ __forceinline__ float2 minus2(float2 a, float2 b) { return add2(a, make_float2(-b.x, -b.y)); }
+// Two weights as sums of three e5m2 (what each leaves is exact in fp32).
+__device__ __forceinline__ void parts(float2 w, uint32_t (&r)[3]) {
+  r[0] = e5m2x2(w);
+  w = minus2(w, e5m2x2_floats(r[0]));
+  r[1] = e5m2x2(w);
+  r[2] = e5m2x2(minus2(w, e5m2x2_floats(r[1])));
+}
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }  // -126 <= e <= 127
 
 // 16 TMEM lanes x 64 bits, four times: thread t of the warp gets lane base + (t >> 2) + 8 (t & 1) and the columns
@@ -251,7 +264,7 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
   if (warp == 0) {
     // ======================= S issuer =======================
     constexpr uint32_t kIdS = ROWS ? idesc_f8(128, kTile, 0, 0, false, false) : idesc_f8(kTile, 2 * NH, 0, 0, false, false);
-    constexpr uint32_t kIdR = ROWS ? idesc_bf16(128, kTile, false, false) : idesc_bf16(kTile, NH, false, false);
+    constexpr uint32_t kIdR = idesc_bf16(64, ROWS ? kTile : NH, false, false);
     int done = 0;
     for (int seg = 0, last = 0; !last; ++seg) {
       Seg sg;
@@ -274,7 +287,7 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
         fence_proxy_async_smem();  // (the rows came by cp.async)
         tc_fence_after();
         if constexpr (ROWS) {
-          // (hi rows of position channels are the first 16 of every 32; the others are anything: no one looks at those sums)
+          // (position channels by M = 64, whose rows are the first 16 lanes of every 32, as the hi rows are of the others)
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             mma_f8_w<4, 2, 2>(d0 + sb * L::SW, b0 + c * (L::Q_CHUNK >> 4), a0 + c * (L::CHUNK >> 4), kIdS, c);
@@ -324,16 +337,18 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
         if (!warp_all(wait_for(bar_p + 8 * (i & 1), (i >> 1) & 1, s_abort, p.wait_limit))) { stop = true; break; }
         fence_proxy_async_smem();
         tc_fence_after();
-        constexpr uint32_t kIdHi = idesc_f8(128, NH, 0, 1, true, false), kIdLo = idesc_f8(128, NH, 0, 0, true, false);
+        constexpr uint32_t kId = idesc_f8(128, NH, 0, 1, true, false);
         const uint64_t va = sdesc_sw128(kv0, 16, 1024) + (uint64_t)(uint32_t)(sl * NCH * (L::CHUNK >> 4));
-        // W: a row for each row of the group, 64 bytes of hi and 64 of lo, or hi rows, then lo rows; keys along K
+        // W: a row for each row of the group, keys along K
         const uint64_t pb = sdesc_sw128(p0, 16, 1024) + (uint64_t)(uint32_t)((i & 1) * (L::P_BLOCK >> 4));
-        constexpr int kLo = ROWS ? 64 >> 4 : NH * 128 >> 4, kStep = 2;
+        constexpr int kSecond = ROWS ? 64 >> 4 : NH * 128 >> 4, kStep = 2;
+        const uint64_t pc = ROWS ? sdesc_sw128(p0 + 2 * L::P_BLOCK, 16, 1024) + (uint64_t)(uint32_t)((i & 1) * (64 >> 4)) : pb + (64 >> 4);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const uint64_t a = va + m * (L::CHUNK >> 4);
-          mma_f8_w<2, (32 * 128 >> 4), kStep>(d0 + L::TM_O + m * NH, a, pb, kIdHi, add);
-          mma_f8_w<2, (32 * 128 >> 4), kStep>(d0 + L::TM_O + m * NH, a, pb + kLo, kIdLo, 1);
+          mma_f8_w<2, (32 * 128 >> 4), kStep>(d0 + L::TM_O + m * NH, a, pb, kId, add);
+          mma_f8_w<2, (32 * 128 >> 4), kStep>(d0 + L::TM_O + m * NH, a, pb + kSecond, kId, 1);
+          mma_f8_w<2, (32 * 128 >> 4), kStep>(d0 + L::TM_O + m * NH, a, pc, kId, 1);
         }
         mma_commit_w(bar_pv + 8 * sl);
       }
@@ -486,7 +501,7 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
         const uint32_t size = hh < s.rows ? 16 : 0;
         cp_async16(raw_at(hh, lane), src, size);
         cp_async16(raw_at(hh, lane + 32), src + 256, size);
-        if (ROPE && lane < 8) cp_async16(sQ + 4 * L::Q_CHUNK + sw128_off(q_row(hh, 0), lane), src + 512, size);
+        if (ROPE && lane < 8) cp_async16(sQ + 4 * L::Q_CHUNK + sw128_off(hh, lane), src + 512, size);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncwarp();
@@ -685,18 +700,20 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
               rescale();
             }
           }
-          uint32_t hi[2], lo[2];
+          uint32_t part[3][2];
 #pragma unroll
           for (int j = 0; j < kKeys / 2; j += 2) {
             l_row = add2(l_row, add2(at2(x, j), at2(x, j + 1)));
-            const uint32_t h0 = e5m2x2(at2(w, j)), h1 = e5m2x2(at2(w, j + 1));
-            hi[j / 2] = h0 | h1 << 16;
-            lo[j / 2] = e4m3x2(minus2(at2(w, j), e5m2x2_floats(h0))) |
-                        e4m3x2(minus2(at2(w, j + 1), e5m2x2_floats(h1))) << 16;
+            uint32_t w0[3], w1[3];
+            parts(at2(w, j), w0);
+            parts(at2(w, j + 1), w1);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) part[k][j / 2] = w0[k] | w1[k] << 16;
           }
-          const uint32_t to = sP + (i & 1) * L::P_BLOCK + (k0 & 8);
-          st_shared_v2(to + sw128_off(my_row, ch), hi[0], hi[1]);
-          st_shared_v2(to + sw128_off(my_row, 4 + ch), lo[0], lo[1]);
+          const uint32_t to = sP + (i & 1) * L::P_BLOCK + (k0 & 8), third = sP + 2 * L::P_BLOCK + (k0 & 8);
+          st_shared_v2(to + sw128_off(my_row, ch), part[0][0], part[0][1]);
+          st_shared_v2(to + sw128_off(my_row, 4 + ch), part[1][0], part[1][1]);
+          st_shared_v2(third + sw128_off(my_row, 4 * (i & 1) + ch), part[2][0], part[2][1]);
         } else {
           uint32_t raw[NQ];
           float2 z[NQ / 2];  // (alternate columns of the half first)
@@ -776,21 +793,22 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
               rescale();
             }
           }
-          uint32_t hi[NQ / 2], lo[NQ / 2];
+          uint32_t part[NQ / 2][3];
 #pragma unroll
           for (int j = 0; j < NQ / 2; ++j) {
             const float2 w = make_float2(ex2(e[j].x), ex2(e[j].y));
             l_part[j] = fma2(w, make_float2(inv_s, inv_s), l_part[j]);
-            hi[j] = e5m2x2(w);
-            lo[j] = e4m3x2(minus2(w, e5m2x2_floats(hi[j])));
+            parts(w, part[j]);
           }
           const uint32_t to = sP + (i & 1) * L::P_BLOCK;
 #pragma unroll
           for (int j = 0; j < NQ; ++j) {
             const int n = n0 + j;
             const uint32_t at = to + (uint32_t)(n * 128 + (((r >> 4) ^ (n & 7)) << 4) + (r & 15));
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(hi[j / 2] >> (8 * (j & 1))) : "memory");
-            asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + NH * 128), "r"(lo[j / 2] >> (8 * (j & 1))) : "memory");
+            const uint32_t third = to + (uint32_t)(n * 128 + (((4 + (r >> 4)) ^ (n & 7)) << 4) + (r & 15));
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(part[j / 2][0] >> (8 * (j & 1))) : "memory");
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + NH * 128), "r"(part[j / 2][1] >> (8 * (j & 1))) : "memory");
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(third), "r"(part[j / 2][2] >> (8 * (j & 1))) : "memory");
           }
         }
         fence_proxy_async_smem();
