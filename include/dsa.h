@@ -670,17 +670,20 @@ dsa_status_t dsa_paged_dequantize(const uint8_t* cache, const int32_t* block_tab
 /*
  * dsa_paged_mla_quant -- dsa_paged_mla over a cache of quantised latents (quant_dim = 512): the same
  * attention, with the rows' values as defined above for kv.  Queries, tables, lists, sink, out and lse
- * as there.  Scores and sums are fp32.  4 bits: products of the scores are exact, a weight has 11 bits
- * (down to 2^-32 of the largest weight times s).  8 bits: a query row counts to 2^-17 of its largest
- * channel among the first 512, a weight to 2^-11 of itself (2^-28 of the largest weight times s).
+ * as there.  Scores and sums are fp32.  4 bits: products of the scores are exact for query channels down to
+ * 2^-31 of a, the row's largest one among the first 512 (2^-24 of its largest position channel where that is
+ * more); smaller ones are off by 2^-39 a at most.  A weight has 11 bits (down to 2^-32 of the largest weight
+ * times s).  8 bits: a query row counts to 2^-17 of its largest channel among the first 512, a weight to
+ * 2^-11 of itself (2^-28 of the largest weight times s).
  *  cache        device bytes [num_pages, page_size, dsa_paged_quant_row_bytes(Dqk, 512, bits)], 16-byte aligned
  *  bits         8 or 4
  *  workspace    >= dsa_paged_mla_quant_workspace_size() bytes, whatever the sizes
  * A row whose s is NaN makes the tokens NaN that see it and no other; a row of zero bytes, which nothing
  * was written to, holds zeros.  A query with a channel that is not finite touches no row of out and lse
  * but its own (8 bits: that becomes NaN if the channel is among the first 512).  4 bits: position channels
- * count divided by s, and overflow above 2^127 s.  num_pages * page_size < 2^31.  The result does not
- * depend on timing: equal calls on equal devices give equal bits.
+ * count divided by s, and overflow above 2^82 s (2^106 s for queries whose position channels are not larger
+ * than the others).  num_pages * page_size < 2^31.  The result does not depend on timing: equal calls on equal
+ * devices give equal bits.
  */
 size_t dsa_paged_mla_quant_workspace_size(void);
 dsa_status_t dsa_paged_mla_quant(const dsa_bf16_t* q, const uint8_t* cache, const int32_t* block_table,

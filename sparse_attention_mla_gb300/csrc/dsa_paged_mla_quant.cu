@@ -9,8 +9,10 @@
 // z_p = s_p <q, v_p> + <q', kv'_p>, with the position channels' part in bf16, divided by s_p (a power of two); and the
 // output sums the weights w_p = e^{z_p} s_p.  The running maximum is that of w, not of e^{z}: w in fp16 (11 bits, 2^15 down
 // to 2^-24 around a maximum of 2^7) then loses nothing that counts, whatever the rows' scales are.  The denominator adds
-// e^{z_p} in fp32.  A query row is divided by a power of two so that its largest channel lies in [2^14, 2^15): the channels
-// that this takes out of fp16 are below 2^-38 of that one.
+// e^{z_p} in fp32.  A query row is divided by a power of two so that the largest of its first 512 channels lies in [2^14, 2^15):
+// channels down to 2^-31 of that one are exact in fp16, smaller ones off by half a step of 2^-24, 2^-39 of it.  Not by the
+// largest of all: one large position channel would take the others out of fp16, which count where s is large.  Where a position
+// channel is more than 2^kOver of the others' largest, it takes part for 2^-kOver of it, so that the scores do not overflow.
 //
 // Split of the work as in dsa_paged_groups.cuh, with tiles of 96 positions and groups of NH = 64 columns, or of 16 while all
 // rows of a request (or a list) fit.  A tile: two warps copy its rows as they are to shared memory; 12 warps take the codes from
@@ -53,6 +55,7 @@ constexpr int kTeam = 96;                 // threads of a column group
 constexpr float kRaise = 15.0f;           // log2 units: the running maximum is raised when a weight passes 2^15
 constexpr float kTop = 7.0f;              // a new maximum is 2^7
 constexpr float kLeast = 3.5527136788005009e-15f;  // 2^-48, the least s
+constexpr int kOver = 24;  // position channels of 2^(15 + 24), times 64 keys' below 2^82 s, are sums below 2^127
 
 template <int DQK, int NH>
 struct Smem {
@@ -683,17 +686,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_mla_quant_kernel(const __gr
           continue;
         }
         uint4 v[3];
-        uint32_t top = 0;
+        uint32_t top[2] = {0, 0};  // of the first 512 channels, of the position channels
 #pragma unroll
         for (int x = 0; x < 3; ++x) {
           const int u = lane + 32 * x;
           v[x] = u < UNITS ? lds16(raw_at(hh, u)) : make_uint4(0, 0, 0, 0);
-          top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[x].x & 0x7fff7fffu, v[x].y & 0x7fff7fffu),
-                                       __vmaxu2(v[x].z & 0x7fff7fffu, v[x].w & 0x7fff7fffu)));
+          top[x / 2] = __vmaxu2(top[x / 2], __vmaxu2(__vmaxu2(v[x].x & 0x7fff7fffu, v[x].y & 0x7fff7fffu),
+                                                     __vmaxu2(v[x].z & 0x7fff7fffu, v[x].w & 0x7fff7fffu)));
         }
         __syncwarp();
-        const uint32_t most = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-        const int e = max((int)(most >> 7) - 127, -112);
+        auto exponent = [&](uint32_t t) {
+          return (int)(__reduce_max_sync(0xffffffffu, max(t & 0xffffu, t >> 16)) >> 7) - 127;
+        };
+        int e = max(exponent(top[0]), -112);
+        if (ROPE) e = max(e, exponent(top[1]) - kOver);
         const float by = pow2(14 - e);
         if (lane == 0) s_col[(run & 1) * 64 + hh] = pow2(e - 14) * p.sl2e;
 #pragma unroll
