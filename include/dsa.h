@@ -674,7 +674,8 @@ dsa_status_t dsa_paged_dequantize(const uint8_t* cache, const int32_t* block_tab
  * 2^-31 of a, the row's largest one among the first 512 (2^-24 of its largest position channel where that is
  * more); smaller ones are off by 2^-39 a at most.  A weight has 11 bits (down to 2^-32 of the largest weight
  * times s).  8 bits: a query row counts to 2^-17 of its largest channel among the first 512, a weight to
- * 2^-11 of itself (2^-28 of the largest weight times s).
+ * 2^-11 of itself (2^-28 of the largest weight times s).  The output's sums are 6
+ * additions for 64 (8 bits) or 96 (4 bits) positions of a CTA's share, each off by 2^-23 of the sum at most.
  *  cache        device bytes [num_pages, page_size, dsa_paged_quant_row_bytes(Dqk, 512, bits)], 16-byte aligned
  *  bits         8 or 4
  *  workspace    >= dsa_paged_mla_quant_workspace_size() bytes, whatever the sizes

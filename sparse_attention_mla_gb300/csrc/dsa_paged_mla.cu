@@ -837,7 +837,7 @@ extern "C" dsa_status_t dsa_paged_mla(const dsa_bf16_t* q, const dsa_bf16_t* cac
     if ((st = make_map_2d_bf16(&map, cache, (uint64_t)num_pages * page_size, Dqk, Dqk, 64, p.box)) != DSA_OK) return st;
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // 16 columns while all rows of a request (or of a list) fit: fewer products of zero columns, a longer ring
+  // 16 columns where a request has no more rows on the average (or a list): fewer products of zero columns, a longer ring
   const int64_t rows = (int64_t)H * (topk_idx ? 1 : (N + B - 1) / B);
   if (rows <= 16) st = Dqk == 576 ? pmla::launch<576, 16>(p, map, ctas, s) : pmla::launch<512, 16>(p, map, ctas, s);
   else st = Dqk == 576 ? pmla::launch<576, 64>(p, map, ctas, s) : pmla::launch<512, 64>(p, map, ctas, s);

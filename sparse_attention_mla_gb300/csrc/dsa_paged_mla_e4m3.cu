@@ -14,23 +14,24 @@
 //    With less a long tail far below one position is off as a whole: its weights are alike, and so are their errors.
 // Position channels are multiplied in bf16 and added by the softmax, since s_p must not reach them.
 //
-// Split of the work as in dsa_paged_groups.cuh, with tiles of 64 positions and groups of 64 rows, or of 16 while all rows of a
-// request (or a list) fit.  A tile:
+// Split of the work as in dsa_paged_groups.cuh, with tiles of 64 positions and groups of 64 rows, or of 16 where a request has
+// no more on the average, or a list.  A tile:
 //  - 64 rows: S[row, key] = Q K^T with hi and lo of the queries as the 128 lanes (M = 128, N = 64 keys), so that a thread of
 //    the softmax has keys of one row.  16 rows: S^T[key, row] = K Q^T (M = 64), hi and lo side by side, which keeps all warps
 //    busy; with 64 rows it took the tensor core, whose M = 64 runs at half its rate, 2000 cycles a tile in place of 1300.
 //  - an online softmax with a lazily raised maximum;
-//  - O^T[channel, row] += V^T W^T (M = 128 channels, K = 32 keys, the weights' parts one after the other into the same columns).  The codes of 128
-//    channels of a key are a row of 128 bytes, which is K-major for the first product and M-major for the second.
+//  - O^T[channel, row] += V^T W^T (M = 128 channels, K = 32 keys, the weights' parts one after the other into the same
+//    columns).  The codes of 128 channels of a key are a row of 128 bytes, which is K-major for the first product and M-major
+//    for the second.
 //
-// What bounds it: 64 requests of 4000 to 16384 positions, 64 heads: 136 us (122 with weights of two parts, e5m2 and e4m3,
+// What bounds it: 64 requests of 4000 to 16384 positions, 64 heads: 133 us (122 with weights of two parts, e5m2 and e4m3,
 // which held 2^-15 of the largest), of which 10 pass before the first scores (cutting the line, the queries), 15 with the
-// launches and the joining; the 430 MB of rows are read at 3.9 TB/s in between, where a copy reaches 6.8.  A tile takes 2700
-// cycles, and its place in the ring (three tiles of 40 KB beside 72 KB of queries) is in use for 9200: 2000 for its copies, 1900
-// for S, 2300 for the softmax, 3000 for P.V, which is issued behind the next tiles' S; the products share shared memory's 128
-// bytes a cycle (260 KB a tile).  Measured beside it, with weights of two parts: the same rows converted to fp16 as the 4-bit
-// kernel does, 220 us; queries in TMEM and four tiles in the ring, 136 (queries that a thread loads by its row cost 13 us a run);
-// copies by TMA boxes, 206.
+// launches and the joining; the 430 MB of rows are read at 4.0 TB/s in between, where a copy reaches 6.8.  A tile takes 2700
+// cycles, and its place in the ring (three tiles of 40 KB beside 72 KB of queries) is in use for 9200: 2000 for its copies,
+// 1900 for S, 2300 for the softmax, 3000 for P.V, which is issued behind the next tiles' S; the products share shared memory's
+// 128 bytes a cycle (260 KB a tile; with the copies and the softmax 82 % of its cycles are taken).  Measured beside it, with
+// weights of two parts: the same rows converted to fp16 as the 4-bit kernel does, 220 us; queries in TMEM and four tiles in
+// the ring, 136 (queries that a thread loads by its row cost 13 us a run); copies by TMA boxes, 206.
 //
 // Warps: 0 issues S, the next 16 (or 8) softmax and epilogue, four copy tiles into the ring, one issues P.V, one announces the
 // runs of tiles that the CTA's range consists of.
@@ -50,7 +51,7 @@ using namespace pgroups;
 constexpr int kTile = 64;
 constexpr int kGather = 4;       // warps that copy
 constexpr float kRaise = 15.0f;    // log2 units: the running maximum is raised when a weight passes 2^15 (e5m2 ends at 1.75 2^15)
-constexpr float kTop = 11.0f;      // a new maximum is 2^11 (2^9: fewer rescales, 133 us in place of 136, and four times the floor)
+constexpr float kTop = 11.0f;      // a new maximum is 2^11 (2^9: fewer rescales, 2 % less time at 64 x 16384; four times the floor)
 constexpr float kMost = 32768.0f;  // 2^kRaise
 constexpr float kLeast = 3.5527136788005009e-15f;  // 2^-48, the least s
 
@@ -342,7 +343,8 @@ __global__ void __launch_bounds__(Smem<DQK, NH>::THREADS, 1) paged_mla_e4m3_kern
         // W: a row for each row of the group, keys along K
         const uint64_t pb = sdesc_sw128(p0, 16, 1024) + (uint64_t)(uint32_t)((i & 1) * (L::P_BLOCK >> 4));
         constexpr int kSecond = ROWS ? 64 >> 4 : NH * 128 >> 4, kStep = 2;
-        const uint64_t pc = ROWS ? sdesc_sw128(p0 + 2 * L::P_BLOCK, 16, 1024) + (uint64_t)(uint32_t)((i & 1) * (64 >> 4)) : pb + (64 >> 4);
+        const uint64_t pc = ROWS ? sdesc_sw128(p0 + 2 * L::P_BLOCK, 16, 1024) + (uint64_t)(uint32_t)((i & 1) * (64 >> 4))
+                                 : pb + (64 >> 4);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const uint64_t a = va + m * (L::CHUNK >> 4);

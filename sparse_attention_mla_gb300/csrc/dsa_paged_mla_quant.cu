@@ -14,19 +14,20 @@
 // largest of all: one large position channel would take the others out of fp16, which count where s is large.  Where a position
 // channel is more than 2^kOver of the others' largest, it takes part for 2^-kOver of it, so that the scores do not overflow.
 //
-// Split of the work as in dsa_paged_groups.cuh, with tiles of 96 positions and groups of NH = 64 columns, or of 16 while all
-// rows of a request (or a list) fit.  A tile: two warps copy its rows as they are to shared memory; 12 warps take the codes from
-// there to registers and form fp16, which is the A operand of S^T[position, column] = V Q^T and, as V^T, of O^T[channel, column]
-// += V^T W^T.  Two quarters of the channels are written to TMEM, position by lane, before P.V of the tile before has left
-// shared memory; one quarter to shared memory, from where both products read it, and the last to TMEM; then the three quarters
-// in TMEM to shared memory too, while S^T is under way.  Then the same warps do the softmax, a position a thread.  96
-// positions, since an fp16 tile of 128, its queries and W leave no room for the next tile's rows as they come.
+// Split of the work as in dsa_paged_groups.cuh, with tiles of 96 positions and groups of NH = 64 columns, or of 16 where a
+// request has no more rows on the average, or a list.  A tile: two warps copy its rows as they are to shared memory; 12 warps
+// take the codes from there to registers and form fp16, which is the A operand of S^T[position, column] = V Q^T and, as V^T, of
+// O^T[channel, column] += V^T W^T.  Two quarters of the channels are written to TMEM, position by lane, before P.V of the tile
+// before has left shared memory; one quarter to shared memory, from where both products read it, and the last to TMEM; then the
+// three quarters in TMEM to shared memory too, while S^T is under way.  Then the same warps do the softmax, a position a
+// thread.  96 positions, since an fp16 tile of 128, its queries and W leave no room for the next tile's rows as they come (with
+// 16 columns, which take the same form, 57 KB are free).
 //
 // A thread's four blocks of 16 channels lie side by side in a row (one load for four scales), but 16 channels apart in every
 // 128 of the products: O^T's row 128 m + 16 y + e is channel 64 y + 16 m + e, and the queries' channels follow.
 //
-// What bounds it: 64 requests of 4000 to 16384 positions, 64 heads: 158 us, where the same over bf16 rows of 2.7 times the
-// bytes takes 159 and over 8 bits (dsa_paged_mla_e4m3.cu, which converts nothing) 121.  A tile takes about 5500 cycles, of which
+// What bounds it: 64 requests of 4000 to 16384 positions, 64 heads: 159 us, where the same over bf16 rows of 2.7 times the
+// bytes takes 161 and over 8 bits (dsa_paged_mla_e4m3.cu, which converts nothing) 133.  A tile takes about 5500 cycles, of which
 // the warps convert for 3900 and do the softmax for 1400, never waiting for a product; shared memory moves 424 KB (rows in
 // and out 84, V in and out 192, W 60, queries 88), 3400 cycles at 128 bytes each.  Measured beside it: with 64 registers
 // a thread and twice the warps 209 us, the next tile's rows in registers during the softmax 171 (half of them: 163), loads by the
@@ -1032,7 +1033,10 @@ extern "C" dsa_status_t dsa_paged_mla_quant(const dsa_bf16_t* q, const uint8_t* 
   p.partial = reinterpret_cast<float*>(ws + pmlaq::kPartialOff);
   p.wait_limit = wait_limit_cycles();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // 16 columns while all rows of a request (or of a list) fit
+  // 16 columns where a request has no more rows on the average (the host does not know cu_q), or a list: 96 requests to 4097,
+  // 8 heads, 61 us and 72 with 64 columns at 4 bits, 52 and 65 at 8; 8 x 8191, 16 heads, 30 and 31, 24 and 28.  An uneven
+  // batch under that average pays for it: one chunk of 128 tokens, 16384 positions, beside 127 single tokens of 4096 takes 280 us
+  // at 4 bits and 212 at 8, one of 130, which takes the average past 16 rows, 185 and 152.
   const int64_t rows = (int64_t)H * (topk_idx ? 1 : (N + B - 1) / B);
   if (bits == 8) st = launch_paged_mla_e4m3(p, p.q, cache, Dqk, p.sl2e, rows <= 16, ctas, s);
   else if (rows <= 16) st = Dqk == 576 ? pmlaq::launch<576, 16>(p, ctas, s) : pmlaq::launch<512, 16>(p, ctas, s);

@@ -4,7 +4,7 @@
 
 namespace dsa {
 
-// The attention's pieces over a cache of 8 bits, without the joining; few: no request or list has more than 16 rows.
+// The attention's pieces over a cache of 8 bits, without the joining; few: groups of 16 rows, in place of 64.
 dsa_status_t launch_paged_mla_e4m3(const pgroups::GroupParams& g, const __nv_bfloat16* q, const uint8_t* cache, int Dqk,
                                    float scale_log2e, bool few, int ctas, cudaStream_t s);
 

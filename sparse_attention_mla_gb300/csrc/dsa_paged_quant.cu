@@ -5,7 +5,9 @@
 // how a quotient was rounded (see nearest_side).  Both directions are bound by memory: a row is read once and written
 // once, 1152 + 420 bytes for a latent in 4 bits.  Reading 12 requests of 7500 to 30000 latents of 4 bits back: 66 us, 5.7
 // TB/s, where a copy reaches 6.8 (8 channels a thread in place of 16, and stores of 16 bytes in place of 32: 73.7); writing
-// 8191 latents of 4 bits and reading them: 10.6 us, two kernels of little more than their launch.
+// 8191 latents of 4 bits and reading them: 11.0 us, two kernels of little more than their launch.  Writing 131072 rows of 128
+// channels of 8 bits: 13.8 us where their bytes take 7.6, 131072 latents 49 (8 bits; bytes 35) and 58 (4 bits; bytes 30): a row's
+// loads wait for another one, its place, and a thread has one row and is gone.
 #include <climits>
 
 #include "dsa_host.h"
@@ -398,8 +400,8 @@ extern "C" dsa_status_t dsa_paged_dequantize(const uint8_t* cache, const int32_t
   p.err = reinterpret_cast<int*>(workspace);
   const uintptr_t lie = reinterpret_cast<uintptr_t>(out) | (N == 1 ? 0 : (uintptr_t)out_stride_t * 2);
   p.align = lie % 32 == 0 ? 32 : lie % 16 == 0 ? 16 : 2;
-  // 64 rows a CTA while that leaves four an SM (units of 8 channels: 131104 rows of 128, written and read, 24.8 us, 28.1 with 32;
-  // 12 x 30000 of 576 read 73 and 74, with 128 78, with 256 90)
+  // 64 rows a CTA while that leaves four an SM (131104 rows of 128, written and read, 24.0 us, 26.8 with 32; 12 x 30000 of 576 read
+  // 65.8 and 65.0; 8191 of 576, written and read, 12.3 and 11.0)
   p.rows = N / 64 >= 4 * pquant::kSms ? 64 : 32;
   const unsigned blocks = (unsigned)(((int64_t)N + p.rows - 1) / p.rows);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
